@@ -295,6 +295,126 @@ laplex_status laplex_gram_weighted(const float* a_sorted, const uint32_t* perm_a
                                    const uint32_t* perm_b, uint64_t k, const float* D, uint64_t row_begin, uint64_t row_count,
                                    float* M, uint64_t ldm, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Layers of sequence models around the same recurrence: decayed linear
+ * attention, layer norm, and embedding.  Their tensors are float32 or
+ * bfloat16 (one type per call), states, statistics and parameter sums are
+ * float32.  The conventions at the top of this header hold, with these
+ * sizes: up to 2^31 - 1 tokens, up to 256 channels per head.
+ * --------------------------------------------------------------------- */
+enum { LAPLEX_F32 = 0, LAPLEX_BF16 = 1 };
+
+/* Shape of a decayed-attention call.  Tokens are packed: token t of head h of
+ * q starts at q + t * q_token + h * q_head elements (so that q, k and v may be
+ * slices of one projection), its channels are contiguous; strides are >= 0.
+ * Sequence s holds tokens [offsets[s], offsets[s + 1]); offsets (DEVICE,
+ * int32, seqs + 1 of them, nondecreasing) NULL means seqs sequences of
+ * tokens / seqs tokens each.  Tokens before offsets[0] or from offsets[seqs]
+ * on belong to no sequence: their output and gradient rows are zero.
+ * Sequences may be empty.  Query head h reads key/value head
+ * h / (heads / kv_heads). */
+typedef struct {
+  int32_t dtype;                       /* LAPLEX_F32 or LAPLEX_BF16: q, k, v, o and their gradients */
+  uint32_t seqs, heads, kv_heads;      /* kv_heads divides heads */
+  uint32_t dk, dv;                     /* channels of q and k, of v and o: 1 .. 256 */
+  uint64_t tokens;                     /* tokens of all sequences */
+  const int32_t* offsets;              /* DEVICE, or NULL: equal lengths */
+  const float* rate;                   /* DEVICE: heads decay rates, >= 0 (+Inf: a token sees only itself) */
+  float scale;                         /* factor of every output */
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;  /* strides in elements */
+} laplex_attn_shape;
+
+enum { LAPLEX_ATTN_FORWARD = 0, LAPLEX_ATTN_BACKWARD = 1 };
+
+/* Bytes of workspace a decayed-attention call needs (pass: LAPLEX_ATTN_FORWARD
+ * or LAPLEX_ATTN_BACKWARD; offsets, rate and strides are not looked at).
+ * Returns 0 when the shape is out of range. */
+size_t laplex_decay_attn_workspace_bytes(int pass, const laplex_attn_shape* shape);
+
+/* Decayed linear attention: the lower half of the Laplace kernel (section 2.2,
+ * symmetric case) on the anchors a_t = rate_h t of a sequence's tokens, each
+ * pair weighted with the product of its query and key,
+ *     o_i = scale sum_{j <= i} exp(-rate_h (i - j)) (q_i . k_j) v_j,
+ * whose scan carries the dk x dv matrix
+ *     S_t = exp(-rate_h) S_{t-1} + k_t v_t^T,    o_t = scale q_t S_t.
+ * state_in: NULL (zero) or S before each sequence's first token (seqs x heads x
+ * dk x dv floats); state_out: NULL or S after each sequence's last token (same
+ * shape; an empty sequence's is its state_in).  o: tokens x heads x dv,
+ * contiguous.  A non-finite value in token j reaches o_i only for i >= j of its
+ * own sequence, where it gives non-finite outputs.
+ * ws: laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_FORWARD, shape) bytes. */
+laplex_status laplex_decay_attn(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
+                                const float* state_in, float* state_out, void* o, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/* Backward of laplex_decay_attn for the upstream gradients go = dL/do (tokens
+ * x heads x dv, contiguous) and dstate_out = dL/dstate_out (NULL: zero).  With
+ * w(n) = exp(-rate_h n) and a sequence of L tokens,
+ *     dq_i = scale [sum_{j<=i} w(i-j) (go_i . v_j) k_j + w(i+1) S_in go_i]
+ *     dk_j = scale sum_{i>=j} w(i-j) (go_i . v_j) q_i + w(L-1-j) dS_out v_j
+ *     dv_j = scale sum_{i>=j} w(i-j) (q_i . k_j) go_i + w(L-1-j) dS_out^T k_j
+ *     dS_in = w(L) dS_out + scale sum_i w(i+1) q_i go_i^T
+ * and drate_h = -sum of every one of these pair terms of head h times its lag
+ * (the argument of its w) over all sequences.  dk and dv of a shared head are
+ * summed over its query heads.  Nothing of the forward call is needed; its
+ * states are formed again.  dq (tokens x heads x dk), dk (tokens x kv_heads x
+ * dk), dv (tokens x kv_heads x dv): contiguous; drate: heads floats, or NULL;
+ * dstate_in: NULL or seqs x heads x dk x dv floats.  Sums are taken in a fixed
+ * order: a call repeated gives the same bits.
+ * ws: laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_BACKWARD, shape) bytes. */
+laplex_status laplex_decay_attn_backward(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
+                                         const void* go, const float* state_in, const float* dstate_out, void* dq, void* dk,
+                                         void* dv, float* drate, float* dstate_in, void* ws, size_t ws_bytes,
+                                         hipStream_t stream);
+
+/* One token for each of `seqs` sequences (shape->tokens == seqs, offsets not
+ * looked at), the recurrent form for decoding: row r updates its state in
+ * place, S = exp(-rate_h) S + k_r v_r^T, and o_r = scale q_r S.  state: pool x
+ * heads x dk x dv floats; slots: NULL (row r has state r; seqs <= pool) or a
+ * DEVICE array of seqs int32, row r's state.  A slot outside [0, pool) marks a
+ * place without a sequence: its o row is zero and no state changes.  Two rows
+ * of one call must not name the same slot. */
+laplex_status laplex_decay_attn_step(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
+                                     const int32_t* slots, uint32_t pool, float* state, void* o, hipStream_t stream);
+
+/* Layer norm of `rows` rows of `width` contiguous elements:
+ *     y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps),
+ * mean and (biased) variance over the row, in float32.  weight, bias: `width`
+ * elements of the tensors' type, or NULL (1 and 0).  mean, rstd: `rows` floats
+ * each (outputs), which the backward reads; either may be NULL. */
+laplex_status laplex_layer_norm(int dtype, uint64_t rows, uint32_t width, const void* x, const void* weight, const void* bias,
+                                float eps, void* y, float* mean, float* rstd, hipStream_t stream);
+
+/* Bytes of workspace of laplex_layer_norm_backward. */
+size_t laplex_layer_norm_workspace_bytes(uint64_t rows, uint32_t width);
+
+/* Backward of laplex_layer_norm for the upstream gradient dy: with z = (x -
+ * mean) rstd and u = dy weight,
+ *     dx = rstd (u - mean(u) - z mean(u z)),   dweight = sum_rows dy z,   dbias = sum_rows dy.
+ * dweight, dbias: `width` floats each, or NULL; the rows are added in a fixed
+ * order.  rows == 0 sets them to zero. */
+laplex_status laplex_layer_norm_backward(int dtype, uint64_t rows, uint32_t width, const void* x, const void* dy,
+                                         const float* mean, const float* rstd, const void* weight, void* dx, float* dweight,
+                                         float* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Embedding lookup y_t = scale table[id_t]: ids: `tokens` integers of
+ * id_bytes (4 or 8) bytes; table: vocab x width; y: tokens x width.  An id
+ * outside [0, vocab) (padding) gives a zero row. */
+laplex_status laplex_embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* table, uint32_t vocab,
+                               uint32_t width, float scale, void* y, hipStream_t stream);
+
+/* Bytes of workspace of laplex_embedding_backward; 0 when out of range. */
+size_t laplex_embedding_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t width);
+
+/* Gradient of the whole table for the upstream gradient dy (tokens x width,
+ * of type dtype):  dtable_v = scale sum_{t: id_t = v} dy_t, zero where v does
+ * not occur.  The tokens are sorted by id (laplex_sort_anchors' stable
+ * sort) and each row's terms added in the order of their tokens, in float32,
+ * rounded once to table_dtype (dtype or LAPLEX_F32). vocab < 2^30. */
+laplex_status laplex_embedding_backward(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
+                                        uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, void* ws,
+                                        size_t ws_bytes, hipStream_t stream);
+
 /* Short English description of a status code (static storage). */
 const char* laplex_status_string(laplex_status s);
 

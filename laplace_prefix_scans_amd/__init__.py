@@ -16,6 +16,16 @@ not been built the calls raise -- there is no fallback.
     dxb, da, db = laplex_backward_general(a_sorted, perm, b_sorted, perm_b, xb, g)
     dx, da, dphi = laplex_backward_phased(a_sorted, perm, phi, x, g)
     M = laplex_gram_weighted(a_sorted, perm, b_sorted, perm_b, D)  # A diag(D) A^T
+
+Layers of sequence models around the same recurrence (float32 or bfloat16):
+
+    o = laplex_decay_attn(q, k, v, rate)             # o_i = sum_{j<=i} exp(-rate (i-j)) (q_i . k_j) v_j
+    dq, dk, dv, drate, _ = laplex_decay_attn_backward(q, k, v, rate, go)
+    o = laplex_decay_attn_step(q, k, v, rate, state)  # one token, the state updated in place
+    y, mean, rstd = laplex_layer_norm(x, weight, bias)
+    dx, dw, db = laplex_layer_norm_backward(x, dy, mean, rstd, weight)
+    y = laplex_embedding(ids, table, scale)
+    dtable = laplex_embedding_backward(ids, dy, vocab, scale)
 """
 from ._binding import (  # noqa: F401
     LAPLEX_OP_GENERAL,
@@ -53,4 +63,14 @@ from ._binding import (  # noqa: F401
     profile_launches,
     route_buffer,
     workspace,
+)
+from ._layers import (  # noqa: F401
+    laplex_decay_attn,
+    laplex_decay_attn_backward,
+    laplex_decay_attn_step,
+    laplex_decay_attn_workspace_bytes,
+    laplex_embedding,
+    laplex_embedding_backward,
+    laplex_layer_norm,
+    laplex_layer_norm_backward,
 )

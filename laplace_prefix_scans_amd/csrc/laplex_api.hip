@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "../../include/laplex.h"
+#include "laplex_host.hpp"
 #include "laplex_kernels.hpp"
 
 namespace laplex {
@@ -17,42 +18,6 @@ using namespace laplex;
 constexpr uint64_t kMaxLen = 0xFFFFFFFFull;  // uint32 permutations
 constexpr uint32_t kMaxCols = 1u << 16;
 constexpr uint64_t kGramMaxLen = 65535ull * 1024;  // columns of the Gram fill grid
-
-// Carves 256-byte aligned regions out of a workspace (base 0: sizing only).
-struct Carver {
-  uintptr_t base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(reinterpret_cast<uintptr_t>(b)) {}
-  template <typename T>
-  T* take(size_t bytes) {
-    off = (off + 255) & ~size_t(255);
-    T* p = reinterpret_cast<T*>(base + off);
-    off += bytes;
-    return p;
-  }
-};
-
-SortWorkspace carve_sort(void* ws, uint64_t n) {
-  Carver c(ws);
-  SortWorkspace w;
-  w.header = c.take<uint32_t>(kSortHeaderBytes);
-  w.hist = w.header + kSortHistOffset / 4;
-  w.offsets = w.header + kSortOffsOffset / 4;
-  w.status = c.take<void>(sort_status_bytes(n));  // directly after the header
-  for (int i = 0; i < 2; ++i) w.kv[i] = c.take<uint2>(n * 8);
-  w.tcount = c.take<uint32_t>(sort_tiles_alloc(n) * 256 * 4);
-  w.gsum = c.take<uint32_t>((size_t)kHistMaxBlocks * 256 * 4);
-  return w;
-}
-size_t sort_bytes(uint64_t n) {
-  Carver c(nullptr);
-  c.take<uint32_t>(kSortHeaderBytes);
-  c.take<void>(sort_status_bytes(n));
-  for (int i = 0; i < 2; ++i) c.take<uint2>(n * 8);
-  c.take<uint32_t>(sort_tiles_alloc(n) * 256 * 4);
-  c.take<uint32_t>((size_t)kHistMaxBlocks * 256 * 4);
-  return (c.off + 255) & ~size_t(255);
-}
 
 // rows_in: length of the gathered input (n symmetric, k general); rows_out:
 // outputs (n); len: scanned length.  Buffers for moving x and y along a sort
@@ -219,17 +184,6 @@ SortGeneralWorkspace carve_sort_general(void* ws, uint64_t k, uint32_t m, size_t
   if (total) *total = (c.off + 255) & ~size_t(255);
   return w;
 }
-
-bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
-bool overlaps(const void* p, size_t pb, const void* q, size_t qb) {
-  if (!p || !q || pb == 0 || qb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(p), a1 = a0 + pb;
-  const uintptr_t b0 = reinterpret_cast<uintptr_t>(q), b1 = b0 + qb;
-  return a0 < b1 && b0 < a1;
-}
-
-laplex_status from_hip(hipError_t e) { return e == hipSuccess ? LAPLEX_OK : LAPLEX_ERR_HIP; }
 
 }  // namespace
 
