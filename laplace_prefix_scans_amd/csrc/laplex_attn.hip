@@ -1,155 +1,149 @@
-// Decayed linear attention: the recurrence S_u = w S_{u-1} + y_u z_u^T,
-// out_u = x_u S_u of a matrix-valued carry.
-#include "laplex_layers.hpp"
-#include "laplex_layers_device.hpp"
+// Decayed linear attention: the passes over a sequence (segments, their join,
+// the launches), the sums over shared heads, and the single-token form.
+#include "laplex_attn_chunk.hpp"
 
 namespace laplex {
 
-// Tokens [first, last) of a packed sequence, clamped into the buffer whatever the offsets hold.
-__device__ __forceinline__ void seq_range(const int32_t* offsets, uint64_t tokens, uint32_t seqs, uint32_t s, int64_t& first,
-                                          int64_t& last) {
-  if (!offsets) {
-    const int64_t len = (int64_t)(tokens / seqs);
-    first = s * len;
-    last = first + len;
-    return;
-  }
-  const int64_t t = (int64_t)tokens;
-  first = min(max((int64_t)offsets[s], (int64_t)0), t);
-  last = min(max((int64_t)offsets[s + 1], first), t);
-}
+template <>
+void attn_chunk_launch<bf16>(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
+template <>
+void attn_chunk_launch<float>(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
 
-constexpr int kCols = 64;  // columns of the carry per block
-constexpr int kRows = 4;   // threads per column
-constexpr int kMaxK = 256;
-
-// Token by token: thread (c, r) holds rows r, r + 4, .. of column c of the carry.
-template <typename T, bool RATE>
-__global__ __launch_bounds__(kCols * kRows) void k_attn_scan(AttnPass p) {
-  __shared__ float xs[kMaxK], ys[kMaxK], red[2][kRows][kCols];
-  const int c = threadIdx.x % kCols, r = threadIdx.x / kCols;
-  const uint32_t h = blockIdx.y, col = blockIdx.z * kCols + c;
-  const bool live = col < p.V;
-  const int K = (int)p.K;
-  auto put = [&](int64_t t, float v) {
-    const uint64_t at = ((uint64_t)t * p.heads + h) * p.V + col;
-    if (p.out_f32)
-      static_cast<float*>(p.out)[at] = v;
-    else
-      static_cast<T*>(p.out)[at] = from_f32<T>(v);
-  };
-  int64_t first, last;
-  if (blockIdx.x >= p.seqs) {  // tokens outside every sequence
-    const int64_t lo = min(max((int64_t)p.offsets[0], (int64_t)0), (int64_t)p.tokens);
-    int64_t f, hi;
-    seq_range(p.offsets, p.tokens, p.seqs, p.seqs - 1, f, hi);
-    if (live && r == 0 && p.out) {
-      for (int64_t t = 0; t < lo; ++t) put(t, 0.f);
-      for (int64_t t = hi; t < (int64_t)p.tokens; ++t) put(t, 0.f);
+// Turns the segments' own final states into the states before each segment,
+// S_k+1 = w(L) S_k + T_k, in place; thread per element.  With lag-weighted
+// states, D_k+1 = w(L) (D_k + L S_k) + E_k.
+template <bool RATE>
+__global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
+  const AttnPass& p = a.p;
+  const uint64_t per = (uint64_t)p.K * p.V, at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t h = blockIdx.y;
+  if (at >= per) return;
+  const int64_t L = a.g.seg_len;
+  const AttnDecay w = attn_decay(attn_rate(p.rate[h]), L);
+  constexpr int N = RATE ? 8 : 16;  // loads in flight
+  for (uint32_t s = blockIdx.z; s < p.seqs; s += gridDim.z) {
+    const int64_t i = (int64_t)s + (a.g.offsets ? 1 : 0), first = seq_bound(a.g, i), len = seq_bound(a.g, i + 1) - first;
+    const int64_t nb = (len + L - 1) / L - 1;  // boundaries inside the sequence
+    if (nb < 1) continue;
+    float cur = 0.f, d = 0.f;
+    if (p.s_in) {
+      const uint64_t row = at / p.V, col = at % p.V;
+      cur = p.s_in[((uint64_t)s * p.heads + h) * per + (p.s_trans ? col * p.K + row : at)];
     }
-    return;
-  }
-  seq_range(p.offsets, p.tokens, p.seqs, blockIdx.x, first, last);
-  const float rate = attn_rate(p.rate[h]), w1 = decay(-rate);
-  const uint64_t sbase = ((uint64_t)blockIdx.x * p.heads + h) * (uint64_t)p.K * p.V;
-  auto sat = [&](int row) { return sbase + (p.s_trans ? (uint64_t)col * p.K + row : (uint64_t)row * p.V + col); };
-  float s[kMaxK / kRows], d[RATE ? kMaxK / kRows : 1];
+    auto pos = [&](int64_t k) { return ((uint64_t)(first / L + k) * p.heads + h) * per + at; };  // boundary k = 1 .. nb
+    for (int64_t k0 = 1; k0 <= nb; k0 += N) {
+      float t[N], e[RATE ? N : 1];
 #pragma unroll
-  for (int i = 0; i < kMaxK / kRows; ++i) {
-    const int row = i * kRows + r;
-    s[i] = (live && row < K && p.s_in) ? p.s_in[sat(row)] : 0.f;
-    if constexpr (RATE) d[i] = 0.f;
-  }
-  const T *x = static_cast<const T*>(p.x.p) + (int64_t)(h / p.x.div) * p.x.head,
-          *y = static_cast<const T*>(p.y.p) + (int64_t)(h / p.y.div) * p.y.head,
-          *z = static_cast<const T*>(p.z.p) + (int64_t)(h / p.z.div) * p.z.head;
-  double dr = 0.0;
-  for (int64_t u = 0; u < last - first; ++u) {
-    const int64_t t = p.reverse ? last - 1 - u : first + u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < K; i += kCols * kRows) {
-      xs[i] = to_f32(x[t * p.x.token + i]);
-      ys[i] = to_f32(y[t * p.y.token + i]);
-    }
-    __syncthreads();
-    const float zv = live ? to_f32(z[t * p.z.token + col]) : 0.f;
-    const float w = (p.reverse && u == 0) ? 1.f : w1;
-    float acc = 0.f, accd = 0.f;
+      for (int k = 0; k < N; ++k) {
+        const uint64_t q = pos(min(k0 + k, nb));
+        t[k] = a.bound[q];
+        if constexpr (RATE) e[k] = a.bound_d[q];
+      }
 #pragma unroll
-    for (int i = 0; i < kMaxK / kRows; ++i) {
-      const int row = i * kRows + r;
-      if (row < K) {
+      for (int k = 0; k < N; ++k) {
+        if (k0 + k > nb) break;
+        const uint64_t q = pos(k0 + k);
         if constexpr (RATE) {
-          d[i] = w * (d[i] + s[i]);
-          accd = fmaf(xs[row], d[i], accd);
+          d = w.of(fmaf((float)L, cur, d)) + e[k];
+          a.bound_d[q] = d;
         }
-        s[i] = fmaf(w, s[i], p.c_add * ys[row] * zv);
-        acc = fmaf(xs[row], s[i], acc);
+        cur = w.of(cur) + t[k];
+        a.bound[q] = cur;
       }
-    }
-    red[0][r][c] = acc;
-    red[1][r][c] = accd;
-    __syncthreads();
-    if (r == 0 && live) {
-      // c_in == c_pair / c_add in every pass, so the carry's output factor is c_in
-      if (p.out) put(t, p.c_in * (red[0][0][c] + red[0][1][c] + red[0][2][c] + red[0][3][c]));
-      if constexpr (RATE) {
-        const T* dot = static_cast<const T*>(p.dot) + (int64_t)(h / p.dot_view.div) * p.dot_view.head;
-        dr += (double)to_f32(dot[t * p.dot_view.token + col]) *
-              (double)(p.c_in * (red[1][0][c] + red[1][1][c] + red[1][2][c] + red[1][3][c]));
-      }
-    }
-  }
-  const float wf = (p.reverse && last > first) ? w1 : 1.f;
-#pragma unroll
-  for (int i = 0; i < kMaxK / kRows; ++i) {
-    const int row = i * kRows + r;
-    if (live && row < K) {
-      if (p.s_out) p.s_out[sat(row)] = wf * s[i];
-      if constexpr (RATE)
-        if (p.ds_out) dr += (double)d[i] * (double)p.ds_out[sat(row)];
-    }
-  }
-  if constexpr (RATE) {
-    __shared__ double all[kCols * kRows];
-    all[threadIdx.x] = dr;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      double sum = 0.0;
-      for (int i = 0; i < kCols * kRows; ++i) sum += all[i];
-      p.drate_part[((uint64_t)blockIdx.x * gridDim.z + blockIdx.z) * p.heads + h] = (float)-sum;
     }
   }
 }
 
-__global__ void k_attn_drate(const float* __restrict__ part, uint64_t parts, uint32_t heads, float* __restrict__ drate) {
-  const uint32_t h = blockIdx.x * blockDim.x + threadIdx.x;
-  if (h >= heads) return;
+// ------------------------------------------------------------------ launches
+struct AttnPlan {
+  int kp, nw;
+  uint32_t slices;
+  int64_t seg_len;
+  uint64_t slots, bounds;
+  bool split;
+};
+static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+  AttnPlan q;
+  q.kp = K <= 64 ? 64 : K <= 128 ? 128 : 256;
+  q.nw = V <= 64 && K <= 64 ? 2 : 4;
+  q.slices = (V + 32 * q.nw - 1) / (32 * q.nw);
+  const uint64_t blocks = q.nw == 2 ? 1024 : 512;  // two waves per SIMD
+  uint64_t len = std::max<uint64_t>(512, tokens * heads * q.slices / blocks);
+  len = (len + 63) / 64 * 64;
+  q.split = len < tokens;
+  if (!q.split) len = std::max<uint64_t>(64, (tokens + 63) / 64 * 64);
+  q.seg_len = (int64_t)len;
+  q.slots = tokens / len + seqs + 3;
+  q.bounds = q.split ? tokens / len + 1 : 0;
+  return q;
+}
+
+size_t attn_pass_bytes(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+  const AttnPlan q = attn_plan(seqs, heads, K, V, tokens);
+  return (size_t)q.bounds * heads * K * V * 4 * (rate ? 2 : 1);
+}
+uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+  const AttnPlan q = attn_plan(seqs, heads, K, V, tokens);
+  return q.slots * q.slices;
+}
+
+static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width, size_t e) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && token * e % 16 == 0 && head * e % 16 == 0 && width * e % 16 == 0;
+}
+
+hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
+  const bool rate = p.drate_part != nullptr, bf = p.dtype == LAPLEX_BF16;
+  const size_t e = bf ? 2 : 4;
+  const AttnPlan q = attn_plan(p.seqs, p.heads, p.K, p.V, p.tokens);
+  AttnChunkArgs a{};
+  a.p = p;
+  a.g = {p.offsets, p.tokens, p.seqs, q.seg_len};
+  a.slices = q.slices;
+  a.tiles = q.slots * p.heads * q.slices;
+  if (q.split) {
+    a.bound = static_cast<float*>(ws);
+    a.bound_d = a.bound + q.bounds * p.heads * p.K * p.V;
+  }
+  a.vec_x = aligned16(p.x.p, p.x.token, p.x.head, p.K, e);
+  a.vec_y = aligned16(p.y.p, p.y.token, p.y.head, p.K, e);
+  a.vec_z = aligned16(p.z.p, p.z.token, p.z.head, p.V, e);
+  a.vec_dot = rate && aligned16(p.dot, p.dot_view.token, p.dot_view.head, p.V, e);
+  a.vec_out = p.V % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  a.drate = p.drate_part;
+  auto run = [&](const char* name, bool full) {
+    LAPLEX_LAUNCH(name, p.tokens, s, {
+      if (bf) attn_chunk_launch<bf16>(a, q.kp, q.nw, full, rate, s);
+      else attn_chunk_launch<float>(a, q.kp, q.nw, full, rate, s);
+    });
+    return hipGetLastError();
+  };
+  hipError_t err;
+  if (q.split) {
+    if ((err = run("k_attn_chunk_state", false)) != hipSuccess) return err;
+    const dim3 grid((unsigned)(((uint64_t)p.K * p.V + 255) / 256), p.heads, std::min(p.seqs, 64u));
+    LAPLEX_LAUNCH("k_attn_join", q.bounds, s, rate ? k_attn_join<true><<<grid, 256, 0, s>>>(a) : k_attn_join<false><<<grid, 256, 0, s>>>(a));
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
+  return run("k_attn_chunk", true);
+}
+
+// drate_h = the sum of its partials in a fixed order
+__global__ __launch_bounds__(256) void k_attn_drate(const double* __restrict__ part, uint64_t parts, uint32_t heads,
+                                                    float* __restrict__ drate) {
+  __shared__ double sh[256];
+  const uint32_t h = blockIdx.x;
   double s = 0.0;
-  for (uint64_t i = 0; i < parts; ++i) s += (double)part[i * heads + h];
-  drate[h] = (float)s;
+  for (uint64_t i = threadIdx.x; i < parts; i += 256) s += part[i * heads + h];
+  sh[threadIdx.x] = s;
+  for (int off = 128; off; off >>= 1) {
+    __syncthreads();
+    if (threadIdx.x < off) sh[threadIdx.x] += sh[threadIdx.x + off];
+  }
+  if (threadIdx.x == 0) drate[h] = (float)sh[0];
 }
 
-size_t attn_pass_bytes(uint32_t, uint32_t, uint32_t, uint32_t, uint64_t) { return 0; }
-uint64_t attn_drate_parts(uint32_t seqs, uint32_t, uint32_t, uint32_t V, uint64_t) {
-  return (uint64_t)seqs * ((V + kCols - 1) / kCols);
-}
-
-hipError_t attn_drate_reduce(const float* part, uint64_t parts, uint32_t heads, float* drate, hipStream_t s) {
-  LAPLEX_LAUNCH("k_attn_drate", heads, s, k_attn_drate<<<(heads + 63) / 64, 64, 0, s>>>(part, parts, heads, drate));
-  return hipGetLastError();
-}
-
-hipError_t attn_pass(const AttnPass& p, void*, hipStream_t s) {
-  const dim3 grid(p.seqs + (p.offsets ? 1 : 0), p.heads, (p.V + kCols - 1) / kCols);
-  LAPLEX_LAUNCH("k_attn_scan", p.tokens, s, {
-    if (p.dtype == LAPLEX_BF16)
-      p.drate_part ? k_attn_scan<bf16, true><<<grid, kCols * kRows, 0, s>>>(p)
-                   : k_attn_scan<bf16, false><<<grid, kCols * kRows, 0, s>>>(p);
-    else
-      p.drate_part ? k_attn_scan<float, true><<<grid, kCols * kRows, 0, s>>>(p)
-                   : k_attn_scan<float, false><<<grid, kCols * kRows, 0, s>>>(p);
-  });
+hipError_t attn_drate_reduce(const double* part, uint64_t parts, uint32_t heads, float* drate, hipStream_t s) {
+  LAPLEX_LAUNCH("k_attn_drate", heads, s, k_attn_drate<<<heads, 256, 0, s>>>(part, parts, heads, drate));
   return hipGetLastError();
 }
 

@@ -12,6 +12,7 @@ using namespace laplex;
 
 constexpr uint64_t kMaxTokens = 0x7FFFFFFFull;  // int32 offsets
 constexpr uint32_t kMaxSeqs = 1u << 20, kMaxHeads = 65535, kMaxChannels = 256, kMaxWidth = 1u << 24;
+constexpr uint64_t kMaxBlocks = 1ull << 28;  // blocks of one launch, before column slices
 constexpr uint64_t kMaxRows = 0xFFFFFFFFull;
 constexpr uint32_t kMaxVocab = (1u << 30) - 1;
 
@@ -25,6 +26,7 @@ laplex_status check_shape(const laplex_attn_shape* a) {
   if (a->heads == 0 || a->kv_heads == 0 || a->heads % a->kv_heads != 0 || a->dk == 0 || a->dv == 0) return LAPLEX_ERR_ARG;
   if (a->tokens > kMaxTokens || a->seqs > kMaxSeqs || a->heads > kMaxHeads || a->dk > kMaxChannels || a->dv > kMaxChannels)
     return LAPLEX_ERR_SIZE;
+  if ((a->seqs + a->tokens / 64 + 3) * a->heads > kMaxBlocks) return LAPLEX_ERR_SIZE;
   return LAPLEX_OK;
 }
 
@@ -64,17 +66,17 @@ bool any_misaligned(const Extent (&v)[N], size_t a) {
 struct AttnWorkspace {
   void* pass;    // of one recurrence pass at a time
   float* sum;    // per query head gradients before they are added over a shared head
-  float* drate;  // partials of the rate gradient
+  double* drate; // partials of the rate gradient
 };
 AttnWorkspace carve_attn(void* ws, int pass, const laplex_attn_shape& a, size_t* total) {
   Carver c(ws);
   AttnWorkspace w{};
-  size_t b = attn_pass_bytes(a.seqs, a.heads, a.dk, a.dv, a.tokens);
-  if (pass == LAPLEX_ATTN_BACKWARD) b = std::max(b, attn_pass_bytes(a.seqs, a.heads, a.dv, a.dk, a.tokens));
+  size_t b = attn_pass_bytes(a.seqs, a.heads, a.dk, a.dv, a.tokens, false);
+  if (pass == LAPLEX_ATTN_BACKWARD) b = std::max(b, attn_pass_bytes(a.seqs, a.heads, a.dv, a.dk, a.tokens, true));
   w.pass = c.take<void>(b);
   if (pass == LAPLEX_ATTN_BACKWARD) {
     if (a.heads != a.kv_heads) w.sum = c.take<float>(a.tokens * a.heads * std::max(a.dk, a.dv) * 4);
-    w.drate = c.take<float>(attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens) * a.heads * 4);
+    w.drate = c.take<double>(attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens) * a.heads * 8);
   }
   *total = (c.off + 255) & ~size_t(255);
   return w;

@@ -25,4 +25,16 @@ __device__ __forceinline__ float wave_sum(float v) {
 // of zero weighs exp(0) = 1 and any other 0.  NaN stays.
 __device__ __forceinline__ float attn_rate(float r) { return r > 3.402823466e38f ? 3.402823466e38f : r; }
 
+// exp(-rate n) as the sum of two floats.  A carry is multiplied by it once per
+// chunk: with one float, the rounding of a weight near 1 would add up, the
+// same way each time, over the thousands of chunks that a slow decay reaches.
+struct AttnDecay {
+  float hi, lo;
+  __device__ __forceinline__ float of(float s) const { return fmaf(s, hi, s * lo); }
+};
+__device__ __forceinline__ AttnDecay attn_decay(float rate, int64_t n) {
+  const double w = exp(-(double)rate * (double)n);
+  return {(float)w, (float)(w - (double)(float)w)};
+}
+
 }  // namespace laplex
