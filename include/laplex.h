@@ -408,9 +408,10 @@ size_t laplex_embedding_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_
 
 /* Gradient of the whole table for the upstream gradient dy (tokens x width,
  * of type dtype):  dtable_v = scale sum_{t: id_t = v} dy_t, zero where v does
- * not occur.  The tokens are sorted by id (laplex_sort_anchors' stable
- * sort) and each row's terms added in the order of their tokens, in float32,
- * rounded once to table_dtype (dtype or LAPLEX_F32). vocab < 2^30. */
+ * not occur.  The tokens are sorted by id (the library's stable sort), each
+ * row's terms are added in float32 in an order that the ids alone fix, and the
+ * sum is rounded once to table_dtype (dtype or LAPLEX_F32).  tokens <= 2^28,
+ * vocab <= 2^26. */
 laplex_status laplex_embedding_backward(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                                         uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, void* ws,
                                         size_t ws_bytes, hipStream_t stream);

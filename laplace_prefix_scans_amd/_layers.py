@@ -302,7 +302,7 @@ def laplex_embedding_backward(ids: torch.Tensor, dy: torch.Tensor, vocab: int, s
                               dtype: Optional[torch.dtype] = None, dtable: Optional[torch.Tensor] = None,
                               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient (vocab, width) of the table for the upstream gradient dy (*ids.shape, width): the rows of dy
-    added by id in token order.  dtype: float32 or the type of dy (the default)."""
+    added by id, in an order that the ids alone fix.  dtype: float32 or the type of dy (the default)."""
     code = _dtype(dy, "dy")
     dev = dy.device
     nb = _ids(ids, dev)

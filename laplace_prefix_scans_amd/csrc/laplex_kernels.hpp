@@ -92,6 +92,9 @@ size_t sort_status_bytes(uint64_t n);
 // point does, so that no apply ever runs on a stalled sort's outputs).
 hipError_t sort_anchors(const SortWorkspace& w, const float* a, uint64_t n, float* a_sorted, uint32_t* perm,
                         const SortRoute* route, hipStream_t s, bool debug_stall = false);
+// The same stable sort of integers up to max_key (< 2^30), with the passes their digits need.
+hipError_t sort_indices(const SortWorkspace& w, const uint32_t* keys, uint64_t n, uint32_t max_key, uint32_t* keys_sorted, uint32_t* perm,
+                        hipStream_t s);
 // The same sort with x (n floats, original order) carried along as the
 // value of each key in place of its index: writes x in sorted order to
 // x_sorted, and no permutation (the route, if given, still records the

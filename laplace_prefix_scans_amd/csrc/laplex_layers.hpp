@@ -78,10 +78,12 @@ hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, 
 struct EmbedWorkspace {
   SortWorkspace sort;
   uint32_t* keys;    // ids, those outside the table as `vocab` (tokens)
-  float* keys_s;     // the same, sorted (as the bits of floats)
+  uint32_t* keys_s;  // the same, sorted
   uint32_t* perm;    // tokens in that order
   uint32_t* starts;  // first sorted position of each row of the table (vocab + 1)
+  float* part;       // partial rows (embed_part_floats)
 };
+uint64_t embed_part_floats(uint64_t tokens, uint32_t width);
 hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s);
 

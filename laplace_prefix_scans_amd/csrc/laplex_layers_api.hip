@@ -11,10 +11,11 @@ namespace {
 using namespace laplex;
 
 constexpr uint64_t kMaxTokens = 0x7FFFFFFFull;  // int32 offsets
-constexpr uint32_t kMaxSeqs = 1u << 20, kMaxHeads = 65535, kMaxChannels = 256, kMaxWidth = 1u << 24;
-constexpr uint64_t kMaxBlocks = 1ull << 28;  // blocks of one launch, before column slices
+constexpr uint32_t kMaxSeqs = 1u << 20, kMaxHeads = 4096, kMaxChannels = 256, kMaxWidth = 1u << 24;
+constexpr uint64_t kMaxBlocks = 1ull << 22;  // sequences x heads: a launch has fewer than 2^32 threads
 constexpr uint64_t kMaxRows = 0xFFFFFFFFull;
-constexpr uint32_t kMaxVocab = (1u << 30) - 1;
+constexpr uint32_t kMaxVocab = 1u << 26;
+constexpr uint64_t kMaxEmbedTokens = 1ull << 28;
 
 inline size_t elem(int dtype) { return dtype == LAPLEX_BF16 ? 2 : 4; }
 inline bool is_dtype(int dtype) { return dtype == LAPLEX_F32 || dtype == LAPLEX_BF16; }
@@ -26,7 +27,7 @@ laplex_status check_shape(const laplex_attn_shape* a) {
   if (a->heads == 0 || a->kv_heads == 0 || a->heads % a->kv_heads != 0 || a->dk == 0 || a->dv == 0) return LAPLEX_ERR_ARG;
   if (a->tokens > kMaxTokens || a->seqs > kMaxSeqs || a->heads > kMaxHeads || a->dk > kMaxChannels || a->dv > kMaxChannels)
     return LAPLEX_ERR_SIZE;
-  if ((a->seqs + a->tokens / 64 + 3) * a->heads > kMaxBlocks) return LAPLEX_ERR_SIZE;
+  if ((a->seqs + 1024ull) * a->heads > kMaxBlocks) return LAPLEX_ERR_SIZE;
   return LAPLEX_OK;
 }
 
@@ -293,15 +294,16 @@ extern "C" laplex_status laplex_layer_norm_backward(int dtype, uint64_t rows, ui
 
 // ------------------------------------------------------------------ embedding
 namespace {
-EmbedWorkspace carve_embed(void* ws, uint64_t tokens, uint32_t vocab, size_t* total) {
+EmbedWorkspace carve_embed(void* ws, uint64_t tokens, uint32_t vocab, uint32_t width, size_t* total) {
   Carver c(ws);
   EmbedWorkspace w{};
   char* sort_base = c.take<char>(sort_bytes(tokens));
   if (ws) w.sort = carve_sort(sort_base, tokens);
   w.keys = c.take<uint32_t>(tokens * 4);
-  w.keys_s = c.take<float>(tokens * 4);
+  w.keys_s = c.take<uint32_t>(tokens * 4);
   w.perm = c.take<uint32_t>(tokens * 4);
   w.starts = c.take<uint32_t>((vocab + 1ull) * 4);
+  w.part = c.take<float>(embed_part_floats(tokens, width) * 4);
   *total = (c.off + 255) & ~size_t(255);
   return w;
 }
@@ -310,7 +312,7 @@ EmbedWorkspace carve_embed(void* ws, uint64_t tokens, uint32_t vocab, size_t* to
 extern "C" laplex_status laplex_embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* table,
                                           uint32_t vocab, uint32_t width, float scale, void* y, hipStream_t stream) {
   if (!is_dtype(dtype) || (id_bytes != 4 && id_bytes != 8) || width == 0) return LAPLEX_ERR_ARG;
-  if (tokens > kMaxTokens || vocab > kMaxVocab || width > kMaxWidth) return LAPLEX_ERR_SIZE;
+  if (tokens > kMaxEmbedTokens || vocab > kMaxVocab || width > kMaxWidth) return LAPLEX_ERR_SIZE;
   if (tokens == 0) return LAPLEX_OK;
   if (!ids || !y || (vocab && !table)) return LAPLEX_ERR_NULL;
   const size_t e = elem(dtype);
@@ -321,9 +323,9 @@ extern "C" laplex_status laplex_embedding(int dtype, const void* ids, int id_byt
 }
 
 extern "C" size_t laplex_embedding_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t width) {
-  if (tokens > kMaxTokens || vocab > kMaxVocab || width > kMaxWidth || width == 0) return 0;
+  if (tokens > kMaxEmbedTokens || vocab > kMaxVocab || width > kMaxWidth || width == 0) return 0;
   size_t total = 0;
-  carve_embed(nullptr, tokens, vocab, &total);
+  carve_embed(nullptr, tokens, vocab, width, &total);
   return total;
 }
 
@@ -332,14 +334,14 @@ extern "C" laplex_status laplex_embedding_backward(int dtype, const void* ids, i
                                                    void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!is_dtype(dtype) || (table_dtype != dtype && table_dtype != LAPLEX_F32) || (id_bytes != 4 && id_bytes != 8) || width == 0)
     return LAPLEX_ERR_ARG;
-  if (tokens > kMaxTokens || vocab > kMaxVocab || width > kMaxWidth) return LAPLEX_ERR_SIZE;
+  if (tokens > kMaxEmbedTokens || vocab > kMaxVocab || width > kMaxWidth) return LAPLEX_ERR_SIZE;
   if (vocab == 0) return LAPLEX_OK;
   if (!dtable || !ws || (tokens && (!ids || !dy))) return LAPLEX_ERR_NULL;
   const size_t e = elem(dtype), te = elem(table_dtype);
   if ((tokens && misaligned(ids, id_bytes)) || misaligned(dy, e) || misaligned(dtable, te) || misaligned(ws, 256))
     return LAPLEX_ERR_ALIGN;
   size_t need = 0;
-  const EmbedWorkspace w = carve_embed(ws, tokens, vocab, &need);
+  const EmbedWorkspace w = carve_embed(ws, tokens, vocab, width, &need);
   if (ws_bytes < need) return LAPLEX_ERR_WORKSPACE;
   const Extent outs[] = {{dtable, (size_t)vocab * width * te}, {ws, need}}, ins[] = {{ids, tokens * id_bytes}, {dy, tokens * width * e}};
   if (any_overlap(outs, ins)) return LAPLEX_ERR_OVERLAP;

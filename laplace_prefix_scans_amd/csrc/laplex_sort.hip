@@ -547,7 +547,7 @@ static uint32_t debug_stall_spins() {
 template <typename ST, int TILE>
 static hipError_t launch_sort_passes(const SortWorkspace& w, const float* a, uint64_t n, float* a_sorted, uint32_t* perm,
                                      const SortRoute* route, const uint32_t* pay, bool table, uint64_t cpb,
-                                     hipStream_t s, bool debug) {
+                                     hipStream_t s, bool debug, int passes) {
   const uint32_t dbg = debug ? debug_stall_spins() : 0u;
   const uint32_t spin_limit = dbg ? dbg : kSpinLimit;
   const bool publish = dbg == 0;
@@ -555,11 +555,12 @@ static hipError_t launch_sort_passes(const SortWorkspace& w, const float* a, uin
   const uint64_t tiles = (n + TILE - 1) / TILE;
   ST* st = reinterpret_cast<ST*>(w.status);
   const uint2* src = nullptr;
-  for (int p = 0; p < 4; ++p) {
+  const int last = passes - 1;
+  for (int p = 0; p < passes; ++p) {
     ST* stp = st + (uint64_t)p * tiles * 256;
-    uint2* dst = (p == 3) ? nullptr : w.kv[p & 1];
-    uint32_t* fk = (p == 3) ? reinterpret_cast<uint32_t*>(a_sorted) : nullptr;
-    uint32_t* fv = (p == 3) ? perm : nullptr;
+    uint2* dst = (p == last) ? nullptr : w.kv[p & 1];
+    uint32_t* fk = (p == last) ? reinterpret_cast<uint32_t*>(a_sorted) : nullptr;
+    uint32_t* fv = (p == last) ? perm : nullptr;
     uint16_t* rl = route ? route->lpos[p] : nullptr;
     uint16_t* rd = route ? route->dstart[p] : nullptr;
     uint32_t* rg = route ? route->gbase[p] : nullptr;
@@ -573,9 +574,9 @@ static hipError_t launch_sort_passes(const SortWorkspace& w, const float* a, uin
       LAPLEX_PASS(0, true, route ? "k_onesweep_first_pay_routed" : "k_onesweep_first_pay");
     else if (p == 0)
       LAPLEX_PASS(0, false, route ? "k_onesweep_first_routed" : "k_onesweep_first");
-    else if (p == 3 && pay)
+    else if (p == last && pay)
       LAPLEX_PASS(2, true, route ? "k_onesweep_last_pay_routed" : "k_onesweep_last_pay");
-    else if (p == 3)
+    else if (p == last)
       LAPLEX_PASS(2, false, route ? "k_onesweep_last_routed" : "k_onesweep_last");
     else
       LAPLEX_PASS(1, false, route ? "k_onesweep_mid_routed" : "k_onesweep_mid");
@@ -594,7 +595,7 @@ size_t sort_status_bytes(uint64_t n) {
 }
 
 static hipError_t sort_impl(const SortWorkspace& w, const float* a, uint64_t n, float* a_sorted, uint32_t* perm,
-                            const SortRoute* route, const uint32_t* pay, hipStream_t s, bool debug) {
+                            const SortRoute* route, const uint32_t* pay, hipStream_t s, bool debug, int passes = 4) {
   if (n == 0) return hipSuccess;
   // clear the header, histograms and look-back status with a fill kernel
   const uint64_t clear_words = (uint64_t)(kSortHeaderBytes / 4) + sort_status_bytes(n) / 4;
@@ -617,14 +618,22 @@ static hipError_t sort_impl(const SortWorkspace& w, const float* a, uint64_t n, 
   LAPLEX_LAUNCH("k_sort_offsets", 1024, s,
                 k_sort_offsets<<<1, kScanThreads, 0, s>>>(w.hist, w.offsets, w.header, w.gsum, table ? hist_blocks : 0));
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (small) return launch_sort_passes<uint32_t, kSortTileSmall>(w, a, n, a_sorted, perm, route, pay, false, cpb, s, debug);
-  if (n <= (1ull << 30)) return launch_sort_passes<uint32_t, kSortTile>(w, a, n, a_sorted, perm, route, pay, table, cpb, s, debug);
-  return launch_sort_passes<uint64_t, kSortTile>(w, a, n, a_sorted, perm, route, pay, table, cpb, s, debug);
+  if (small) return launch_sort_passes<uint32_t, kSortTileSmall>(w, a, n, a_sorted, perm, route, pay, false, cpb, s, debug, passes);
+  if (n <= (1ull << 30)) return launch_sort_passes<uint32_t, kSortTile>(w, a, n, a_sorted, perm, route, pay, table, cpb, s, debug, passes);
+  return launch_sort_passes<uint64_t, kSortTile>(w, a, n, a_sorted, perm, route, pay, table, cpb, s, debug, passes);
 }
 
 hipError_t sort_anchors(const SortWorkspace& w, const float* a, uint64_t n, float* a_sorted, uint32_t* perm,
                         const SortRoute* route, hipStream_t s, bool debug_stall) {
   return sort_impl(w, a, n, a_sorted, perm, route, nullptr, s, debug_stall);
+}
+
+hipError_t sort_indices(const SortWorkspace& w, const uint32_t* keys, uint64_t n, uint32_t max_key, uint32_t* keys_sorted, uint32_t* perm,
+                        hipStream_t s) {
+  // the bits of a nonnegative int, read as a float, sort in the same order; passes over digits that are all zero are left out
+  const int passes = max_key < (1u << 16) ? 2 : max_key < (1u << 24) ? 3 : 4;
+  return sort_impl(w, reinterpret_cast<const float*>(keys), n, reinterpret_cast<float*>(keys_sorted), perm, nullptr, nullptr, s, false,
+                   passes);
 }
 
 hipError_t sort_anchors_payload(const SortWorkspace& w, const float* a, const float* x, uint64_t n, float* a_sorted,
