@@ -15,8 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblaplex.so")
-SOURCES = ["laplex_sort.hip", "laplex_route.hip", "laplex_apply.hip", "laplex_api.hip", "laplex_attn.hip", "laplex_attn_bf16.hip",
-           "laplex_attn_f32.hip", "laplex_norm.hip", "laplex_embed.hip", "laplex_layers_api.hip"]
+SOURCES = ["laplex_sort.hip", "laplex_route.hip", "laplex_apply.hip", "laplex_api.hip", "laplex_attn.hip", "laplex_attn_bf16_vec.hip",
+           "laplex_attn_bf16_any.hip", "laplex_attn_f32_vec.hip", "laplex_attn_f32_any.hip", "laplex_norm.hip", "laplex_embed.hip", "laplex_layers_api.hip"]
 PROBE_LIB = os.path.join(HERE, "liblaplex_probe.so")
 PROBE_SOURCES = ["laplex_probe.hip"]
 ARCH = "gfx950"

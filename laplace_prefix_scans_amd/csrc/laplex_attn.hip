@@ -4,11 +4,6 @@
 
 namespace laplex {
 
-template <>
-void attn_chunk_launch<bf16>(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
-template <>
-void attn_chunk_launch<float>(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
-
 // Turns the segments' own final states into the states before each segment,
 // S_k+1 = w(L) S_k + T_k, in place; thread per element.  With lag-weighted
 // states, D_k+1 = w(L) (D_k + L S_k) + E_k.
@@ -59,7 +54,7 @@ struct AttnPlan {
   int kp, nw;
   uint32_t slices;
   int64_t seg_len;
-  uint64_t slots, bounds;
+  uint64_t bounds;
   bool split;
 };
 static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
@@ -73,7 +68,6 @@ static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V,
   q.split = len < tokens;
   if (!q.split) len = std::max<uint64_t>(64, (tokens + 63) / 64 * 64);
   q.seg_len = (int64_t)len;
-  q.slots = tokens / len + seqs + 3;
   q.bounds = q.split ? tokens / len + 1 : 0;
   return q;
 }
@@ -82,9 +76,9 @@ size_t attn_pass_bytes(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, ui
   const AttnPlan q = attn_plan(seqs, heads, K, V, tokens);
   return (size_t)q.bounds * heads * K * V * 4 * (rate ? 2 : 1);
 }
-uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets) {
   const AttnPlan q = attn_plan(seqs, heads, K, V, tokens);
-  return q.slots * q.slices;
+  return attn_slots({offsets, tokens, seqs, q.seg_len}) * q.slices;
 }
 
 static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width, size_t e) {
@@ -99,21 +93,21 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   a.p = p;
   a.g = {p.offsets, p.tokens, p.seqs, q.seg_len};
   a.slices = q.slices;
-  a.tiles = q.slots * p.heads * q.slices;
+  a.slots = attn_slots(a.g);
+  a.group = std::max(p.x.div, std::max(p.y.div, p.z.div));
   if (q.split) {
     a.bound = static_cast<float*>(ws);
     a.bound_d = a.bound + q.bounds * p.heads * p.K * p.V;
   }
-  a.vec_x = aligned16(p.x.p, p.x.token, p.x.head, p.K, e);
-  a.vec_y = aligned16(p.y.p, p.y.token, p.y.head, p.K, e);
-  a.vec_z = aligned16(p.z.p, p.z.token, p.z.head, p.V, e);
-  a.vec_dot = rate && aligned16(p.dot, p.dot_view.token, p.dot_view.head, p.V, e);
-  a.vec_out = p.V % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  const bool vec = aligned16(p.x.p, p.x.token, p.x.head, p.K, e) && aligned16(p.y.p, p.y.token, p.y.head, p.K, e) &&
+                   aligned16(p.z.p, p.z.token, p.z.head, p.V, e) &&
+                   (!rate || aligned16(p.dot, p.dot_view.token, p.dot_view.head, p.V, e)) &&
+                   reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
   a.drate = p.drate_part;
   auto run = [&](const char* name, bool full) {
     LAPLEX_LAUNCH(name, p.tokens, s, {
-      if (bf) attn_chunk_launch<bf16>(a, q.kp, q.nw, full, rate, s);
-      else attn_chunk_launch<float>(a, q.kp, q.nw, full, rate, s);
+      if (bf) (vec ? attn_chunk_bf16_vec : attn_chunk_bf16_any)(a, q.kp, q.nw, full, rate, s);
+      else (vec ? attn_chunk_f32_vec : attn_chunk_f32_any)(a, q.kp, q.nw, full, rate, s);
     });
     return hipGetLastError();
   };

@@ -114,70 +114,126 @@ __device__ __forceinline__ int tile_at(int r, int c) {
   return r * P + (((c / E) ^ swz<T, P>(r)) * E) + c % E;
 }
 
-// A tile's 16-byte pieces on their way from memory to LDS.
-template <typename T, int ROWS, int P, int THREADS>
+// A tile's 16-byte pieces on their way from memory to LDS: thread -> column
+// piece threadIdx.x % (P / E) of every RPI-th row.
+template <typename T, int ROWS, int P, int THREADS, bool VEC>
 struct Stage {
-  static constexpr int E = 16 / sizeof(T), N = ROWS * P / E / THREADS;
-  static_assert(ROWS * P / E % THREADS == 0, "pieces divide evenly");
+  static constexpr int E = 16 / sizeof(T), RPI = THREADS / (P / E), N = ROWS / RPI;
+  static_assert(THREADS % (P / E) == 0 && ROWS % RPI == 0, "pieces divide evenly");
   uint4 v[N];
-  // Rows [0, rows) of the chunk that starts at processing position u (row r is
-  // token base + r * step), columns [col0, width); the rest is zero.
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int64_t token, int step, int rows, int col0, int width, bool vec) {
+  const T* at;       // this thread's first piece in the next chunk
+  int64_t rows_it;   // elements from one of its pieces to the next
+  int cols;          // columns from its piece's first to the end of the row
+  // p: the row of the first token, col0: the tile's first column, stride: elements from a row of the tile to the next
+  __device__ __forceinline__ void init(const T* p, int64_t stride, int col0, int width) {
+    const int r = threadIdx.x / (P / E), c = col0 + threadIdx.x % (P / E) * E;
+    at = p + r * stride + c;
+    rows_it = RPI * stride;
+    cols = width - c;
+  }
+  // The next chunk's rows [0, rows); rows and columns past the end are zero.
+  __device__ __forceinline__ void load(int rows) {
+    const int r0 = threadIdx.x / (P / E);
+    const T* src = at;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * THREADS + threadIdx.x, r = at / (P / E), c = col0 + at % (P / E) * E;
       uint4 q = make_uint4(0, 0, 0, 0);
-      if (r < rows && c < width) {
-        const T* src = p + (token + (int64_t)r * step) * stride + c;
-        if (vec) {
-          q = *reinterpret_cast<const uint4*>(src);
-        } else {
-          T e[E];
+      if constexpr (VEC) {
+        if (r0 + i * RPI < rows && cols > 0) q = *reinterpret_cast<const uint4*>(src);
+      } else {
+        T e[E];
 #pragma unroll
-          for (int j = 0; j < E; ++j) e[j] = c + j < width ? src[j] : T(0.f);
-          __builtin_memcpy(&q, e, 16);
-        }
+        for (int j = 0; j < E; ++j) e[j] = r0 + i * RPI < rows && j < cols ? src[j] : T(0.f);
+        __builtin_memcpy(&q, e, 16);
       }
       v[i] = q;
+      src += rows_it;
     }
+    at = src;
   }
   __device__ __forceinline__ void store(T* tile) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * THREADS + threadIdx.x, r = at / (P / E), c = at % (P / E);
+      const int r = threadIdx.x / (P / E) + i * RPI, c = threadIdx.x % (P / E);
       *reinterpret_cast<uint4*>(tile + r * P + ((c ^ swz<T, P>(r)) * E)) = v[i];
     }
   }
-  // whether any piece holds an infinity or NaN
-  __device__ __forceinline__ bool nonfinite() const {
-    bool bad = false;
+  // Replaces infinities and NaN by 0 and lowers first[column of the tile] to their row; whether there were any.
+  __device__ __forceinline__ bool clean(int* first) {
+    bool any = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      bool bad = false;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (sizeof(T) == 2) bad |= (w[j] & 0x7F80u) == 0x7F80u;
         bad |= (w[j] & 0x7F800000u) == 0x7F800000u;
       }
+      if (bad) {
+        any = true;
+        T e[E];
+        __builtin_memcpy(e, w, 16);
+        for (int j = 0; j < E; ++j)
+          if (bits_nonfinite(__float_as_uint(to_f32(e[j])))) {
+            e[j] = T(0.f);
+            atomicMin(first + threadIdx.x % (P / E) * E + j, (int)threadIdx.x / (P / E) + i * RPI);
+          }
+        __builtin_memcpy(&v[i], e, 16);
+      }
     }
-    return bad;
+    return any;
   }
 };
 
-// x = hi + lo (+ lo2) in bfloat16 parts, 2^-17 (2^-25) of x left over.
-__device__ __forceinline__ void split_pair(float a, float b, bf16x2& hi, f32x2& rest) {
-  hi = bf16x2{(__bf16)a, (__bf16)b};
-  rest = f32x2{a - (float)hi[0], b - (float)hi[1]};
+// Two floats as a pair of bfloat16, and what the pair leaves over: x = hi + lo
+// (+ lo2) in two (three) parts loses 2^-17 (2^-25) of x.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
+  const uint32_t w = pack_bf16(a, b);
+  a -= __uint_as_float(w << 16);
+  b -= __uint_as_float(w & 0xFFFF0000u);
+  return w;
+}
+struct Parts2 {
+  bf16x8 hi, lo;
+};
+__device__ __forceinline__ Parts2 split2(const float (&x)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+    h[i] = split_pair(a, b);
+    l[i] = pack_bf16(a, b);
+  }
+  return {__builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3])), __builtin_bit_cast(bf16x8, make_uint4(l[0], l[1], l[2], l[3]))};
+}
+struct Parts3 {
+  bf16x8 hi, lo, lo2;
+};
+__device__ __forceinline__ Parts3 split3(const float (&x)[8]) {
+  uint32_t h[4], l[4], m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+    h[i] = split_pair(a, b);
+    l[i] = split_pair(a, b);
+    m[i] = pack_bf16(a, b);
+  }
+  return {__builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3])), __builtin_bit_cast(bf16x8, make_uint4(l[0], l[1], l[2], l[3])),
+          __builtin_bit_cast(bf16x8, make_uint4(m[0], m[1], m[2], m[3]))};
 }
 
 struct AttnChunkArgs {
   AttnPass p;
   AttnSegs g;
   uint32_t slices;   // blocks across the V columns
-  uint64_t tiles;    // slots x heads x slices
+  uint32_t group;    // query heads per shared head
+  uint64_t slots;    // segments, with room for unused ones
   float* bound;      // states at segment boundaries ([boundary][head][K][V]), or null
   float* bound_d;    // the lag-weighted ones (rate gradient)
-  bool vec_x, vec_y, vec_z, vec_dot, vec_out;  // 16-byte loads and 4-element stores are aligned
   double* drate;     // Rate: partials [slot][slice][head]
 };
 
@@ -215,7 +271,7 @@ __device__ __forceinline__ f32x16 mfma(float a, float b, f32x16 c) {
 
 // A 32 x 32 tile of the carry (KT of them per wave, one under the other): a
 // float register per element, column = lane % 32.
-template <typename T, int KP, int NW, bool FULL, bool RATE>
+template <typename T, int KP, int NW, bool FULL, bool RATE, bool VEC>
 __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_chunk(AttnChunkArgs a) {
   constexpr int C = kAttnC<T>, KT = KP / 32, BV = 32 * NW, THREADS = NW * kWave, IT = C / 32;
   constexpr bool BF = sizeof(T) == 2, DOT = FULL && RATE;
@@ -226,15 +282,21 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   __shared__ __attribute__((aligned(16))) T dots[DOT ? C * BV : 8];
   __shared__ __attribute__((aligned(16))) float down[C], downlag[RATE ? C : 4];
   __shared__ float wt[FULL ? 2 * C : 1];
-  __shared__ int bad_chunk[2];
+  // bf16: operand [tile][channel half][part] of a lane (the lag-weighted ones behind them); float: [wave][register quad]
+  using Pair = std::conditional_t<BF, bf16x8, float4>;
+  __shared__ Pair pairs[(FULL ? (BF ? (RATE ? 24 : 12) : NW * 4) : 1) * kWave];
+  __shared__ int bad_chunk[2], bad_row[2][FULL ? BV : 1];
   __shared__ double red[NW];
 
-  uint64_t tile;
-  if (!xcd_tile(a.tiles, tile)) return;
-  const uint32_t slice = (uint32_t)(tile % a.slices), h = (uint32_t)(tile / a.slices % p.heads);
-  const uint64_t slot = tile / a.slices / p.heads;
+  // Blocks that read the same rows (the column slices and the heads of one shared head) follow each other on
+  // one XCD; these units go to the XCDs in turn, so that unused slots leave none of them with less work.
+  const uint32_t per = a.group * a.slices, at_xcd = blockIdx.x / kXcds;
+  const uint64_t unit = (uint64_t)(at_xcd / per) * kXcds + blockIdx.x % kXcds, shared = p.heads / a.group;
+  const uint32_t slice = at_xcd % a.slices, h = (uint32_t)(unit % shared) * a.group + at_xcd % per / a.slices;
+  const uint64_t slot = unit / shared;
+  if (slot >= a.slots) return;
   const AttnSeg sg = find_seg(a.g, slot);
-  const int wave = threadIdx.x / kWave, lane = lane_id(), half = lane >> 5, lc = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id(), half = lane >> 5, lc = lane & 31;
   const int col = slice * BV + wave * 32 + lc;  // this lane's column of the carry
   const int K = (int)p.K, V = (int)p.V;
   const bool active = (int)slice * BV + wave * 32 < V;  // the wave has columns (all waves move tiles)
@@ -257,31 +319,39 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   const float rate = attn_rate(p.rate[h]);
   const int lead = p.reverse ? 0 : 1;
   const bool keep = !last_seg || p.s_out || (DOT && p.ds_out);  // the carry after the last chunk is needed
+  // states in memory: element (row, column) at row * rs + column * cs of the caller's ([seq][head], either order) or of a boundary's
   const uint64_t sbase = ((uint64_t)sg.seq * p.heads + h) * (uint64_t)K * V;
-  // element (row, column) of a state in the caller's layout
-  auto sat = [&](int row, int c) { return sbase + (p.s_trans ? (uint64_t)c * K + row : (uint64_t)row * V + c); };
+  const int rs = p.s_trans ? 1 : V, cs = p.s_trans ? K : 1;
   const uint64_t per_bound = (uint64_t)K * V;
   auto bound_at = [&](int64_t u) { return ((uint64_t)((sg.first + u) / a.g.seg_len) * p.heads + h) * per_bound; };
+  auto load_state = [&](f32x16 (&s)[KT], const float* src, int rs, int cs) {
+    if (col >= V) return;
+    src += (int64_t)col * cs;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = 32 * t + carry_row<T>(i / 4, i % 4, half);
+        const float v = src[min(row, K - 1) * rs];
+        s[t][i] = row < K ? v : 0.f;
+      }
+  };
 
   f32x16 S[KT], D[RATE ? KT : 1];
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int row = 32 * t + carry_row<T>(i / 4, i % 4, half);
-      float v = 0.f, d = 0.f;
-      if (row < K && col < V) {
-        if (FULL && sg.u0 > 0) {
-          const uint64_t at = bound_at(sg.u0) + (uint64_t)row * V + col;
-          v = a.bound[at];
-          if constexpr (RATE) d = a.bound_d[at];
-        } else if (FULL && p.s_in) {
-          v = p.s_in[sat(row, col)];
-        }
-      }
-      S[t][i] = v;
-      if constexpr (RATE) D[t][i] = d;
+  for (int t = 0; t < KT; ++t) {
+    S[t] = f32x16{};
+    if constexpr (RATE) D[t] = f32x16{};
+  }
+  if constexpr (FULL) {
+    if (sg.u0 > 0) {
+      const uint64_t at = bound_at(sg.u0);
+      load_state(S, a.bound + at, V, 1);
+      if constexpr (RATE) load_state(D, a.bound_d + at, V, 1);
+    } else if (p.s_in) {
+      load_state(S, p.s_in + sbase, rs, cs);
     }
+  }
 
   // weights of a pair inside a chunk by its lag, 0 for the pairs above the diagonal
   if constexpr (FULL)
@@ -306,18 +376,65 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   const int step = p.reverse ? -1 : 1;
   auto token = [&](int64_t u) { return p.reverse ? sg.first + sg.len - 1 - u : sg.first + u; };
 
-  Stage<T, C, KP, THREADS> sx, sy;
-  Stage<T, C, BV, THREADS> sz, sd;
+  Stage<T, C, KP, THREADS, VEC> sx, sy;
+  Stage<T, C, BV, THREADS, VEC> sz, sd;
+  const int64_t t0 = token(sg.u0);
+  if constexpr (FULL) sx.init(x + t0 * p.x.token, step * p.x.token, 0, K);
+  sy.init(y + t0 * p.y.token, step * p.y.token, 0, K);
+  sz.init(z + t0 * p.z.token, step * p.z.token, slice * BV, V);
+  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, step * p.dot_view.token, slice * BV, V);
   auto load = [&](int64_t u) {
     const int rows = (int)min((int64_t)C, sg.u0 + sg.n - u);
-    const int64_t t = token(u);
-    if constexpr (FULL) sx.load(x, p.x.token, t, step, rows, 0, K, a.vec_x);
-    sy.load(y, p.y.token, t, step, rows, 0, K, a.vec_y);
-    sz.load(z, p.z.token, t, step, rows, slice * BV, V, a.vec_z);
-    if constexpr (DOT) sd.load(dot, p.dot_view.token, t, step, rows, slice * BV, V, a.vec_dot);
+    if constexpr (FULL) sx.load(rows);
+    sy.load(rows);
+    sz.load(rows);
+    if constexpr (DOT) sd.load(rows);
+  };
+  f32x16 O[FULL ? IT : 1];
+  // Writes the outputs of the chunk at u.  Called when the next chunk is in LDS: stores are counted with the
+  // loads, so writing before would make the wait for the next chunk's rows one for the stores too.
+  auto put = [&](int64_t u) {
+    if (!active || !p.out) return;
+    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u);
+#pragma unroll
+    for (int t = 0; t < IT; ++t) {
+      const int i = 32 * t + lc;  // this lane's token
+      if (i >= n) continue;
+      const int c0 = slice * BV + wave * 32 + 4 * half;
+      const uint64_t at = ((uint64_t)token(u + i) * p.heads + h) * V + c0;
+      if (p.out_f32 || !BF) {
+        float* dst = static_cast<float*>(p.out) + at;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (VEC) {
+            if (c0 + 8 * r < V)
+              *reinterpret_cast<float4*>(dst + 8 * r) = make_float4(O[t][4 * r], O[t][4 * r + 1], O[t][4 * r + 2], O[t][4 * r + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c0 + 8 * r + e < V) dst[8 * r + e] = O[t][4 * r + e];
+          }
+        }
+      } else {
+        T* dst = static_cast<T*>(p.out) + at;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (VEC) {
+            if (c0 + 8 * r < V)
+              *reinterpret_cast<uint2*>(dst + 8 * r) = make_uint2(pack_bf16(O[t][4 * r], O[t][4 * r + 1]), pack_bf16(O[t][4 * r + 2], O[t][4 * r + 3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c0 + 8 * r + e < V) dst[8 * r + e] = from_f32<T>(O[t][4 * r + e]);
+          }
+        }
+      }
+    }
   };
   double dr = 0.0;
   if (threadIdx.x < 2) bad_chunk[threadIdx.x] = 0;
+  if constexpr (FULL)
+    for (int i = threadIdx.x; i < 2 * BV; i += THREADS) bad_row[i / BV][i % BV] = C;
   set_down((int)min((int64_t)C, sg.n));
   if (sg.n > 0) load(sg.u0);
   int parity = 0;
@@ -326,100 +443,136 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     __syncthreads();  // the previous chunk's reads are done
     if constexpr (FULL) sx.store(xs);
     sy.store(ys);
+    // A masked pair weighs 0, but 0 times an infinity is NaN: infinities and NaN in z are taken out of the
+    // tile, and what they reach -- their own and later tokens of their column, the carry -- is set to NaN below.
+    if (FULL && sz.clean(bad_row[parity])) bad_chunk[parity] = 1;
     sz.store(zs);
     if constexpr (DOT) sd.store(dots);
-    if (FULL && sz.nonfinite()) bad_chunk[parity] = 1;
     if (threadIdx.x == 0) bad_chunk[parity ^ 1] = 0;
+    if (FULL && (int)threadIdx.x < BV) bad_row[parity ^ 1][threadIdx.x] = C;
     if (n < C && u > sg.u0) set_down(n);
     __syncthreads();
     const bool more = u + C < sg.u0 + sg.n;
+    if (FULL && u > sg.u0) put(u - C);
     if (more) load(u + C);
-    // a masked pair weighs 0, but 0 times an infinity is NaN: a chunk with one in z takes care
     const bool bad = FULL && bad_chunk[parity] != 0;
-    if (!active) continue;
     // the lane as the compiler sees it changes with every chunk: the many LDS offsets made from it are
     // then formed where they are used (an xor each) instead of each holding a register over the loop
     int ln = lane;
     asm volatile("" : "+v"(ln));
     const int half = ln >> 5, lc = ln & 31;
 
-    f32x16 O[FULL ? IT : 1], OD[DOT ? IT : 1], Pd[FULL ? IT : 1], Po;
+    f32x16 OD[DOT ? IT : 1];
     if constexpr (FULL) {
-#pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        O[t] = f32x16{};
-        Pd[t] = f32x16{};
-        if constexpr (RATE) OD[t] = f32x16{};
-      }
-      Po = f32x16{};
-      // P^T = y x^T (rows j, columns i) and out^T = S^T x^T (rows V, columns i): x is the same operand in both
+      // The weighted pairs are the same for every column: the waves share them out and pass them on through LDS.
       if constexpr (BF) {
+        // P^T tiles (rows j, columns i): (0, 0), (1, 1) on the diagonal and (0, 1), as operands of two bfloat16 parts
+        for (int tile = wave; tile < 3; tile += NW) {
+          const int j0 = tile == 1 ? 32 : 0, i0 = tile == 0 ? 0 : 32;
+          f32x16 P = {};
 #pragma unroll
-        for (int ks = 0; ks < KP / 16; ++ks) {
-          __builtin_amdgcn_sched_barrier(0);  // operands are read as they are needed: held ahead they would spill
-          bf16x8 xf[IT], yf[IT], sh, sl, dh, dl;
-#pragma unroll
-          for (int t = 0; t < IT; ++t) {
-            xf[t] = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(32 * t + lc, 16 * ks + 8 * half));
-            yf[t] = *reinterpret_cast<const bf16x8*>(ys + tile_at<T, KP>(32 * t + lc, 16 * ks + 8 * half));
+          for (int ks = 0; ks < KP / 16; ++ks) {
+            const bf16x8 xf = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(i0 + lc, 16 * ks + 8 * half));
+            const bf16x8 yf = *reinterpret_cast<const bf16x8*>(ys + tile_at<T, KP>(j0 + lc, 16 * ks + 8 * half));
+            P = mfma(yf, xf, P);
           }
+          const float* w0 = wt + C + i0 - j0 + lc - 4 * half;
 #pragma unroll
-          for (int t = 0; t < IT; ++t) Pd[t] = mfma(yf[t], xf[t], Pd[t]);
-          if constexpr (IT == 2) Po = mfma(yf[0], xf[1], Po);
-          // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
+          for (int s = 0; s < 2; ++s) {
+            float pv[8], pd[8];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            bf16x2 hi;
-            f32x2 rest;
-            split_pair(S[ks / 2][8 * (ks % 2) + e], S[ks / 2][8 * (ks % 2) + e + 1], hi, rest);
-            sh[e] = hi[0], sh[e + 1] = hi[1];
-            sl[e] = (__bf16)rest[0], sl[e + 1] = (__bf16)rest[1];
-            if constexpr (RATE) {
-              split_pair(D[ks / 2][8 * (ks % 2) + e], D[ks / 2][8 * (ks % 2) + e + 1], hi, rest);
-              dh[e] = hi[0], dh[e + 1] = hi[1];
-              dl[e] = (__bf16)rest[0], dl[e + 1] = (__bf16)rest[1];
+            for (int e = 0; e < 8; ++e) {
+              const int i = 8 * s + e, j = 8 * (i / 4) + i % 4;
+              const float w = w0[-j];
+              pv[e] = w != 0.f ? P[i] * w : 0.f;  // a masked pair is 0 whatever its product
+              if constexpr (RATE) pd[e] = pv[e] * (float)(i0 - j0 + lc - 4 * half - j);
             }
-          }
-#pragma unroll
-          for (int t = 0; t < IT; ++t) {
-            O[t] = mfma(sh, xf[t], O[t]);
-            O[t] = mfma(sl, xf[t], O[t]);
+            const Parts2 p2 = split2(pv);
+            pairs[((tile * 2 + s) * 2) * kWave + ln] = p2.hi;
+            pairs[((tile * 2 + s) * 2 + 1) * kWave + ln] = p2.lo;
             if constexpr (RATE) {
-              OD[t] = mfma(dh, xf[t], OD[t]);
-              OD[t] = mfma(dl, xf[t], OD[t]);
+              const Parts2 d2 = split2(pd);
+              pairs[((6 + tile * 2 + s) * 2) * kWave + ln] = d2.hi;
+              pairs[((6 + tile * 2 + s) * 2 + 1) * kWave + ln] = d2.lo;
             }
           }
         }
       } else {
+        // each wave adds a share of the channels of P^T
+        f32x16 P = {};
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+        for (int k = 0; k < KP / NW / 8; ++k) {
+          const int ch = wave * (KP / NW) + 8 * k + 4 * half;
+          const float4 xf = *reinterpret_cast<const float4*>(xs + tile_at<T, KP>(lc, ch));
+          const float4 yf = *reinterpret_cast<const float4*>(ys + tile_at<T, KP>(lc, ch));
+          P = mfma(yf.x, xf.x, P);
+          P = mfma(yf.y, xf.y, P);
+          P = mfma(yf.z, xf.z, P);
+          P = mfma(yf.w, xf.w, P);
+        }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            __builtin_amdgcn_sched_barrier(0);
-            const float4 xf = *reinterpret_cast<const float4*>(xs + tile_at<T, KP>(lc, 32 * t + 8 * r + 4 * half));
-            const float4 yf = *reinterpret_cast<const float4*>(ys + tile_at<T, KP>(lc, 32 * t + 8 * r + 4 * half));
-            const float xe[4] = {xf.x, xf.y, xf.z, xf.w}, ye[4] = {yf.x, yf.y, yf.z, yf.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              Pd[0] = mfma(ye[e], xe[e], Pd[0]);
-              O[0] = mfma(S[t][4 * r + e], xe[e], O[0]);
-              if constexpr (RATE) OD[0] = mfma(D[t][4 * r + e], xe[e], OD[0]);
-            }
-          }
+        for (int r = 0; r < 4; ++r)
+          pairs[(wave * 4 + r) * kWave + ln] = make_float4(P[4 * r], P[4 * r + 1], P[4 * r + 2], P[4 * r + 3]);
       }
 #pragma unroll
-      for (int t = 0; t < IT; ++t)
+      for (int t = 0; t < IT; ++t) {
+        O[t] = f32x16{};
+        if constexpr (RATE) OD[t] = f32x16{};
+      }
+      if (active) {
+        // out^T = S^T x^T (rows V, columns i)
+        if constexpr (BF) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if constexpr (RATE) OD[t][i] = up[t] * fmaf((float)(32 * t + lc + lead), O[t][i], OD[t][i]);
-          O[t][i] *= up[t];
-          const float w = wt[C + lc - (8 * (i / 4) + 4 * half + i % 4)];
-          Pd[t][i] = w != 0.f ? Pd[t][i] * w : 0.f;  // a masked pair is 0 whatever its product
+          for (int ks = 0; ks < KP / 16; ++ks) {
+            bf16x8 xf[IT];
+#pragma unroll
+            for (int t = 0; t < IT; ++t) xf[t] = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(32 * t + lc, 16 * ks + 8 * half));
+            // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
+            float sv[8], dv[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              sv[e] = S[ks / 2][8 * (ks % 2) + e];
+              if constexpr (RATE) dv[e] = D[ks / 2][8 * (ks % 2) + e];
+            }
+            const Parts2 s2 = split2(sv);
+#pragma unroll
+            for (int t = 0; t < IT; ++t) O[t] = mfma(s2.hi, xf[t], O[t]);
+#pragma unroll
+            for (int t = 0; t < IT; ++t) O[t] = mfma(s2.lo, xf[t], O[t]);
+            if constexpr (RATE) {
+              const Parts2 d2 = split2(dv);
+#pragma unroll
+              for (int t = 0; t < IT; ++t) {
+                OD[t] = mfma(d2.hi, xf[t], OD[t]);
+                OD[t] = mfma(d2.lo, xf[t], OD[t]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float4 xf = *reinterpret_cast<const float4*>(xs + tile_at<T, KP>(lc, 32 * t + 8 * r + 4 * half));
+              const float xe[4] = {xf.x, xf.y, xf.z, xf.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                O[0] = mfma(S[t][4 * r + e], xe[e], O[0]);
+                if constexpr (RATE) OD[0] = mfma(D[t][4 * r + e], xe[e], OD[0]);
+              }
+            }
         }
-      if constexpr (IT == 2)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) Po[i] *= wt[C + 32 + lc - (8 * (i / 4) + 4 * half + i % 4)];
+        for (int t = 0; t < IT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if constexpr (RATE) OD[t][i] = up[t] * fmaf((float)(32 * t + lc + lead), O[t][i], OD[t][i]);
+            O[t][i] *= up[t];
+          }
+      }
+      __syncthreads();  // every wave's share of the pairs is there
     }
+    if (!active) continue;
 
     // the carry over the chunk, with the lag-weighted one ahead of it
     const bool carry = !FULL || more || keep;
@@ -439,121 +592,74 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     if constexpr (BF) {
 #pragma unroll
       for (int js = 0; js < C / 16; ++js) {
-        __builtin_amdgcn_sched_barrier(0);
         const bf16x8 zf = read_tr8<BV, false>(zs, ln, 16 * js, wave * 32);
         if constexpr (FULL) {
-          bf16x8 zp = zf, zn;
-          if (bad) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const bool hit = bits_nonfinite(__float_as_uint((float)zf[e]));
-              zn[e] = hit ? (__bf16)3.3e38f : (__bf16)0.f;
-              if (hit) zp[e] = (__bf16)0.f;
-            }
-          }
 #pragma unroll
           for (int t = 0; t < IT; ++t) {
             if (js >= 2 * (t + 1)) continue;  // pairs above the diagonal
-            const f32x16& P = js >= 2 * t ? Pd[t] : Po;
-            bf16x8 ph, pl, rh, rl;
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const int i = 8 * (js % 2) + e;
-              bf16x2 hi;
-              f32x2 rest;
-              // two parts, as for the carry
-              split_pair(P[i], P[i + 1], hi, rest);
-              ph[e] = hi[0], ph[e + 1] = hi[1];
-              pl[e] = (__bf16)rest[0], pl[e + 1] = (__bf16)rest[1];
-              if constexpr (RATE) {
-                const int j = 8 * (i / 4) + 4 * half + i % 4 - (js >= 2 * t ? 0 : 32);
-                split_pair(P[i] * (float)(lc - j), P[i + 1] * (float)(lc - j - 1), hi, rest);
-                rh[e] = hi[0], rh[e + 1] = hi[1];
-                rl[e] = (__bf16)rest[0], rl[e + 1] = (__bf16)rest[1];
-              }
-            }
-            O[t] = mfma(zp, ph, O[t]);
-            O[t] = mfma(zp, pl, O[t]);
+            const bf16x8* pf = pairs + (((js >= 2 * t ? t : 2) * 2 + js % 2) * 2) * kWave + ln;
+            O[t] = mfma(zf, pf[0], O[t]);
+            O[t] = mfma(zf, pf[kWave], O[t]);
             if constexpr (RATE) {
-              OD[t] = mfma(zp, rh, OD[t]);
-              OD[t] = mfma(zp, rl, OD[t]);
-            }
-            if (bad) {  // large finite stand-ins times 0 or 1, often enough to overflow
-              bf16x8 one;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int i = 8 * (js % 2) + e, j = 8 * (i / 4) + 4 * half + i % 4;
-                one[e] = js < 2 * t || lc >= j ? (__bf16)1.f : (__bf16)0.f;
-              }
-#pragma unroll
-              for (int k = 0; k < 3; ++k) {
-                O[t] = mfma(zn, one, O[t]);
-                if constexpr (RATE) OD[t] = mfma(zn, one, OD[t]);
-              }
+              OD[t] = mfma(zf, pf[12 * kWave], OD[t]);
+              OD[t] = mfma(zf, pf[13 * kWave], OD[t]);
             }
           }
         }
         if (carry) {
           // z weighted by its decay to the chunk's end, as three bfloat16 parts: the carry keeps float32's bits
-          bf16x8 z0, z1, z2, l0, l1;
-          const float4 da = *reinterpret_cast<const float4*>(down + 16 * js + 4 * half),
-                       db = *reinterpret_cast<const float4*>(down + 16 * js + 8 + 4 * half);
-          const float dw[8] = {da.x, da.y, da.z, da.w, db.x, db.y, db.z, db.w};
+          auto weighted = [&](const float* w, float (&out)[8]) {
+            const float4 wa = *reinterpret_cast<const float4*>(w + 16 * js + 4 * half),
+                         wb = *reinterpret_cast<const float4*>(w + 16 * js + 8 + 4 * half);
+            const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            bf16x2 hi;
-            f32x2 rest, rest2;
-            split_pair((float)zf[e] * dw[e], (float)zf[e + 1] * dw[e + 1], hi, rest);
-            z0[e] = hi[0], z0[e + 1] = hi[1];
-            split_pair(rest[0], rest[1], hi, rest2);
-            z1[e] = hi[0], z1[e + 1] = hi[1];
-            z2[e] = (__bf16)rest2[0], z2[e + 1] = (__bf16)rest2[1];
-          }
+            for (int e = 0; e < 8; ++e) out[e] = (float)zf[e] * ws[e];
+          };
+          float zw[8], zl[8];
+          weighted(down, zw);
+          const Parts3 z3 = split3(zw);
+          Parts2 l2;
           if constexpr (RATE) {
-            const float4 la = *reinterpret_cast<const float4*>(downlag + 16 * js + 4 * half),
-                         lb = *reinterpret_cast<const float4*>(downlag + 16 * js + 8 + 4 * half);
-            const float lw[8] = {la.x, la.y, la.z, la.w, lb.x, lb.y, lb.z, lb.w};
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              bf16x2 hi;
-              f32x2 rest;
-              split_pair((float)zf[e] * lw[e], (float)zf[e + 1] * lw[e + 1], hi, rest);
-              l0[e] = hi[0], l0[e + 1] = hi[1];
-              l1[e] = (__bf16)rest[0], l1[e + 1] = (__bf16)rest[1];
-            }
+            weighted(downlag, zl);
+            l2 = split2(zl);
           }
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
             const bf16x8 yt = read_tr8<KP, true>(ys, ln, 16 * js, 32 * t);
-            S[t] = mfma(yt, z0, S[t]);
-            S[t] = mfma(yt, z1, S[t]);
-            S[t] = mfma(yt, z2, S[t]);
+            S[t] = mfma(yt, z3.hi, S[t]);
+            S[t] = mfma(yt, z3.lo, S[t]);
+            S[t] = mfma(yt, z3.lo2, S[t]);
             if constexpr (RATE) {
-              D[t] = mfma(yt, l0, D[t]);
-              D[t] = mfma(yt, l1, D[t]);
+              D[t] = mfma(yt, l2.hi, D[t]);
+              D[t] = mfma(yt, l2.lo, D[t]);
             }
           }
         }
       }
     } else {
+      f32x16 P = {};
+      if constexpr (FULL) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float4 s = pairs[r * kWave + ln];
+#pragma unroll
+          for (int k = 1; k < NW; ++k) {
+            const float4 v = pairs[(k * 4 + r) * kWave + ln];
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+          }
+          const float* w = wt + C + lc - 4 * half - 8 * r;
+          const float pv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) P[4 * r + e] = w[-e] != 0.f ? pv[e] * w[-e] : 0.f;  // a masked pair is 0 whatever its product
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
         const int j = 8 * (i / 4) + 4 * half + i % 4;
         const float zf = zs[tile_at<T, BV>(j, wave * 32 + lc)];
         if constexpr (FULL) {
-          const bool hit = bad && bits_nonfinite(__float_as_uint(zf));
-          const float zp = hit ? 0.f : zf;
-          O[0] = mfma(zp, Pd[0][i], O[0]);
-          if constexpr (RATE) OD[0] = mfma(zp, Pd[0][i] * (float)(lc - j), OD[0]);
-          if (bad) {  // large finite stand-ins times 0 or 1, often enough to overflow
-            const float zn = hit ? 3.3e38f : 0.f, one = lc >= j ? 1.f : 0.f;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              O[0] = mfma(zn, one, O[0]);
-              if constexpr (RATE) OD[0] = mfma(zn, one, OD[0]);
-            }
-          }
+          O[0] = mfma(zf, P[i], O[0]);
+          if constexpr (RATE) OD[0] = mfma(zf, P[i] * (float)(lc - j), OD[0]);
         }
         if (carry) {
           const float zw = zf * down[j];
@@ -570,59 +676,68 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     }
 
     if constexpr (FULL) {
+      if (bad) {
+        const float nan = __builtin_nanf("");
+        const int* first = bad_row[parity] + wave * 32;
+        const bool gone = first[lc] < C;
 #pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        const int i = 32 * t + lc;  // this lane's token
-        if (i >= n) continue;
-        const int64_t tok = token(u + i);
+        for (int i = 0; i < 16; ++i) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int c0 = wave * 32 + 8 * r + 4 * half, c = slice * BV + c0;
-          const float o[4] = {O[t][4 * r], O[t][4 * r + 1], O[t][4 * r + 2], O[t][4 * r + 3]};
-          if constexpr (RATE) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dr += (double)(OD[t][4 * r + e] * to_f32(dots[tile_at<T, BV>(i, c0 + e)]));
+          for (int t = 0; t < IT; ++t) {
+            const bool hit = 32 * t + lc >= first[8 * (i / 4) + 4 * half + i % 4];
+            O[t][i] = hit ? nan : O[t][i];
+            if constexpr (RATE) OD[t][i] = hit ? nan : OD[t][i];
           }
-          if (!p.out || c >= V) continue;
-          const uint64_t at = ((uint64_t)tok * p.heads + h) * V + c;
-          if (p.out_f32 || !BF) {
-            float* dst = static_cast<float*>(p.out) + at;
-            if (a.vec_out) *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-            else
-              for (int e = 0; e < 4; ++e)
-                if (c + e < V) dst[e] = o[e];
-          } else {
-            T* dst = static_cast<T*>(p.out) + at;
-            if (a.vec_out) {
-              const bf16x4 v = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-              *reinterpret_cast<bf16x4*>(dst) = v;
-            } else {
-              for (int e = 0; e < 4; ++e)
-                if (c + e < V) dst[e] = from_f32<T>(o[e]);
-            }
+#pragma unroll
+          for (int t = 0; t < KT; ++t) {
+            S[t][i] = gone ? nan : S[t][i];
+            if constexpr (RATE) D[t][i] = gone ? nan : D[t][i];
           }
         }
       }
+      if constexpr (DOT) {
+#pragma unroll
+        for (int t = 0; t < IT; ++t)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)  // rows past the end are zero in the tile
+            dr += (double)(OD[t][k] * to_f32(dots[tile_at<T, BV>(32 * t + lc, wave * 32 + 8 * (k / 4) + 4 * half + k % 4)]));
+      }
     }
   }
+  if (FULL && sg.n > 0) put(sg.u0 + (sg.n - 1) / C * C);
 
   // the carry after the segment
-  float* to = nullptr;
   int colf = col, halff = half;
   asm volatile("" : "+v"(colf), "+v"(halff));  // the row and column tests are made again, not kept over the loop
-  if (!FULL) to = a.bound + bound_at(sg.u0 + sg.n);
-  else if (last_seg && p.s_out) to = p.s_out;
+  auto each = [&](int rs, int cs, auto&& f) {
+    if (colf >= V) return;
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int row = 32 * t + carry_row<T>(i / 4, i % 4, halff);
-      if (row >= K || colf >= V) continue;
-      if (to) to[FULL ? sat(row, colf) : (uint64_t)row * V + colf] = S[t][i];
-      if constexpr (RATE && !FULL) a.bound_d[bound_at(sg.u0 + sg.n) + (uint64_t)row * V + colf] = D[t][i];
-      if constexpr (DOT)
-        if (last_seg && p.ds_out) dr += (double)(D[t][i] * p.ds_out[sat(row, colf)]);
+      for (int i = 0; i < 16; ++i) {
+        const int row = 32 * t + carry_row<T>(i / 4, i % 4, halff);
+        if (row < K) f(t, i, row * rs + colf * cs);
+      }
+  };
+  if constexpr (!FULL) {
+    const uint64_t at = bound_at(sg.u0 + sg.n);
+    float* to = a.bound + at;
+    each(V, 1, [&](int t, int i, int o) { to[o] = S[t][i]; });
+    if constexpr (RATE) {
+      float* tod = a.bound_d + at;
+      each(V, 1, [&](int t, int i, int o) { tod[o] = D[t][i]; });
     }
+  } else if (last_seg) {
+    if (p.s_out) {
+      float* to = p.s_out + sbase;
+      each(rs, cs, [&](int t, int i, int o) { to[o] = S[t][i]; });
+    }
+    if constexpr (RATE)
+      if (p.ds_out) {
+        const float* g = p.ds_out + sbase;
+        each(rs, cs, [&](int t, int i, int o) { dr += (double)(D[t][i] * g[o]); });
+      }
+  }
   if constexpr (DOT) {
     for (int off = 32; off; off >>= 1) dr += __shfl_xor(dr, off);
     if (lane == 0) red[wave] = dr;
@@ -636,27 +751,30 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
 }
 
 // kp: K rounded up to 64, 128 or 256; nw: waves per block, 32 columns each (4, or 2 where K and V are at most 64)
-template <typename T>
-void attn_chunk_launch(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
-
-template <typename T, int KP, int NW>
+template <typename T, int KP, int NW, bool VEC>
 void attn_chunk_launch_at(const AttnChunkArgs& a, bool full, bool rate, hipStream_t s) {
-  const dim3 grid((unsigned)xcd_blocks(a.tiles)), block(NW * kWave);
+  const uint64_t units = a.slots * (a.p.heads / a.group);
+  const dim3 grid((unsigned)(xcd_blocks(units) * a.group * a.slices)), block(NW * kWave);
   if (full) {
-    if (rate) k_attn_chunk<T, KP, NW, true, true><<<grid, block, 0, s>>>(a);
-    else k_attn_chunk<T, KP, NW, true, false><<<grid, block, 0, s>>>(a);
+    if (rate) k_attn_chunk<T, KP, NW, true, true, VEC><<<grid, block, 0, s>>>(a);
+    else k_attn_chunk<T, KP, NW, true, false, VEC><<<grid, block, 0, s>>>(a);
   } else {
-    if (rate) k_attn_chunk<T, KP, NW, false, true><<<grid, block, 0, s>>>(a);
-    else k_attn_chunk<T, KP, NW, false, false><<<grid, block, 0, s>>>(a);
+    if (rate) k_attn_chunk<T, KP, NW, false, true, VEC><<<grid, block, 0, s>>>(a);
+    else k_attn_chunk<T, KP, NW, false, false, VEC><<<grid, block, 0, s>>>(a);
   }
 }
-#define LAPLEX_ATTN_CHUNK_SIZES(T)                                                                         \
-  template <>                                                                                              \
-  void attn_chunk_launch<T>(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s) { \
-    if (kp == 64 && nw == 2) attn_chunk_launch_at<T, 64, 2>(a, full, rate, s);                             \
-    else if (kp == 64) attn_chunk_launch_at<T, 64, 4>(a, full, rate, s);                                   \
-    else if (kp == 128) attn_chunk_launch_at<T, 128, 4>(a, full, rate, s);                                 \
-    else attn_chunk_launch_at<T, 256, 4>(a, full, rate, s);                                                \
-  }
+template <typename T, bool VEC>
+void attn_chunk_launch(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s) {
+  if (kp == 64 && nw == 2) attn_chunk_launch_at<T, 64, 2, VEC>(a, full, rate, s);
+  else if (kp == 64) attn_chunk_launch_at<T, 64, 4, VEC>(a, full, rate, s);
+  else if (kp == 128) attn_chunk_launch_at<T, 128, 4, VEC>(a, full, rate, s);
+  else attn_chunk_launch_at<T, 256, 4, VEC>(a, full, rate, s);
+}
+
+// The instantiations, each in a source file of its own.  vec: every row of x, y, z, dot and out is 16-byte aligned.
+void attn_chunk_bf16_vec(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
+void attn_chunk_bf16_any(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
+void attn_chunk_f32_vec(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
+void attn_chunk_f32_any(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s);
 
 }  // namespace laplex

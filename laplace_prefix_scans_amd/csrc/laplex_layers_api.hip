@@ -64,6 +64,13 @@ bool any_misaligned(const Extent (&v)[N], size_t a) {
   return false;
 }
 
+// partials of the rate gradient with or without offsets
+uint64_t drate_parts_most(const laplex_attn_shape& a) {
+  static const int32_t some = 0;
+  return std::max(attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens, &some),
+                  attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens, nullptr));
+}
+
 struct AttnWorkspace {
   void* pass;    // of one recurrence pass at a time
   float* sum;    // per query head gradients before they are added over a shared head
@@ -77,7 +84,7 @@ AttnWorkspace carve_attn(void* ws, int pass, const laplex_attn_shape& a, size_t*
   w.pass = c.take<void>(b);
   if (pass == LAPLEX_ATTN_BACKWARD) {
     if (a.heads != a.kv_heads) w.sum = c.take<float>(a.tokens * a.heads * std::max(a.dk, a.dv) * 4);
-    w.drate = c.take<double>(attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens) * a.heads * 8);
+    w.drate = c.take<double>(a.seqs ? drate_parts_most(a) * a.heads * 8 : 0);
   }
   *total = (c.off + 255) & ~size_t(255);
   return w;
@@ -197,7 +204,7 @@ extern "C" laplex_status laplex_decay_attn_backward(const laplex_attn_shape* sha
     }
     if ((err = attn_pass(p, w.pass, stream)) != hipSuccess) return from_hip(err);
     if (drate) {
-      const uint64_t parts = attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens);
+      const uint64_t parts = attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens, a.offsets);
       if ((err = attn_drate_reduce(w.drate, parts, a.heads, drate, stream)) != hipSuccess) return from_hip(err);
     }
   }
