@@ -10,42 +10,44 @@ namespace laplex {
 template <bool RATE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
   const AttnPass& p = a.p;
-  const uint64_t per = (uint64_t)p.K * p.V, at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t per = p.K * p.V, at = blockIdx.x * 256 + threadIdx.x;
   const uint32_t h = blockIdx.y;
-  if (at >= per) return;
   const int64_t L = a.g.seg_len;
-  const AttnDecay w = attn_decay(attn_rate(p.rate[h]), L);
-  constexpr int N = RATE ? 8 : 16;  // loads in flight
+  AttnDecay w{};
+  bool have = false;
   for (uint32_t s = blockIdx.z; s < p.seqs; s += gridDim.z) {
     const int64_t i = (int64_t)s + (a.g.offsets ? 1 : 0), first = seq_bound(a.g, i), len = seq_bound(a.g, i + 1) - first;
-    const int64_t nb = (len + L - 1) / L - 1;  // boundaries inside the sequence
-    if (nb < 1) continue;
+    if (len <= L) continue;  // no boundary inside the sequence
+    if (!have) w = attn_decay(attn_rate(p.rate[h]), L);
+    have = true;
+    if (at >= per) continue;
+    const int nb = (int)((len + L - 1) / L) - 1;
     float cur = 0.f, d = 0.f;
-    if (p.s_in) {
-      const uint64_t row = at / p.V, col = at % p.V;
-      cur = p.s_in[((uint64_t)s * p.heads + h) * per + (p.s_trans ? col * p.K + row : at)];
-    }
-    auto pos = [&](int64_t k) { return ((uint64_t)(first / L + k) * p.heads + h) * per + at; };  // boundary k = 1 .. nb
-    for (int64_t k0 = 1; k0 <= nb; k0 += N) {
-      float t[N], e[RATE ? N : 1];
+    if (p.s_in) cur = p.s_in[((uint64_t)s * p.heads + h) * per + (p.s_trans ? at % p.V * p.K + at / p.V : at)];
+    const uint64_t step = (uint64_t)p.heads * per;  // from a boundary to the next
+    uint64_t q = ((uint64_t)(first / L + 1) * p.heads + h) * per + at;
+    auto join = [&](uint64_t q, float t, float e) {
+      if constexpr (RATE) {
+        d = w.of(fmaf((float)L, cur, d)) + e;
+        a.bound_d[q] = d;
+      }
+      cur = w.of(cur) + t;
+      a.bound[q] = cur;
+    };
+    constexpr int N = 8;  // loads in flight
+    int k = 0;
+    for (; k + N <= nb; k += N) {
+      float t[N], e[N];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const uint64_t q = pos(min(k0 + k, nb));
-        t[k] = a.bound[q];
-        if constexpr (RATE) e[k] = a.bound_d[q];
+      for (int j = 0; j < N; ++j) {
+        t[j] = a.bound[q + j * step];
+        e[j] = RATE ? a.bound_d[q + j * step] : 0.f;
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (k0 + k > nb) break;
-        const uint64_t q = pos(k0 + k);
-        if constexpr (RATE) {
-          d = w.of(fmaf((float)L, cur, d)) + e[k];
-          a.bound_d[q] = d;
-        }
-        cur = w.of(cur) + t[k];
-        a.bound[q] = cur;
-      }
+      for (int j = 0; j < N; ++j) join(q + j * step, t[j], e[j]);
+      q += N * step;
     }
+    for (; k < nb; ++k, q += step) join(q, a.bound[q], RATE ? a.bound_d[q] : 0.f);
   }
 }
 

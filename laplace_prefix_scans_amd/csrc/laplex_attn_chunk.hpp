@@ -91,6 +91,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
@@ -131,10 +132,19 @@ struct Stage {
     rows_it = RPI * stride;
     cols = width - c;
   }
-  // The next chunk's rows [0, rows); rows and columns past the end are zero.
-  __device__ __forceinline__ void load(int rows) {
+  // The next chunk's rows [0, rows); rows and columns past the end are zero.  whole: every column is there.
+  __device__ __forceinline__ void load(int rows, bool whole) {
     const int r0 = threadIdx.x / (P / E);
     const T* src = at;
+    if (VEC && whole && rows == ROWS) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = *reinterpret_cast<const uint4*>(src);
+        src += rows_it;
+      }
+      at = src;
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       uint4 q = make_uint4(0, 0, 0, 0);
@@ -160,29 +170,37 @@ struct Stage {
   }
   // Replaces infinities and NaN by 0 and lowers first[column of the tile] to their row; whether there were any.
   __device__ __forceinline__ bool clean(int* first) {
-    bool any = false;
+    // the largest magnitude, as an integer: infinities and NaN are above every finite one
+    bool bad;
+    if constexpr (sizeof(T) == 2) {
+      u16x2 top = {0, 0};
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu));
+      }
+      bad = top[0] >= 0x7F80u || top[1] >= 0x7F80u;
+    } else {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) top = max(max(max(top, v[i].x & 0x7FFFFFFFu), max(v[i].y & 0x7FFFFFFFu, v[i].z & 0x7FFFFFFFu)), v[i].w & 0x7FFFFFFFu);
+      bad = top >= 0x7F800000u;
+    }
+    if (!bad) return false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      bool bad = false;
+      T e[E];
+      __builtin_memcpy(e, &v[i], 16);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2) bad |= (w[j] & 0x7F80u) == 0x7F80u;
-        bad |= (w[j] & 0x7F800000u) == 0x7F800000u;
-      }
-      if (bad) {
-        any = true;
-        T e[E];
-        __builtin_memcpy(e, w, 16);
-        for (int j = 0; j < E; ++j)
-          if (bits_nonfinite(__float_as_uint(to_f32(e[j])))) {
-            e[j] = T(0.f);
-            atomicMin(first + threadIdx.x % (P / E) * E + j, (int)threadIdx.x / (P / E) + i * RPI);
-          }
-        __builtin_memcpy(&v[i], e, 16);
-      }
+      for (int j = 0; j < E; ++j)
+        if (bits_nonfinite(__float_as_uint(to_f32(e[j])))) {
+          e[j] = T(0.f);
+          atomicMin(first + threadIdx.x % (P / E) * E + j, (int)threadIdx.x / (P / E) + i * RPI);
+        }
+      __builtin_memcpy(&v[i], e, 16);
     }
-    return any;
+    return true;
   }
 };
 
@@ -360,7 +378,11 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   if constexpr (FULL)
 #pragma unroll
     for (int t = 0; t < IT; ++t) up[t] = p.c_in * decay(-rate * (float)(32 * t + lc + lead));
-  const AttnDecay wc = attn_decay(rate, C);  // the carry's decay over a chunk
+  // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
+  // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
+  // so far back to the exact one.
+  const double wc = exp(-(double)rate * (double)C);
+  double owed = 1.0;
   auto set_down = [&](int n) {
     if (threadIdx.x < C) {
       const int j = threadIdx.x, lag = n - 1 - j;
@@ -378,6 +400,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
 
   Stage<T, C, KP, THREADS, VEC> sx, sy;
   Stage<T, C, BV, THREADS, VEC> sz, sd;
+  const bool whole_v = ((int)slice + 1) * BV <= V;
   const int64_t t0 = token(sg.u0);
   if constexpr (FULL) sx.init(x + t0 * p.x.token, step * p.x.token, 0, K);
   sy.init(y + t0 * p.y.token, step * p.y.token, 0, K);
@@ -385,10 +408,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, step * p.dot_view.token, slice * BV, V);
   auto load = [&](int64_t u) {
     const int rows = (int)min((int64_t)C, sg.u0 + sg.n - u);
-    if constexpr (FULL) sx.load(rows);
-    sy.load(rows);
-    sz.load(rows);
-    if constexpr (DOT) sd.load(rows);
+    if constexpr (FULL) sx.load(rows, K == KP);
+    sy.load(rows, K == KP);
+    sz.load(rows, whole_v);
+    if constexpr (DOT) sd.load(rows, whole_v);
   };
   f32x16 O[FULL ? IT : 1];
   // Writes the outputs of the chunk at u.  Called when the next chunk is in LDS: stores are counted with the
@@ -577,16 +600,17 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     // the carry over the chunk, with the lag-weighted one ahead of it
     const bool carry = !FULL || more || keep;
     if (carry) {
-      AttnDecay w = wc;
-      if (n != C) w = attn_decay(rate, n);
+      const double exact = (n == C ? wc : exp(-(double)rate * (double)n)) * owed;
+      const float w = (float)exact;
+      owed = w != 0.f ? exact / (double)w : 1.0;
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if constexpr (RATE) {
-            D[t][i] = w.of(fmaf((float)n, S[t][i], D[t][i]));
+            D[t][i] = w * fmaf((float)n, S[t][i], D[t][i]);
           }
-          S[t][i] = w.of(S[t][i]);
+          S[t][i] *= w;
         }
     }
     if constexpr (BF) {
