@@ -9,22 +9,22 @@ namespace laplex {
 // states, D_k+1 = w(L) (D_k + L S_k) + E_k.
 template <bool RATE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
+  __shared__ AttnDecay sw;
   const AttnPass& p = a.p;
   const uint32_t per = p.K * p.V, at = blockIdx.x * 256 + threadIdx.x;
   const uint32_t h = blockIdx.y;
   const int64_t L = a.g.seg_len;
-  AttnDecay w{};
-  bool have = false;
+  if (threadIdx.x == 0) sw = attn_decay(attn_rate(p.rate[h]), L);
+  __syncthreads();
+  const AttnDecay w = sw;
+  if (at >= per) return;
+  const uint64_t step = (uint64_t)p.heads * per;  // from a boundary to the next
   for (uint32_t s = blockIdx.z; s < p.seqs; s += gridDim.z) {
     const int64_t i = (int64_t)s + (a.g.offsets ? 1 : 0), first = seq_bound(a.g, i), len = seq_bound(a.g, i + 1) - first;
     if (len <= L) continue;  // no boundary inside the sequence
-    if (!have) w = attn_decay(attn_rate(p.rate[h]), L);
-    have = true;
-    if (at >= per) continue;
     const int nb = (int)((len + L - 1) / L) - 1;
     float cur = 0.f, d = 0.f;
     if (p.s_in) cur = p.s_in[((uint64_t)s * p.heads + h) * per + (p.s_trans ? at % p.V * p.K + at / p.V : at)];
-    const uint64_t step = (uint64_t)p.heads * per;  // from a boundary to the next
     uint64_t q = ((uint64_t)(first / L + 1) * p.heads + h) * per + at;
     auto join = [&](uint64_t q, float t, float e) {
       if constexpr (RATE) {
@@ -52,6 +52,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
 }
 
 // ------------------------------------------------------------------ launches
+constexpr uint64_t kAttnMinSeg = 128;
 struct AttnPlan {
   int kp, nw;
   uint32_t slices;
@@ -59,18 +60,22 @@ struct AttnPlan {
   uint64_t bounds;
   bool split;
 };
+// The split depends on K and V alike, so that a pass and the one with K and V exchanged share their segments.
+static int64_t attn_seg_len(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+  const uint32_t wide = std::max(K, V), slices = wide > 128 ? 2 : 1;
+  const uint64_t blocks = wide <= 64 ? 1024 : 512;  // two waves (wide <= 64) or four per SIMD
+  uint64_t len = std::max<uint64_t>(kAttnMinSeg, tokens * heads * slices / blocks);
+  len = (len + 63) / 64 * 64;
+  return (int64_t)(len + len / 2 < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
+}
 static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
   AttnPlan q;
   q.kp = K <= 64 ? 64 : K <= 128 ? 128 : 256;
-  q.nw = V <= 64 && K <= 64 ? 2 : 4;
-  q.slices = (V + 32 * q.nw - 1) / (32 * q.nw);
-  const uint64_t blocks = q.nw == 2 ? 1024 : 512;  // two waves per SIMD
-  uint64_t len = std::max<uint64_t>(512, tokens * heads * q.slices / blocks);
-  len = (len + 63) / 64 * 64;
-  q.split = len < tokens;
-  if (!q.split) len = std::max<uint64_t>(64, (tokens + 63) / 64 * 64);
-  q.seg_len = (int64_t)len;
-  q.bounds = q.split ? tokens / len + 1 : 0;
+  q.nw = V <= 64 && K <= 64 ? 4 : 8;
+  q.slices = (V + 16 * q.nw - 1) / (16 * q.nw);
+  q.seg_len = attn_seg_len(seqs, heads, K, V, tokens);
+  q.split = (uint64_t)q.seg_len < tokens;
+  q.bounds = q.split ? tokens / q.seg_len + 1 : 0;
   return q;
 }
 
@@ -84,7 +89,8 @@ uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V,
 }
 
 static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width, size_t e) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && token * e % 16 == 0 && head * e % 16 == 0 && width * e % 16 == 0;
+  // (and the 64 rows of a chunk lie within 2^31 bytes)
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (uint64_t)token * e < (1u << 25) && token * e % 16 == 0 && head * e % 16 == 0 && width * e % 16 == 0;
 }
 
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
@@ -105,6 +111,8 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
                    aligned16(p.z.p, p.z.token, p.z.head, p.V, e) &&
                    (!rate || aligned16(p.dot, p.dot_view.token, p.dot_view.head, p.V, e)) &&
                    reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  a.bound_trans = p.bound_ready;
+  a.fine = p.s_out != nullptr;
   a.drate = p.drate_part;
   auto run = [&](const char* name, bool full) {
     LAPLEX_LAUNCH(name, p.tokens, s, {
@@ -114,7 +122,7 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
     return hipGetLastError();
   };
   hipError_t err;
-  if (q.split) {
+  if (q.split && !p.bound_ready) {
     if ((err = run("k_attn_chunk_state", false)) != hipSuccess) return err;
     const dim3 grid((unsigned)(((uint64_t)p.K * p.V + 255) / 256), p.heads, std::min(p.seqs, 64u));
     LAPLEX_LAUNCH("k_attn_join", q.bounds, s, rate ? k_attn_join<true><<<grid, 256, 0, s>>>(a) : k_attn_join<false><<<grid, 256, 0, s>>>(a));

@@ -86,7 +86,7 @@ __device__ __forceinline__ AttnSeg find_seg(const AttnSegs& g, uint64_t b) {
 }
 
 // ------------------------------------------------------------------ tiles in LDS
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -95,17 +95,18 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
-// Rows of a tile are 16-byte chunks; chunk c of row r is kept at c ^ swz(r), so
-// that both kinds of reads meet 64 different banks: 16 bytes from each of 16
-// rows (row operands), and for the transposed operands 64 contiguous bytes
-// from each of 4 rows (bf16) or 128 from two rows 4 apart (float).
+// Rows of a tile are 16-byte pieces; piece c of row r is kept at c ^ swz(r), so
+// that the reads spread over the 64 banks: 16 bytes from each of 16 rows (row
+// operands), and for the transposed operands 8 rows of 32 bytes (bf16) or four
+// rows 4 apart of 64 (float).
 template <typename T, int P>
 __device__ __forceinline__ int swz(int r) {
   if constexpr (sizeof(T) == 2) {
-    if constexpr (P == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-    else return ((r & 3) << 2) | ((r >> 2) & 3);
+    const int low = (((r >> 2) & 1) << 1) | ((r >> 3) & 1);
+    if constexpr (P == 64) return (((r >> 1) & 1) << 2) | low;
+    else return ((r & 3) << 2) | low;
   } else {
-    return (((r >> 2) & 1) << 3) | (((r >> 3) & 1) << 2) | (r & 3);
+    return (((r >> 2) & 3) << 2) | (r & 3);
   }
 }
 // element offset of column c (any) of row r
@@ -122,44 +123,50 @@ struct Stage {
   static constexpr int E = 16 / sizeof(T), RPI = THREADS / (P / E), N = ROWS / RPI;
   static_assert(THREADS % (P / E) == 0 && ROWS % RPI == 0, "pieces divide evenly");
   uint4 v[N];
-  const T* at;       // this thread's first piece in the next chunk
-  int64_t rows_it;   // elements from one of its pieces to the next
-  int cols;          // columns from its piece's first to the end of the row
-  // p: the row of the first token, col0: the tile's first column, stride: elements from a row of the tile to the next
-  __device__ __forceinline__ void init(const T* p, int64_t stride, int col0, int width) {
+  // The thread's piece of the next chunk's row group i is at at + i * rows_it + off: a pointer all threads share
+  // and 32 bits of its own (VEC: the host has seen that RPI rows span less than 2^31 bytes).
+  const T* at;
+  int64_t rows_it;
+  uint32_t off;
+  int cols;  // columns from its piece's first to the end of the row
+  // p: the first token's row, col0: the tile's first column, stride: elements from a row to the next token's,
+  // step: 1, or -1 where the tokens run backwards
+  __device__ __forceinline__ void init(const T* p, int64_t stride, int step, int col0, int width) {
     const int r = threadIdx.x / (P / E), c = col0 + threadIdx.x % (P / E) * E;
-    at = p + r * stride + c;
-    rows_it = RPI * stride;
     cols = width - c;
+    rows_it = RPI * stride * step;
+    if constexpr (VEC) {
+      at = step > 0 ? p : p - (RPI - 1) * stride;
+      off = (uint32_t)(((step > 0 ? r : RPI - 1 - r) * stride + c) * sizeof(T));
+    } else {
+      at = p + r * stride * step + c;
+    }
+  }
+  __device__ __forceinline__ uint4 piece(int i) const {
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(at + i * rows_it) + off);
   }
   // The next chunk's rows [0, rows); rows and columns past the end are zero.  whole: every column is there.
   __device__ __forceinline__ void load(int rows, bool whole) {
     const int r0 = threadIdx.x / (P / E);
-    const T* src = at;
     if (VEC && whole && rows == ROWS) {
 #pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = piece(i);
+    } else {
+#pragma unroll
       for (int i = 0; i < N; ++i) {
-        v[i] = *reinterpret_cast<const uint4*>(src);
-        src += rows_it;
-      }
-      at = src;
-      return;
-    }
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if constexpr (VEC) {
+          if (r0 + i * RPI < rows && cols > 0) q = piece(i);
+        } else {
+          T e[E];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint4 q = make_uint4(0, 0, 0, 0);
-      if constexpr (VEC) {
-        if (r0 + i * RPI < rows && cols > 0) q = *reinterpret_cast<const uint4*>(src);
-      } else {
-        T e[E];
-#pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = r0 + i * RPI < rows && j < cols ? src[j] : T(0.f);
-        __builtin_memcpy(&q, e, 16);
+          for (int j = 0; j < E; ++j) e[j] = r0 + i * RPI < rows && j < cols ? at[i * rows_it + j] : T(0.f);
+          __builtin_memcpy(&q, e, 16);
+        }
+        v[i] = q;
       }
-      v[i] = q;
-      src += rows_it;
     }
-    at = src;
+    at += N * rows_it;
   }
   __device__ __forceinline__ void store(T* tile) const {
 #pragma unroll
@@ -218,7 +225,8 @@ __device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
 struct Parts2 {
   bf16x8 hi, lo;
 };
-__device__ __forceinline__ Parts2 split2(const float (&x)[8]) {
+__device__ __forceinline__ Parts2 split2(const f32x4& u, const f32x4& v) {
+  const float x[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -231,7 +239,8 @@ __device__ __forceinline__ Parts2 split2(const float (&x)[8]) {
 struct Parts3 {
   bf16x8 hi, lo, lo2;
 };
-__device__ __forceinline__ Parts3 split3(const float (&x)[8]) {
+__device__ __forceinline__ Parts3 split3(const f32x4& u, const f32x4& v) {
+  const float x[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
   uint32_t h[4], l[4], m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -249,8 +258,10 @@ struct AttnChunkArgs {
   AttnSegs g;
   uint32_t slices;   // blocks across the V columns
   uint32_t group;    // query heads per shared head
+  bool fine;         // the carry is an output
   uint64_t slots;    // segments, with room for unused ones
   float* bound;      // states at segment boundaries ([boundary][head][K][V]), or null
+  bool bound_trans;  // they are [V][K], from a pass with the roles of K and V exchanged
   float* bound_d;    // the lag-weighted ones (rate gradient)
   double* drate;     // Rate: partials [slot][slice][head]
 };
@@ -258,51 +269,68 @@ struct AttnChunkArgs {
 template <typename T>
 constexpr int kAttnC = sizeof(T) == 2 ? 64 : 32;  // tokens per chunk
 
-// Row of the carry that register (r, e) of a 32-row tile holds in lane half h.
-// bf16: the order in which 8 consecutive channels of x form one operand.
+// Row of the carry that register r of 16-row tile t holds in lane group g.
+// bf16: two tiles side by side hold the 32 rows in the order in which a lane's
+// 8 consecutive channels of x are one operand.
 template <typename T>
-__device__ __forceinline__ int carry_row(int r, int e, int h) {
-  if constexpr (sizeof(T) == 2) return 16 * (r >> 1) + 8 * h + 4 * (r & 1) + e;
-  else return 8 * r + 4 * h + e;
+__device__ __forceinline__ int carry_row(int t, int g, int r) {
+  if constexpr (sizeof(T) == 2) return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r;
+  else return 16 * t + 4 * g + r;
 }
 
-// transposed operand: column 16 * (lane / 16 % 2) + lane % 16 (bf16 carry order if PERM) of rows row0 + 4 h + {0..3}
-template <int P, bool PERM>
-__device__ __forceinline__ s16x4 read_tr(const __bf16* tile, int l, int row0, int col0) {
-  const int q = l & 3, row = row0 + 4 * (l >> 5) + ((l >> 2) & 3);
-  const int quad = PERM ? ((q & 1) << 1 | (q >> 1)) : q;
-  const int c = col0 + 16 * ((l >> 4) & 1) + 4 * quad;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + tile_at<__bf16, P>(row, c)));
+// a value that every lane holds, in scalar registers
+__device__ __forceinline__ double uniform(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-template <int P, bool PERM>
-__device__ __forceinline__ bf16x8 read_tr8(const __bf16* tile, int l, int row0, int col0) {
-  struct { s16x4 a, b; } v = {read_tr<P, PERM>(tile, l, row0, col0), read_tr<P, PERM>(tile, l, row0 + 8, col0)};
+
+// Transposed operand: this lane's column of rows row0 + 4 g + {0..3} and 16 further on.  A group of 16 lanes
+// reads 4 rows x 16 columns, each lane 4 columns of one row, and gets its column's 4 rows back.
+// col: the first column that this lane reads (its lane % 4 -th quad of the 16).
+template <int P>
+__device__ __forceinline__ bf16x8 read_tr(const __bf16* tile, int l, int row0, int col) {
+  const int row = row0 + 4 * (l >> 4) + ((l >> 2) & 3);
+  struct { s16x4 a, b; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + tile_at<__bf16, P>(row, col))),
+                              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + tile_at<__bf16, P>(row + 16, col)))};
   return __builtin_bit_cast(bf16x8, v);
 }
 
-__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16 mfma(float a, float b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
-}
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-// A 32 x 32 tile of the carry (KT of them per wave, one under the other): a
-// float register per element, column = lane % 32.
-template <typename T, int KP, int NW, bool FULL, bool RATE, bool VEC>
-__global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_chunk(AttnChunkArgs a) {
-  constexpr int C = kAttnC<T>, KT = KP / 32, BV = 32 * NW, THREADS = NW * kWave, IT = C / 32;
+// sum of a tile's four registers' products and the like: loops over the registers of KT tiles
+#define LAPLEX_EACH(t, n, r)   \
+  _Pragma("unroll") for (int t = 0; t < (n); ++t) _Pragma("unroll") for (int r = 0; r < 4; ++r)
+
+// One block: a segment's chunks in turn, one head, 16 columns of the carry per
+// wave.  The carry's 16 x 16 tiles stay in the accumulators' layout (column =
+// lane % 16, row = 4 (lane / 16) + register), which is that of an operand of
+// the same column and consecutive rows: the carry enters the products of the
+// next chunk without leaving the registers.
+//   P^T = y x^T, weighted        (the waves share its tiles out)
+//   out^T = up (S^T x^T) + z^T P
+//   S = w(n) S + y^T (down z)
+// With 16 columns a wave holds 32 registers of a 128-row carry, so that four
+// waves share a SIMD and one's conversions run beside another's products;
+// 32 columns in half as many waves took as long without, and twice as long with the rate's gradient.
+// FINE: the carry goes out as float32 (otherwise it only enters results of type T).
+template <typename T, int KP, int NW, bool FULL, bool RATE, bool FINE, bool VEC>
+__global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_chunk(AttnChunkArgs a) {
+  constexpr int C = kAttnC<T>, KT = KP / 16, BV = 16 * NW, THREADS = NW * kWave, IT = C / 16;
   constexpr bool BF = sizeof(T) == 2, DOT = FULL && RATE;
+  constexpr int WK = NW < KP / 16 ? NW : KP / 16;  // float: waves that share the channels of P^T
   const AttnPass& p = a.p;
   __shared__ __attribute__((aligned(16))) T xs[FULL ? C * KP : 8];
   __shared__ __attribute__((aligned(16))) T ys[C * KP];
   __shared__ __attribute__((aligned(16))) T zs[C * BV];
   __shared__ __attribute__((aligned(16))) T dots[DOT ? C * BV : 8];
   __shared__ __attribute__((aligned(16))) float down[C], downlag[RATE ? C : 4];
-  __shared__ float wt[FULL ? 2 * C : 1];
-  // bf16: operand [tile][channel half][part] of a lane (the lag-weighted ones behind them); float: [wave][register quad]
-  using Pair = std::conditional_t<BF, bf16x8, float4>;
-  __shared__ Pair pairs[(FULL ? (BF ? (RATE ? 24 : 12) : NW * 4) : 1) * kWave];
+  __shared__ float wt[FULL ? 2 * C : 1], up[FULL ? C : 1];
+  // bf16: operand [32 rows j][tile i][part] of a lane (the lag-weighted ones behind them); float: [wave][tile]
+  using Pair = std::conditional_t<BF, bf16x8, f32x4>;
+  constexpr int PAIRS = 2 * IT * 2 * kWave;
+  __shared__ Pair pairs[FULL ? (BF ? (RATE ? 2 : 1) * PAIRS : WK * 3 * kWave) : 1];
   __shared__ int bad_chunk[2], bad_row[2][FULL ? BV : 1];
   __shared__ double red[NW];
 
@@ -314,10 +342,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   const uint64_t slot = unit / shared;
   if (slot >= a.slots) return;
   const AttnSeg sg = find_seg(a.g, slot);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id(), half = lane >> 5, lc = lane & 31;
-  const int col = slice * BV + wave * 32 + lc;  // this lane's column of the carry
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id(), g = lane >> 4, lc = lane & 15;
+  const int col = slice * BV + wave * 16 + lc;  // this lane's column of the carry
   const int K = (int)p.K, V = (int)p.V;
-  const bool active = (int)slice * BV + wave * 32 < V;  // the wave has columns (all waves move tiles)
+  const bool active = (int)slice * BV + wave * 16 < V;  // the wave has columns (all waves move tiles)
   if (DOT && threadIdx.x == 0 && (!sg.valid || sg.outside)) a.drate[(slot * a.slices + slice) * p.heads + h] = 0.0;
   if (!sg.valid) return;
   if (sg.outside) {
@@ -341,30 +369,27 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   const uint64_t sbase = ((uint64_t)sg.seq * p.heads + h) * (uint64_t)K * V;
   const int rs = p.s_trans ? 1 : V, cs = p.s_trans ? K : 1;
   const uint64_t per_bound = (uint64_t)K * V;
+  const int brs = a.bound_trans ? 1 : V, bcs = a.bound_trans ? K : 1;
   auto bound_at = [&](int64_t u) { return ((uint64_t)((sg.first + u) / a.g.seg_len) * p.heads + h) * per_bound; };
-  auto load_state = [&](f32x16 (&s)[KT], const float* src, int rs, int cs) {
+  auto load_state = [&](f32x4 (&s)[KT], const float* src, int rs, int cs) {
     if (col >= V) return;
     src += (int64_t)col * cs;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = 32 * t + carry_row<T>(i / 4, i % 4, half);
-        const float v = src[min(row, K - 1) * rs];
-        s[t][i] = row < K ? v : 0.f;
-      }
+    LAPLEX_EACH(t, KT, r) {
+      const int row = carry_row<T>(t, g, r);
+      const float v = src[min(row, K - 1) * rs];
+      s[t][r] = row < K ? v : 0.f;
+    }
   };
-
-  f32x16 S[KT], D[RATE ? KT : 1];
+  f32x4 S[KT], D[RATE ? KT : 1];
 #pragma unroll
   for (int t = 0; t < KT; ++t) {
-    S[t] = f32x16{};
-    if constexpr (RATE) D[t] = f32x16{};
+    S[t] = f32x4{};
+    if constexpr (RATE) D[t] = f32x4{};
   }
   if constexpr (FULL) {
     if (sg.u0 > 0) {
       const uint64_t at = bound_at(sg.u0);
-      load_state(S, a.bound + at, V, 1);
+      load_state(S, a.bound + at, brs, bcs);
       if constexpr (RATE) load_state(D, a.bound_d + at, V, 1);
     } else if (p.s_in) {
       load_state(S, p.s_in + sbase, rs, cs);
@@ -372,16 +397,16 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   }
 
   // weights of a pair inside a chunk by its lag, 0 for the pairs above the diagonal
-  if constexpr (FULL)
+  if constexpr (FULL) {
     for (int i = threadIdx.x; i < 2 * C; i += THREADS) wt[i] = i >= C ? p.c_pair * decay(-rate * (float)(i - C)) : 0.f;
-  float up[IT];
-  if constexpr (FULL)
-#pragma unroll
-    for (int t = 0; t < IT; ++t) up[t] = p.c_in * decay(-rate * (float)(32 * t + lc + lead));
+    if (threadIdx.x < C) up[threadIdx.x] = p.c_in * decay(-rate * (float)((int)threadIdx.x + lead));
+    if constexpr (BF)  // tiles above the diagonal stay zero
+      for (int i = threadIdx.x; i < (int)(sizeof(pairs) / sizeof(Pair)); i += THREADS) pairs[i] = Pair{};
+  }
   // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
   // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
   // so far back to the exact one.
-  const double wc = exp(-(double)rate * (double)C);
+  const double wc = uniform(exp(-(double)rate * (double)C));
   double owed = 1.0;
   auto set_down = [&](int n) {
     if (threadIdx.x < C) {
@@ -397,15 +422,14 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   const T* dot = DOT ? static_cast<const T*>(p.dot) + (int64_t)(h / p.dot_view.div) * p.dot_view.head : nullptr;
   const int step = p.reverse ? -1 : 1;
   auto token = [&](int64_t u) { return p.reverse ? sg.first + sg.len - 1 - u : sg.first + u; };
-
   Stage<T, C, KP, THREADS, VEC> sx, sy;
   Stage<T, C, BV, THREADS, VEC> sz, sd;
   const bool whole_v = ((int)slice + 1) * BV <= V;
   const int64_t t0 = token(sg.u0);
-  if constexpr (FULL) sx.init(x + t0 * p.x.token, step * p.x.token, 0, K);
-  sy.init(y + t0 * p.y.token, step * p.y.token, 0, K);
-  sz.init(z + t0 * p.z.token, step * p.z.token, slice * BV, V);
-  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, step * p.dot_view.token, slice * BV, V);
+  if constexpr (FULL) sx.init(x + t0 * p.x.token, p.x.token, step, 0, K);
+  sy.init(y + t0 * p.y.token, p.y.token, step, 0, K);
+  sz.init(z + t0 * p.z.token, p.z.token, step, slice * BV, V);
+  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, p.dot_view.token, step, slice * BV, V);
   auto load = [&](int64_t u) {
     const int rows = (int)min((int64_t)C, sg.u0 + sg.n - u);
     if constexpr (FULL) sx.load(rows, K == KP);
@@ -413,43 +437,36 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     sz.load(rows, whole_v);
     if constexpr (DOT) sd.load(rows, whole_v);
   };
-  f32x16 O[FULL ? IT : 1];
+  f32x4 O[FULL ? IT : 1];
   // Writes the outputs of the chunk at u.  Called when the next chunk is in LDS: stores are counted with the
   // loads, so writing before would make the wait for the next chunk's rows one for the stores too.
   auto put = [&](int64_t u) {
     if (!active || !p.out) return;
-    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u);
+    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u), c = slice * BV + wave * 16 + 4 * g;
+    // a pointer all threads share and 32 bits of each lane's own: 16 rows of at most 4096 x 256 floats
+    const int64_t row = (int64_t)p.heads * V, base = (token(u) - (p.reverse ? 15 : 0)) * row + (int64_t)h * V;
+    const uint32_t own = (uint32_t)((p.reverse ? 15 - lc : lc) * row) + c;
 #pragma unroll
     for (int t = 0; t < IT; ++t) {
-      const int i = 32 * t + lc;  // this lane's token
-      if (i >= n) continue;
-      const int c0 = slice * BV + wave * 32 + 4 * half;
-      const uint64_t at = ((uint64_t)token(u + i) * p.heads + h) * V + c0;
+      if (16 * t + lc >= n) continue;
+      const int64_t at = base + 16 * t * row * step;
       if (p.out_f32 || !BF) {
         float* dst = static_cast<float*>(p.out) + at;
+        if constexpr (VEC) {
+          if (c < V) *reinterpret_cast<f32x4*>(dst + own) = O[t];
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (VEC) {
-            if (c0 + 8 * r < V)
-              *reinterpret_cast<float4*>(dst + 8 * r) = make_float4(O[t][4 * r], O[t][4 * r + 1], O[t][4 * r + 2], O[t][4 * r + 3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c0 + 8 * r + e < V) dst[8 * r + e] = O[t][4 * r + e];
-          }
+          for (int e = 0; e < 4; ++e)
+            if (c + e < V) dst[own + e] = O[t][e];
         }
       } else {
         T* dst = static_cast<T*>(p.out) + at;
+        if constexpr (VEC) {
+          if (c < V) *reinterpret_cast<uint2*>(dst + own) = make_uint2(pack_bf16(O[t][0], O[t][1]), pack_bf16(O[t][2], O[t][3]));
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (VEC) {
-            if (c0 + 8 * r < V)
-              *reinterpret_cast<uint2*>(dst + 8 * r) = make_uint2(pack_bf16(O[t][4 * r], O[t][4 * r + 1]), pack_bf16(O[t][4 * r + 2], O[t][4 * r + 3]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c0 + 8 * r + e < V) dst[8 * r + e] = from_f32<T>(O[t][4 * r + e]);
-          }
+          for (int e = 0; e < 4; ++e)
+            if (c + e < V) dst[own + e] = from_f32<T>(O[t][e]);
         }
       }
     }
@@ -483,115 +500,101 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     // then formed where they are used (an xor each) instead of each holding a register over the loop
     int ln = lane;
     asm volatile("" : "+v"(ln));
-    const int half = ln >> 5, lc = ln & 31;
+    const int g = ln >> 4, lc = ln & 15;
 
-    f32x16 OD[DOT ? IT : 1];
+    f32x4 OD[DOT ? IT : 1];
     if constexpr (FULL) {
       // The weighted pairs are the same for every column: the waves share them out and pass them on through LDS.
       if constexpr (BF) {
-        // P^T tiles (rows j, columns i): (0, 0), (1, 1) on the diagonal and (0, 1), as operands of two bfloat16 parts
-        for (int tile = wave; tile < 3; tile += NW) {
-          const int j0 = tile == 1 ? 32 : 0, i0 = tile == 0 ? 0 : 32;
-          f32x16 P = {};
+        // the ten 16 x 16 tiles of P^T (rows j, columns i) on and below the diagonal, as operands of two bfloat16 parts
+        for (int tile = wave; tile < IT * (IT + 1) / 2; tile += NW) {
+          const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
+          f32x4 P = {};
 #pragma unroll
-          for (int ks = 0; ks < KP / 16; ++ks) {
-            const bf16x8 xf = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(i0 + lc, 16 * ks + 8 * half));
-            const bf16x8 yf = *reinterpret_cast<const bf16x8*>(ys + tile_at<T, KP>(j0 + lc, 16 * ks + 8 * half));
-            P = mfma(yf, xf, P);
+          for (int ks = 0; ks < KP / 32; ++ks)
+            P = mfma(*reinterpret_cast<const bf16x8*>(ys + tile_at<T, KP>(16 * jt + lc, 32 * ks + 8 * g)),
+                     *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(16 * it + lc, 32 * ks + 8 * g)), P);
+          const int lag0 = 16 * (it - jt) + lc - 4 * g;
+          float pv[4], pd[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float w = wt[C + lag0 - r];
+            pv[r] = w != 0.f ? P[r] * w : 0.f;  // a masked pair is 0 whatever its product
+            if constexpr (RATE) pd[r] = pv[r] * (float)(lag0 - r);
           }
-          const float* w0 = wt + C + i0 - j0 + lc - 4 * half;
+          auto put_pair = [&](float (&v)[4], int base) {
+            uint2* dst = reinterpret_cast<uint2*>(pairs + base + (((jt >> 1) * IT + it) * 2) * kWave + ln) + (jt & 1);
+            const uint32_t h0 = split_pair(v[0], v[1]), h1 = split_pair(v[2], v[3]);
+            dst[0] = make_uint2(h0, h1);
+            dst[2 * kWave] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+          };
+          put_pair(pv, 0);
+          if constexpr (RATE) put_pair(pd, PAIRS);
+        }
+      } else if (wave < WK) {
+        // each of WK waves adds a share of the channels of the tiles (0, 0), (0, 1), (1, 1)
+        f32x4 P[3] = {};
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            float pv[8], pd[8];
+        for (int k = 0; k < KP / WK / 16; ++k) {
+          const int ch = wave * (KP / WK) + 16 * k + 4 * g;
+          f32x4 xf[2], yf[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int i = 8 * s + e, j = 8 * (i / 4) + i % 4;
-              const float w = w0[-j];
-              pv[e] = w != 0.f ? P[i] * w : 0.f;  // a masked pair is 0 whatever its product
-              if constexpr (RATE) pd[e] = pv[e] * (float)(i0 - j0 + lc - 4 * half - j);
-            }
-            const Parts2 p2 = split2(pv);
-            pairs[((tile * 2 + s) * 2) * kWave + ln] = p2.hi;
-            pairs[((tile * 2 + s) * 2 + 1) * kWave + ln] = p2.lo;
-            if constexpr (RATE) {
-              const Parts2 d2 = split2(pd);
-              pairs[((6 + tile * 2 + s) * 2) * kWave + ln] = d2.hi;
-              pairs[((6 + tile * 2 + s) * 2 + 1) * kWave + ln] = d2.lo;
-            }
+          for (int t = 0; t < 2; ++t) {
+            xf[t] = *reinterpret_cast<const f32x4*>(xs + tile_at<T, KP>(16 * t + lc, ch));
+            yf[t] = *reinterpret_cast<const f32x4*>(ys + tile_at<T, KP>(16 * t + lc, ch));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            P[0] = mfma(yf[0][e], xf[0][e], P[0]);
+            P[1] = mfma(yf[0][e], xf[1][e], P[1]);
+            P[2] = mfma(yf[1][e], xf[1][e], P[2]);
           }
         }
-      } else {
-        // each wave adds a share of the channels of P^T
-        f32x16 P = {};
 #pragma unroll
-        for (int k = 0; k < KP / NW / 8; ++k) {
-          const int ch = wave * (KP / NW) + 8 * k + 4 * half;
-          const float4 xf = *reinterpret_cast<const float4*>(xs + tile_at<T, KP>(lc, ch));
-          const float4 yf = *reinterpret_cast<const float4*>(ys + tile_at<T, KP>(lc, ch));
-          P = mfma(yf.x, xf.x, P);
-          P = mfma(yf.y, xf.y, P);
-          P = mfma(yf.z, xf.z, P);
-          P = mfma(yf.w, xf.w, P);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          pairs[(wave * 4 + r) * kWave + ln] = make_float4(P[4 * r], P[4 * r + 1], P[4 * r + 2], P[4 * r + 3]);
-      }
-#pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        O[t] = f32x16{};
-        if constexpr (RATE) OD[t] = f32x16{};
+        for (int i = 0; i < 3; ++i) pairs[(wave * 3 + i) * kWave + ln] = P[i];
       }
       if (active) {
         // out^T = S^T x^T (rows V, columns i)
         if constexpr (BF) {
 #pragma unroll
-          for (int ks = 0; ks < KP / 16; ++ks) {
-            bf16x8 xf[IT];
-#pragma unroll
-            for (int t = 0; t < IT; ++t) xf[t] = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(32 * t + lc, 16 * ks + 8 * half));
+          for (int ks = 0; ks < KP / 32; ++ks) {
             // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
-            float sv[8], dv[8];
+            const Parts2 s2 = split2(S[2 * ks], S[2 * ks + 1]);
+            Parts2 d2;
+            if constexpr (RATE) d2 = split2(D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              sv[e] = S[ks / 2][8 * (ks % 2) + e];
-              if constexpr (RATE) dv[e] = D[ks / 2][8 * (ks % 2) + e];
-            }
-            const Parts2 s2 = split2(sv);
-#pragma unroll
-            for (int t = 0; t < IT; ++t) O[t] = mfma(s2.hi, xf[t], O[t]);
-#pragma unroll
-            for (int t = 0; t < IT; ++t) O[t] = mfma(s2.lo, xf[t], O[t]);
-            if constexpr (RATE) {
-              const Parts2 d2 = split2(dv);
-#pragma unroll
-              for (int t = 0; t < IT; ++t) {
-                OD[t] = mfma(d2.hi, xf[t], OD[t]);
-                OD[t] = mfma(d2.lo, xf[t], OD[t]);
+            for (int t = 0; t < IT; ++t) {
+              const bf16x8 xf = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(16 * t + lc, 32 * ks + 8 * g));
+              O[t] = mfma(s2.hi, xf, ks ? O[t] : f32x4{});
+              O[t] = mfma(s2.lo, xf, O[t]);
+              if constexpr (RATE) {
+                OD[t] = mfma(d2.hi, xf, ks ? OD[t] : f32x4{});
+                OD[t] = mfma(d2.lo, xf, OD[t]);
               }
             }
           }
         } else {
 #pragma unroll
-          for (int t = 0; t < KT; ++t)
+          for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float4 xf = *reinterpret_cast<const float4*>(xs + tile_at<T, KP>(lc, 32 * t + 8 * r + 4 * half));
-              const float xe[4] = {xf.x, xf.y, xf.z, xf.w};
+            for (int t = 0; t < IT; ++t) {
+              const f32x4 xf = *reinterpret_cast<const f32x4*>(xs + tile_at<T, KP>(16 * t + lc, 16 * k + 4 * g));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                O[0] = mfma(S[t][4 * r + e], xe[e], O[0]);
-                if constexpr (RATE) OD[0] = mfma(D[t][4 * r + e], xe[e], OD[0]);
+                O[t] = mfma(S[k][e], xf[e], k + e ? O[t] : f32x4{});
+                if constexpr (RATE) OD[t] = mfma(D[k][e], xf[e], k + e ? OD[t] : f32x4{});
               }
             }
         }
 #pragma unroll
-        for (int t = 0; t < IT; ++t)
+        for (int t = 0; t < IT; ++t) {
+          const float f = up[16 * t + lc];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if constexpr (RATE) OD[t][i] = up[t] * fmaf((float)(32 * t + lc + lead), O[t][i], OD[t][i]);
-            O[t][i] *= up[t];
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (RATE) OD[t][r] = f * fmaf((float)(16 * t + lc + lead), O[t][r], OD[t][r]);
+            O[t][r] *= f;
           }
+        }
       }
       __syncthreads();  // every wave's share of the pairs is there
     }
@@ -602,57 +605,57 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     if (carry) {
       const double exact = (n == C ? wc : exp(-(double)rate * (double)n)) * owed;
       const float w = (float)exact;
-      owed = w != 0.f ? exact / (double)w : 1.0;
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if constexpr (RATE) {
-            D[t][i] = w * fmaf((float)n, S[t][i], D[t][i]);
-          }
-          S[t][i] *= w;
-        }
+      owed = uniform(w != 0.f ? exact / (double)w : 1.0);
+      LAPLEX_EACH(t, KT, r) {
+        if constexpr (RATE) D[t][r] = w * fmaf((float)n, S[t][r], D[t][r]);
+        S[t][r] *= w;
+      }
     }
     if constexpr (BF) {
 #pragma unroll
-      for (int js = 0; js < C / 16; ++js) {
-        const bf16x8 zf = read_tr8<BV, false>(zs, ln, 16 * js, wave * 32);
+      for (int s = 0; s < C / 32; ++s) {
+        const bf16x8 zf = read_tr<BV>(zs, ln, 32 * s, wave * 16 + 4 * (ln & 3));
         if constexpr (FULL) {
 #pragma unroll
-          for (int t = 0; t < IT; ++t) {
-            if (js >= 2 * (t + 1)) continue;  // pairs above the diagonal
-            const bf16x8* pf = pairs + (((js >= 2 * t ? t : 2) * 2 + js % 2) * 2) * kWave + ln;
+          for (int t = 2 * s; t < IT; ++t) {
+            const bf16x8* pf = pairs + ((s * IT + t) * 2) * kWave + ln;
             O[t] = mfma(zf, pf[0], O[t]);
             O[t] = mfma(zf, pf[kWave], O[t]);
             if constexpr (RATE) {
-              OD[t] = mfma(zf, pf[12 * kWave], OD[t]);
-              OD[t] = mfma(zf, pf[13 * kWave], OD[t]);
+              OD[t] = mfma(zf, pf[PAIRS], OD[t]);
+              OD[t] = mfma(zf, pf[PAIRS + kWave], OD[t]);
             }
           }
         }
         if (carry) {
-          // z weighted by its decay to the chunk's end, as three bfloat16 parts: the carry keeps float32's bits
-          auto weighted = [&](const float* w, float (&out)[8]) {
-            const float4 wa = *reinterpret_cast<const float4*>(w + 16 * js + 4 * half),
-                         wb = *reinterpret_cast<const float4*>(w + 16 * js + 8 + 4 * half);
-            const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+          // z weighted by its decay to the chunk's end, as bfloat16 parts: three where the carry goes out as float32
+          // (it keeps float32's bits), two where it only enters bfloat16 results
+          auto weighted = [&](const float* w, f32x4& lo, f32x4& hi) {
+            lo = *reinterpret_cast<const f32x4*>(w + 32 * s + 4 * g);
+            hi = *reinterpret_cast<const f32x4*>(w + 32 * s + 16 + 4 * g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) out[e] = (float)zf[e] * ws[e];
+            for (int e = 0; e < 4; ++e) lo[e] *= (float)zf[e], hi[e] *= (float)zf[4 + e];
           };
-          float zw[8], zl[8];
-          weighted(down, zw);
-          const Parts3 z3 = split3(zw);
+          f32x4 z0, z1;
+          weighted(down, z0, z1);
+          Parts3 z3;
+          if constexpr (FINE) {
+            z3 = split3(z0, z1);
+          } else {
+            const Parts2 z2 = split2(z0, z1);
+            z3.hi = z2.hi, z3.lo = z2.lo;
+          }
           Parts2 l2;
           if constexpr (RATE) {
-            weighted(downlag, zl);
-            l2 = split2(zl);
+            weighted(downlag, z0, z1);
+            l2 = split2(z0, z1);
           }
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            const bf16x8 yt = read_tr8<KP, true>(ys, ln, 16 * js, 32 * t);
+            const bf16x8 yt = read_tr<KP>(ys, ln, 32 * s, 32 * (t >> 1) + 8 * (ln & 3) + 4 * (t & 1));
             S[t] = mfma(yt, z3.hi, S[t]);
             S[t] = mfma(yt, z3.lo, S[t]);
-            S[t] = mfma(yt, z3.lo2, S[t]);
+            if constexpr (FINE) S[t] = mfma(yt, z3.lo2, S[t]);
             if constexpr (RATE) {
               D[t] = mfma(yt, l2.hi, D[t]);
               D[t] = mfma(yt, l2.lo, D[t]);
@@ -661,29 +664,30 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
         }
       }
     } else {
-      f32x16 P = {};
+      f32x4 P[3];
       if constexpr (FULL) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float4 s = pairs[r * kWave + ln];
+        for (int i = 0; i < 3; ++i) {
+          P[i] = pairs[i * kWave + ln];
 #pragma unroll
-          for (int k = 1; k < NW; ++k) {
-            const float4 v = pairs[(k * 4 + r) * kWave + ln];
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+          for (int k = 1; k < WK; ++k) P[i] += pairs[(k * 3 + i) * kWave + ln];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float w = wt[C + (i == 1 ? 16 : 0) + lc - 4 * g - r];
+            P[i][r] = w != 0.f ? P[i][r] * w : 0.f;  // a masked pair is 0 whatever its product
           }
-          const float* w = wt + C + lc - 4 * half - 8 * r;
-          const float pv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) P[4 * r + e] = w[-e] != 0.f ? pv[e] * w[-e] : 0.f;  // a masked pair is 0 whatever its product
         }
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = 8 * (i / 4) + 4 * half + i % 4;
-        const float zf = zs[tile_at<T, BV>(j, wave * 32 + lc)];
+      LAPLEX_EACH(s, C / 16, r) {
+        const int j = 16 * s + 4 * g + r;
+        const float zf = zs[tile_at<T, BV>(j, wave * 16 + lc)];
         if constexpr (FULL) {
-          O[0] = mfma(zf, P[i], O[0]);
-          if constexpr (RATE) OD[0] = mfma(zf, P[i] * (float)(lc - j), OD[0]);
+#pragma unroll
+          for (int t = s; t < IT; ++t) {
+            const float pr = P[s + t][r];
+            O[t] = mfma(zf, pr, O[t]);
+            if constexpr (RATE) OD[t] = mfma(zf, pr * (float)(16 * t + lc - j), OD[t]);
+          }
         }
         if (carry) {
           const float zw = zf * down[j];
@@ -691,7 +695,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
           if constexpr (RATE) zl = zf * downlag[j];
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            const float yt = ys[tile_at<T, KP>(j, 32 * t + lc)];
+            const float yt = ys[tile_at<T, KP>(j, 16 * t + lc)];
             S[t] = mfma(yt, zw, S[t]);
             if constexpr (RATE) D[t] = mfma(yt, zl, D[t]);
           }
@@ -702,64 +706,53 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
     if constexpr (FULL) {
       if (bad) {
         const float nan = __builtin_nanf("");
-        const int* first = bad_row[parity] + wave * 32;
+        const int* first = bad_row[parity] + wave * 16;
         const bool gone = first[lc] < C;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-#pragma unroll
-          for (int t = 0; t < IT; ++t) {
-            const bool hit = 32 * t + lc >= first[8 * (i / 4) + 4 * half + i % 4];
-            O[t][i] = hit ? nan : O[t][i];
-            if constexpr (RATE) OD[t][i] = hit ? nan : OD[t][i];
-          }
-#pragma unroll
-          for (int t = 0; t < KT; ++t) {
-            S[t][i] = gone ? nan : S[t][i];
-            if constexpr (RATE) D[t][i] = gone ? nan : D[t][i];
-          }
+        LAPLEX_EACH(t, IT, r) {
+          const bool hit = 16 * t + lc >= first[4 * g + r];
+          O[t][r] = hit ? nan : O[t][r];
+          if constexpr (RATE) OD[t][r] = hit ? nan : OD[t][r];
+        }
+        LAPLEX_EACH(t, KT, r) {
+          S[t][r] = gone ? nan : S[t][r];
+          if constexpr (RATE) D[t][r] = gone ? nan : D[t][r];
         }
       }
       if constexpr (DOT) {
-#pragma unroll
-        for (int t = 0; t < IT; ++t)
-#pragma unroll
-          for (int k = 0; k < 16; ++k)  // rows past the end are zero in the tile
-            dr += (double)(OD[t][k] * to_f32(dots[tile_at<T, BV>(32 * t + lc, wave * 32 + 8 * (k / 4) + 4 * half + k % 4)]));
+        LAPLEX_EACH(t, IT, r)  // rows past the end are zero in the tile
+          dr += (double)(OD[t][r] * to_f32(dots[tile_at<T, BV>(16 * t + lc, wave * 16 + 4 * g + r)]));
       }
     }
   }
   if (FULL && sg.n > 0) put(sg.u0 + (sg.n - 1) / C * C);
 
   // the carry after the segment
-  int colf = col, halff = half;
-  asm volatile("" : "+v"(colf), "+v"(halff));  // the row and column tests are made again, not kept over the loop
+  int colf = col, gf = g;
+  asm volatile("" : "+v"(colf), "+v"(gf));  // the row and column tests are made again, not kept over the loop
   auto each = [&](int rs, int cs, auto&& f) {
     if (colf >= V) return;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = 32 * t + carry_row<T>(i / 4, i % 4, halff);
-        if (row < K) f(t, i, row * rs + colf * cs);
-      }
+    LAPLEX_EACH(t, KT, r) {
+      const int row = carry_row<T>(t, gf, r);
+      if (row < K) f(t, r, row * rs + colf * cs);
+    }
   };
   if constexpr (!FULL) {
     const uint64_t at = bound_at(sg.u0 + sg.n);
     float* to = a.bound + at;
-    each(V, 1, [&](int t, int i, int o) { to[o] = S[t][i]; });
+    each(V, 1, [&](int t, int r, int o) { to[o] = S[t][r]; });
     if constexpr (RATE) {
       float* tod = a.bound_d + at;
-      each(V, 1, [&](int t, int i, int o) { tod[o] = D[t][i]; });
+      each(V, 1, [&](int t, int r, int o) { tod[o] = D[t][r]; });
     }
   } else if (last_seg) {
     if (p.s_out) {
       float* to = p.s_out + sbase;
-      each(rs, cs, [&](int t, int i, int o) { to[o] = S[t][i]; });
+      each(rs, cs, [&](int t, int r, int o) { to[o] = S[t][r]; });
     }
     if constexpr (RATE)
       if (p.ds_out) {
-        const float* g = p.ds_out + sbase;
-        each(rs, cs, [&](int t, int i, int o) { dr += (double)(D[t][i] * g[o]); });
+        const float* gd = p.ds_out + sbase;
+        each(rs, cs, [&](int t, int r, int o) { dr += (double)(D[t][r] * gd[o]); });
       }
   }
   if constexpr (DOT) {
@@ -774,25 +767,28 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 1 : 2) void k_attn_
   }
 }
 
-// kp: K rounded up to 64, 128 or 256; nw: waves per block, 32 columns each (4, or 2 where K and V are at most 64)
+// kp: K rounded up to 64, 128 or 256; nw: waves per block, 16 columns each (8, or 4 where K and V are at most 64)
 template <typename T, int KP, int NW, bool VEC>
 void attn_chunk_launch_at(const AttnChunkArgs& a, bool full, bool rate, hipStream_t s) {
   const uint64_t units = a.slots * (a.p.heads / a.group);
   const dim3 grid((unsigned)(xcd_blocks(units) * a.group * a.slices)), block(NW * kWave);
+  constexpr bool BF = sizeof(T) == 2;  // (float keeps its bits either way)
   if (full) {
-    if (rate) k_attn_chunk<T, KP, NW, true, true, VEC><<<grid, block, 0, s>>>(a);
-    else k_attn_chunk<T, KP, NW, true, false, VEC><<<grid, block, 0, s>>>(a);
+    if (rate) k_attn_chunk<T, KP, NW, true, true, false, VEC><<<grid, block, 0, s>>>(a);
+    else if (a.fine && BF) k_attn_chunk<T, KP, NW, true, false, BF, VEC><<<grid, block, 0, s>>>(a);
+    else k_attn_chunk<T, KP, NW, true, false, false, VEC><<<grid, block, 0, s>>>(a);
   } else {
-    if (rate) k_attn_chunk<T, KP, NW, false, true, VEC><<<grid, block, 0, s>>>(a);
-    else k_attn_chunk<T, KP, NW, false, false, VEC><<<grid, block, 0, s>>>(a);
+    if (rate) k_attn_chunk<T, KP, NW, false, true, false, VEC><<<grid, block, 0, s>>>(a);
+    else if (a.fine && BF) k_attn_chunk<T, KP, NW, false, false, BF, VEC><<<grid, block, 0, s>>>(a);
+    else k_attn_chunk<T, KP, NW, false, false, false, VEC><<<grid, block, 0, s>>>(a);
   }
 }
 template <typename T, bool VEC>
 void attn_chunk_launch(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s) {
-  if (kp == 64 && nw == 2) attn_chunk_launch_at<T, 64, 2, VEC>(a, full, rate, s);
-  else if (kp == 64) attn_chunk_launch_at<T, 64, 4, VEC>(a, full, rate, s);
-  else if (kp == 128) attn_chunk_launch_at<T, 128, 4, VEC>(a, full, rate, s);
-  else attn_chunk_launch_at<T, 256, 4, VEC>(a, full, rate, s);
+  if (kp == 64 && nw == 4) attn_chunk_launch_at<T, 64, 4, VEC>(a, full, rate, s);
+  else if (kp == 64) attn_chunk_launch_at<T, 64, 8, VEC>(a, full, rate, s);
+  else if (kp == 128) attn_chunk_launch_at<T, 128, 8, VEC>(a, full, rate, s);
+  else attn_chunk_launch_at<T, 256, 8, VEC>(a, full, rate, s);
 }
 
 // The instantiations, each in a source file of its own.  vec: every row of x, y, z, dot and out is 16-byte aligned.

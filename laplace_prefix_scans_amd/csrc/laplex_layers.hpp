@@ -38,6 +38,7 @@ struct AttnPass {
   const float* s_in;   // seqs x heads x K x V, or null
   float* s_out;        // the same, or null
   bool s_trans;        // s_in, s_out are V x K per head
+  bool bound_ready;    // the workspace holds the segments' states of the pass before, which had K and V (and y and z) exchanged
   // rate gradient (dq pass only): -c_pair sum_u <dot_u, sum_u' (u - u') w x.y z> and the final state's part
   const void* dot;     // rows (V) the lag-weighted outputs are multiplied with, strides as dot_view
   AttnView dot_view;

@@ -218,7 +218,7 @@ extern "C" laplex_status laplex_decay_attn_backward(const laplex_attn_shape* sha
     p.z = i == 0 ? vg : vq;
     p.K = i == 0 ? a.dk : a.dv;
     p.V = i == 0 ? a.dv : a.dk;
-    p.s_trans = i == 1;
+    p.s_trans = p.bound_ready = i == 1;
     p.c_pair = p.c_add = a.scale;
     p.c_in = 1.f;
     p.s_in = dstate_out;
