@@ -53,6 +53,16 @@ def _lib():
     return _ready
 
 
+# These calls are often a few microseconds of GPU work each (one token, one
+# row), so the checks read every attribute of a tensor once and the stream
+# comes as the raw handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev: torch.device) -> int:
+    return _raw_stream(dev.index) if _raw_stream is not None else _stream(dev)
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
@@ -74,7 +84,7 @@ def _like(t, name: str, shape, dtype, dev) -> Optional[torch.Tensor]:
         raise ValueError("%s must be on %s" % (name, dev))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -85,49 +95,51 @@ def _out(t, name: str, shape, dtype, dev) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else _like(t, name, shape, dtype, dev)
 
 
-def _bytes(ws: Optional[torch.Tensor], need: int, dev) -> torch.Tensor:
+def _bytes(ws: Optional[torch.Tensor], need: int, dev) -> Tuple[Optional[torch.Tensor], int]:
+    """The workspace and its size; none where none is needed."""
     if ws is None:
-        return torch.empty(max(256, need), dtype=torch.uint8, device=dev)
+        return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
     if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
-    return ws
+    return ws, ws.numel()
 
 
 # ------------------------------------------------------------------ decayed attention
-def _strides(t: torch.Tensor, name: str, batched: bool) -> Tuple[int, int]:
+def _strides(t: torch.Tensor, shape, name: str, batched: bool) -> Tuple[int, int]:
     st = t.stride()
-    if t.shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s must have contiguous channels" % name)
-    if batched and t.shape[0] > 1 and t.shape[1] > 0 and st[0] != t.shape[1] * st[1]:
+    if not batched:
+        return st[0], st[1]
+    if shape[0] > 1 and shape[1] > 0 and st[0] != shape[1] * st[1]:
         raise ValueError("%s: the tokens of a batch must lie one sequence after the other" % name)
-    token, head = st[-3], st[-2]
-    if batched and t.shape[1] == 1:
-        token = st[0]
-    return token, head
+    return (st[0] if shape[1] == 1 else st[1]), st[2]
 
 
 def _shape(q, k, v, rate, offsets, scale) -> _Shape:
     code = _dtype(q, "q")
-    dev = q.device
-    for t, name in ((k, "k"), (v, "v")):
-        if _dtype(t, name) != code or t.device != dev:
-            raise TypeError("%s must have the type and device of q" % name)
-        if t.dim() != q.dim():
-            raise ValueError("q, k and v must all be (tokens, heads, channels) or (batch, tokens, heads, channels)")
-    if q.dim() not in (3, 4):
+    dev, dtype, qs = q.device, q.dtype, q.shape
+    dims = len(qs)
+    if dims != 3 and dims != 4:
         raise ValueError("q must be (tokens, heads, channels) or (batch, tokens, heads, channels)")
-    batched = q.dim() == 4
-    lead = q.shape[:-2]
-    if k.shape[:-2] != lead or v.shape[:-2] != lead or k.shape[-2] != v.shape[-2] or k.shape[-1] != q.shape[-1]:
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch tensor" % name)
+        if t.dtype != dtype or t.device != dev:
+            raise TypeError("%s must have the type and device of q" % name)
+    ks, vs = k.shape, v.shape
+    batched = dims == 4
+    lead = qs[:-2]
+    if len(ks) != dims or len(vs) != dims or ks[:-2] != lead or vs[:-1] != ks[:-1] or ks[-1] != qs[-1]:
         raise ValueError("k must have the tokens and channels of q, v the tokens and heads of k: got q %s, k %s, v %s"
-                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
-    heads, kv_heads = q.shape[-2], k.shape[-2]
+                         % (tuple(qs), tuple(ks), tuple(vs)))
+    heads, kv_heads = qs[-2], ks[-2]
     if kv_heads == 0 or heads % kv_heads:
         raise ValueError("the %d heads of k and v must divide the %d of q" % (kv_heads, heads))
-    _like(rate, "rate", (heads,), torch.float32, dev)
     if rate is None:
         raise TypeError("rate must be a torch tensor")
-    seqs = q.shape[0] if batched else 1
+    _like(rate, "rate", (heads,), torch.float32, dev)
+    seqs = qs[0] if batched else 1
     if offsets is not None:
         if batched:
             raise ValueError("offsets go with packed (tokens, heads, channels) tensors")
@@ -135,9 +147,10 @@ def _shape(q, k, v, rate, offsets, scale) -> _Shape:
             raise ValueError("offsets must be a 1-D tensor of sequence starts and the end of the last")
         _like(offsets, "offsets", offsets.shape, torch.int32, dev)
         seqs = offsets.numel() - 1
-    tokens = q.shape[0] * q.shape[1] if batched else q.shape[0]
-    (qt, qh), (kt, kh), (vt, vh) = _strides(q, "q", batched), _strides(k, "k", batched), _strides(v, "v", batched)
-    return _Shape(code, seqs, heads, kv_heads, q.shape[-1], v.shape[-1], tokens, _ptr(offsets), rate.data_ptr(), scale,
+    tokens = qs[0] * qs[1] if batched else qs[0]
+    (qt, qh), (kt, kh), (vt, vh) = (_strides(q, qs, "q", batched), _strides(k, ks, "k", batched),
+                                    _strides(v, vs, "v", batched))
+    return _Shape(code, seqs, heads, kv_heads, qs[-1], vs[-1], tokens, _ptr(offsets), rate.data_ptr(), scale,
                   qt, qh, kt, kh, vt, vh)
 
 
@@ -167,9 +180,9 @@ def laplex_decay_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rate: t
     _like(state_out, "state_out", st, torch.float32, dev)
     o = _out(o, "o", (*q.shape[:-1], s.dv), q.dtype, dev)
     L = _lib()
-    ws = _bytes(ws, L.laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_FORWARD, ctypes.byref(s)), dev)
+    ws, ws_bytes = _bytes(ws, L.laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_FORWARD, ctypes.byref(s)), dev)
     _check(L.laplex_decay_attn(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(state_in), _ptr(state_out), _ptr(o), _ptr(ws),
-                               ws.numel(), _stream(dev)), "laplex_decay_attn")
+                               ws_bytes, _stream_of(dev)), "laplex_decay_attn")
     return o
 
 
@@ -193,10 +206,10 @@ def laplex_decay_attn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     drate = torch.empty(s.heads, dtype=torch.float32, device=dev) if rate_grad else None
     dstate_in = torch.empty(st, dtype=torch.float32, device=dev) if state_in is not None else None
     L = _lib()
-    ws = _bytes(ws, L.laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_BACKWARD, ctypes.byref(s)), dev)
+    ws, ws_bytes = _bytes(ws, L.laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_BACKWARD, ctypes.byref(s)), dev)
     _check(L.laplex_decay_attn_backward(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(go), _ptr(state_in), _ptr(dstate_out),
-                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(drate), _ptr(dstate_in), _ptr(ws), ws.numel(),
-                                        _stream(dev)), "laplex_decay_attn_backward")
+                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(drate), _ptr(dstate_in), _ptr(ws), ws_bytes,
+                                        _stream_of(dev)), "laplex_decay_attn_backward")
     return dq, dk, dv, drate, dstate_in
 
 
@@ -221,7 +234,7 @@ def laplex_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ra
         raise ValueError("state must have a row for each of the %d tokens" % s.seqs)
     o = _out(o, "o", (s.seqs, s.heads, s.dv), q.dtype, dev)
     _check(_lib().laplex_decay_attn_step(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(slots), state.shape[0], _ptr(state),
-                                         _ptr(o), _stream(dev)), "laplex_decay_attn_step")
+                                         _ptr(o), _stream_of(dev)), "laplex_decay_attn_step")
     return o
 
 
@@ -245,10 +258,9 @@ def laplex_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bi
     _like(weight, "weight", (width,), x.dtype, dev)
     _like(bias, "bias", (width,), x.dtype, dev)
     y = _out(y, "y", x.shape, x.dtype, dev)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
     _check(_lib().laplex_layer_norm(code, rows, width, _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean), _ptr(rstd),
-                                    _stream(dev)), "laplex_layer_norm")
+                                    _stream_of(dev)), "laplex_layer_norm")
     return y, mean, rstd
 
 
@@ -269,9 +281,9 @@ def laplex_layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Te
     dw = torch.empty(width, dtype=torch.float32, device=dev) if param_grads else None
     db = torch.empty(width, dtype=torch.float32, device=dev) if param_grads else None
     L = _lib()
-    ws = _bytes(ws, L.laplex_layer_norm_workspace_bytes(rows, width), dev)
+    ws, ws_bytes = _bytes(ws, L.laplex_layer_norm_workspace_bytes(rows, width), dev)
     _check(L.laplex_layer_norm_backward(code, rows, width, _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
-                                        _ptr(dw), _ptr(db), _ptr(ws), ws.numel(), _stream(dev)), "laplex_layer_norm_backward")
+                                        _ptr(dw), _ptr(db), _ptr(ws), ws_bytes, _stream_of(dev)), "laplex_layer_norm_backward")
     return dx, dw, db
 
 
@@ -294,7 +306,7 @@ def laplex_embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
         raise ValueError("table must be a contiguous (vocab, width) tensor")
     y = _out(y, "y", (*ids.shape, table.shape[1]), table.dtype, dev)
     _check(_lib().laplex_embedding(code, _ptr(ids), nb, ids.numel(), _ptr(table), table.shape[0], table.shape[1], scale, _ptr(y),
-                                   _stream(dev)), "laplex_embedding")
+                                   _stream_of(dev)), "laplex_embedding")
     return y
 
 
@@ -316,7 +328,7 @@ def laplex_embedding_backward(ids: torch.Tensor, dy: torch.Tensor, vocab: int, s
         raise TypeError("the table's gradient is float32 or of the type of dy")
     dtable = _out(dtable, "dtable", (vocab, width), dtype, dev)
     L = _lib()
-    ws = _bytes(ws, L.laplex_embedding_workspace_bytes(ids.numel(), vocab, width), dev)
+    ws, ws_bytes = _bytes(ws, L.laplex_embedding_workspace_bytes(ids.numel(), vocab, width), dev)
     _check(L.laplex_embedding_backward(code, _ptr(ids), nb, ids.numel(), _ptr(dy), vocab, width, scale, _DTYPES[dtype],
-                                       _ptr(dtable), _ptr(ws), ws.numel(), _stream(dev)), "laplex_embedding_backward")
+                                       _ptr(dtable), _ptr(ws), ws_bytes, _stream_of(dev)), "laplex_embedding_backward")
     return dtable

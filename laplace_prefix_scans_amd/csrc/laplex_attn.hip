@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
   for (uint32_t s = blockIdx.z; s < p.seqs; s += gridDim.z) {
     const int64_t i = (int64_t)s + (a.g.offsets ? 1 : 0), first = seq_bound(a.g, i), len = seq_bound(a.g, i + 1) - first;
     if (len <= L) continue;  // no boundary inside the sequence
-    const int nb = (int)((len + L - 1) / L) - 1;
+    const int nb = (int)((len - 1) / L);
     float cur = 0.f, d = 0.f;
     if (p.s_in) cur = p.s_in[((uint64_t)s * p.heads + h) * per + (p.s_trans ? at % p.V * p.K + at / p.V : at)];
     uint64_t q = ((uint64_t)(first / L + 1) * p.heads + h) * per + at;
@@ -124,8 +124,10 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   hipError_t err;
   if (q.split && !p.bound_ready) {
     if ((err = run("k_attn_chunk_state", false)) != hipSuccess) return err;
-    const dim3 grid((unsigned)(((uint64_t)p.K * p.V + 255) / 256), p.heads, std::min(p.seqs, 64u));
-    LAPLEX_LAUNCH("k_attn_join", q.bounds, s, rate ? k_attn_join<true><<<grid, 256, 0, s>>>(a) : k_attn_join<false><<<grid, 256, 0, s>>>(a));
+    const uint64_t longest = p.offsets ? p.tokens : p.tokens / p.seqs;  // at most
+    const dim3 grid((unsigned)(((uint64_t)p.K * p.V + 255) / 256), p.heads, std::min(p.seqs, 8u));
+    if ((int64_t)longest > q.seg_len)
+      LAPLEX_LAUNCH("k_attn_join", q.bounds, s, rate ? k_attn_join<true><<<grid, 256, 0, s>>>(a) : k_attn_join<false><<<grid, 256, 0, s>>>(a));
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   return run("k_attn_chunk", true);

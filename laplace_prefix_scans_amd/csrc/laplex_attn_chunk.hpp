@@ -600,14 +600,14 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
     }
     if (!active) continue;
 
-    // the carry over the chunk, with the lag-weighted one ahead of it
+    // out^T += z^T P, and the carry over the chunk
     const bool carry = !FULL || more || keep;
     if (carry) {
       const double exact = (n == C ? wc : exp(-(double)rate * (double)n)) * owed;
       const float w = (float)exact;
       owed = uniform(w != 0.f ? exact / (double)w : 1.0);
       LAPLEX_EACH(t, KT, r) {
-        if constexpr (RATE) D[t][r] = w * fmaf((float)n, S[t][r], D[t][r]);
+        if constexpr (RATE) D[t][r] = w * fmaf((float)n, S[t][r], D[t][r]);  // the lag-weighted carry ahead of the other
         S[t][r] *= w;
       }
     }
@@ -664,8 +664,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
         }
       }
     } else {
-      f32x4 P[3];
+      f32x4 zf[C / 16];
+      LAPLEX_EACH(s, C / 16, r) zf[s][r] = zs[tile_at<T, BV>(16 * s + 4 * g + r, wave * 16 + lc)];
       if constexpr (FULL) {
+        f32x4 P[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           P[i] = pairs[i * kWave + ln];
@@ -677,27 +679,27 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
             P[i][r] = w != 0.f ? P[i][r] * w : 0.f;  // a masked pair is 0 whatever its product
           }
         }
-      }
-      LAPLEX_EACH(s, C / 16, r) {
-        const int j = 16 * s + 4 * g + r;
-        const float zf = zs[tile_at<T, BV>(j, wave * 16 + lc)];
-        if constexpr (FULL) {
+        LAPLEX_EACH(s, C / 16, r) {
 #pragma unroll
           for (int t = s; t < IT; ++t) {
-            const float pr = P[s + t][r];
-            O[t] = mfma(zf, pr, O[t]);
-            if constexpr (RATE) OD[t] = mfma(zf, pr * (float)(16 * t + lc - j), OD[t]);
+            O[t] = mfma(zf[s][r], P[s + t][r], O[t]);
+            if constexpr (RATE) OD[t] = mfma(zf[s][r], P[s + t][r] * (float)(16 * (t - s) + lc - 4 * g - r), OD[t]);
           }
         }
-        if (carry) {
-          const float zw = zf * down[j];
-          float zl = 0.f;
-          if constexpr (RATE) zl = zf * downlag[j];
+      }
+      if (carry) {  // all of it in one piece, so that reads run ahead of the products
+        f32x4 zw[C / 16], zl[C / 16];
+#pragma unroll
+        for (int s = 0; s < C / 16; ++s) {
+          if constexpr (RATE) zl[s] = zf[s] * *reinterpret_cast<const f32x4*>(downlag + 16 * s + 4 * g);
+          zw[s] = zf[s] * *reinterpret_cast<const f32x4*>(down + 16 * s + 4 * g);
+        }
+        LAPLEX_EACH(s, C / 16, r) {
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            const float yt = ys[tile_at<T, KP>(j, 16 * t + lc)];
-            S[t] = mfma(yt, zw, S[t]);
-            if constexpr (RATE) D[t] = mfma(yt, zl, D[t]);
+            const float yt = ys[tile_at<T, KP>(16 * s + 4 * g + r, 16 * t + lc)];
+            S[t] = mfma(yt, zw[s][r], S[t]);
+            if constexpr (RATE) D[t] = mfma(yt, zl[s][r], D[t]);
           }
         }
       }
