@@ -72,31 +72,171 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed(const void* __restrict__ 
   }
 }
 
-// Ids as sort keys; those outside the table sort behind every row.
-__global__ void k_embed_keys(const void* __restrict__ ids, int id_bytes, uint64_t tokens, uint32_t vocab, uint32_t* __restrict__ keys) {
-  const uint64_t t = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (t >= tokens) return;
-  const int64_t id = load_id(ids, id_bytes, t);
-  keys[t] = (id >= 0 && id < (int64_t)vocab) ? (uint32_t)id : vocab;
+// Sort keys.  Any order that brings equal ids together will do, and frequent
+// ids are often neighbours (a vocabulary in order of frequency), so an id's 6
+// lowest bits become its key's highest: key ranges of equal size then hold
+// about as many tokens.  Keys have `bits` bits; ids outside the table get the
+// key 2^bits, behind every row.
+constexpr int kTopBits = 6, kTops = 1 << kTopBits;
+__host__ __device__ __forceinline__ int key_bits(uint32_t vocab) {
+  int b = kTopBits;
+  while ((1u << b) < vocab) ++b;
+  return b;
+}
+__device__ __forceinline__ uint32_t key_of(int64_t id, uint32_t vocab, int bits) {
+  if (id < 0 || id >= (int64_t)vocab) return 1u << bits;
+  return ((uint32_t)id & (kTops - 1)) << (bits - kTopBits) | (uint32_t)id >> kTopBits;
+}
+__device__ __forceinline__ uint32_t row_of(uint32_t key, int bits) {
+  return (key & ((1u << (bits - kTopBits)) - 1)) << kTopBits | key >> (bits - kTopBits);
 }
 
-// starts[v] = first sorted position whose key is >= v, for v = 0 .. vocab.
-__global__ void k_embed_starts(const uint32_t* __restrict__ keys, uint64_t tokens, uint32_t vocab, uint32_t* __restrict__ starts) {
-  const uint64_t v = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (v > vocab) return;
+__global__ void k_embed_keys(const void* __restrict__ ids, int id_bytes, uint64_t tokens, uint32_t vocab, int bits,
+                             uint32_t* __restrict__ keys) {
+  const uint64_t t = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (t < tokens) keys[t] = key_of(load_id(ids, id_bytes, t), vocab, bits);
+}
+
+// Stable sort of up to kEmbedSmall tokens by key in one launch: block b reads
+// all of them, takes those of the key range b (range kTops: outside the table)
+// in order, counts those of the ranges before it -- where its part of the
+// result starts -- and sorts its own in LDS by the remaining bits (stable LSD
+// passes of 6).  No block waits for another.  16384 tokens: 9 us; sorted by one
+// block 31 us, by the general sort's eight launches about as long.
+constexpr int kEmbedSmall = 16384, kSortThreads = 1024, kSortWaves = kSortThreads / kWave, kSortBits = 6, kSortBins = 1 << kSortBits;
+
+// lanes whose digit is this lane's
+__device__ __forceinline__ uint64_t peers6(uint32_t d) {
+  uint64_t peers = ~0ull;
+#pragma unroll
+  for (int b = 0; b < kSortBits; ++b) {
+    const uint64_t m = __ballot((d >> b) & 1);
+    peers &= (d >> b) & 1 ? m : ~m;
+  }
+  return peers;
+}
+
+// LDS written by one lane and read by another of the same wave
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int E>
+__global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restrict__ ids, int id_bytes, uint32_t tokens, uint32_t vocab,
+                                                             int bits, uint32_t* __restrict__ keys, uint32_t* __restrict__ perm) {
+  __shared__ uint32_t sk[E * kSortThreads];
+  __shared__ uint16_t sp[E * kSortThreads];
+  __shared__ uint32_t count[kSortWaves][kSortBins];
+  __shared__ uint32_t base[kSortBins], mine[kSortWaves], below[kSortWaves];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int low = bits - kTopBits;
+  uint32_t k[E], v[E];
+  uint32_t in = 0, under = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {  // wave w reads [w * 64 E, (w + 1) * 64 E)
+    const uint32_t at = (wave * E + e) * kWave + lane;
+    k[e] = at < tokens ? key_of(load_id(ids, id_bytes, at), vocab, bits) : 0xFFFFFFFFu;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint32_t at = (wave * E + e) * kWave + lane;
+    in += (uint32_t)__popcll(__ballot(at < tokens && k[e] >> low == blockIdx.x));
+    under += (uint32_t)__popcll(__ballot(at < tokens && k[e] >> low < blockIdx.x));
+  }
+  if (lane == 0) {
+    mine[wave] = in;
+    below[wave] = under;
+  }
+  __syncthreads();
+  uint32_t start = 0, m = 0, to = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    to += w < wave ? mine[w] : 0;
+    m += mine[w];
+    start += below[w];
+  }
+  if (m == 0) return;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint32_t at = (wave * E + e) * kWave + lane;
+    const bool own = at < tokens && k[e] >> low == blockIdx.x;
+    const uint64_t b = __ballot(own);
+    if (own) {
+      sk[to + lanes_below(b)] = k[e];
+      sp[to + lanes_below(b)] = (uint16_t)at;
+    }
+    to += (uint32_t)__popcll(b);
+  }
+  const int per = (int)((m + kSortThreads - 1) / kSortThreads);  // of the m taken, wave w holds [w * 64 per, (w + 1) * 64 per)
+  const bool one_key = blockIdx.x == kTops;
+  for (int shift = 0; shift < low && !one_key; shift += kSortBits) {
+    __syncthreads();
+    count[wave][lane] = 0;  // a wave's own row
+    wave_sync();
+    uint32_t rank[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (e >= per) break;
+      const uint32_t at = (wave * per + e) * kWave + lane;
+      k[e] = at < m ? sk[at] : 0xFFFFFFFFu;  // past the end: behind every key of the range
+      v[e] = at < m ? sp[at] : 0;
+      const uint32_t d = at < m ? (k[e] >> shift) & (kSortBins - 1) : kSortBins - 1;
+      const uint64_t peers = peers6(d);
+      const uint32_t before = count[wave][d];
+      rank[e] = before + lanes_below(peers);
+      wave_sync();
+      if (lanes_below(peers) == 0) count[wave][d] = before + (uint32_t)__popcll(peers);
+      wave_sync();
+    }
+    __syncthreads();
+    if (threadIdx.x < kSortBins) {  // one wave: totals over the waves, then their exclusive scan over the digits
+      uint32_t sum = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = count[w][lane];
+        count[w][lane] = sum;
+        sum += c;
+      }
+      base[lane] = wave_incl_sum_u32(sum) - sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (e >= per) break;
+      const uint32_t at = (wave * per + e) * kWave + lane;
+      if (at >= m) continue;
+      const uint32_t d = (k[e] >> shift) & (kSortBins - 1), dst = base[d] + count[wave][d] + rank[e];
+      sk[dst] = k[e];
+      sp[dst] = (uint16_t)v[e];
+    }
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < m; i += kSortThreads) {
+    keys[start + i] = sk[i];
+    perm[start + i] = sp[i];
+  }
+}
+
+// starts[u] = first sorted position whose key is >= u, for u = 0 .. 2^bits.
+__global__ void k_embed_starts(const uint32_t* __restrict__ keys, uint64_t tokens, int bits, uint32_t* __restrict__ starts) {
+  const uint64_t u = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (u > (1ull << bits)) return;
   uint64_t lo = 0, hi = tokens;
   while (lo < hi) {
     const uint64_t mid = (lo + hi) / 2;
-    if (keys[mid] < v) lo = mid + 1;
+    if (keys[mid] < u) lo = mid + 1;
     else hi = mid;
   }
-  starts[v] = (uint32_t)lo;
+  starts[u] = (uint32_t)lo;
 }
 
 struct EmbedGrad {
   const uint32_t *keys, *perm, *starts;
   uint64_t tokens;
   uint32_t vocab, width, chunk, lanes;
+  int bits;  // of a key
   uint64_t chunk_blocks;  // blocks of the chunks; the rest zero rows
   float scale;
   float* part;  // [chunk][0: the stretch begun earlier, 1: the one that goes on][width]
@@ -112,8 +252,10 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGrad g, const T
     float zero[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) zero[j] = 0.f;
-    for (uint64_t v = v0; v < v0 + kEmbedZeroRows && v < g.vocab; ++v)
-      if (g.starts[v] == g.starts[v + 1]) store_row<O, E>(dtable + v * g.width + c, zero, 0.f);
+    for (uint64_t v = v0; v < v0 + kEmbedZeroRows && v < g.vocab; ++v) {
+      const uint32_t u = key_of((int64_t)v, g.vocab, g.bits);
+      if (g.starts[u] == g.starts[u + 1]) store_row<O, E>(dtable + v * g.width + c, zero, 0.f);
+    }
     return;
   }
   const uint64_t ch = (uint64_t)blockIdx.x * groups + group, p0 = ch * g.chunk;
@@ -125,9 +267,9 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGrad g, const T
 #pragma unroll
   for (int j = 0; j < E; ++j) acc[j] = 0.f;
   auto flush = [&](bool goes_on) {
-    if (cur >= g.vocab) return;
+    if (cur >> g.bits) return;  // outside the table
     if (head || goes_on) store_row<float, E>(g.part + (ch * 2 + (head ? 0 : 1)) * g.width + c, acc, 1.f);
-    else store_row<O, E>(dtable + (uint64_t)cur * g.width + c, acc, g.scale);
+    else store_row<O, E>(dtable + (uint64_t)row_of(cur, g.bits) * g.width + c, acc, g.scale);
   };
   constexpr int B = 8;  // rows in flight
   for (uint64_t q = p0; q < p1; q += B) {
@@ -162,9 +304,9 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_join(EmbedGrad g, O* __re
   __shared__ float sh[4][64];
   const uint64_t ch = blockIdx.x, p0 = ch * g.chunk, p1 = p0 + g.chunk;
   if (p1 >= g.tokens) return;
-  const uint32_t v = g.keys[p1 - 1];
-  if (v >= g.vocab || g.keys[p1] != v || g.starts[v] < p0) return;
-  const uint64_t last = ((uint64_t)g.starts[v + 1] - 1) / g.chunk;
+  const uint32_t u = g.keys[p1 - 1];
+  if (u >> g.bits || g.keys[p1] != u || g.starts[u] < p0) return;
+  const uint64_t last = ((uint64_t)g.starts[u + 1] - 1) / g.chunk, v = row_of(u, g.bits);
   const uint32_t r = threadIdx.x / 64;
   for (uint32_t c = blockIdx.y * 64 + threadIdx.x % 64; c - threadIdx.x % 64 < g.width; c += gridDim.y * 64) {
     float a = 0.f;
@@ -176,7 +318,7 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_join(EmbedGrad g, O* __re
     sh[r][threadIdx.x % 64] = a;
     __syncthreads();
     if (r == 0 && c < g.width)
-      dtable[(uint64_t)v * g.width + c] = from_f32<O>(g.scale * (sh[0][threadIdx.x] + sh[1][threadIdx.x] + sh[2][threadIdx.x] + sh[3][threadIdx.x]));
+      dtable[v * g.width + c] = from_f32<O>(g.scale * (sh[0][threadIdx.x] + sh[1][threadIdx.x] + sh[2][threadIdx.x] + sh[3][threadIdx.x]));
     __syncthreads();
   }
 }
@@ -219,6 +361,7 @@ hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, 
 }
 
 uint32_t embed_chunk(uint64_t tokens) { return tokens <= 32768 ? 32 : 64; }
+uint64_t embed_starts(uint32_t vocab) { return (1ull << key_bits(vocab)) + 1; }
 uint64_t embed_part_floats(uint64_t tokens, uint32_t width) {
   const uint32_t c = embed_chunk(tokens);
   return (tokens + c - 1) / c * 2 * width;
@@ -243,17 +386,26 @@ static void embed_grad_launch(EmbedGrad g, const void* dy, void* dtable, hipStre
 hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s) {
   hipError_t e;
-  if (tokens) {
-    LAPLEX_LAUNCH("k_embed_keys", tokens, s,
-                  k_embed_keys<<<(unsigned)((tokens + 255) / 256), 256, 0, s>>>(ids, id_bytes, tokens, vocab, w.keys));
+  const int bits = key_bits(vocab);
+  if (tokens && tokens <= (uint64_t)kEmbedSmall) {
+    LAPLEX_LAUNCH("k_embed_sort", tokens, s, {
+      const uint32_t n = (uint32_t)tokens;
+      if (n <= kSortThreads) k_embed_sort<1><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm);
+      else if (n <= 4 * kSortThreads) k_embed_sort<4><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm);
+      else k_embed_sort<16><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm);
+    });
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = sort_indices(w.sort, w.keys, tokens, vocab, w.keys_s, w.perm, s)) != hipSuccess) return e;
+  } else if (tokens) {
+    LAPLEX_LAUNCH("k_embed_keys", tokens, s,
+                  k_embed_keys<<<(unsigned)((tokens + 255) / 256), 256, 0, s>>>(ids, id_bytes, tokens, vocab, bits, w.keys));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = sort_indices(w.sort, w.keys, tokens, 1u << bits, w.keys_s, w.perm, s)) != hipSuccess) return e;
   }
-  LAPLEX_LAUNCH("k_embed_starts", vocab, s, k_embed_starts<<<vocab / 256 + 1, 256, 0, s>>>(w.keys_s, tokens, vocab, w.starts));
+  LAPLEX_LAUNCH("k_embed_starts", vocab, s, k_embed_starts<<<(1u << bits) / 256 + 1, 256, 0, s>>>(w.keys_s, tokens, bits, w.starts));
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const size_t te = table_dtype == LAPLEX_BF16 ? 2 : 4;
   const bool vec = embed_vec(width, dtype == LAPLEX_BF16 ? 2 : 4, te, {dy, dtable});
-  const EmbedGrad g{w.keys_s, w.perm, w.starts, tokens, vocab, width, embed_chunk(tokens), 0, 0, scale, w.part};
+  const EmbedGrad g{w.keys_s, w.perm, w.starts, tokens, vocab, width, embed_chunk(tokens), 0, bits, 0, scale, w.part};
   LAPLEX_LAUNCH("k_embed_grad", tokens, s, {
     if (dtype != LAPLEX_BF16)
       vec ? embed_grad_launch<float, float, 4>(g, dy, dtable, s) : embed_grad_launch<float, float, 1>(g, dy, dtable, s);

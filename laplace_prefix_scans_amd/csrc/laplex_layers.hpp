@@ -79,12 +79,13 @@ hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, 
 // the sorted tokens of an embedding backward
 struct EmbedWorkspace {
   SortWorkspace sort;
-  uint32_t* keys;    // ids, those outside the table as `vocab` (tokens)
+  uint32_t* keys;    // the ids' sort keys (tokens)
   uint32_t* keys_s;  // the same, sorted
   uint32_t* perm;    // tokens in that order
-  uint32_t* starts;  // first sorted position of each row of the table (vocab + 1)
+  uint32_t* starts;  // first sorted position of each key (embed_starts)
   float* part;       // partial rows (embed_part_floats)
 };
+uint64_t embed_starts(uint32_t vocab);
 uint64_t embed_part_floats(uint64_t tokens, uint32_t width);
 hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s);

@@ -309,7 +309,7 @@ EmbedWorkspace carve_embed(void* ws, uint64_t tokens, uint32_t vocab, uint32_t w
   w.keys = c.take<uint32_t>(tokens * 4);
   w.keys_s = c.take<uint32_t>(tokens * 4);
   w.perm = c.take<uint32_t>(tokens * 4);
-  w.starts = c.take<uint32_t>((vocab + 1ull) * 4);
+  w.starts = c.take<uint32_t>(embed_starts(vocab) * 4);
   w.part = c.take<float>(embed_part_floats(tokens, width) * 4);
   *total = (c.off + 255) & ~size_t(255);
   return w;

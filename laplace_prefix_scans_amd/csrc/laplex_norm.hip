@@ -17,6 +17,7 @@
 namespace laplex {
 
 constexpr int kNormBlock = 256;
+constexpr uint32_t kNormBlocks = 2048;  // 256-thread blocks of a forward pass (eight a CU), each taking rows in turn
 constexpr uint32_t kNormParts = 512;  // at most so many partials of the weight gradient (two 256-thread blocks a CU)
 
 // ------------------------------------------------------------------ rows in registers
@@ -91,8 +92,13 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void k_norm(uint64_t rows,
   if (w) rw.load(w, width, t);
   if (b) rb.load(b, width, t);
   // uniform over the threads of a row, and over the block where a row takes all of it
-  for (uint64_t row = (uint64_t)blockIdx.x * Row::ROWS + threadIdx.x / TPR; row < rows; row += (uint64_t)gridDim.x * Row::ROWS) {
-    r.load(x + row * width, width, t);
+  const uint64_t stride = (uint64_t)gridDim.x * Row::ROWS;
+  uint64_t row = (uint64_t)blockIdx.x * Row::ROWS + threadIdx.x / TPR;
+  Row next;  // on its way while this row is reduced
+  if (row < rows) next.load(x + row * width, width, t);
+  for (; row < rows; row += stride) {
+    r = next;
+    if (row + stride < rows) next.load(x + (row + stride) * width, width, t);
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < Row::N; ++k) s += to_f32(r.e[k]);
@@ -344,7 +350,7 @@ struct NormForward {
   template <int TPR, int VPT>
   void operator()() const {
     constexpr int TH = TPR < 256 ? 256 : TPR, R = TH / TPR;
-    const unsigned blocks = (unsigned)std::min<uint64_t>((rows + R - 1) / R, 1u << 20);
+    const unsigned blocks = (unsigned)std::min<uint64_t>((rows + R - 1) / R, kNormBlocks * 256 / TH);
     if (vec) k_norm<T, TPR, VPT, true><<<blocks, TH, 0, s>>>(rows, width, x, w, b, eps, y, mean, rstd);
     else k_norm<T, TPR, VPT, false><<<blocks, TH, 0, s>>>(rows, width, x, w, b, eps, y, mean, rstd);
   }
