@@ -61,30 +61,32 @@ struct AttnPlan {
   bool split;
 };
 // The split depends on K and V alike, so that a pass and the one with K and V exchanged share their segments.
-static int64_t attn_seg_len(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+static int64_t attn_seg_len(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   const uint32_t wide = std::max(K, V), slices = wide > 128 ? 2 : 1;
-  const uint64_t blocks = wide <= 64 ? 1024 : 512;  // two waves (wide <= 64) or four per SIMD
+  // Blocks that run at once: 256 CUs with two of eight waves or four of four; half with the lag-weighted carry.
+  // (65536 tokens x 8 heads, 128 x 128: 248 us; with half as many blocks 331, twice 279, four times 339.)
+  const uint64_t blocks = (wide <= 64 ? 1024 : 512) / (rate ? 2 : 1);
   uint64_t len = std::max<uint64_t>(kAttnMinSeg, tokens * heads * slices / blocks);
   len = (len + 63) / 64 * 64;
   return (int64_t)(len + len / 2 < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
 }
-static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+static AttnPlan attn_plan(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   AttnPlan q;
   q.kp = K <= 64 ? 64 : K <= 128 ? 128 : 256;
   q.nw = V <= 64 && K <= 64 ? 4 : 8;
   q.slices = (V + 16 * q.nw - 1) / (16 * q.nw);
-  q.seg_len = attn_seg_len(seqs, heads, K, V, tokens);
+  q.seg_len = attn_seg_len(heads, K, V, tokens, rate);
   q.split = (uint64_t)q.seg_len < tokens;
   q.bounds = q.split ? tokens / q.seg_len + 1 : 0;
   return q;
 }
 
-size_t attn_pass_bytes(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
-  const AttnPlan q = attn_plan(seqs, heads, K, V, tokens);
+size_t attn_pass_bytes(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+  const AttnPlan q = attn_plan(heads, K, V, tokens, rate);
   return (size_t)q.bounds * heads * K * V * 4 * (rate ? 2 : 1);
 }
 uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets) {
-  const AttnPlan q = attn_plan(seqs, heads, K, V, tokens);
+  const AttnPlan q = attn_plan(heads, K, V, tokens, true);
   return attn_slots({offsets, tokens, seqs, q.seg_len}) * q.slices;
 }
 
@@ -96,7 +98,7 @@ static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   const bool rate = p.drate_part != nullptr, bf = p.dtype == LAPLEX_BF16;
   const size_t e = bf ? 2 : 4;
-  const AttnPlan q = attn_plan(p.seqs, p.heads, p.K, p.V, p.tokens);
+  const AttnPlan q = attn_plan(p.heads, p.K, p.V, p.tokens, rate);
   AttnChunkArgs a{};
   a.p = p;
   a.g = {p.offsets, p.tokens, p.seqs, q.seg_len};

@@ -46,7 +46,7 @@ struct AttnPass {
   double* drate_part;  // partials of the rate gradient ([attn_drate_parts][head])
 };
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s);
-size_t attn_pass_bytes(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate);
+size_t attn_pass_bytes(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate);
 // number of partials per head an attn_pass with drate_part writes ([partial][head])
 // (largest with offsets, whatever they hold)
 uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets);

@@ -79,8 +79,8 @@ struct AttnWorkspace {
 AttnWorkspace carve_attn(void* ws, int pass, const laplex_attn_shape& a, size_t* total) {
   Carver c(ws);
   AttnWorkspace w{};
-  size_t b = attn_pass_bytes(a.seqs, a.heads, a.dk, a.dv, a.tokens, false);
-  if (pass == LAPLEX_ATTN_BACKWARD) b = std::max(b, attn_pass_bytes(a.seqs, a.heads, a.dv, a.dk, a.tokens, true));
+  size_t b = attn_pass_bytes(a.heads, a.dk, a.dv, a.tokens, false);
+  if (pass == LAPLEX_ATTN_BACKWARD) b = std::max({b, attn_pass_bytes(a.heads, a.dv, a.dk, a.tokens, false), attn_pass_bytes(a.heads, a.dv, a.dk, a.tokens, true)});
   w.pass = c.take<void>(b);
   if (pass == LAPLEX_ATTN_BACKWARD) {
     if (a.heads != a.kv_heads) w.sum = c.take<float>(a.tokens * a.heads * std::max(a.dk, a.dv) * 4);
