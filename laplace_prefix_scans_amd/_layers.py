@@ -278,8 +278,7 @@ def laplex_layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Te
     _like(rstd, "rstd", x.shape[:-1], torch.float32, dev)
     _like(weight, "weight", (width,), x.dtype, dev)
     dx = torch.empty_like(x)
-    dw = torch.empty(width, dtype=torch.float32, device=dev) if param_grads else None
-    db = torch.empty(width, dtype=torch.float32, device=dev) if param_grads else None
+    dw, db = torch.empty((2, width), dtype=torch.float32, device=dev).unbind(0) if param_grads else (None, None)
     L = _lib()
     ws, ws_bytes = _bytes(ws, L.laplex_layer_norm_workspace_bytes(rows, width), dev)
     _check(L.laplex_layer_norm_backward(code, rows, width, _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),

@@ -560,16 +560,17 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           for (int ks = 0; ks < KP / 32; ++ks) {
             // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
             const Parts2 s2 = split2(S[2 * ks], S[2 * ks + 1]);
-            Parts2 d2;
-            if constexpr (RATE) d2 = split2(D[2 * ks], D[2 * ks + 1]);
+            Parts3 d3;  // (its result is a float32 sum: three)
+            if constexpr (RATE) d3 = split3(D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
             for (int t = 0; t < IT; ++t) {
               const bf16x8 xf = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(16 * t + lc, 32 * ks + 8 * g));
               O[t] = mfma(s2.hi, xf, ks ? O[t] : f32x4{});
               O[t] = mfma(s2.lo, xf, O[t]);
               if constexpr (RATE) {
-                OD[t] = mfma(d2.hi, xf, ks ? OD[t] : f32x4{});
-                OD[t] = mfma(d2.lo, xf, OD[t]);
+                OD[t] = mfma(d3.hi, xf, ks ? OD[t] : f32x4{});
+                OD[t] = mfma(d3.lo, xf, OD[t]);
+                OD[t] = mfma(d3.lo2, xf, OD[t]);
               }
             }
           }
@@ -629,7 +630,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
         }
         if (carry) {
           // z weighted by its decay to the chunk's end, as bfloat16 parts: three where the carry goes out as float32
-          // (it keeps float32's bits), two where it only enters bfloat16 results
+          // or into the rate's gradient (it keeps float32's bits), two where it only enters bfloat16 results
           auto weighted = [&](const float* w, f32x4& lo, f32x4& hi) {
             lo = *reinterpret_cast<const f32x4*>(w + 32 * s + 4 * g);
             hi = *reinterpret_cast<const f32x4*>(w + 32 * s + 16 + 4 * g);
@@ -639,26 +640,27 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           f32x4 z0, z1;
           weighted(down, z0, z1);
           Parts3 z3;
-          if constexpr (FINE) {
+          if constexpr (FINE || RATE) {
             z3 = split3(z0, z1);
           } else {
             const Parts2 z2 = split2(z0, z1);
             z3.hi = z2.hi, z3.lo = z2.lo;
           }
-          Parts2 l2;
+          Parts3 l3;
           if constexpr (RATE) {
             weighted(downlag, z0, z1);
-            l2 = split2(z0, z1);
+            l3 = split3(z0, z1);
           }
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
             const bf16x8 yt = read_tr<KP>(ys, ln, 32 * s, 32 * (t >> 1) + 8 * (ln & 3) + 4 * (t & 1));
             S[t] = mfma(yt, z3.hi, S[t]);
             S[t] = mfma(yt, z3.lo, S[t]);
-            if constexpr (FINE) S[t] = mfma(yt, z3.lo2, S[t]);
+            if constexpr (FINE || RATE) S[t] = mfma(yt, z3.lo2, S[t]);
             if constexpr (RATE) {
-              D[t] = mfma(yt, l2.hi, D[t]);
-              D[t] = mfma(yt, l2.lo, D[t]);
+              D[t] = mfma(yt, l3.hi, D[t]);
+              D[t] = mfma(yt, l3.lo, D[t]);
+              D[t] = mfma(yt, l3.lo2, D[t]);
             }
           }
         }

@@ -101,8 +101,10 @@ __global__ void k_embed_keys(const void* __restrict__ ids, int id_bytes, uint64_
 // all of them, takes those of the key range b (range kTops: outside the table)
 // in order, counts those of the ranges before it -- where its part of the
 // result starts -- and sorts its own in LDS by the remaining bits (stable LSD
-// passes of 6).  No block waits for another.  16384 tokens: 9 us; sorted by one
+// passes of 6), and for vocabularies up to 2^kFindBits writes its keys' first
+// positions too.  No block waits for another.  16384 tokens: 9 us; sorted by one
 // block 31 us, by the general sort's eight launches about as long.
+constexpr int kFindBits = 18;
 constexpr int kEmbedSmall = 16384, kSortThreads = 1024, kSortWaves = kSortThreads / kWave, kSortBits = 6, kSortBins = 1 << kSortBits;
 
 // lanes whose digit is this lane's
@@ -125,7 +127,8 @@ __device__ __forceinline__ void wave_sync() {
 
 template <int E>
 __global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restrict__ ids, int id_bytes, uint32_t tokens, uint32_t vocab,
-                                                             int bits, uint32_t* __restrict__ keys, uint32_t* __restrict__ perm) {
+                                                             int bits, uint32_t* __restrict__ keys, uint32_t* __restrict__ perm,
+                                                             uint32_t* __restrict__ starts) {
   __shared__ uint32_t sk[E * kSortThreads];
   __shared__ uint16_t sp[E * kSortThreads];
   __shared__ uint32_t count[kSortWaves][kSortBins];
@@ -157,7 +160,6 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restr
     m += mine[w];
     start += below[w];
   }
-  if (m == 0) return;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const uint32_t at = (wave * E + e) * kWave + lane;
@@ -216,6 +218,18 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restr
   for (uint32_t i = threadIdx.x; i < m; i += kSortThreads) {
     keys[start + i] = sk[i];
     perm[start + i] = sp[i];
+  }
+  if (!starts) return;
+  // the first position of each key of the range
+  const uint32_t k0 = blockIdx.x << low, n = one_key ? 1 : 1u << low;
+  for (uint32_t i = threadIdx.x; i < n; i += kSortThreads) {
+    uint32_t lo = 0, hi = m;
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (sk[mid] < k0 + i) lo = mid + 1;
+      else hi = mid;
+    }
+    starts[k0 + i] = start + lo;
   }
 }
 
@@ -387,12 +401,13 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s) {
   hipError_t e;
   const int bits = key_bits(vocab);
+  uint32_t* starts = tokens && tokens <= (uint64_t)kEmbedSmall && bits <= kFindBits ? w.starts : nullptr;  // found by the sort
   if (tokens && tokens <= (uint64_t)kEmbedSmall) {
     LAPLEX_LAUNCH("k_embed_sort", tokens, s, {
       const uint32_t n = (uint32_t)tokens;
-      if (n <= kSortThreads) k_embed_sort<1><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm);
-      else if (n <= 4 * kSortThreads) k_embed_sort<4><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm);
-      else k_embed_sort<16><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm);
+      if (n <= kSortThreads) k_embed_sort<1><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm, starts);
+      else if (n <= 4 * kSortThreads) k_embed_sort<4><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm, starts);
+      else k_embed_sort<16><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm, starts);
     });
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else if (tokens) {
@@ -401,7 +416,8 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = sort_indices(w.sort, w.keys, tokens, 1u << bits, w.keys_s, w.perm, s)) != hipSuccess) return e;
   }
-  LAPLEX_LAUNCH("k_embed_starts", vocab, s, k_embed_starts<<<(1u << bits) / 256 + 1, 256, 0, s>>>(w.keys_s, tokens, bits, w.starts));
+  if (!starts)
+    LAPLEX_LAUNCH("k_embed_starts", vocab, s, k_embed_starts<<<(1u << bits) / 256 + 1, 256, 0, s>>>(w.keys_s, tokens, bits, w.starts));
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const size_t te = table_dtype == LAPLEX_BF16 ? 2 : 4;
   const bool vec = embed_vec(width, dtype == LAPLEX_BF16 ? 2 : 4, te, {dy, dtable});
