@@ -285,14 +285,29 @@ __device__ __forceinline__ double uniform(double v) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Transposed operand: this lane's column of rows row0 + 4 g + {0..3} and 16 further on.  A group of 16 lanes
-// reads 4 rows x 16 columns, each lane 4 columns of one row, and gets its column's 4 rows back.
-// col: the first column that this lane reads (its lane % 4 -th quad of the 16).
+// Operands from LDS.  The piece index of a tile is xored with swz(row), and every
+// step over channels changes only bits above the two that a lane group or quad
+// sets: a lane's byte offset for step k is its first xor (k << 6), and steps of 16
+// rows, which swz does not see, are constants.  So three offsets per lane
+// serve all reads of a chunk.
+template <typename T, int P>
+__device__ __forceinline__ uint32_t row_operand(int l) {  // row l % 16, the 16 bytes of lane group l / 16
+  return tile_at<T, P>(l & 15, (l >> 4) * (16 / (int)sizeof(T))) * sizeof(T);
+}
+template <typename T>
+__device__ __forceinline__ const T& lds_at(const void* tile, uint32_t bytes) {
+  return *reinterpret_cast<const T*>(static_cast<const char*>(tile) + bytes);
+}
+// Transposed (bf16): a group of 16 lanes reads 4 rows x 16 columns, each lane 4 columns of one row, and gets
+// its column's 4 rows back.  Rows 4 (l / 16) + l / 4 % 4, columns from `col` (< 32).
 template <int P>
-__device__ __forceinline__ bf16x8 read_tr(const __bf16* tile, int l, int row0, int col) {
-  const int row = row0 + 4 * (l >> 4) + ((l >> 2) & 3);
-  struct { s16x4 a, b; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + tile_at<__bf16, P>(row, col))),
-                              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + tile_at<__bf16, P>(row + 16, col)))};
+__device__ __forceinline__ uint32_t tr_operand(int l, int col) {
+  return tile_at<__bf16, P>(4 * (l >> 4) + ((l >> 2) & 3), col) * 2;
+}
+template <int P>  // those rows and the ones 16 on
+__device__ __forceinline__ bf16x8 read_tr(const __bf16* tile, uint32_t bytes) {
+  struct { s16x4 a, b; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(reinterpret_cast<const char*>(tile) + bytes)),
+                              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(reinterpret_cast<const char*>(tile) + bytes + 32 * P))};
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -471,6 +486,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
       }
     }
   };
+  // byte offsets of this lane's operands
+  const uint32_t row_at = row_operand<T, KP>(lane);
+  const uint32_t y_at = BF ? tr_operand<KP>(lane, 8 * (lane & 3)) : tile_at<float, KP>(4 * g, lc) * 4;
+  const uint32_t z_at = BF ? tr_operand<BV>(lane, wave * 16 % 32 + 4 * (lane & 3)) ^ (wave / 2 << 6) : 0;
   double dr = 0.0;
   if (threadIdx.x < 2) bad_chunk[threadIdx.x] = 0;
   if constexpr (FULL)
@@ -512,8 +531,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           f32x4 P = {};
 #pragma unroll
           for (int ks = 0; ks < KP / 32; ++ks)
-            P = mfma(*reinterpret_cast<const bf16x8*>(ys + tile_at<T, KP>(16 * jt + lc, 32 * ks + 8 * g)),
-                     *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(16 * it + lc, 32 * ks + 8 * g)), P);
+            P = mfma(lds_at<bf16x8>(ys + 16 * jt * KP, row_at ^ (ks << 6)), lds_at<bf16x8>(xs + 16 * it * KP, row_at ^ (ks << 6)), P);
           const int lag0 = 16 * (it - jt) + lc - 4 * g;
           float pv[4], pd[4];
 #pragma unroll
@@ -536,12 +554,12 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
         f32x4 P[3] = {};
 #pragma unroll
         for (int k = 0; k < KP / WK / 16; ++k) {
-          const int ch = wave * (KP / WK) + 16 * k + 4 * g;
+          const uint32_t at = row_at ^ ((wave * (KP / WK / 16) + k) << 6);
           f32x4 xf[2], yf[2];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            xf[t] = *reinterpret_cast<const f32x4*>(xs + tile_at<T, KP>(16 * t + lc, ch));
-            yf[t] = *reinterpret_cast<const f32x4*>(ys + tile_at<T, KP>(16 * t + lc, ch));
+            xf[t] = lds_at<f32x4>(xs + 16 * t * KP, at);
+            yf[t] = lds_at<f32x4>(ys + 16 * t * KP, at);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -564,7 +582,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
             if constexpr (RATE) d3 = split3(D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
             for (int t = 0; t < IT; ++t) {
-              const bf16x8 xf = *reinterpret_cast<const bf16x8*>(xs + tile_at<T, KP>(16 * t + lc, 32 * ks + 8 * g));
+              const bf16x8 xf = lds_at<bf16x8>(xs + 16 * t * KP, row_at ^ (ks << 6));
               O[t] = mfma(s2.hi, xf, ks ? O[t] : f32x4{});
               O[t] = mfma(s2.lo, xf, O[t]);
               if constexpr (RATE) {
@@ -579,7 +597,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int t = 0; t < IT; ++t) {
-              const f32x4 xf = *reinterpret_cast<const f32x4*>(xs + tile_at<T, KP>(16 * t + lc, 16 * k + 4 * g));
+              const f32x4 xf = lds_at<f32x4>(xs + 16 * t * KP, row_at ^ (k << 6));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 O[t] = mfma(S[k][e], xf[e], k + e ? O[t] : f32x4{});
@@ -615,7 +633,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
     if constexpr (BF) {
 #pragma unroll
       for (int s = 0; s < C / 32; ++s) {
-        const bf16x8 zf = read_tr<BV>(zs, ln, 32 * s, wave * 16 + 4 * (ln & 3));
+        const bf16x8 zf = read_tr<BV>(zs + 32 * s * BV, z_at);
         if constexpr (FULL) {
 #pragma unroll
           for (int t = 2 * s; t < IT; ++t) {
@@ -653,7 +671,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           }
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            const bf16x8 yt = read_tr<KP>(ys, ln, 32 * s, 32 * (t >> 1) + 8 * (ln & 3) + 4 * (t & 1));
+            const bf16x8 yt = read_tr<KP>(ys + 32 * s * KP + 4 * (t & 1), y_at ^ (t >> 1 << 6));
             S[t] = mfma(yt, z3.hi, S[t]);
             S[t] = mfma(yt, z3.lo, S[t]);
             if constexpr (FINE || RATE) S[t] = mfma(yt, z3.lo2, S[t]);
@@ -699,7 +717,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
         LAPLEX_EACH(s, C / 16, r) {
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            const float yt = ys[tile_at<T, KP>(16 * s + 4 * g + r, 16 * t + lc)];
+            const float yt = lds_at<float>(ys + (16 * s + r) * KP, y_at ^ (t << 6 | r << 4));
             S[t] = mfma(yt, zw[s][r], S[t]);
             if constexpr (RATE) D[t] = mfma(yt, zl[s][r], D[t]);
           }
