@@ -41,6 +41,15 @@ inline uint64_t attn_slots(const AttnSegs& g) {
 // apart over all sequences, so position / seg_len numbers them uniquely.
 inline uint64_t attn_bounds(uint64_t tokens, int64_t seg_len) { return tokens / seg_len + 1; }
 
+// a value that every lane holds, in scalar registers
+template <typename V>
+__device__ __forceinline__ V uniform(V v) {
+  static_assert(sizeof(V) == 8, "two words");
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+}
+
 struct AttnSeg {
   int64_t first, len;  // the sequence's tokens
   int64_t u0, n;       // the segment's first token in processing order, its length
@@ -80,7 +89,11 @@ __device__ __forceinline__ AttnSeg find_seg(const AttnSegs& g, uint64_t b) {
     // an empty sequence still has one segment: its final state is its initial one
     s.valid = seg >= 0 && (seg == 0 || seg * g.seg_len < s.len);
   }
-  s.u0 = seg * g.seg_len;
+  // every lane has found the same: what follows from it then needs no vector registers
+  s.first = uniform(s.first);
+  s.len = uniform(s.len);
+  s.seq = __builtin_amdgcn_readfirstlane(s.seq);
+  s.u0 = uniform(seg) * g.seg_len;
   s.n = min(g.seg_len, s.len - s.u0);
   return s;
 }
@@ -91,6 +104,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
@@ -116,6 +131,30 @@ __device__ __forceinline__ int tile_at(int r, int c) {
   return r * P + (((c / E) ^ swz<T, P>(r)) * E) + c % E;
 }
 
+// Global memory at a pointer that all threads share and 32 bits of each lane's own: one vector register an
+// address.  (The empty asm keeps the sum from being formed ahead, in two.)
+typedef __attribute__((address_space(1))) char* GlobalPtr;
+template <typename V>
+__device__ __forceinline__ V load_global(const void* base, uint32_t off) {
+  GlobalPtr p = (GlobalPtr)uniform((uint64_t)(uintptr_t)base);
+  asm volatile("" : "+v"(off));
+  return *reinterpret_cast<__attribute__((address_space(1))) V*>(p + off);
+}
+template <typename V>
+__device__ __forceinline__ void store_global(void* base, uint32_t off, V v) {
+  GlobalPtr p = (GlobalPtr)uniform((uint64_t)(uintptr_t)base);
+  asm volatile("" : "+v"(off));
+  *reinterpret_cast<__attribute__((address_space(1))) V*>(p + off) = v;
+}
+
+// The thread's number, as something the compiler takes to change with every call: what is made from it is
+// then formed where it is used instead of holding a register over the loop.
+__device__ __forceinline__ int thread_now() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 // A tile's 16-byte pieces on their way from memory to LDS: thread -> column
 // piece threadIdx.x % (P / E) of every RPI-th row.
 template <typename T, int ROWS, int P, int THREADS, bool VEC>
@@ -123,55 +162,49 @@ struct Stage {
   static constexpr int E = 16 / sizeof(T), RPI = THREADS / (P / E), N = ROWS / RPI;
   static_assert(THREADS % (P / E) == 0 && ROWS % RPI == 0, "pieces divide evenly");
   uint4 v[N];
-  // The thread's piece of the next chunk's row group i is at at + i * rows_it + off: a pointer all threads share
-  // and 32 bits of its own (VEC: the host has seen that RPI rows span less than 2^31 bytes).
-  const T* at;
-  int64_t rows_it;
-  uint32_t off;
-  int cols;  // columns from its piece's first to the end of the row
-  // p: the first token's row, col0: the tile's first column, stride: elements from a row to the next token's,
-  // step: 1, or -1 where the tokens run backwards
-  __device__ __forceinline__ void init(const T* p, int64_t stride, int step, int col0, int width) {
-    const int r = threadIdx.x / (P / E), c = col0 + threadIdx.x % (P / E) * E;
-    cols = width - c;
-    rows_it = RPI * stride * step;
-    if constexpr (VEC) {
-      at = step > 0 ? p : p - (RPI - 1) * stride;
-      off = (uint32_t)(((step > 0 ? r : RPI - 1 - r) * stride + c) * sizeof(T));
-    } else {
-      at = p + r * stride * step + c;
-    }
-  }
-  __device__ __forceinline__ uint4 piece(int i) const {
-    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(at + i * rows_it) + off);
+  // All of these are the same for every thread; a thread's own offsets are formed anew each time.
+  const T* at;     // the next chunk's first row (VEC and backward: its RPI-th), at the tile's first column
+  int64_t stride;  // elements from a row to the next token's
+  int step;        // 1, or -1 where the tokens run backwards
+  int width;       // columns from the tile's first to the end of the row
+  __device__ __forceinline__ void init(const T* p, int64_t stride_, int step_, int col0, int width_) {
+    stride = stride_, step = step_, width = width_ - col0;
+    at = p + col0 - (VEC && step < 0 ? (RPI - 1) * stride : 0);
   }
   // The next chunk's rows [0, rows); rows and columns past the end are zero.  whole: every column is there.
+  // (VEC: the host has seen that RPI rows span less than 2^31 bytes.)
   __device__ __forceinline__ void load(int rows, bool whole) {
-    const int r0 = threadIdx.x / (P / E);
-    if (VEC && whole && rows == ROWS) {
+    const int t = thread_now(), r0 = t / (P / E), c = t % (P / E) * E;
+    const int64_t rows_it = RPI * stride * step;
+    if constexpr (VEC) {
+      const uint32_t off = ((uint32_t)(step > 0 ? r0 : RPI - 1 - r0) * (uint32_t)stride + c) * (uint32_t)sizeof(T);
+      if (whole && rows == ROWS) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = piece(i);
+        for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(uint4, load_global<u32x4>(at + i * rows_it, off));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (r0 + i * RPI < rows && c < width) v[i] = __builtin_bit_cast(uint4, load_global<u32x4>(at + i * rows_it, off));
+        }
+      }
     } else {
+      const T* p = at + r0 * stride * step + c;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if constexpr (VEC) {
-          if (r0 + i * RPI < rows && cols > 0) q = piece(i);
-        } else {
-          T e[E];
+        T e[E];
 #pragma unroll
-          for (int j = 0; j < E; ++j) e[j] = r0 + i * RPI < rows && j < cols ? at[i * rows_it + j] : T(0.f);
-          __builtin_memcpy(&q, e, 16);
-        }
-        v[i] = q;
+        for (int j = 0; j < E; ++j) e[j] = r0 + i * RPI < rows && c + j < width ? p[i * rows_it + j] : T(0.f);
+        __builtin_memcpy(&v[i], e, 16);
       }
     }
     at += N * rows_it;
   }
   __device__ __forceinline__ void store(T* tile) const {
+    const int t = thread_now();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = threadIdx.x / (P / E) + i * RPI, c = threadIdx.x % (P / E);
+      const int r = t / (P / E) + i * RPI, c = t % (P / E);
       *reinterpret_cast<uint4*>(tile + r * P + ((c ^ swz<T, P>(r)) * E)) = v[i];
     }
   }
@@ -269,34 +302,27 @@ struct AttnChunkArgs {
 template <typename T>
 constexpr int kAttnC = sizeof(T) == 2 ? 64 : 32;  // tokens per chunk
 
-// Row of the carry that register r of 16-row tile t holds in lane group g.
-// bf16: two tiles side by side hold the 32 rows in the order in which a lane's
-// 8 consecutive channels of x are one operand.
-template <typename T>
-__device__ __forceinline__ int carry_row(int t, int g, int r) {
-  if constexpr (sizeof(T) == 2) return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r;
-  else return 16 * t + 4 * g + r;
-}
-
-// a value that every lane holds, in scalar registers
-__device__ __forceinline__ double uniform(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
+// row of the carry that register r of 16-row tile t holds in lane group g
+__device__ __forceinline__ int carry_row(int t, int g, int r) { return 16 * t + 4 * g + r; }
 
 // Operands from LDS.  The piece index of a tile is xored with swz(row), and every
-// step over channels changes only bits above the two that a lane group or quad
+// step over channels changes only bits above the ones that a lane group or quad
 // sets: a lane's byte offset for step k is its first xor (k << 6), and steps of 16
 // rows, which swz does not see, are constants.  So three offsets per lane
 // serve all reads of a chunk.
 template <typename T, int P>
-__device__ __forceinline__ uint32_t row_operand(int l) {  // row l % 16, the 16 bytes of lane group l / 16
-  return tile_at<T, P>(l & 15, (l >> 4) * (16 / (int)sizeof(T))) * sizeof(T);
+__device__ __forceinline__ uint32_t row_operand(int l) {  // row l % 16, channels 4 (l / 16) + {0..3}
+  return tile_at<T, P>(l & 15, (l >> 4) * 4) * sizeof(T);
 }
 template <typename T>
 __device__ __forceinline__ const T& lds_at(const void* tile, uint32_t bytes) {
   return *reinterpret_cast<const T*>(static_cast<const char*>(tile) + bytes);
+}
+// Row operand of a bf16 product over 32 channels: those of the carry's tiles 2k and 2k + 1 in lane group g,
+// 32 k + 4 g + {0..3} and 16 on, so that the carry's registers are the other operand as they are.
+__device__ __forceinline__ bf16x8 read_row(const __bf16* tile, uint32_t bytes) {
+  struct { uint2 a, b; } v = {lds_at<uint2>(tile, bytes), lds_at<uint2>(tile, bytes ^ 32)};
+  return __builtin_bit_cast(bf16x8, v);
 }
 // Transposed (bf16): a group of 16 lanes reads 4 rows x 16 columns, each lane 4 columns of one row, and gets
 // its column's 4 rows back.  Rows 4 (l / 16) + l / 4 % 4, columns from `col` (< 32).
@@ -324,27 +350,29 @@ __device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) { return __buil
 // the same column and consecutive rows: the carry enters the products of the
 // next chunk without leaving the registers.
 //   P^T = y x^T, weighted        (the waves share its tiles out)
-//   out^T = up (S^T x^T) + z^T P
+//   out^T = up (S^T x^T)
 //   S = w(n) S + y^T (down z)
+//   out^T += z^T P
 // With 16 columns a wave holds 32 registers of a 128-row carry, so that four
 // waves share a SIMD and one's conversions run beside another's products;
-// 32 columns in half as many waves took as long without, and twice as long with the rate's gradient.
+// 32 columns in half as many waves took as long without the rate's gradient, and a quarter longer with it.
 // FINE: the carry goes out as float32 (otherwise it only enters results of type T).
 template <typename T, int KP, int NW, bool FULL, bool RATE, bool FINE, bool VEC>
 __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_chunk(AttnChunkArgs a) {
   constexpr int C = kAttnC<T>, KT = KP / 16, BV = 16 * NW, THREADS = NW * kWave, IT = C / 16;
   constexpr bool BF = sizeof(T) == 2, DOT = FULL && RATE;
-  constexpr int WK = NW < KP / 16 ? NW : KP / 16;  // float: waves that share the channels of P^T
+  constexpr int WK = KP / 16 < 4 ? KP / 16 : 4;    // float: waves that share the channels of P^T
+  constexpr int ZB = FULL ? 2 : 1;                 // buffers of z
   const AttnPass& p = a.p;
   __shared__ __attribute__((aligned(16))) T xs[FULL ? C * KP : 8];
   __shared__ __attribute__((aligned(16))) T ys[C * KP];
-  __shared__ __attribute__((aligned(16))) T zs[C * BV];
-  __shared__ __attribute__((aligned(16))) T dots[DOT ? C * BV : 8];
+  __shared__ __attribute__((aligned(16))) T zs[ZB][C * BV];
+  __shared__ __attribute__((aligned(16))) T dots[2][DOT ? C * BV : 8];
   __shared__ __attribute__((aligned(16))) float down[C], downlag[RATE ? C : 4];
   __shared__ float wt[FULL ? 2 * C : 1], up[FULL ? C : 1];
-  // bf16: operand [32 rows j][tile i][part] of a lane (the lag-weighted ones behind them); float: [wave][tile]
+  // bf16: operand [32 rows j and tile i: i + 2 (j / 32)][part] of a lane (the lag-weighted ones behind them); float: [wave][tile]
   using Pair = std::conditional_t<BF, bf16x8, f32x4>;
-  constexpr int PAIRS = 2 * IT * 2 * kWave;
+  constexpr int PAIRS = 6 * 2 * kWave;
   __shared__ Pair pairs[FULL ? (BF ? (RATE ? 2 : 1) * PAIRS : WK * 3 * kWave) : 1];
   __shared__ int bad_chunk[2], bad_row[2][FULL ? BV : 1];
   __shared__ double red[NW];
@@ -377,7 +405,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   }
   const bool last_seg = sg.u0 + sg.n >= sg.len;
   if (!FULL && last_seg) return;  // nothing reads this segment's state
-  const float rate = attn_rate(p.rate[h]);
+  const float rate = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(attn_rate(p.rate[h]))));
   const int lead = p.reverse ? 0 : 1;
   const bool keep = !last_seg || p.s_out || (DOT && p.ds_out);  // the carry after the last chunk is needed
   // states in memory: element (row, column) at row * rs + column * cs of the caller's ([seq][head], either order) or of a boundary's
@@ -390,7 +418,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
     if (col >= V) return;
     src += (int64_t)col * cs;
     LAPLEX_EACH(t, KT, r) {
-      const int row = carry_row<T>(t, g, r);
+      const int row = carry_row(t, g, r);
       const float v = src[min(row, K - 1) * rs];
       s[t][r] = row < K ? v : 0.f;
     }
@@ -421,9 +449,13 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
   // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
   // so far back to the exact one.
-  const double wc = uniform(exp(-(double)rate * (double)C));
+  const int tail = (int)((sg.n - 1) % C) + 1;  // tokens of the last chunk
+  const double wc = uniform(exp(-(double)rate * (double)C)), wtail = uniform(exp(-(double)rate * (double)tail));
   double owed = 1.0;
+  int down_of = -1;
   auto set_down = [&](int n) {
+    if (n == down_of) return;
+    down_of = n;
     if (threadIdx.x < C) {
       const int j = threadIdx.x, lag = n - 1 - j;
       down[j] = lag >= 0 ? p.c_add * decay(-rate * (float)(lag + 1 - lead)) : 0.f;
@@ -457,27 +489,29 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   // loads, so writing before would make the wait for the next chunk's rows one for the stores too.
   auto put = [&](int64_t u) {
     if (!active || !p.out) return;
+    const int ln = thread_now() & (kWave - 1), g = ln >> 4, lc = ln & 15;
     const int n = (int)min((int64_t)C, sg.u0 + sg.n - u), c = slice * BV + wave * 16 + 4 * g;
     // a pointer all threads share and 32 bits of each lane's own: 16 rows of at most 4096 x 256 floats
     const int64_t row = (int64_t)p.heads * V, base = (token(u) - (p.reverse ? 15 : 0)) * row + (int64_t)h * V;
     const uint32_t own = (uint32_t)((p.reverse ? 15 - lc : lc) * row) + c;
+    char* out = static_cast<char*>(p.out) + base * (p.out_f32 ? 4 : (int)sizeof(T));
 #pragma unroll
     for (int t = 0; t < IT; ++t) {
       if (16 * t + lc >= n) continue;
-      const int64_t at = base + 16 * t * row * step;
+      const int64_t at = 16 * t * row * step;
       if (p.out_f32 || !BF) {
-        float* dst = static_cast<float*>(p.out) + at;
+        float* dst = reinterpret_cast<float*>(out) + at;
         if constexpr (VEC) {
-          if (c < V) *reinterpret_cast<f32x4*>(dst + own) = O[t];
+          if (c < V) store_global<f32x4>(dst, own * 4, O[t]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (c + e < V) dst[own + e] = O[t][e];
         }
       } else {
-        T* dst = static_cast<T*>(p.out) + at;
+        T* dst = reinterpret_cast<T*>(out) + at;
         if constexpr (VEC) {
-          if (c < V) *reinterpret_cast<uint2*>(dst + own) = make_uint2(pack_bf16(O[t][0], O[t][1]), pack_bf16(O[t][2], O[t][3]));
+          if (c < V) store_global<u32x2>(dst, own * 2, u32x2{pack_bf16(O[t][0], O[t][1]), pack_bf16(O[t][2], O[t][3])});
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -486,40 +520,45 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
       }
     }
   };
-  // byte offsets of this lane's operands
-  const uint32_t row_at = row_operand<T, KP>(lane);
-  const uint32_t y_at = BF ? tr_operand<KP>(lane, 8 * (lane & 3)) : tile_at<float, KP>(4 * g, lc) * 4;
-  const uint32_t z_at = BF ? tr_operand<BV>(lane, wave * 16 % 32 + 4 * (lane & 3)) ^ (wave / 2 << 6) : 0;
   double dr = 0.0;
   if (threadIdx.x < 2) bad_chunk[threadIdx.x] = 0;
   if constexpr (FULL)
     for (int i = threadIdx.x; i < 2 * BV; i += THREADS) bad_row[i / BV][i % BV] = C;
-  set_down((int)min((int64_t)C, sg.n));
-  if (sg.n > 0) load(sg.u0);
-  int parity = 0;
-  for (int64_t u = sg.u0; u < sg.u0 + sg.n; u += C, parity ^= 1) {
-    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u);
-    __syncthreads();  // the previous chunk's reads are done
+  __syncthreads();
+  // the loaded rows of a chunk of n tokens into LDS, z and dot into buffer `to`
+  auto fill = [&](int n, int to) {
     if constexpr (FULL) sx.store(xs);
     sy.store(ys);
     // A masked pair weighs 0, but 0 times an infinity is NaN: infinities and NaN in z are taken out of the
     // tile, and what they reach -- their own and later tokens of their column, the carry -- is set to NaN below.
-    if (FULL && sz.clean(bad_row[parity])) bad_chunk[parity] = 1;
-    sz.store(zs);
-    if constexpr (DOT) sd.store(dots);
-    if (threadIdx.x == 0) bad_chunk[parity ^ 1] = 0;
-    if (FULL && (int)threadIdx.x < BV) bad_row[parity ^ 1][threadIdx.x] = C;
-    if (n < C && u > sg.u0) set_down(n);
-    __syncthreads();
+    if (FULL && sz.clean(bad_row[to])) bad_chunk[to] = 1;
+    sz.store(zs[FULL ? to : 0]);
+    if constexpr (DOT) sd.store(dots[to]);
+    set_down(n);
+  };
+  if (sg.n > 0) {
+    load(sg.u0);
+    fill((int)min((int64_t)C, sg.n), 0);
+  }
+  __syncthreads();
+  // Two barriers a chunk: between the first and the second the next chunk's rows go to LDS beside the products
+  // of the pairs, which are all that is left of this one (z has two buffers).
+  int now = 0;
+  for (int64_t u = sg.u0; u < sg.u0 + sg.n; u += C, now ^= 1) {
+    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u);
     const bool more = u + C < sg.u0 + sg.n;
-    if (FULL && u > sg.u0) put(u - C);
     if (more) load(u + C);
-    const bool bad = FULL && bad_chunk[parity] != 0;
-    // the lane as the compiler sees it changes with every chunk: the many LDS offsets made from it are
-    // then formed where they are used (an xor each) instead of each holding a register over the loop
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
+    if (FULL && u > sg.u0) put(u - C);
+    const bool bad = FULL && bad_chunk[now] != 0;
+    if (threadIdx.x == 0) bad_chunk[now ^ 1] = 0;
+    if (FULL && (int)threadIdx.x < BV) bad_row[now ^ 1][threadIdx.x] = C;
+    const int ln = thread_now() & (kWave - 1);
     const int g = ln >> 4, lc = ln & 15;
+
+    // byte offsets of this lane's operands
+    const uint32_t row_at = row_operand<T, KP>(ln);
+    const uint32_t y_at = BF ? tr_operand<KP>(ln, 4 * (ln & 3)) : tile_at<float, KP>(4 * g, lc) * 4;
+    const uint32_t z_at = BF ? tr_operand<BV>(ln, wave * 16 % 32 + 4 * (ln & 3)) ^ (wave / 2 << 6) : 0;
 
     f32x4 OD[DOT ? IT : 1];
     if constexpr (FULL) {
@@ -531,7 +570,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           f32x4 P = {};
 #pragma unroll
           for (int ks = 0; ks < KP / 32; ++ks)
-            P = mfma(lds_at<bf16x8>(ys + 16 * jt * KP, row_at ^ (ks << 6)), lds_at<bf16x8>(xs + 16 * it * KP, row_at ^ (ks << 6)), P);
+            P = mfma(read_row(ys + 16 * jt * KP, row_at ^ (ks << 6)), read_row(xs + 16 * it * KP, row_at ^ (ks << 6)), P);
           const int lag0 = 16 * (it - jt) + lc - 4 * g;
           float pv[4], pd[4];
 #pragma unroll
@@ -541,7 +580,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
             if constexpr (RATE) pd[r] = pv[r] * (float)(lag0 - r);
           }
           auto put_pair = [&](float (&v)[4], int base) {
-            uint2* dst = reinterpret_cast<uint2*>(pairs + base + (((jt >> 1) * IT + it) * 2) * kWave + ln) + (jt & 1);
+            uint2* dst = reinterpret_cast<uint2*>(pairs + base + (it + (jt & 2)) * 2 * kWave + ln) + (jt & 1);
             const uint32_t h0 = split_pair(v[0], v[1]), h1 = split_pair(v[2], v[3]);
             dst[0] = make_uint2(h0, h1);
             dst[2 * kWave] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
@@ -582,7 +621,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
             if constexpr (RATE) d3 = split3(D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
             for (int t = 0; t < IT; ++t) {
-              const bf16x8 xf = lds_at<bf16x8>(xs + 16 * t * KP, row_at ^ (ks << 6));
+              const bf16x8 xf = read_row(xs + 16 * t * KP, row_at ^ (ks << 6));
               O[t] = mfma(s2.hi, xf, ks ? O[t] : f32x4{});
               O[t] = mfma(s2.lo, xf, O[t]);
               if constexpr (RATE) {
@@ -615,38 +654,22 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           }
         }
       }
-      __syncthreads();  // every wave's share of the pairs is there
     }
-    if (!active) continue;
-
-    // out^T += z^T P, and the carry over the chunk
-    const bool carry = !FULL || more || keep;
-    if (carry) {
-      const double exact = (n == C ? wc : exp(-(double)rate * (double)n)) * owed;
+    // the carry over the chunk
+    const T* z = zs[FULL ? now : 0];
+    if (active && (!FULL || more || keep)) {
+      const double exact = uniform((more ? wc : wtail) * owed);
       const float w = (float)exact;
-      owed = uniform(w != 0.f ? exact / (double)w : 1.0);
+      // (a subnormal w has no reciprocal, and nothing that a later chunk could show)
+      owed = w >= 0x1p-126f ? 1.0 + (double)((float)(exact - (double)w) * __builtin_amdgcn_rcpf(w)) : 1.0;
       LAPLEX_EACH(t, KT, r) {
         if constexpr (RATE) D[t][r] = w * fmaf((float)n, S[t][r], D[t][r]);  // the lag-weighted carry ahead of the other
         S[t][r] *= w;
       }
-    }
-    if constexpr (BF) {
+      if constexpr (BF) {
 #pragma unroll
-      for (int s = 0; s < C / 32; ++s) {
-        const bf16x8 zf = read_tr<BV>(zs + 32 * s * BV, z_at);
-        if constexpr (FULL) {
-#pragma unroll
-          for (int t = 2 * s; t < IT; ++t) {
-            const bf16x8* pf = pairs + ((s * IT + t) * 2) * kWave + ln;
-            O[t] = mfma(zf, pf[0], O[t]);
-            O[t] = mfma(zf, pf[kWave], O[t]);
-            if constexpr (RATE) {
-              OD[t] = mfma(zf, pf[PAIRS], OD[t]);
-              OD[t] = mfma(zf, pf[PAIRS + kWave], OD[t]);
-            }
-          }
-        }
-        if (carry) {
+        for (int s = 0; s < C / 32; ++s) {
+          const bf16x8 zf = read_tr<BV>(z + 32 * s * BV, z_at);
           // z weighted by its decay to the chunk's end, as bfloat16 parts: three where the carry goes out as float32
           // or into the rate's gradient (it keeps float32's bits), two where it only enters bfloat16 results
           auto weighted = [&](const float* w, f32x4& lo, f32x4& hi) {
@@ -671,7 +694,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           }
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            const bf16x8 yt = read_tr<KP>(ys + 32 * s * KP + 4 * (t & 1), y_at ^ (t >> 1 << 6));
+            const bf16x8 yt = read_tr<KP>(ys + 32 * s * KP, y_at ^ (t >> 1 << 6 | (t & 1) << 5));
             S[t] = mfma(yt, z3.hi, S[t]);
             S[t] = mfma(yt, z3.lo, S[t]);
             if constexpr (FINE || RATE) S[t] = mfma(yt, z3.lo2, S[t]);
@@ -682,11 +705,52 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
             }
           }
         }
+      } else {
+        f32x4 zw[C / 16], zl[C / 16];
+#pragma unroll
+        for (int s = 0; s < C / 16; ++s) {
+          f32x4 zf;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) zf[r] = z[tile_at<T, BV>(16 * s + 4 * g + r, wave * 16 + lc)];
+          if constexpr (RATE) zl[s] = zf * *reinterpret_cast<const f32x4*>(downlag + 16 * s + 4 * g);
+          zw[s] = zf * *reinterpret_cast<const f32x4*>(down + 16 * s + 4 * g);
+        }
+        LAPLEX_EACH(s, C / 16, r) {
+#pragma unroll
+          for (int t = 0; t < KT; ++t) {
+            const float yt = lds_at<float>(ys + (16 * s + r) * KP, y_at ^ (t << 6 | r << 4));
+            S[t] = mfma(yt, zw[s][r], S[t]);
+            if constexpr (RATE) D[t] = mfma(yt, zl[s][r], D[t]);
+          }
+        }
       }
-    } else {
-      f32x4 zf[C / 16];
-      LAPLEX_EACH(s, C / 16, r) zf[s][r] = zs[tile_at<T, BV>(16 * s + 4 * g + r, wave * 16 + lc)];
-      if constexpr (FULL) {
+      if (bad && bad_row[now][wave * 16 + lc] < C) {
+        LAPLEX_EACH(t, KT, r) {
+          S[t][r] = __builtin_nanf("");
+          if constexpr (RATE) D[t][r] = __builtin_nanf("");
+        }
+      }
+    }
+    __syncthreads();  // every wave's share of the pairs is there, and x and y are read
+    if (more) fill((int)min((int64_t)C, sg.u0 + sg.n - u - C), now ^ 1);
+    if (FULL && active) {
+      // out^T += z^T P
+      if constexpr (BF) {
+#pragma unroll
+        for (int s = 0; s < C / 32; ++s) {
+          const bf16x8 zf = read_tr<BV>(z + 32 * s * BV, z_at);
+#pragma unroll
+          for (int t = 2 * s; t < IT; ++t) {
+            const bf16x8* pf = pairs + (t + 2 * s) * 2 * kWave + ln;
+            O[t] = mfma(zf, pf[0], O[t]);
+            O[t] = mfma(zf, pf[kWave], O[t]);
+            if constexpr (RATE) {
+              OD[t] = mfma(zf, pf[PAIRS], OD[t]);
+              OD[t] = mfma(zf, pf[PAIRS + kWave], OD[t]);
+            }
+          }
+        }
+      } else {
         f32x4 P[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -700,61 +764,36 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
           }
         }
         LAPLEX_EACH(s, C / 16, r) {
+          const float zf = z[tile_at<T, BV>(16 * s + 4 * g + r, wave * 16 + lc)];
 #pragma unroll
           for (int t = s; t < IT; ++t) {
-            O[t] = mfma(zf[s][r], P[s + t][r], O[t]);
-            if constexpr (RATE) OD[t] = mfma(zf[s][r], P[s + t][r] * (float)(16 * (t - s) + lc - 4 * g - r), OD[t]);
+            O[t] = mfma(zf, P[s + t][r], O[t]);
+            if constexpr (RATE) OD[t] = mfma(zf, P[s + t][r] * (float)(16 * (t - s) + lc - 4 * g - r), OD[t]);
           }
         }
       }
-      if (carry) {  // all of it in one piece, so that reads run ahead of the products
-        f32x4 zw[C / 16], zl[C / 16];
-#pragma unroll
-        for (int s = 0; s < C / 16; ++s) {
-          if constexpr (RATE) zl[s] = zf[s] * *reinterpret_cast<const f32x4*>(downlag + 16 * s + 4 * g);
-          zw[s] = zf[s] * *reinterpret_cast<const f32x4*>(down + 16 * s + 4 * g);
-        }
-        LAPLEX_EACH(s, C / 16, r) {
-#pragma unroll
-          for (int t = 0; t < KT; ++t) {
-            const float yt = lds_at<float>(ys + (16 * s + r) * KP, y_at ^ (t << 6 | r << 4));
-            S[t] = mfma(yt, zw[s][r], S[t]);
-            if constexpr (RATE) D[t] = mfma(yt, zl[s][r], D[t]);
-          }
-        }
-      }
-    }
-
-    if constexpr (FULL) {
       if (bad) {
-        const float nan = __builtin_nanf("");
-        const int* first = bad_row[parity] + wave * 16;
-        const bool gone = first[lc] < C;
         LAPLEX_EACH(t, IT, r) {
-          const bool hit = 16 * t + lc >= first[4 * g + r];
-          O[t][r] = hit ? nan : O[t][r];
-          if constexpr (RATE) OD[t][r] = hit ? nan : OD[t][r];
-        }
-        LAPLEX_EACH(t, KT, r) {
-          S[t][r] = gone ? nan : S[t][r];
-          if constexpr (RATE) D[t][r] = gone ? nan : D[t][r];
+          const bool hit = 16 * t + lc >= bad_row[now][wave * 16 + 4 * g + r];
+          O[t][r] = hit ? __builtin_nanf("") : O[t][r];
+          if constexpr (RATE) OD[t][r] = hit ? __builtin_nanf("") : OD[t][r];
         }
       }
       if constexpr (DOT) {
         LAPLEX_EACH(t, IT, r)  // rows past the end are zero in the tile
-          dr += (double)(OD[t][r] * to_f32(dots[tile_at<T, BV>(16 * t + lc, wave * 16 + 4 * g + r)]));
+          dr += (double)(OD[t][r] * to_f32(dots[now][tile_at<T, BV>(16 * t + lc, wave * 16 + 4 * g + r)]));
       }
     }
+    __syncthreads();
   }
   if (FULL && sg.n > 0) put(sg.u0 + (sg.n - 1) / C * C);
 
   // the carry after the segment
-  int colf = col, gf = g;
-  asm volatile("" : "+v"(colf), "+v"(gf));  // the row and column tests are made again, not kept over the loop
+  const int lnf = thread_now() & (kWave - 1), gf = lnf >> 4, colf = slice * BV + wave * 16 + (lnf & 15);
   auto each = [&](int rs, int cs, auto&& f) {
     if (colf >= V) return;
     LAPLEX_EACH(t, KT, r) {
-      const int row = carry_row<T>(t, gf, r);
+      const int row = carry_row(t, gf, r);
       if (row < K) f(t, r, row * rs + colf * cs);
     }
   };
