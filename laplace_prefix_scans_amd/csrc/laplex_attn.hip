@@ -91,8 +91,8 @@ uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V,
 }
 
 static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width, size_t e) {
-  // (and the 64 rows of a chunk lie within 2^31 bytes)
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (uint64_t)token * e < (1u << 25) && token * e % 16 == 0 && head * e % 16 == 0 && width * e % 16 == 0;
+  // (and rows follow each other without overlap, a chunk's 64 within 2^30 bytes)
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && token >= (int64_t)width && (uint64_t)token * e < (1u << 24) && token * e % 16 == 0 && head * e % 16 == 0 && width * e % 16 == 0;
 }
 
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {

@@ -131,20 +131,13 @@ __device__ __forceinline__ int tile_at(int r, int c) {
   return r * P + (((c / E) ^ swz<T, P>(r)) * E) + c % E;
 }
 
-// Global memory at a pointer that all threads share and 32 bits of each lane's own: one vector register an
-// address.  (The empty asm keeps the sum from being formed ahead, in two.)
-typedef __attribute__((address_space(1))) char* GlobalPtr;
-template <typename V>
-__device__ __forceinline__ V load_global(const void* base, uint32_t off) {
-  GlobalPtr p = (GlobalPtr)uniform((uint64_t)(uintptr_t)base);
-  asm volatile("" : "+v"(off));
-  return *reinterpret_cast<__attribute__((address_space(1))) V*>(p + off);
-}
-template <typename V>
-__device__ __forceinline__ void store_global(void* base, uint32_t off, V v) {
-  GlobalPtr p = (GlobalPtr)uniform((uint64_t)(uintptr_t)base);
-  asm volatile("" : "+v"(off));
-  *reinterpret_cast<__attribute__((address_space(1))) V*>(p + off) = v;
+// Memory by a descriptor of its first byte and its length, both the same for every thread, and 32 bits of each
+// thread's own: one vector register an address, and the hardware's bounds check in place of branches -- a read
+// past the length is 0 and a write there is dropped.  kNowhere is past every length, by a chunk's rows to either side.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* first, uint32_t bytes) {
+  void* p = reinterpret_cast<void*>(uniform((uint64_t)reinterpret_cast<uintptr_t>(first)));
+  return __builtin_amdgcn_make_buffer_rsrc(p, 0, __builtin_amdgcn_readfirstlane(bytes), 0x00027000);  // raw, 32-bit words
 }
 
 // The thread's number, as something the compiler takes to change with every call: what is made from it is
@@ -163,42 +156,35 @@ struct Stage {
   static_assert(THREADS % (P / E) == 0 && ROWS % RPI == 0, "pieces divide evenly");
   uint4 v[N];
   // All of these are the same for every thread; a thread's own offsets are formed anew each time.
-  const T* at;     // the next chunk's first row (VEC and backward: its RPI-th), at the tile's first column
-  int64_t stride;  // elements from a row to the next token's
-  int step;        // 1, or -1 where the tokens run backwards
-  int width;       // columns from the tile's first to the end of the row
-  __device__ __forceinline__ void init(const T* p, int64_t stride_, int step_, int col0, int width_) {
-    stride = stride_, step = step_, width = width_ - col0;
-    at = p + col0 - (VEC && step < 0 ? (RPI - 1) * stride : 0);
+  using Bytes = std::conditional_t<VEC, int32_t, int64_t>;  // (VEC: the host has seen that a chunk's rows span less than 2^30 bytes)
+  const char* at;  // the next chunk's first row, at the tile's first column
+  Bytes pitch;     // bytes from a row to the next token's: negative where the tokens run backwards
+  __device__ __forceinline__ void init(const T* p, int64_t stride, int step, int col0) {
+    pitch = (Bytes)(stride * step) * (Bytes)sizeof(T);
+    at = reinterpret_cast<const char*>(p + col0);
   }
-  // The next chunk's rows [0, rows); rows and columns past the end are zero.  whole: every column is there.
-  // (VEC: the host has seen that RPI rows span less than 2^31 bytes.)
-  __device__ __forceinline__ void load(int rows, bool whole) {
+  // The next chunk's rows [0, rows); rows, and columns from `width` on, are zero.
+  __device__ __forceinline__ void load(int rows, int width) {
     const int t = thread_now(), r0 = t / (P / E), c = t % (P / E) * E;
-    const int64_t rows_it = RPI * stride * step;
     if constexpr (VEC) {
-      const uint32_t off = ((uint32_t)(step > 0 ? r0 : RPI - 1 - r0) * (uint32_t)stride + c) * (uint32_t)sizeof(T);
-      if (whole && rows == ROWS) {
+      // (rows do not overlap, so those outside [0, rows) lie outside the descriptor's bytes)
+      const int32_t back = min((rows - 1) * pitch, 0), span = abs((rows - 1) * pitch);
+      const __amdgpu_buffer_rsrc_t m = rows_at(at + back, (uint32_t)span + (uint32_t)width * (uint32_t)sizeof(T));
+      const uint32_t off = c < width ? (uint32_t)(r0 * pitch - back) + c * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(uint4, load_global<u32x4>(at + i * rows_it, off));
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (r0 + i * RPI < rows && c < width) v[i] = __builtin_bit_cast(uint4, load_global<u32x4>(at + i * rows_it, off));
-        }
-      }
+      for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(m, off + (uint32_t)(i * RPI * pitch), 0, 0));
     } else {
-      const T* p = at + r0 * stride * step + c;
+      const T* p = reinterpret_cast<const T*>(at + r0 * pitch) + c;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         T e[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = r0 + i * RPI < rows && c + j < width ? p[i * rows_it + j] : T(0.f);
+        for (int j = 0; j < E; ++j)
+          e[j] = r0 + i * RPI < rows && c + j < width ? *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p + j) + i * RPI * pitch) : T(0.f);
         __builtin_memcpy(&v[i], e, 16);
       }
     }
-    at += N * rows_it;
+    at += (int64_t)(ROWS * pitch);
   }
   __device__ __forceinline__ void store(T* tile) const {
     const int t = thread_now();
@@ -449,13 +435,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
   // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
   // so far back to the exact one.
-  const int tail = (int)((sg.n - 1) % C) + 1;  // tokens of the last chunk
+  const int tail = __builtin_amdgcn_readfirstlane((int)((sg.n - 1) % C) + 1);  // tokens of the last chunk
   const double wc = uniform(exp(-(double)rate * (double)C)), wtail = uniform(exp(-(double)rate * (double)tail));
   double owed = 1.0;
-  int down_of = -1;
   auto set_down = [&](int n) {
-    if (n == down_of) return;
-    down_of = n;
     if (threadIdx.x < C) {
       const int j = threadIdx.x, lag = n - 1 - j;
       down[j] = lag >= 0 ? p.c_add * decay(-rate * (float)(lag + 1 - lead)) : 0.f;
@@ -471,62 +454,57 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   auto token = [&](int64_t u) { return p.reverse ? sg.first + sg.len - 1 - u : sg.first + u; };
   Stage<T, C, KP, THREADS, VEC> sx, sy;
   Stage<T, C, BV, THREADS, VEC> sz, sd;
-  const bool whole_v = ((int)slice + 1) * BV <= V;
   const int64_t t0 = token(sg.u0);
-  if constexpr (FULL) sx.init(x + t0 * p.x.token, p.x.token, step, 0, K);
-  sy.init(y + t0 * p.y.token, p.y.token, step, 0, K);
-  sz.init(z + t0 * p.z.token, p.z.token, step, slice * BV, V);
-  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, p.dot_view.token, step, slice * BV, V);
-  auto load = [&](int64_t u) {
-    const int rows = (int)min((int64_t)C, sg.u0 + sg.n - u);
-    if constexpr (FULL) sx.load(rows, K == KP);
-    sy.load(rows, K == KP);
-    sz.load(rows, whole_v);
-    if constexpr (DOT) sd.load(rows, whole_v);
+  if constexpr (FULL) sx.init(x + t0 * p.x.token, p.x.token, step, 0);
+  sy.init(y + t0 * p.y.token, p.y.token, step, 0);
+  sz.init(z + t0 * p.z.token, p.z.token, step, slice * BV);
+  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, p.dot_view.token, step, slice * BV);
+  auto load = [&](int rows) {
+    if constexpr (FULL) sx.load(rows, K);
+    sy.load(rows, K);
+    sz.load(rows, V - (int)slice * BV);
+    if constexpr (DOT) sd.load(rows, V - (int)slice * BV);
   };
   f32x4 O[FULL ? IT : 1];
-  // Writes the outputs of the chunk at u.  Called when the next chunk is in LDS: stores are counted with the
+  // where the next chunk's first output row goes, and bytes to the next (64 rows of at most 4096 x 256 floats)
+  const bool wide = p.out_f32 || !BF, puts = active && p.out;
+  const int32_t out_pitch = (int32_t)(p.heads * V) * (wide ? 4 : 2) * step;
+  char* out = static_cast<char*>(p.out) + (t0 * p.heads + h) * V * (wide ? 4 : 2);
+  // Writes the outputs of a chunk of n tokens.  Called when the next chunk is in LDS: stores are counted with the
   // loads, so writing before would make the wait for the next chunk's rows one for the stores too.
-  auto put = [&](int64_t u) {
-    if (!active || !p.out) return;
-    const int ln = thread_now() & (kWave - 1), g = ln >> 4, lc = ln & 15;
-    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u), c = slice * BV + wave * 16 + 4 * g;
-    // a pointer all threads share and 32 bits of each lane's own: 16 rows of at most 4096 x 256 floats
-    const int64_t row = (int64_t)p.heads * V, base = (token(u) - (p.reverse ? 15 : 0)) * row + (int64_t)h * V;
-    const uint32_t own = (uint32_t)((p.reverse ? 15 - lc : lc) * row) + c;
-    char* out = static_cast<char*>(p.out) + base * (p.out_f32 ? 4 : (int)sizeof(T));
+  auto put = [&](int n) {
+    if (!puts) return;
+    const int ln = thread_now() & (kWave - 1), g = ln >> 4, lc = ln & 15, c = slice * BV + wave * 16 + 4 * g;
+    if constexpr (VEC) {
+      const int32_t back = min((n - 1) * out_pitch, 0), span = abs((n - 1) * out_pitch), size = wide ? 4 : 2;
+      const __amdgpu_buffer_rsrc_t m = rows_at(out + back, (uint32_t)(span + V * size));
+      const uint32_t off = c < V ? (uint32_t)(lc * out_pitch - back + c * size) : kNowhere;
 #pragma unroll
-    for (int t = 0; t < IT; ++t) {
-      if (16 * t + lc >= n) continue;
-      const int64_t at = 16 * t * row * step;
-      if (p.out_f32 || !BF) {
-        float* dst = reinterpret_cast<float*>(out) + at;
-        if constexpr (VEC) {
-          if (c < V) store_global<f32x4>(dst, own * 4, O[t]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < V) dst[own + e] = O[t][e];
-        }
-      } else {
-        T* dst = reinterpret_cast<T*>(out) + at;
-        if constexpr (VEC) {
-          if (c < V) store_global<u32x2>(dst, own * 2, u32x2{pack_bf16(O[t][0], O[t][1]), pack_bf16(O[t][2], O[t][3])});
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < V) dst[own + e] = from_f32<T>(O[t][e]);
-        }
+      for (int t = 0; t < IT; ++t) {
+        const uint32_t at = off + (uint32_t)(16 * t * out_pitch);
+        if (wide) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t]), m, at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[t][0], O[t][1]), pack_bf16(O[t][2], O[t][3])}, m, at, 0, 0);
       }
+    } else {
+#pragma unroll
+      for (int t = 0; t < IT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (16 * t + lc >= n || c + e >= V) continue;
+          char* to = out + (int64_t)((16 * t + lc) * out_pitch);
+          if (wide) reinterpret_cast<float*>(to)[c + e] = O[t][e];
+          else reinterpret_cast<T*>(to)[c + e] = from_f32<T>(O[t][e]);
+        }
     }
+    out += (int64_t)(C * out_pitch);
   };
   double dr = 0.0;
   if (threadIdx.x < 2) bad_chunk[threadIdx.x] = 0;
   if constexpr (FULL)
     for (int i = threadIdx.x; i < 2 * BV; i += THREADS) bad_row[i / BV][i % BV] = C;
   __syncthreads();
-  // the loaded rows of a chunk of n tokens into LDS, z and dot into buffer `to`
-  auto fill = [&](int n, int to) {
+  // the loaded rows of a chunk into LDS, z and dot into buffer `to`
+  auto fill = [&](int to) {
     if constexpr (FULL) sx.store(xs);
     sy.store(ys);
     // A masked pair weighs 0, but 0 times an infinity is NaN: infinities and NaN in z are taken out of the
@@ -534,21 +512,22 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
     if (FULL && sz.clean(bad_row[to])) bad_chunk[to] = 1;
     sz.store(zs[FULL ? to : 0]);
     if constexpr (DOT) sd.store(dots[to]);
-    set_down(n);
   };
-  if (sg.n > 0) {
-    load(sg.u0);
-    fill((int)min((int64_t)C, sg.n), 0);
+  const uint32_t chunks = sg.n > 0 ? __builtin_amdgcn_readfirstlane((uint32_t)((sg.n + C - 1) / C)) : 0;  // (the last of `tail` tokens)
+  if (chunks) {
+    load(chunks > 1 ? C : tail);
+    fill(0);
+    set_down(chunks > 1 ? C : tail);
   }
   __syncthreads();
   // Two barriers a chunk: between the first and the second the next chunk's rows go to LDS beside the products
   // of the pairs, which are all that is left of this one (z has two buffers).
   int now = 0;
-  for (int64_t u = sg.u0; u < sg.u0 + sg.n; u += C, now ^= 1) {
-    const int n = (int)min((int64_t)C, sg.u0 + sg.n - u);
-    const bool more = u + C < sg.u0 + sg.n;
-    if (more) load(u + C);
-    if (FULL && u > sg.u0) put(u - C);
+  for (uint32_t left = chunks; left; --left, now ^= 1) {
+    const int n = left > 1 ? C : tail;
+    const bool more = left > 1;
+    if (more) load(left > 2 ? C : tail);
+    if (FULL && left < chunks) put(C);
     const bool bad = FULL && bad_chunk[now] != 0;
     if (threadIdx.x == 0) bad_chunk[now ^ 1] = 0;
     if (FULL && (int)threadIdx.x < BV) bad_row[now ^ 1][threadIdx.x] = C;
@@ -732,7 +711,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
       }
     }
     __syncthreads();  // every wave's share of the pairs is there, and x and y are read
-    if (more) fill((int)min((int64_t)C, sg.u0 + sg.n - u - C), now ^ 1);
+    if (more) {
+      fill(now ^ 1);
+      if (left == 2 && tail != C) set_down(tail);
+    }
     if (FULL && active) {
       // out^T += z^T P
       if constexpr (BF) {
@@ -786,7 +768,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
     }
     __syncthreads();
   }
-  if (FULL && sg.n > 0) put(sg.u0 + (sg.n - 1) / C * C);
+  if (FULL && chunks) put(tail);
 
   // the carry after the segment
   const int lnf = thread_now() & (kWave - 1), gf = lnf >> 4, colf = slice * BV + wave * 16 + (lnf & 15);
