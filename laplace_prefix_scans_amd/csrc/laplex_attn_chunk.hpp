@@ -214,6 +214,7 @@ struct Stage {
       bad = top >= 0x7F800000u;
     }
     if (!bad) return false;
+    const int t = thread_now();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       T e[E];
@@ -222,7 +223,7 @@ struct Stage {
       for (int j = 0; j < E; ++j)
         if (bits_nonfinite(__float_as_uint(to_f32(e[j])))) {
           e[j] = T(0.f);
-          atomicMin(first + threadIdx.x % (P / E) * E + j, (int)threadIdx.x / (P / E) + i * RPI);
+          atomicMin(first + t % (P / E) * E + j, t / (P / E) + i * RPI);
         }
       __builtin_memcpy(&v[i], e, 16);
     }
@@ -307,7 +308,9 @@ __device__ __forceinline__ const T& lds_at(const void* tile, uint32_t bytes) {
 // Row operand of a bf16 product over 32 channels: those of the carry's tiles 2k and 2k + 1 in lane group g,
 // 32 k + 4 g + {0..3} and 16 on, so that the carry's registers are the other operand as they are.
 __device__ __forceinline__ bf16x8 read_row(const __bf16* tile, uint32_t bytes) {
-  struct { uint2 a, b; } v = {lds_at<uint2>(tile, bytes), lds_at<uint2>(tile, bytes ^ 32)};
+  // (volatile: the compiler would join the reads of two row tiles into one and move the halves about after it)
+  typedef const volatile __attribute__((address_space(3))) u32x2* Lds;
+  struct { u32x2 a, b; } v = {*(Lds)(reinterpret_cast<const char*>(tile) + bytes), *(Lds)(reinterpret_cast<const char*>(tile) + (bytes ^ 32))};
   return __builtin_bit_cast(bf16x8, v);
 }
 // Transposed (bf16): a group of 16 lanes reads 4 rows x 16 columns, each lane 4 columns of one row, and gets
@@ -439,11 +442,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   const double wc = uniform(exp(-(double)rate * (double)C)), wtail = uniform(exp(-(double)rate * (double)tail));
   double owed = 1.0;
   auto set_down = [&](int n) {
-    if (threadIdx.x < C) {
-      const int j = threadIdx.x, lag = n - 1 - j;
-      down[j] = lag >= 0 ? p.c_add * decay(-rate * (float)(lag + 1 - lead)) : 0.f;
-      if constexpr (RATE) downlag[j] = lag >= 0 ? (float)lag * down[j] : 0.f;
-    }
+    const int j = thread_now(), lag = n - 1 - j;
+    if (j >= C) return;
+    down[j] = lag >= 0 ? p.c_add * decay(-rate * (float)(lag + 1 - lead)) : 0.f;
+    if constexpr (RATE) downlag[j] = lag >= 0 ? (float)lag * down[j] : 0.f;
   };
 
   const T* x = static_cast<const T*>(p.x.p) + (int64_t)(h / p.x.div) * p.x.head;
@@ -529,9 +531,9 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
     if (more) load(left > 2 ? C : tail);
     if (FULL && left < chunks) put(C);
     const bool bad = FULL && bad_chunk[now] != 0;
-    if (threadIdx.x == 0) bad_chunk[now ^ 1] = 0;
-    if (FULL && (int)threadIdx.x < BV) bad_row[now ^ 1][threadIdx.x] = C;
-    const int ln = thread_now() & (kWave - 1);
+    const int tid = thread_now(), ln = tid & (kWave - 1);
+    if (tid == 0) bad_chunk[now ^ 1] = 0;
+    if (FULL && tid < BV) bad_row[now ^ 1][tid] = C;
     const int g = ln >> 4, lc = ln & 15;
 
     // byte offsets of this lane's operands
@@ -547,9 +549,18 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
         for (int tile = wave; tile < IT * (IT + 1) / 2; tile += NW) {
           const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
           f32x4 P = {};
+          bf16x8 f[2][2];
+          auto read = [&](int ks) {
+            f[ks & 1][0] = read_row(ys + 16 * jt * KP, row_at ^ (ks << 6));
+            f[ks & 1][1] = read_row(xs + 16 * it * KP, row_at ^ (ks << 6));
+          };
+          read(0);
 #pragma unroll
-          for (int ks = 0; ks < KP / 32; ++ks)
-            P = mfma(read_row(ys + 16 * jt * KP, row_at ^ (ks << 6)), read_row(xs + 16 * it * KP, row_at ^ (ks << 6)), P);
+          for (int ks = 0; ks < KP / 32; ++ks) {
+            if (ks + 1 < KP / 32) read(ks + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            P = mfma(f[ks & 1][0], f[ks & 1][1], P);
+          }
           const int lag0 = 16 * (it - jt) + lc - 4 * g;
           float pv[4], pd[4];
 #pragma unroll
@@ -592,22 +603,39 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
       if (active) {
         // out^T = S^T x^T (rows V, columns i)
         if constexpr (BF) {
+          constexpr int STEPS = KP / 32 * (IT / 2);
+          bf16x8 xf[2][2];
+          auto read = [&](int i) {
 #pragma unroll
-          for (int ks = 0; ks < KP / 32; ++ks) {
-            // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
-            const Parts2 s2 = split2(S[2 * ks], S[2 * ks + 1]);
-            Parts3 d3;  // (its result is a float32 sum: three)
-            if constexpr (RATE) d3 = split3(D[2 * ks], D[2 * ks + 1]);
+            for (int e = 0; e < 2; ++e) xf[i & 1][e] = read_row(xs + 16 * (i % (IT / 2) * 2 + e) * KP, row_at ^ (i / (IT / 2) << 6));
+          };
+          Parts2 s2;
+          Parts3 d3;
+          read(0);
 #pragma unroll
-            for (int t = 0; t < IT; ++t) {
-              const bf16x8 xf = read_row(xs + 16 * t * KP, row_at ^ (ks << 6));
-              O[t] = mfma(s2.hi, xf, ks ? O[t] : f32x4{});
-              O[t] = mfma(s2.lo, xf, O[t]);
-              if constexpr (RATE) {
-                OD[t] = mfma(d3.hi, xf, ks ? OD[t] : f32x4{});
-                OD[t] = mfma(d3.lo, xf, OD[t]);
-                OD[t] = mfma(d3.lo2, xf, OD[t]);
-              }
+          for (int i = 0; i < STEPS; ++i) {
+            const int ks = i / (IT / 2), t = i % (IT / 2) * 2;
+            if (i + 1 < STEPS) read(i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            if (t == 0) {
+              // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
+              s2 = split2(S[2 * ks], S[2 * ks + 1]);
+              // (its result is a float32 sum: three)
+              if constexpr (RATE) d3 = split3(D[2 * ks], D[2 * ks + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) O[t + e] = mfma(s2.hi, xf[i & 1][e], ks ? O[t + e] : f32x4{});
+            if constexpr (RATE) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) OD[t + e] = mfma(d3.hi, xf[i & 1][e], ks ? OD[t + e] : f32x4{});
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) O[t + e] = mfma(s2.lo, xf[i & 1][e], O[t + e]);
+            if constexpr (RATE) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) OD[t + e] = mfma(d3.lo, xf[i & 1][e], OD[t + e]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) OD[t + e] = mfma(d3.lo2, xf[i & 1][e], OD[t + e]);
             }
           }
         } else {
@@ -640,49 +668,62 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
       const double exact = uniform((more ? wc : wtail) * owed);
       const float w = (float)exact;
       // (a subnormal w has no reciprocal, and nothing that a later chunk could show)
-      owed = w >= 0x1p-126f ? 1.0 + (double)((float)(exact - (double)w) * __builtin_amdgcn_rcpf(w)) : 1.0;
+      owed = __builtin_amdgcn_readfirstlane(__float_as_uint(w)) >= 0x00800000u ? 1.0 + (double)((float)(exact - (double)w) * __builtin_amdgcn_rcpf(w)) : 1.0;
       LAPLEX_EACH(t, KT, r) {
         if constexpr (RATE) D[t][r] = w * fmaf((float)n, S[t][r], D[t][r]);  // the lag-weighted carry ahead of the other
         S[t][r] *= w;
       }
       if constexpr (BF) {
+        bf16x8 zf, yt[2][2];
+        auto read = [&](int i) {
 #pragma unroll
-        for (int s = 0; s < C / 32; ++s) {
-          const bf16x8 zf = read_tr<BV>(z + 32 * s * BV, z_at);
-          // z weighted by its decay to the chunk's end, as bfloat16 parts: three where the carry goes out as float32
-          // or into the rate's gradient (it keeps float32's bits), two where it only enters bfloat16 results
-          auto weighted = [&](const float* w, f32x4& lo, f32x4& hi) {
-            lo = *reinterpret_cast<const f32x4*>(w + 32 * s + 4 * g);
-            hi = *reinterpret_cast<const f32x4*>(w + 32 * s + 16 + 4 * g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) lo[e] *= (float)zf[e], hi[e] *= (float)zf[4 + e];
-          };
-          f32x4 z0, z1;
-          weighted(down, z0, z1);
-          Parts3 z3;
-          if constexpr (FINE || RATE) {
-            z3 = split3(z0, z1);
-          } else {
-            const Parts2 z2 = split2(z0, z1);
-            z3.hi = z2.hi, z3.lo = z2.lo;
+          for (int e = 0; e < 2; ++e) {
+            const int t = i % (KT / 2) * 2 + e;
+            yt[i & 1][e] = read_tr<KP>(ys + 32 * (i / (KT / 2)) * KP, y_at ^ (t >> 1 << 6 | (t & 1) << 5));
           }
-          Parts3 l3;
-          if constexpr (RATE) {
-            weighted(downlag, z0, z1);
-            l3 = split3(z0, z1);
-          }
+          if (i % (KT / 2) == 0) zf = read_tr<BV>(z + 32 * (i / (KT / 2)) * BV, z_at);
+        };
+        read(0);
+        Parts3 z3, l3;
 #pragma unroll
-          for (int t = 0; t < KT; ++t) {
-            const bf16x8 yt = read_tr<KP>(ys + 32 * s * KP, y_at ^ (t >> 1 << 6 | (t & 1) << 5));
-            S[t] = mfma(yt, z3.hi, S[t]);
-            S[t] = mfma(yt, z3.lo, S[t]);
-            if constexpr (FINE || RATE) S[t] = mfma(yt, z3.lo2, S[t]);
+        for (int i = 0; i < C / 32 * (KT / 2); ++i) {
+          const int s = i / (KT / 2), t = i % (KT / 2) * 2;
+          if (i + 1 < C / 32 * (KT / 2)) read(i + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          if (t == 0) {
+            // z weighted by its decay to the chunk's end, as bfloat16 parts: three where the carry goes out as float32
+            // or into the rate's gradient (it keeps float32's bits), two where it only enters bfloat16 results
+            auto weighted = [&](const float* w, f32x4& lo, f32x4& hi) {
+              lo = *reinterpret_cast<const f32x4*>(w + 32 * s + 4 * g);
+              hi = *reinterpret_cast<const f32x4*>(w + 32 * s + 16 + 4 * g);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) lo[e] *= (float)zf[e], hi[e] *= (float)zf[4 + e];
+            };
+            f32x4 z0, z1;
+            weighted(down, z0, z1);
+            if constexpr (FINE || RATE) {
+              z3 = split3(z0, z1);
+            } else {
+              const Parts2 z2 = split2(z0, z1);
+              z3.hi = z2.hi, z3.lo = z2.lo;
+            }
             if constexpr (RATE) {
-              D[t] = mfma(yt, l3.hi, D[t]);
-              D[t] = mfma(yt, l3.lo, D[t]);
-              D[t] = mfma(yt, l3.lo2, D[t]);
+              weighted(downlag, z0, z1);
+              l3 = split3(z0, z1);
             }
           }
+          auto add = [&](f32x4 (&s)[KT], const Parts3& p) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[t + e] = mfma(yt[i & 1][e], p.hi, s[t + e]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[t + e] = mfma(yt[i & 1][e], p.lo, s[t + e]);
+            if constexpr (FINE || RATE) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) s[t + e] = mfma(yt[i & 1][e], p.lo2, s[t + e]);
+            }
+          };
+          add(S, z3);
+          if constexpr (RATE) add(D, l3);
         }
       } else {
         f32x4 zw[C / 16], zl[C / 16];
