@@ -70,23 +70,28 @@ static int64_t attn_seg_len(uint32_t heads, uint32_t K, uint32_t V, uint64_t tok
   len = (len + 63) / 64 * 64;
   return (int64_t)(len + len / 2 < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
 }
-static AttnPlan attn_plan(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   AttnPlan q;
   q.kp = K <= 64 ? 64 : K <= 128 ? 128 : 256;
-  q.nw = V <= 64 && K <= 64 ? 4 : 8;
-  q.slices = (V + 16 * q.nw - 1) / (16 * q.nw);
   q.seg_len = attn_seg_len(heads, K, V, tokens, rate);
+  // V of at most 64 needs four waves (16384 tokens x 16 heads, 128 x 64, forward and backward: 498 us with eight, 469).
+  // Where blocks of 128 columns would leave a good part of the 256 CUs idle, blocks of 64 share a chunk's work out
+  // among twice as many (131 tokens x 4 heads, 80 x 96, float: 34 -> 25 us; 2048 x 8 heads, 128 x 128, bfloat16, 136
+  // blocks, forward and backward: 182 -> 161; at 264 blocks 209 -> 223, at 250 without backward 23 -> 26.5).
+  const uint64_t blocks = (tokens / q.seg_len + seqs) * heads * ((V + 127) / 128);
+  q.nw = q.kp <= 128 && (V <= 64 || blocks <= 160) ? 4 : 8;
+  q.slices = (V + 16 * q.nw - 1) / (16 * q.nw);
   q.split = (uint64_t)q.seg_len < tokens;
   q.bounds = q.split ? tokens / q.seg_len + 1 : 0;
   return q;
 }
 
 size_t attn_pass_bytes(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
-  const AttnPlan q = attn_plan(heads, K, V, tokens, rate);
+  const AttnPlan q = attn_plan(1, heads, K, V, tokens, rate);
   return (size_t)q.bounds * heads * K * V * 4 * (rate ? 2 : 1);
 }
 uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets) {
-  const AttnPlan q = attn_plan(heads, K, V, tokens, true);
+  const AttnPlan q = attn_plan(seqs, heads, K, V, tokens, true);
   return attn_slots({offsets, tokens, seqs, q.seg_len}) * q.slices;
 }
 
@@ -98,7 +103,7 @@ static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   const bool rate = p.drate_part != nullptr, bf = p.dtype == LAPLEX_BF16;
   const size_t e = bf ? 2 : 4;
-  const AttnPlan q = attn_plan(p.heads, p.K, p.V, p.tokens, rate);
+  const AttnPlan q = attn_plan(p.seqs, p.heads, p.K, p.V, p.tokens, rate);
   AttnChunkArgs a{};
   a.p = p;
   a.g = {p.offsets, p.tokens, p.seqs, q.seg_len};

@@ -347,7 +347,7 @@ __device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) { return __buil
 // 32 columns in half as many waves took as long without the rate's gradient, and a quarter longer with it.
 // FINE: the carry goes out as float32 (otherwise it only enters results of type T).
 template <typename T, int KP, int NW, bool FULL, bool RATE, bool FINE, bool VEC>
-__global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_chunk(AttnChunkArgs a) {
+__global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW == 4) ? 2 : 4) void k_attn_chunk(AttnChunkArgs a) {
   constexpr int C = kAttnC<T>, KT = KP / 16, BV = 16 * NW, THREADS = NW * kWave, IT = C / 16;
   constexpr bool BF = sizeof(T) == 2, DOT = FULL && RATE;
   constexpr int WK = KP / 16 < 4 ? KP / 16 : 4;    // float: waves that share the channels of P^T
@@ -851,7 +851,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE ? 2 : 4) void k_attn_
   }
 }
 
-// kp: K rounded up to 64, 128 or 256; nw: waves per block, 16 columns each (8, or 4 where K and V are at most 64)
+// kp: K rounded up to 64, 128 or 256; nw: waves per block, 16 columns each (8, or 4 where V is at most 64 or blocks are few)
 template <typename T, int KP, int NW, bool VEC>
 void attn_chunk_launch_at(const AttnChunkArgs& a, bool full, bool rate, hipStream_t s) {
   const uint64_t units = a.slots * (a.p.heads / a.group);
@@ -871,6 +871,7 @@ template <typename T, bool VEC>
 void attn_chunk_launch(const AttnChunkArgs& a, int kp, int nw, bool full, bool rate, hipStream_t s) {
   if (kp == 64 && nw == 4) attn_chunk_launch_at<T, 64, 4, VEC>(a, full, rate, s);
   else if (kp == 64) attn_chunk_launch_at<T, 64, 8, VEC>(a, full, rate, s);
+  else if (kp == 128 && nw == 4) attn_chunk_launch_at<T, 128, 4, VEC>(a, full, rate, s);
   else if (kp == 128) attn_chunk_launch_at<T, 128, 8, VEC>(a, full, rate, s);
   else attn_chunk_launch_at<T, 256, 8, VEC>(a, full, rate, s);
 }
