@@ -21,6 +21,9 @@ constexpr uint32_t kNormBlocks = 2048;  // 256-thread blocks of a forward pass (
 constexpr uint32_t kNormParts = 512;  // at most so many partials of the weight gradient (two 256-thread blocks a CU)
 
 // ------------------------------------------------------------------ rows in registers
+// VEC: every row begins at a multiple of 16 bytes and has whole 16-byte pieces.  Without, the pieces are the same
+// ones, read and written at the alignment of T but for the row's last: columns keep their threads, so that a row's
+// sums, and with them its results, are the same bits whatever its alignment.
 template <typename T, int TPR, int VPT, bool VEC>
 struct NormRow {
   static constexpr int E = 16 / sizeof(T), N = VPT * E;
@@ -28,7 +31,7 @@ struct NormRow {
   T e[N];
   // column of element k of thread t of the row
   static __device__ __forceinline__ uint32_t col(int k, int t) {
-    return VEC ? (uint32_t)((k / E * TPR + t) * E + k % E) : (uint32_t)(k * TPR + t);
+    return (uint32_t)((k / E * TPR + t) * E + k % E);
   }
   __device__ __forceinline__ void load(const T* p, uint32_t width, int t) {
     if constexpr (VEC) {
@@ -40,7 +43,15 @@ struct NormRow {
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) e[k] = col(k, t) < width ? p[col(k, t)] : T(0.f);
+      for (int i = 0; i < VPT; ++i) {
+        const uint32_t c = col(i * E, t);
+        if (c + E <= width) {
+          __builtin_memcpy(e + i * E, p + c, 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) e[i * E + j] = c + j < width ? p[c + j] : T(0.f);
+        }
+      }
     }
   }
   __device__ __forceinline__ void store(T* p, uint32_t width, int t) const {
@@ -53,8 +64,16 @@ struct NormRow {
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (col(k, t) < width) p[col(k, t)] = e[k];
+      for (int i = 0; i < VPT; ++i) {
+        const uint32_t c = col(i * E, t);
+        if (c + E <= width) {
+          __builtin_memcpy(p + c, e + i * E, 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (c + j < width) p[c + j] = e[i * E + j];
+        }
+      }
     }
   }
 };
