@@ -97,14 +97,16 @@ __global__ void k_embed_keys(const void* __restrict__ ids, int id_bytes, uint64_
   if (t < tokens) keys[t] = key_of(load_id(ids, id_bytes, t), vocab, bits);
 }
 
-// Stable sort of up to kEmbedSmall tokens by key in one launch: block b reads
+// Stable sort of a tile of up to kEmbedSmall tokens by key in one launch: block b reads
 // all of them, takes those of the key range b (range kTops: outside the table)
 // in order, counts those of the ranges before it -- where its part of the
 // result starts -- and sorts its own in LDS by the remaining bits (stable LSD
 // passes of 6), and for vocabularies up to 2^kFindBits writes its keys' first
-// positions too.  No block waits for another.  16384 tokens: 9 us; sorted by one
-// block 31 us, by the general sort's eight launches about as long.
-constexpr int kFindBits = 18;
+// positions too.  No block waits for another.  A whole gradient over 16384
+// tokens (65536 x 128) takes 36 us with the lookup, 66 with the general sort's
+// nine launches in place of this one; over 4096 tokens (257 x 513) 24 and 51.
+// More tokens are sorted in tiles of kEmbedSmall and joined (k_embed_merge).
+constexpr int kFindBits = 18, kEmbedTiles = 8;
 constexpr int kEmbedSmall = 16384, kSortThreads = 1024, kSortWaves = kSortThreads / kWave, kSortBits = 6, kSortBins = 1 << kSortBits;
 
 // lanes whose digit is this lane's
@@ -126,9 +128,13 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 template <int E>
-__global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restrict__ ids, int id_bytes, uint32_t tokens, uint32_t vocab,
+__global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restrict__ ids, int id_bytes, uint32_t all, uint32_t vocab,
                                                              int bits, uint32_t* __restrict__ keys, uint32_t* __restrict__ perm,
                                                              uint32_t* __restrict__ starts) {
+  const uint32_t t0 = blockIdx.y * kEmbedSmall, tokens = min(all - t0, (uint32_t)kEmbedSmall);
+  keys += t0;
+  perm += t0;
+  if (starts) starts += (uint64_t)blockIdx.y * ((1u << bits) + 1);
   __shared__ uint32_t sk[E * kSortThreads];
   __shared__ uint16_t sp[E * kSortThreads];
   __shared__ uint32_t count[kSortWaves][kSortBins];
@@ -140,7 +146,7 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restr
 #pragma unroll
   for (int e = 0; e < E; ++e) {  // wave w reads [w * 64 E, (w + 1) * 64 E)
     const uint32_t at = (wave * E + e) * kWave + lane;
-    k[e] = at < tokens ? key_of(load_id(ids, id_bytes, at), vocab, bits) : 0xFFFFFFFFu;
+    k[e] = at < tokens ? key_of(load_id(ids, id_bytes, (uint64_t)t0 + at), vocab, bits) : 0xFFFFFFFFu;
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -217,7 +223,7 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restr
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < m; i += kSortThreads) {
     keys[start + i] = sk[i];
-    perm[start + i] = sp[i];
+    perm[start + i] = t0 + sp[i];
   }
   if (!starts) return;
   // the first position of each key of the range
@@ -231,6 +237,35 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(const void* __restr
     }
     starts[k0 + i] = start + lo;
   }
+}
+
+// Joins sorted tiles: an element's place is its place among its tile's equal keys, behind all smaller keys and the
+// equal ones of earlier tiles.  The tiles' starts give every term, so an element needs no search; the last blocks
+// add them up to the starts of the whole.
+__global__ __launch_bounds__(256) void k_embed_merge(const uint32_t* __restrict__ tile_keys, const uint32_t* __restrict__ tile_perm,
+                                                     const uint32_t* __restrict__ tile_starts, uint32_t tokens, uint32_t tiles, int bits,
+                                                     uint32_t* __restrict__ keys, uint32_t* __restrict__ perm, uint32_t* __restrict__ starts) {
+  const uint32_t n = 1u << bits, blocks = (tokens + 255) / 256;
+  if (blockIdx.x >= blocks) {
+    const uint32_t u = (blockIdx.x - blocks) * 256 + threadIdx.x;
+    if (u > n) return;
+    uint32_t s = 0;
+    for (uint32_t j = 0; j < tiles; ++j) s += tile_starts[(uint64_t)j * (n + 1) + u];
+    starts[u] = s;
+    return;
+  }
+  const uint32_t p = blockIdx.x * 256 + threadIdx.x;
+  if (p >= tokens) return;
+  const uint32_t tile = p / kEmbedSmall, u = tile_keys[p];
+  uint32_t to = p % kEmbedSmall;
+  for (uint32_t j = 0; j < tiles; ++j) {
+    const uint32_t* st = tile_starts + (uint64_t)j * (n + 1) + u;
+    const uint32_t first = st[0];
+    if (j < tile) to += u < n ? st[1] : min(tokens - j * kEmbedSmall, (uint32_t)kEmbedSmall);  // all up to its equal keys
+    else if (j > tile) to += first;
+  }
+  keys[to] = u;
+  perm[to] = tile_perm[p];
 }
 
 // starts[u] = first sorted position whose key is >= u, for u = 0 .. 2^bits.
@@ -376,6 +411,12 @@ hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, 
 
 uint32_t embed_chunk(uint64_t tokens) { return tokens <= 32768 ? 32 : 64; }
 uint64_t embed_starts(uint32_t vocab) { return (1ull << key_bits(vocab)) + 1; }
+// The general sort takes seven to nine launches whatever the size; tiles take two, and reads of every tile's starts
+// by every token (lookup and gradient, 49625 tokens, 58298 x 136: 82 -> 53 us; 131072 tokens, 65536 x 64: 88 -> 74).
+uint32_t embed_tiles(uint64_t tokens, uint32_t vocab) {
+  return tokens > (uint64_t)kEmbedSmall && tokens <= kEmbedTiles * (uint64_t)kEmbedSmall && key_bits(vocab) <= kFindBits
+             ? (uint32_t)((tokens + kEmbedSmall - 1) / kEmbedSmall) : 0;
+}
 uint64_t embed_part_floats(uint64_t tokens, uint32_t width) {
   const uint32_t c = embed_chunk(tokens);
   return (tokens + c - 1) / c * 2 * width;
@@ -401,8 +442,17 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s) {
   hipError_t e;
   const int bits = key_bits(vocab);
-  uint32_t* starts = tokens && tokens <= (uint64_t)kEmbedSmall && bits <= kFindBits ? w.starts : nullptr;  // found by the sort
-  if (tokens && tokens <= (uint64_t)kEmbedSmall) {
+  const uint32_t tiles = embed_tiles(tokens, vocab);
+  uint32_t* starts = tiles || (tokens && tokens <= (uint64_t)kEmbedSmall && bits <= kFindBits) ? w.starts : nullptr;  // found by the sort
+  if (tiles) {
+    const uint32_t n = (uint32_t)tokens;
+    LAPLEX_LAUNCH("k_embed_sort", tokens, s,
+                  k_embed_sort<16><<<dim3(kTops + 1, tiles), kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys, w.tile_perm, w.tile_starts));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    LAPLEX_LAUNCH("k_embed_merge", tokens, s,
+                  k_embed_merge<<<(n + 255) / 256 + (1u << bits) / 256 + 1, 256, 0, s>>>(w.keys, w.tile_perm, w.tile_starts, n, tiles, bits, w.keys_s, w.perm, starts));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else if (tokens && tokens <= (uint64_t)kEmbedSmall) {
     LAPLEX_LAUNCH("k_embed_sort", tokens, s, {
       const uint32_t n = (uint32_t)tokens;
       if (n <= kSortThreads) k_embed_sort<1><<<kTops + 1, kSortThreads, 0, s>>>(ids, id_bytes, n, vocab, bits, w.keys_s, w.perm, starts);

@@ -84,8 +84,11 @@ struct EmbedWorkspace {
   uint32_t* perm;    // tokens in that order
   uint32_t* starts;  // first sorted position of each key (embed_starts)
   float* part;       // partial rows (embed_part_floats)
+  // where the tokens are sorted in tiles first (embed_tiles): each tile's tokens and starts (its keys are in `keys`)
+  uint32_t *tile_perm, *tile_starts;
 };
 uint64_t embed_starts(uint32_t vocab);
+uint32_t embed_tiles(uint64_t tokens, uint32_t vocab);
 uint64_t embed_part_floats(uint64_t tokens, uint32_t width);
 hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s);

@@ -311,6 +311,9 @@ EmbedWorkspace carve_embed(void* ws, uint64_t tokens, uint32_t vocab, uint32_t w
   w.perm = c.take<uint32_t>(tokens * 4);
   w.starts = c.take<uint32_t>(embed_starts(vocab) * 4);
   w.part = c.take<float>(embed_part_floats(tokens, width) * 4);
+  const uint32_t tiles = embed_tiles(tokens, vocab);
+  w.tile_perm = c.take<uint32_t>(tiles ? tokens * 4 : 0);
+  w.tile_starts = c.take<uint32_t>(tiles * embed_starts(vocab) * 4);
   *total = (c.off + 255) & ~size_t(255);
   return w;
 }

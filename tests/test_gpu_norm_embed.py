@@ -179,6 +179,22 @@ def test_embedding(shape, kind, dt, wide):
     near("dtable", host(grad.float()), want, env, tokens, out == torch.bfloat16)
 
 
+@pytest.mark.parametrize("shape", [(16385, 300, 33), (40000, 1, 8), (70001, 5000, 40), (131072, 250000, 5), (131073, 4000, 17),
+                                   (20000, 300000, 9)], ids=str)
+@pytest.mark.parametrize("kind", ["zipf", "uniform", "same", "outside"])
+def test_embedding_gradient_of_many_tokens(shape, kind):
+    """Tokens that are sorted in tiles, a whole and a broken last tile, and more or larger ids than tiles are for."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    tokens, vocab, width = shape
+    print("embed many", shape, kind, flush=True)
+    ids = ids_of(kind, tokens, vocab, tokens)
+    dy = torch.randn(tokens, width, generator=torch.Generator().manual_seed(tokens))
+    grad = lp.laplex_embedding_backward(torch.from_numpy(ids).to(torch.int64).cuda(), dy.cuda(), vocab, scale=0.5)
+    want = ref.embedding_backward(ids, dy.numpy(), vocab, 0.5)
+    near("dtable", host(grad), want, ref.embedding_backward(ids, np.abs(dy.numpy()), vocab, 0.5), tokens)
+
+
 def test_embedding_gradient_against_differences():
     """<dy, y> is linear in the table: a difference with a step of 1 has rounding errors only."""
     import torch
