@@ -433,7 +433,7 @@ static void embed_grad_launch(EmbedGrad g, const void* dy, void* dtable, hipStre
   const dim3 grid((unsigned)(g.chunk_blocks + zero_blocks), (pieces + g.lanes - 1) / g.lanes);
   k_embed_grad<T, O, E><<<grid, kEmbedBlock, 0, s>>>(g, (const T*)dy, (O*)dtable);
   if (chunks > 1) {
-    const dim3 jgrid((unsigned)(chunks - 1), std::min<uint32_t>((g.width + 63) / 64, 8));
+    const dim3 jgrid((unsigned)(chunks - 1), std::min<uint32_t>((g.width + 63) / 64, 32));
     k_embed_join<O><<<jgrid, kEmbedBlock, 0, s>>>(g, (O*)dtable);
   }
 }
