@@ -341,7 +341,8 @@ size_t laplex_decay_attn_workspace_bytes(int pass, const laplex_attn_shape* shap
  * dk x dv floats); state_out: NULL or S after each sequence's last token (same
  * shape; an empty sequence's is its state_in).  o: tokens x heads x dv,
  * contiguous.  A non-finite value in token j reaches o_i only for i >= j of its
- * own sequence, where it gives non-finite outputs.
+ * own sequence, where it gives non-finite outputs (or, where its weight has
+ * decayed to zero, none).
  * ws: laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_FORWARD, shape) bytes. */
 laplex_status laplex_decay_attn(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
                                 const float* state_in, float* state_out, void* o, void* ws, size_t ws_bytes,

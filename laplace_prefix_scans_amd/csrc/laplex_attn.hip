@@ -6,7 +6,9 @@ namespace laplex {
 
 // Turns the segments' own final states into the states before each segment,
 // S_k+1 = w(L) S_k + T_k, in place; thread per element.  With lag-weighted
-// states, D_k+1 = w(L) (D_k + L S_k) + E_k.
+// states, D_k+1 = w(L) (D_k + L S_k) + E_k.  One read and one write of the states: bound by HBM (512 boundaries of
+// 128 x 128 floats, 67 MB: 14 us, 4.8 TB/s).  Joined in the next pass's first lines instead, each segment reads
+// all of its predecessors: 100 us of that pass became 134.
 template <bool RATE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
   __shared__ AttnDecay sw;
@@ -64,7 +66,8 @@ struct AttnPlan {
 static int64_t attn_seg_len(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   const uint32_t wide = std::max(K, V), slices = wide > 128 ? 2 : 1;
   // Blocks that run at once: 256 CUs with two of eight waves or four of four; half with the lag-weighted carry.
-  // (65536 tokens x 8 heads, 128 x 128: 248 us; with half as many blocks 331, twice 279, four times 339.)
+  // (65536 tokens x 8 heads, 128 x 128: 234 us; with half as many blocks 274, with twice as many 263.  16384 tokens
+  // x 16 heads forward and backward: 609, 680, 729.)
   const uint64_t blocks = (wide <= 64 ? 1024 : 512) / (rate ? 2 : 1);
   uint64_t len = std::max<uint64_t>(kAttnMinSeg, tokens * heads * slices / blocks);
   len = (len + 63) / 64 * 64;
@@ -140,7 +143,7 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   return run("k_attn_chunk", true);
 }
 
-// drate_h = the sum of its partials in a fixed order
+// drate_h = the sum of its partials in a fixed order (a launch's latency: 5 us)
 __global__ __launch_bounds__(256) void k_attn_drate(const double* __restrict__ part, uint64_t parts, uint32_t heads,
                                                     float* __restrict__ drate) {
   __shared__ double sh[256];
