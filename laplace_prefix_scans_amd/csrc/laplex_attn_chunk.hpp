@@ -418,6 +418,28 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
       s[t][r] = row < K ? v : 0.f;
     }
   };
+  const T* x = static_cast<const T*>(p.x.p) + (int64_t)(h / p.x.div) * p.x.head;
+  const T* y = static_cast<const T*>(p.y.p) + (int64_t)(h / p.y.div) * p.y.head;
+  const T* z = static_cast<const T*>(p.z.p) + (int64_t)(h / p.z.div) * p.z.head;
+  const T* dot = DOT ? static_cast<const T*>(p.dot) + (int64_t)(h / p.dot_view.div) * p.dot_view.head : nullptr;
+  const int step = p.reverse ? -1 : 1;
+  auto token = [&](int64_t u) { return p.reverse ? sg.first + sg.len - 1 - u : sg.first + u; };
+  Stage<T, C, KP, THREADS, VEC> sx, sy;
+  Stage<T, C, BV, THREADS, VEC> sz, sd;
+  const int64_t t0 = token(sg.u0);
+  if constexpr (FULL) sx.init(x + t0 * p.x.token, p.x.token, step, 0);
+  sy.init(y + t0 * p.y.token, p.y.token, step, 0);
+  sz.init(z + t0 * p.z.token, p.z.token, step, slice * BV);
+  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, p.dot_view.token, step, slice * BV);
+  auto load = [&](int rows) {
+    if constexpr (FULL) sx.load(rows, K);
+    sy.load(rows, K);
+    sz.load(rows, V - (int)slice * BV);
+    if constexpr (DOT) sd.load(rows, V - (int)slice * BV);
+  };
+  const int tail = __builtin_amdgcn_readfirstlane((int)((sg.n - 1) % C) + 1);  // tokens of the last chunk
+  const uint32_t chunks = sg.n > 0 ? __builtin_amdgcn_readfirstlane((uint32_t)((sg.n + C - 1) / C)) : 0;  // (the last of `tail` tokens)
+  if (chunks) load(chunks > 1 ? C : tail);  // on their way while the states are read and the weights formed
   f32x4 S[KT], D[RATE ? KT : 1];
 #pragma unroll
   for (int t = 0; t < KT; ++t) {
@@ -444,7 +466,6 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
   // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
   // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
   // so far back to the exact one.
-  const int tail = __builtin_amdgcn_readfirstlane((int)((sg.n - 1) % C) + 1);  // tokens of the last chunk
   const double wc = uniform(exp(-(double)rate * (double)C)), wtail = uniform(exp(-(double)rate * (double)tail));
   double owed = 1.0;
   auto set_down = [&](int n) {
@@ -454,25 +475,6 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
     if constexpr (RATE) downlag[j] = lag >= 0 ? (float)lag * down[j] : 0.f;
   };
 
-  const T* x = static_cast<const T*>(p.x.p) + (int64_t)(h / p.x.div) * p.x.head;
-  const T* y = static_cast<const T*>(p.y.p) + (int64_t)(h / p.y.div) * p.y.head;
-  const T* z = static_cast<const T*>(p.z.p) + (int64_t)(h / p.z.div) * p.z.head;
-  const T* dot = DOT ? static_cast<const T*>(p.dot) + (int64_t)(h / p.dot_view.div) * p.dot_view.head : nullptr;
-  const int step = p.reverse ? -1 : 1;
-  auto token = [&](int64_t u) { return p.reverse ? sg.first + sg.len - 1 - u : sg.first + u; };
-  Stage<T, C, KP, THREADS, VEC> sx, sy;
-  Stage<T, C, BV, THREADS, VEC> sz, sd;
-  const int64_t t0 = token(sg.u0);
-  if constexpr (FULL) sx.init(x + t0 * p.x.token, p.x.token, step, 0);
-  sy.init(y + t0 * p.y.token, p.y.token, step, 0);
-  sz.init(z + t0 * p.z.token, p.z.token, step, slice * BV);
-  if constexpr (DOT) sd.init(dot + t0 * p.dot_view.token, p.dot_view.token, step, slice * BV);
-  auto load = [&](int rows) {
-    if constexpr (FULL) sx.load(rows, K);
-    sy.load(rows, K);
-    sz.load(rows, V - (int)slice * BV);
-    if constexpr (DOT) sd.load(rows, V - (int)slice * BV);
-  };
   f32x4 O[FULL ? IT : 1];
   // where the next chunk's first output row goes, and bytes to the next (64 rows of at most 4096 x 256 floats)
   const bool wide = p.out_f32 || !BF, puts = active && p.out;
@@ -521,9 +523,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
     sz.store(zs[FULL ? to : 0]);
     if constexpr (DOT) sd.store(dots[to]);
   };
-  const uint32_t chunks = sg.n > 0 ? __builtin_amdgcn_readfirstlane((uint32_t)((sg.n + C - 1) / C)) : 0;  // (the last of `tail` tokens)
   if (chunks) {
-    load(chunks > 1 ? C : tail);
     fill(0);
     set_down(chunks > 1 ? C : tail);
   }
