@@ -54,7 +54,6 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnChunkArgs a) {
 }
 
 // ------------------------------------------------------------------ launches
-constexpr uint64_t kAttnMinSeg = 128;
 struct AttnPlan {
   int kp, nw;
   uint32_t slices;
@@ -63,20 +62,22 @@ struct AttnPlan {
   bool split;
 };
 // The split depends on K and V alike, so that a pass and the one with K and V exchanged share their segments.
-static int64_t attn_seg_len(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+static int64_t attn_seg_len(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   const uint32_t wide = std::max(K, V), slices = wide > 128 ? 2 : 1;
   // Blocks that run at once: 256 CUs with two of eight waves or four of four; half with the lag-weighted carry.
   // (65536 tokens x 8 heads, 128 x 128: 234 us; with half as many blocks 274, with twice as many 263.  16384 tokens
-  // x 16 heads forward and backward: 609, 680, 729.)
+  // x 16 heads forward and backward: 609, 680, 729.)  At least two chunks each (1000 tokens x 8 heads of
+  // floats forward and backward: 173 us, with four chunks 216; 128 tokens x 64 heads in bfloat16: 16, with one chunk 36).
   const uint64_t blocks = (wide <= 64 ? 1024 : 512) / (rate ? 2 : 1);
-  uint64_t len = std::max<uint64_t>(kAttnMinSeg, tokens * heads * slices / blocks);
+  uint64_t len = std::max<uint64_t>(dtype == LAPLEX_BF16 ? 128 : 64, tokens * heads * slices / blocks);
   len = (len + 63) / 64 * 64;
-  return (int64_t)(len + len / 2 < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
+  // Two segments cost more than one of twice the length (2048 tokens x 256 heads: 247 us, 208; 256 x 8: 24, 19).
+  return (int64_t)(2 * len < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
 }
-static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+static AttnPlan attn_plan(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   AttnPlan q;
   q.kp = K <= 64 ? 64 : K <= 128 ? 128 : 256;
-  q.seg_len = attn_seg_len(heads, K, V, tokens, rate);
+  q.seg_len = attn_seg_len(dtype, heads, K, V, tokens, rate);
   // V of at most 64 needs four waves (16384 tokens x 16 heads, 128 x 64, forward and backward: 498 us with eight, 469).
   // Where blocks of 128 columns would leave a good part of the 256 CUs idle, blocks of 64 share a chunk's work out
   // among twice as many (131 tokens x 4 heads, 80 x 96, float: 34 -> 25 us; 2048 x 8 heads, 128 x 128, bfloat16, 136
@@ -89,12 +90,12 @@ static AttnPlan attn_plan(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V,
   return q;
 }
 
-size_t attn_pass_bytes(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
-  const AttnPlan q = attn_plan(1, heads, K, V, tokens, rate);
+size_t attn_pass_bytes(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+  const AttnPlan q = attn_plan(dtype, 1, heads, K, V, tokens, rate);
   return (size_t)q.bounds * heads * K * V * 4 * (rate ? 2 : 1);
 }
-uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets) {
-  const AttnPlan q = attn_plan(seqs, heads, K, V, tokens, true);
+uint64_t attn_drate_parts(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets) {
+  const AttnPlan q = attn_plan(dtype, seqs, heads, K, V, tokens, true);
   return attn_slots({offsets, tokens, seqs, q.seg_len}) * q.slices;
 }
 
@@ -106,7 +107,7 @@ static bool aligned16(const void* p, int64_t token, int64_t head, uint32_t width
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   const bool rate = p.drate_part != nullptr, bf = p.dtype == LAPLEX_BF16;
   const size_t e = bf ? 2 : 4;
-  const AttnPlan q = attn_plan(p.seqs, p.heads, p.K, p.V, p.tokens, rate);
+  const AttnPlan q = attn_plan(p.dtype, p.seqs, p.heads, p.K, p.V, p.tokens, rate);
   AttnChunkArgs a{};
   a.p = p;
   a.g = {p.offsets, p.tokens, p.seqs, q.seg_len};

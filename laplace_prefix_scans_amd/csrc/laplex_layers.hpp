@@ -46,10 +46,10 @@ struct AttnPass {
   double* drate_part;  // partials of the rate gradient ([attn_drate_parts][head])
 };
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s);
-size_t attn_pass_bytes(uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate);
+size_t attn_pass_bytes(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate);
 // number of partials per head an attn_pass with drate_part writes ([partial][head])
 // (largest with offsets, whatever they hold)
-uint64_t attn_drate_parts(uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets);
+uint64_t attn_drate_parts(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets);
 hipError_t attn_drate_reduce(const double* part, uint64_t parts, uint32_t heads, float* drate, hipStream_t s);
 // dst[t][g][c] = sum of src[t][g * group + i][c] over i < group (src in float)
 hipError_t attn_group_sum(int dtype, const float* src, uint64_t tokens, uint32_t kv_heads, uint32_t group, uint32_t width,

@@ -67,8 +67,8 @@ bool any_misaligned(const Extent (&v)[N], size_t a) {
 // partials of the rate gradient with or without offsets
 uint64_t drate_parts_most(const laplex_attn_shape& a) {
   static const int32_t some = 0;
-  return std::max(attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens, &some),
-                  attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens, nullptr));
+  return std::max(attn_drate_parts(a.dtype, a.seqs, a.heads, a.dv, a.dk, a.tokens, &some),
+                  attn_drate_parts(a.dtype, a.seqs, a.heads, a.dv, a.dk, a.tokens, nullptr));
 }
 
 struct AttnWorkspace {
@@ -79,8 +79,8 @@ struct AttnWorkspace {
 AttnWorkspace carve_attn(void* ws, int pass, const laplex_attn_shape& a, size_t* total) {
   Carver c(ws);
   AttnWorkspace w{};
-  size_t b = attn_pass_bytes(a.heads, a.dk, a.dv, a.tokens, false);
-  if (pass == LAPLEX_ATTN_BACKWARD) b = std::max({b, attn_pass_bytes(a.heads, a.dv, a.dk, a.tokens, false), attn_pass_bytes(a.heads, a.dv, a.dk, a.tokens, true)});
+  size_t b = attn_pass_bytes(a.dtype, a.heads, a.dk, a.dv, a.tokens, false);
+  if (pass == LAPLEX_ATTN_BACKWARD) b = std::max({b, attn_pass_bytes(a.dtype, a.heads, a.dv, a.dk, a.tokens, false), attn_pass_bytes(a.dtype, a.heads, a.dv, a.dk, a.tokens, true)});
   w.pass = c.take<void>(b);
   if (pass == LAPLEX_ATTN_BACKWARD) {
     if (a.heads != a.kv_heads) w.sum = c.take<float>(a.tokens * a.heads * std::max(a.dk, a.dv) * 4);
@@ -204,7 +204,7 @@ extern "C" laplex_status laplex_decay_attn_backward(const laplex_attn_shape* sha
     }
     if ((err = attn_pass(p, w.pass, stream)) != hipSuccess) return from_hip(err);
     if (drate) {
-      const uint64_t parts = attn_drate_parts(a.seqs, a.heads, a.dv, a.dk, a.tokens, a.offsets);
+      const uint64_t parts = attn_drate_parts(a.dtype, a.seqs, a.heads, a.dv, a.dk, a.tokens, a.offsets);
       if ((err = attn_drate_reduce(w.drate, parts, a.heads, drate, stream)) != hipSuccess) return from_hip(err);
     }
   }
