@@ -174,14 +174,27 @@ struct Stage {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(m, off + (uint32_t)(i * RPI * pitch), 0, 0));
     } else {
-      const T* p = reinterpret_cast<const T*>(at + r0 * pitch) + c;
+      // Pieces at the alignment of T.  A row's last one is read 16 bytes before its end and shifted down; rows
+      // shorter than a piece are read one by one.
+      const char* p = at + r0 * pitch;
+      const int past = max(c + E - width, 0);  // elements of the piece behind the row's end
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        T e[E];
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          e[j] = r0 + i * RPI < rows && c + j < width ? *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p + j) + i * RPI * pitch) : T(0.f);
-        __builtin_memcpy(&v[i], e, 16);
+        unsigned __int128 w = 0;
+        if (r0 + i * RPI < rows && c < width) {
+          const T* q = reinterpret_cast<const T*>(p + i * RPI * pitch);
+          if (width >= E) {
+            __builtin_memcpy(&w, q + (c - past), 16);
+            if (past) w >>= past * (int)sizeof(T) * 8;
+          } else {
+            for (int j = width - 1; j >= 0; --j) {
+              uint32_t one = 0;
+              __builtin_memcpy(&one, q + j, sizeof(T));
+              w = w << sizeof(T) * 8 | one;
+            }
+          }
+        }
+        __builtin_memcpy(&v[i], &w, 16);
       }
     }
     at += (int64_t)(ROWS * pitch);
@@ -497,14 +510,29 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < IT; ++t)
+      for (int t = 0; t < IT; ++t) {
+        if (16 * t + lc >= n || c >= V) continue;
+        char* to = out + (int64_t)((16 * t + lc) * out_pitch) + c * (wide ? 4 : 2);
+        const int left = min(V - c, 4);
+        if (wide) {
+          if (left == 4) {
+            __builtin_memcpy(reinterpret_cast<float*>(to), &O[t], 16);
+          } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (16 * t + lc >= n || c + e >= V) continue;
-          char* to = out + (int64_t)((16 * t + lc) * out_pitch);
-          if (wide) reinterpret_cast<float*>(to)[c + e] = O[t][e];
-          else reinterpret_cast<T*>(to)[c + e] = from_f32<T>(O[t][e]);
+            for (int e = 0; e < 3; ++e)
+              if (e < left) reinterpret_cast<float*>(to)[e] = O[t][e];
+          }
+        } else {
+          const u32x2 w = {pack_bf16(O[t][0], O[t][1]), pack_bf16(O[t][2], O[t][3])};
+          if (left == 4) {
+            __builtin_memcpy(reinterpret_cast<uint16_t*>(to), &w, 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              if (e < left) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> 16 * (e % 2));
+          }
         }
+      }
     }
     out += (int64_t)(C * out_pitch);
   };
