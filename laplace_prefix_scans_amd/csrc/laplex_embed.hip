@@ -18,42 +18,58 @@
 namespace laplex {
 
 constexpr int kEmbedBlock = 256;
+constexpr size_t kEmbedLong = 2560;  // bytes from which rows that are not whole aligned pieces are moved in 16 bytes
 constexpr int kEmbedZeroRows = 8;  // table rows a thread group looks at for zeroing
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, uint64_t t) {
   return id_bytes == 8 ? static_cast<const int64_t*>(ids)[t] : (int64_t)static_cast<const int32_t*>(ids)[t];
 }
 
-// `E` consecutive elements where rows are 16-byte aligned, else one
-template <typename T, int E>
+// Rows are moved in pieces of E elements.  WHOLE: they are 16 bytes, aligned and whole.  Otherwise they are read and
+// written at the alignment of an element: long rows in 16 bytes too, of which a row's last begin E elements before its
+// end (two threads then form and write the same values in some columns), short ones an element a thread, for there the
+// threads on the way count.  Lookup and gradient, 16384 tokens: 65536 x 2047 bfloat16 166 us, by elements 272; 5000 x
+// 1001 float 61 and 65; but 257 x 513 float, 4096 tokens, 25.6 and 24, and 23748 x 107, 17368 tokens, 45 and 36.
+template <int E, bool WHOLE>
+__device__ __forceinline__ uint32_t piece_at(uint32_t c, uint32_t width) {
+  return WHOLE || width < (uint32_t)E ? c : min(c, width - E);
+}
+template <typename T, int E, bool WHOLE>
 struct Piece {
   T e[E];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (E > 1) {
+  __device__ __forceinline__ void load(const T* p, uint32_t left) {
+    if constexpr (WHOLE) {
       const uint4 q = *reinterpret_cast<const uint4*>(p);
       __builtin_memcpy(e, &q, 16);
+    } else if (left >= (uint32_t)E) {
+      __builtin_memcpy(e, p, sizeof(e));
     } else {
-      e[0] = *p;
+#pragma unroll
+      for (int j = 0; j < E; ++j) e[j] = j < (int)left ? p[j] : T(0.f);
     }
   }
 };
-template <typename O, int E>
-__device__ __forceinline__ void store_row(O* p, const float (&v)[E], float scale) {
+template <typename O, int E, bool WHOLE>
+__device__ __forceinline__ void store_row(O* p, const float (&v)[E], float scale, uint32_t left) {
   O o[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) o[j] = from_f32<O>(scale * v[j]);
-  if constexpr (E == 1) {
-    *p = o[0];
-  } else {
-    uint4 q[(E * sizeof(O) + 15) / 16];
+  if constexpr (WHOLE) {
+    uint4 q[E * sizeof(O) / 16];
     __builtin_memcpy(q, o, E * sizeof(O));
 #pragma unroll
     for (int i = 0; i < (int)(E * sizeof(O) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
+  } else if (left >= (uint32_t)E) {
+    __builtin_memcpy(p, o, E * sizeof(O));
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (j < (int)left) p[j] = o[j];
   }
 }
 
 // Thread per piece of a row; `lanes` threads share a token and step over its pieces.
-template <typename T, int E>
+template <typename T, int E, bool WHOLE>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed(const void* __restrict__ ids, int id_bytes, uint64_t tokens,
                                                        const T* __restrict__ table, uint32_t vocab, uint32_t width, float scale,
                                                        T* __restrict__ y, uint32_t lanes) {
@@ -61,17 +77,18 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed(const void* __restrict__ 
   for (uint64_t t = (uint64_t)blockIdx.x * per + threadIdx.x / lanes; t < tokens; t += (uint64_t)gridDim.x * per) {
     const int64_t id = load_id(ids, id_bytes, t);
     const bool live = id >= 0 && id < (int64_t)vocab;
-    for (uint32_t c = threadIdx.x % lanes * E; c < width; c += lanes * E) {
+    for (uint32_t c0 = threadIdx.x % lanes * E; c0 < width; c0 += lanes * E) {
+      const uint32_t c = piece_at<E, WHOLE>(c0, width);
       float v[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) v[j] = 0.f;
       if (live) {
-        Piece<T, E> p;
-        p.load(table + (uint64_t)id * width + c);
+        Piece<T, E, WHOLE> p;
+        p.load(table + (uint64_t)id * width + c, width - c);
 #pragma unroll
         for (int j = 0; j < E; ++j) v[j] = to_f32(p.e[j]);
       }
-      store_row<T, E>(y + t * width + c, v, live ? scale : 0.f);
+      store_row<T, E, WHOLE>(y + t * width + c, v, live ? scale : 0.f, width - c);
     }
   }
 }
@@ -295,11 +312,12 @@ struct EmbedGrad {
   float* part;  // [chunk][0: the stretch begun earlier, 1: the one that goes on][width]
 };
 
-template <typename T, typename O, int E>
+template <typename T, typename O, int E, bool WHOLE>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGrad g, const T* __restrict__ dy, O* __restrict__ dtable) {
   const uint32_t groups = kEmbedBlock / g.lanes, group = threadIdx.x / g.lanes;
-  const uint32_t c = (blockIdx.y * g.lanes + threadIdx.x % g.lanes) * E;
-  if (c >= g.width) return;
+  const uint32_t c0 = (blockIdx.y * g.lanes + threadIdx.x % g.lanes) * E;
+  if (c0 >= g.width) return;
+  const uint32_t c = piece_at<E, WHOLE>(c0, g.width), left = g.width - c;
   if (blockIdx.x >= g.chunk_blocks) {
     const uint64_t v0 = ((blockIdx.x - g.chunk_blocks) * groups + group) * kEmbedZeroRows;
     float zero[E];
@@ -307,7 +325,7 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGrad g, const T
     for (int j = 0; j < E; ++j) zero[j] = 0.f;
     for (uint64_t v = v0; v < v0 + kEmbedZeroRows && v < g.vocab; ++v) {
       const uint32_t u = key_of((int64_t)v, g.vocab, g.bits);
-      if (g.starts[u] == g.starts[u + 1]) store_row<O, E>(dtable + v * g.width + c, zero, 0.f);
+      if (g.starts[u] == g.starts[u + 1]) store_row<O, E, WHOLE>(dtable + v * g.width + c, zero, 0.f, left);
     }
     return;
   }
@@ -321,18 +339,18 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGrad g, const T
   for (int j = 0; j < E; ++j) acc[j] = 0.f;
   auto flush = [&](bool goes_on) {
     if (cur >> g.bits) return;  // outside the table
-    if (head || goes_on) store_row<float, E>(g.part + (ch * 2 + (head ? 0 : 1)) * g.width + c, acc, 1.f);
-    else store_row<O, E>(dtable + (uint64_t)row_of(cur, g.bits) * g.width + c, acc, g.scale);
+    if (head || goes_on) store_row<float, E, WHOLE>(g.part + (ch * 2 + (head ? 0 : 1)) * g.width + c, acc, 1.f, left);
+    else store_row<O, E, WHOLE>(dtable + (uint64_t)row_of(cur, g.bits) * g.width + c, acc, g.scale, left);
   };
   constexpr int B = 8;  // rows in flight
   for (uint64_t q = p0; q < p1; q += B) {
     uint32_t key[B];
-    Piece<T, E> row[B];
+    Piece<T, E, WHOLE> row[B];
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       const uint64_t at = min(q + i, p1 - 1);
       key[i] = g.keys[at];
-      row[i].load(dy + (uint64_t)g.perm[at] * g.width + c);
+      row[i].load(dy + (uint64_t)g.perm[at] * g.width + c, left);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -390,25 +408,22 @@ static uint32_t embed_lanes(uint32_t pieces) {
   return l;
 }
 
-template <typename T, int E>
+template <typename T, int E, bool WHOLE>
 static void embed_launch(const void* ids, int id_bytes, uint64_t tokens, const void* table, uint32_t vocab, uint32_t width,
                          float scale, void* y, hipStream_t s) {
   const uint32_t lanes = embed_lanes((width + E - 1) / E), per = kEmbedBlock / lanes;
-  k_embed<T, E><<<(unsigned)std::min<uint64_t>((tokens + per - 1) / per, 1u << 20), kEmbedBlock, 0, s>>>(ids, id_bytes, tokens, (const T*)table, vocab, width,
+  k_embed<T, E, WHOLE><<<(unsigned)std::min<uint64_t>((tokens + per - 1) / per, 1u << 20), kEmbedBlock, 0, s>>>(ids, id_bytes, tokens, (const T*)table, vocab, width,
                                                                             scale, (T*)y, lanes);
 }
 
 hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* table, uint32_t vocab, uint32_t width,
                      float scale, void* y, hipStream_t s) {
   const size_t e = dtype == LAPLEX_BF16 ? 2 : 4;
-  const bool vec = embed_vec(width, e, e, {table, y});
+  const bool vec = embed_vec(width, e, e, {table, y}), wide = width * e >= kEmbedLong;
+  auto run = [&](auto f) { f(ids, id_bytes, tokens, table, vocab, width, scale, y, s); };
   LAPLEX_LAUNCH("k_embed", tokens, s, {
-    if (dtype == LAPLEX_BF16)
-      vec ? embed_launch<bf16, 8>(ids, id_bytes, tokens, table, vocab, width, scale, y, s)
-          : embed_launch<bf16, 1>(ids, id_bytes, tokens, table, vocab, width, scale, y, s);
-    else
-      vec ? embed_launch<float, 4>(ids, id_bytes, tokens, table, vocab, width, scale, y, s)
-          : embed_launch<float, 1>(ids, id_bytes, tokens, table, vocab, width, scale, y, s);
+    if (dtype == LAPLEX_BF16) run(vec ? embed_launch<bf16, 8, true> : wide ? embed_launch<bf16, 8, false> : embed_launch<bf16, 1, false>);
+    else run(vec ? embed_launch<float, 4, true> : wide ? embed_launch<float, 4, false> : embed_launch<float, 1, false>);
   });
   return hipGetLastError();
 }
@@ -426,7 +441,7 @@ uint64_t embed_part_floats(uint64_t tokens, uint32_t width) {
   return (tokens + c - 1) / c * 2 * width;
 }
 
-template <typename T, typename O, int E>
+template <typename T, typename O, int E, bool WHOLE>
 static void embed_grad_launch(EmbedGrad g, const void* dy, void* dtable, hipStream_t s) {
   const uint32_t pieces = (g.width + E - 1) / E;
   g.lanes = embed_lanes(pieces);
@@ -435,7 +450,7 @@ static void embed_grad_launch(EmbedGrad g, const void* dy, void* dtable, hipStre
   g.chunk_blocks = (chunks + groups - 1) / groups;
   const uint64_t zero_blocks = ((uint64_t)g.vocab + groups * kEmbedZeroRows - 1) / (groups * kEmbedZeroRows);
   const dim3 grid((unsigned)(g.chunk_blocks + zero_blocks), (pieces + g.lanes - 1) / g.lanes);
-  k_embed_grad<T, O, E><<<grid, kEmbedBlock, 0, s>>>(g, (const T*)dy, (O*)dtable);
+  k_embed_grad<T, O, E, WHOLE><<<grid, kEmbedBlock, 0, s>>>(g, (const T*)dy, (O*)dtable);
   if (chunks > 1) {
     const dim3 jgrid((unsigned)(chunks - 1), std::min<uint32_t>((g.width + 63) / 64, 32));
     k_embed_join<O><<<jgrid, kEmbedBlock, 0, s>>>(g, (O*)dtable);
@@ -474,15 +489,17 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
     LAPLEX_LAUNCH("k_embed_starts", vocab, s, k_embed_starts<<<(1u << bits) / 256 + 1, 256, 0, s>>>(w.keys_s, tokens, bits, w.starts));
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const size_t te = table_dtype == LAPLEX_BF16 ? 2 : 4;
-  const bool vec = embed_vec(width, dtype == LAPLEX_BF16 ? 2 : 4, te, {dy, dtable});
+  const size_t de = dtype == LAPLEX_BF16 ? 2 : 4;
+  const bool vec = embed_vec(width, de, te, {dy, dtable}), wide = width * de >= kEmbedLong;
   const EmbedGrad g{w.keys_s, w.perm, w.starts, tokens, vocab, width, embed_chunk(tokens), 0, bits, 0, scale, w.part};
+  auto run = [&](auto f) { f(g, dy, dtable, s); };
   LAPLEX_LAUNCH("k_embed_grad", tokens, s, {
     if (dtype != LAPLEX_BF16)
-      vec ? embed_grad_launch<float, float, 4>(g, dy, dtable, s) : embed_grad_launch<float, float, 1>(g, dy, dtable, s);
+      run(vec ? embed_grad_launch<float, float, 4, true> : wide ? embed_grad_launch<float, float, 4, false> : embed_grad_launch<float, float, 1, false>);
     else if (table_dtype == LAPLEX_F32)
-      vec ? embed_grad_launch<bf16, float, 8>(g, dy, dtable, s) : embed_grad_launch<bf16, float, 1>(g, dy, dtable, s);
+      run(vec ? embed_grad_launch<bf16, float, 8, true> : wide ? embed_grad_launch<bf16, float, 8, false> : embed_grad_launch<bf16, float, 1, false>);
     else
-      vec ? embed_grad_launch<bf16, bf16, 8>(g, dy, dtable, s) : embed_grad_launch<bf16, bf16, 1>(g, dy, dtable, s);
+      run(vec ? embed_grad_launch<bf16, bf16, 8, true> : wide ? embed_grad_launch<bf16, bf16, 8, false> : embed_grad_launch<bf16, bf16, 1, false>);
   });
   return hipGetLastError();
 }

@@ -195,6 +195,31 @@ def test_embedding_gradient_of_many_tokens(shape, kind):
     near("dtable", host(grad), want, ref.embedding_backward(ids, np.abs(dy.numpy()), vocab, 0.5), tokens)
 
 
+@pytest.mark.parametrize("width", [641, 1283, 2600, 5003])
+@pytest.mark.parametrize("dt", ["f32", "bf16", "bf16_f32"])
+def test_embedding_of_long_odd_rows(width, dt):
+    """Rows that are no whole number of aligned pieces, by width and by address."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    tokens, vocab = 300, 40
+    print("embed odd", width, dt, flush=True)
+    dtype = torch.float32 if dt == "f32" else torch.bfloat16
+    g = torch.Generator().manual_seed(width)
+    buf = torch.randn(1 + (tokens + vocab) * width, generator=g).to(dtype)
+    ids = ids_of("zipf", tokens, vocab + 1, width)
+    dev = buf.cuda()
+    table, dy = (b[1:1 + vocab * width].view(vocab, width) for b in (buf, dev)), (b[1 + vocab * width:].view(tokens, width) for b in (buf, dev))
+    (table, table_d), (dy, dy_d) = table, dy
+    ids_d = torch.from_numpy(ids).cuda()
+    live = ids < vocab
+    want = np.where(live[:, None], 2.5 * table.float().numpy().astype(np.float64)[np.where(live, ids, 0)], 0.0)
+    near("y", host(lp.laplex_embedding(ids_d, table_d, scale=2.5).float()), want, np.abs(want), 1, dtype == torch.bfloat16)
+    out = torch.float32 if dt == "bf16_f32" else dtype
+    grad = lp.laplex_embedding_backward(ids_d, dy_d, vocab, scale=2.5, dtype=out)
+    want = ref.embedding_backward(ids, dy.float().numpy(), vocab, 2.5)
+    near("dtable", host(grad.float()), want, ref.embedding_backward(ids, np.abs(dy.float().numpy()), vocab, 2.5), tokens, out == torch.bfloat16)
+
+
 def test_embedding_gradient_against_differences():
     """<dy, y> is linear in the table: a difference with a step of 1 has rounding errors only."""
     import torch
