@@ -342,7 +342,10 @@ size_t laplex_decay_attn_workspace_bytes(int pass, const laplex_attn_shape* shap
  * shape; an empty sequence's is its state_in).  o: tokens x heads x dv,
  * contiguous.  A non-finite value in token j reaches o_i only for i >= j of its
  * own sequence, where it gives non-finite outputs (or, where its weight has
- * decayed to zero, none).
+ * decayed to zero, none).  All sums are float32 whatever the type.  A call
+ * repeated gives the same bits, with or without state_out; another number of
+ * tokens in all, of sequences or of heads may cut a sequence into other
+ * segments, whose float32 sums are taken in another order.
  * ws: laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_FORWARD, shape) bytes. */
 laplex_status laplex_decay_attn(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
                                 const float* state_in, float* state_out, void* o, void* ws, size_t ws_bytes,

@@ -123,7 +123,6 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
                    (!rate || aligned16(p.dot, p.dot_view.token, p.dot_view.head, p.V, e)) &&
                    reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
   a.bound_trans = p.bound_ready;
-  a.fine = p.s_out != nullptr;
   a.drate = p.drate_part;
   auto run = [&](const char* name, bool full) {
     LAPLEX_LAUNCH(name, p.tokens, s, {

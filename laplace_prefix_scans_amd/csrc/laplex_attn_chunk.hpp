@@ -140,6 +140,30 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* first, uin
   return __builtin_amdgcn_make_buffer_rsrc(p, 0, __builtin_amdgcn_readfirstlane(bytes), 0x00027000);  // raw, 32-bit words
 }
 
+template <typename T>
+constexpr int kAttnC = sizeof(T) == 2 ? 64 : 32;  // tokens per chunk
+
+// The ten 16 x 16 tiles of the weighted pairs on and below the diagonal, as operands over 32 rows j: per operand three
+// parts of 64 lanes' 16 bytes, and 8 bytes in the two whose second 16 rows lie above the diagonal.  15 KB, so that two
+// blocks of eight waves and 128 rows of the carry fit the LDS of a CU.  First 8-byte word of tile i's operand of rows 32 s on:
+__device__ __forceinline__ constexpr int pair_at(int i, int s) {
+  return i == 2 * s ? (4 * 2 + s) * 3 * kWave : (i == 1 ? 0 : i - 1 + (i == 3 ? s : 0)) * 2 * 3 * kWave;
+}
+
+// The first rows with an infinity or NaN, a byte per column of a tile (kNoRow: none; a chunk has at most 64 rows).
+constexpr uint32_t kNoRow = 0x40404040u;
+__device__ __forceinline__ int row_byte(const uint32_t* rows, int col) { return (rows[col / 4] >> col % 4 * 8) & 0xFF; }
+__device__ __forceinline__ void lower_row_byte(uint32_t* rows, int col, uint32_t row) {
+  uint32_t* at = rows + col / 4;
+  const int shift = col % 4 * 8;
+  uint32_t old = *at;
+  while ((old >> shift & 0xFF) > row) {  // (a swap fails only where another lowered a byte of the word: a bounded number of times)
+    const uint32_t seen = atomicCAS(at, old, (old & ~(0xFFu << shift)) | row << shift);
+    if (seen == old) break;
+    old = seen;
+  }
+}
+
 // The thread's number, as something the compiler takes to change with every call: what is made from it is
 // then formed where it is used instead of holding a register over the loop.
 __device__ __forceinline__ int thread_now() {
@@ -207,8 +231,8 @@ struct Stage {
       *reinterpret_cast<uint4*>(tile + r * P + ((c ^ swz<T, P>(r)) * E)) = v[i];
     }
   }
-  // Replaces infinities and NaN by 0 and lowers first[column of the tile] to their row; whether there were any.
-  __device__ __forceinline__ bool clean(int* first) {
+  // Replaces infinities and NaN by 0 and lowers the byte of their column in `first` to their row; whether there were any.
+  __device__ __forceinline__ bool clean(uint32_t* first) {
     // the largest magnitude, as an integer: infinities and NaN are above every finite one
     bool bad;
     if constexpr (sizeof(T) == 2) {
@@ -236,7 +260,7 @@ struct Stage {
       for (int j = 0; j < E; ++j)
         if (bits_nonfinite(__float_as_uint(to_f32(e[j])))) {
           e[j] = T(0.f);
-          atomicMin(first + t % (P / E) * E + j, t / (P / E) + i * RPI);
+          lower_row_byte(first, t % (P / E) * E + j, t / (P / E) + i * RPI);
         }
       __builtin_memcpy(&v[i], e, 16);
     }
@@ -244,8 +268,10 @@ struct Stage {
   }
 };
 
-// Two floats as a pair of bfloat16, and what the pair leaves over: x = hi + lo
-// (+ lo2) in two (three) parts loses 2^-17 (2^-25) of x.
+// Two floats as a pair of bfloat16, and what the pair leaves over.  Three parts of 8 bits, x = hi + lo + lo2, hold the
+// 24 of a float (short of 2^-110): carries, pairs and weighted rows enter bfloat16 products with all of their bits, and
+// every sum is float32's.  Two parts would lose 2^-18 of each, a thousandth of a bfloat16 result's own rounding, but more than
+// float32 does (65536 tokens x 8 heads, 128 x 128: whole pass 193 us, with two parts 154; states alone 73 and 66).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
@@ -255,24 +281,10 @@ __device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
   b -= __uint_as_float(w & 0xFFFF0000u);
   return w;
 }
-struct Parts2 {
-  bf16x8 hi, lo;
-};
-__device__ __forceinline__ Parts2 split2(const f32x4& u, const f32x4& v) {
-  const float x[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = x[2 * i], b = x[2 * i + 1];
-    h[i] = split_pair(a, b);
-    l[i] = pack_bf16(a, b);
-  }
-  return {__builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3])), __builtin_bit_cast(bf16x8, make_uint4(l[0], l[1], l[2], l[3]))};
-}
-struct Parts3 {
+struct Parts {
   bf16x8 hi, lo, lo2;
 };
-__device__ __forceinline__ Parts3 split3(const f32x4& u, const f32x4& v) {
+__device__ __forceinline__ Parts split(const f32x4& u, const f32x4& v) {
   const float x[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
   uint32_t h[4], l[4], m[4];
 #pragma unroll
@@ -291,16 +303,12 @@ struct AttnChunkArgs {
   AttnSegs g;
   uint32_t slices;   // blocks across the V columns
   uint32_t group;    // query heads per shared head
-  bool fine;         // the carry is an output
   uint64_t slots;    // segments, with room for unused ones
   float* bound;      // states at segment boundaries ([boundary][head][K][V]), or null
   bool bound_trans;  // they are [V][K], from a pass with the roles of K and V exchanged
   float* bound_d;    // the lag-weighted ones (rate gradient)
   double* drate;     // Rate: partials [slot][slice][head]
 };
-
-template <typename T>
-constexpr int kAttnC = sizeof(T) == 2 ? 64 : 32;  // tokens per chunk
 
 // row of the carry that register r of 16-row tile t holds in lane group g
 __device__ __forceinline__ int carry_row(int t, int g, int r) { return 16 * t + 4 * g + r; }
@@ -358,14 +366,13 @@ __device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) { return __buil
 // With 16 columns a wave holds 32 registers of a 128-row carry, so that four
 // waves share a SIMD and one's conversions run beside another's products;
 // 32 columns in half as many waves took as long without the rate's gradient, and a quarter longer with it.
-// Measured (bfloat16, 128 x 128).  States alone, 65536 tokens x 8 heads: 65 us for 302 MB, 4.6 TB/s, at the rate of a
-// copy.  The whole pass there: 142 us for 570 MB, 4.0 TB/s; with the products left out 110 us, so the bound is HBM and a
-// quarter over it what the four waves of a SIMD do not hide of products, conversions and waits.  With the rate's
-// gradient, 16384 tokens x 16 heads: 180 us, 85 with the products left out; a second carry in three parts, and
-// registers for two waves a SIMD, make it bound by conversions and products.  (Two parts: 165 us and four times the error
-// of the gradient.)
-// FINE: the carry goes out as float32 (otherwise it only enters results of type T).
-template <typename T, int KP, int NW, bool FULL, bool RATE, bool FINE, bool VEC>
+// Measured (bfloat16, 128 x 128; averages).  States alone, 65536 tokens x 8 heads: 73 us for 302 MB, 4.1 TB/s.  The whole
+// pass there: 193 us for 570 MB, 3.0 TB/s.  Reads and writes alone take 110 us; the rest is what the four waves of a SIMD do
+// not hide of 119 products and about 650 vector instructions a chunk and wave.  Products that do not follow one they add to, and
+// fewer instructions to split a float (by two-element dot products), changed nothing.  With the rate's
+// gradient, 16384 tokens x 16 heads: 206 us, against 101 without; it has a second carry in three parts and registers for two
+// waves a SIMD.
+template <typename T, int KP, int NW, bool FULL, bool RATE, bool VEC>
 __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW == 4) ? 2 : 4) void k_attn_chunk(AttnChunkArgs a) {
   constexpr int C = kAttnC<T>, KT = KP / 16, BV = 16 * NW, THREADS = NW * kWave, IT = C / 16;
   constexpr bool BF = sizeof(T) == 2, DOT = FULL && RATE;
@@ -377,13 +384,13 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
   __shared__ __attribute__((aligned(16))) T zs[ZB][C * BV];
   __shared__ __attribute__((aligned(16))) T dots[2][DOT ? C * BV : 8];
   __shared__ __attribute__((aligned(16))) float down[C], downlag[RATE ? C : 4];
-  __shared__ float wt[FULL ? 2 * C : 1], up[FULL ? C : 1];
-  // bf16: operand [32 rows j and tile i: i + 2 (j / 32)][part] of a lane (the lag-weighted ones behind them); float: [wave][tile]
-  using Pair = std::conditional_t<BF, bf16x8, f32x4>;
-  constexpr int PAIRS = 6 * 2 * kWave;
-  __shared__ Pair pairs[FULL ? (BF ? (RATE ? 2 : 1) * PAIRS : WK * 3 * kWave) : 1];
-  __shared__ int bad_chunk[2], bad_row[2][FULL ? BV : 1];
-  __shared__ double red[NW];
+  __shared__ float dec[FULL ? C + 1 : 1];  // exp(-rate n)
+  // bf16: operands of the weighted pairs (pair_at; the lag-weighted ones behind them); float: [wave][tile]
+  constexpr int PAIRS = 10 * 3 * kWave;  // 8-byte words
+  __shared__ __attribute__((aligned(16))) uint2 pairs[FULL ? (BF ? (RATE ? 2 : 1) * PAIRS : WK * 3 * kWave * 2) : 2];
+  __shared__ int bad_chunk[2];
+  __shared__ uint32_t bad_row[2][FULL ? BV / 4 : 1];  // a byte per column
+  __shared__ double red[DOT ? NW : 1];
 
   // Blocks that read the same rows (the column slices and the heads of one shared head) follow each other on
   // one XCD; these units go to the XCDs in turn, so that unused slots leave none of them with less work.
@@ -469,13 +476,10 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
     }
   }
 
-  // weights of a pair inside a chunk by its lag, 0 for the pairs above the diagonal
   if constexpr (FULL) {
-    for (int i = threadIdx.x; i < 2 * C; i += THREADS) wt[i] = i >= C ? p.c_pair * decay(-rate * (float)(i - C)) : 0.f;
-    if (threadIdx.x < C) up[threadIdx.x] = p.c_in * decay(-rate * (float)((int)threadIdx.x + lead));
-    if constexpr (BF)  // tiles above the diagonal stay zero
-      for (int i = threadIdx.x; i < (int)(sizeof(pairs) / sizeof(Pair)); i += THREADS) pairs[i] = Pair{};
+    if (threadIdx.x <= C) dec[threadIdx.x] = decay(-rate * (float)threadIdx.x);
   }
+  auto pair_weight = [&](int lag) { return lag >= 0 ? p.c_pair * dec[lag] : 0.f; };
   // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
   // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
   // so far back to the exact one.
@@ -539,7 +543,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
   double dr = 0.0;
   if (threadIdx.x < 2) bad_chunk[threadIdx.x] = 0;
   if constexpr (FULL)
-    for (int i = threadIdx.x; i < 2 * BV; i += THREADS) bad_row[i / BV][i % BV] = C;
+    for (int i = threadIdx.x; i < 2 * BV / 4; i += THREADS) bad_row[i / (BV / 4)][i % (BV / 4)] = kNoRow;
   __syncthreads();
   // the loaded rows of a chunk into LDS, z and dot into buffer `to`
   auto fill = [&](int to) {
@@ -567,7 +571,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
     const bool bad = FULL && bad_chunk[now] != 0;
     const int tid = thread_now(), ln = tid & (kWave - 1);
     if (tid == 0) bad_chunk[now ^ 1] = 0;
-    if (FULL && tid < BV) bad_row[now ^ 1][tid] = C;
+    if (FULL && tid < BV / 4) bad_row[now ^ 1][tid] = kNoRow;
     const int g = ln >> 4, lc = ln & 15;
 
     // byte offsets of this lane's operands
@@ -579,7 +583,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
     if constexpr (FULL) {
       // The weighted pairs are the same for every column: the waves share them out and pass them on through LDS.
       if constexpr (BF) {
-        // the ten 16 x 16 tiles of P^T (rows j, columns i) on and below the diagonal, as operands of two bfloat16 parts
+        // the ten 16 x 16 tiles of P^T (rows j, columns i) on and below the diagonal, as operands of three bfloat16 parts
         for (int tile = wave; tile < IT * (IT + 1) / 2; tile += NW) {
           const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
           f32x4 P = {};
@@ -599,15 +603,19 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
           float pv[4], pd[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float w = wt[C + lag0 - r];
+            const float w = pair_weight(lag0 - r);
             pv[r] = w != 0.f ? P[r] * w : 0.f;  // a masked pair is 0 whatever its product
             if constexpr (RATE) pd[r] = pv[r] * (float)(lag0 - r);
           }
           auto put_pair = [&](float (&v)[4], int base) {
-            uint2* dst = reinterpret_cast<uint2*>(pairs + base + (it + (jt & 2)) * 2 * kWave + ln) + (jt & 1);
-            const uint32_t h0 = split_pair(v[0], v[1]), h1 = split_pair(v[2], v[3]);
-            dst[0] = make_uint2(h0, h1);
-            dst[2 * kWave] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            const bool half = jt == it && !(it & 1);
+            uint2* dst = pairs + base + pair_at(it, jt >> 1) + (half ? ln : 2 * ln + (jt & 1));
+            const int part = half ? kWave : 2 * kWave;
+            uint32_t w0 = split_pair(v[0], v[1]), w1 = split_pair(v[2], v[3]);
+            dst[0] = make_uint2(w0, w1);
+            w0 = split_pair(v[0], v[1]), w1 = split_pair(v[2], v[3]);
+            dst[part] = make_uint2(w0, w1);
+            dst[2 * part] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
           };
           put_pair(pv, 0);
           if constexpr (RATE) put_pair(pd, PAIRS);
@@ -632,45 +640,32 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
           }
         }
 #pragma unroll
-        for (int i = 0; i < 3; ++i) pairs[(wave * 3 + i) * kWave + ln] = P[i];
+        for (int i = 0; i < 3; ++i) reinterpret_cast<f32x4*>(pairs)[(wave * 3 + i) * kWave + ln] = P[i];
       }
       if (active) {
         // out^T = S^T x^T (rows V, columns i)
         if constexpr (BF) {
-          constexpr int STEPS = KP / 32 * (IT / 2);
-          bf16x8 xf[2][2];
-          auto read = [&](int i) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) xf[i & 1][e] = read_row(xs + 16 * (i % (IT / 2) * 2 + e) * KP, row_at ^ (i / (IT / 2) << 6));
-          };
-          Parts2 s2;
-          Parts3 d3;
+          constexpr int STEPS = KP / 32 * IT;
+          bf16x8 xf[2];
+          auto read = [&](int i) { xf[i & 1] = read_row(xs + 16 * (i % IT) * KP, row_at ^ (i / IT << 6)); };
+          Parts sp, dp;
           read(0);
 #pragma unroll
           for (int i = 0; i < STEPS; ++i) {
-            const int ks = i / (IT / 2), t = i % (IT / 2) * 2;
+            const int ks = i / IT, t = i % IT;
             if (i + 1 < STEPS) read(i + 1);
             __builtin_amdgcn_sched_barrier(0);
             if (t == 0) {
-              // the carry enters as two bfloat16 parts: with one, its rounding would show beside the output's own
-              s2 = split2(S[2 * ks], S[2 * ks + 1]);
-              // (its result is a float32 sum: three)
-              if constexpr (RATE) d3 = split3(D[2 * ks], D[2 * ks + 1]);
+              sp = split(S[2 * ks], S[2 * ks + 1]);
+              if constexpr (RATE) dp = split(D[2 * ks], D[2 * ks + 1]);
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) O[t + e] = mfma(s2.hi, xf[i & 1][e], ks ? O[t + e] : f32x4{});
-            if constexpr (RATE) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) OD[t + e] = mfma(d3.hi, xf[i & 1][e], ks ? OD[t + e] : f32x4{});
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) O[t + e] = mfma(s2.lo, xf[i & 1][e], O[t + e]);
-            if constexpr (RATE) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) OD[t + e] = mfma(d3.lo, xf[i & 1][e], OD[t + e]);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) OD[t + e] = mfma(d3.lo2, xf[i & 1][e], OD[t + e]);
-            }
+            auto add = [&](f32x4& o, const Parts& c) {
+              o = mfma(c.hi, xf[i & 1], ks ? o : f32x4{});
+              o = mfma(c.lo, xf[i & 1], o);
+              o = mfma(c.lo2, xf[i & 1], o);
+            };
+            add(O[t], sp);
+            if constexpr (RATE) add(OD[t], dp);
           }
         } else {
 #pragma unroll
@@ -687,7 +682,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
         }
 #pragma unroll
         for (int t = 0; t < IT; ++t) {
-          const float f = up[16 * t + lc];
+          const float f = p.c_in * dec[16 * t + lc + lead];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if constexpr (RATE) OD[t][r] = f * fmaf((float)(16 * t + lc + lead), O[t][r], OD[t][r]);
@@ -708,25 +703,22 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
         S[t][r] *= w;
       }
       if constexpr (BF) {
-        bf16x8 zf, yt[2][2];
+        constexpr int STEPS = C / 32 * KT;
+        bf16x8 zf, yt[2];
         auto read = [&](int i) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = i % (KT / 2) * 2 + e;
-            yt[i & 1][e] = read_tr<KP>(ys + 32 * (i / (KT / 2)) * KP, y_at ^ (t >> 1 << 6 | (t & 1) << 5));
-          }
-          if (i % (KT / 2) == 0) zf = read_tr<BV>(z + 32 * (i / (KT / 2)) * BV, z_at);
+          const int t = i % KT;
+          yt[i & 1] = read_tr<KP>(ys + 32 * (i / KT) * KP, y_at ^ (t >> 1 << 6 | (t & 1) << 5));
+          if (t == 0) zf = read_tr<BV>(z + 32 * (i / KT) * BV, z_at);
         };
         read(0);
-        Parts3 z3, l3;
+        Parts zp, lp;
 #pragma unroll
-        for (int i = 0; i < C / 32 * (KT / 2); ++i) {
-          const int s = i / (KT / 2), t = i % (KT / 2) * 2;
-          if (i + 1 < C / 32 * (KT / 2)) read(i + 1);
+        for (int i = 0; i < STEPS; ++i) {
+          const int s = i / KT, t = i % KT;
+          if (i + 1 < STEPS) read(i + 1);
           __builtin_amdgcn_sched_barrier(0);
           if (t == 0) {
-            // z weighted by its decay to the chunk's end, as bfloat16 parts: three where the carry goes out as float32
-            // or into the rate's gradient (it keeps float32's bits), two where it only enters bfloat16 results
+            // z weighted by its decay to the chunk's end
             auto weighted = [&](const float* w, f32x4& lo, f32x4& hi) {
               lo = *reinterpret_cast<const f32x4*>(w + 32 * s + 4 * g);
               hi = *reinterpret_cast<const f32x4*>(w + 32 * s + 16 + 4 * g);
@@ -735,29 +727,19 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
             };
             f32x4 z0, z1;
             weighted(down, z0, z1);
-            if constexpr (FINE || RATE) {
-              z3 = split3(z0, z1);
-            } else {
-              const Parts2 z2 = split2(z0, z1);
-              z3.hi = z2.hi, z3.lo = z2.lo;
-            }
+            zp = split(z0, z1);
             if constexpr (RATE) {
               weighted(downlag, z0, z1);
-              l3 = split3(z0, z1);
+              lp = split(z0, z1);
             }
           }
-          auto add = [&](f32x4 (&s)[KT], const Parts3& p) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[t + e] = mfma(yt[i & 1][e], p.hi, s[t + e]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[t + e] = mfma(yt[i & 1][e], p.lo, s[t + e]);
-            if constexpr (FINE || RATE) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) s[t + e] = mfma(yt[i & 1][e], p.lo2, s[t + e]);
-            }
+          auto add = [&](f32x4& s, const Parts& p) {
+            s = mfma(yt[i & 1], p.hi, s);
+            s = mfma(yt[i & 1], p.lo, s);
+            s = mfma(yt[i & 1], p.lo2, s);
           };
-          add(S, z3);
-          if constexpr (RATE) add(D, l3);
+          add(S[t], zp);
+          if constexpr (RATE) add(D[t], lp);
         }
       } else {
         f32x4 zw[C / 16], zl[C / 16];
@@ -778,7 +760,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
           }
         }
       }
-      if (bad && bad_row[now][wave * 16 + lc] < C) {
+      if (bad && row_byte(bad_row[now], wave * 16 + lc) < C) {
         LAPLEX_EACH(t, KT, r) {
           S[t][r] = __builtin_nanf("");
           if constexpr (RATE) D[t][r] = __builtin_nanf("");
@@ -798,25 +780,35 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
           const bf16x8 zf = read_tr<BV>(z + 32 * s * BV, z_at);
 #pragma unroll
           for (int t = 2 * s; t < IT; ++t) {
-            const bf16x8* pf = pairs + (t + 2 * s) * 2 * kWave + ln;
-            O[t] = mfma(zf, pf[0], O[t]);
-            O[t] = mfma(zf, pf[kWave], O[t]);
-            if constexpr (RATE) {
-              OD[t] = mfma(zf, pf[PAIRS], OD[t]);
-              OD[t] = mfma(zf, pf[PAIRS + kWave], OD[t]);
-            }
+            auto add = [&](f32x4& o, int base) {
+              const uint2* from = pairs + base + pair_at(t, s);
+#pragma unroll
+              for (int part = 0; part < 3; ++part) {
+                bf16x8 w;
+                if (t == 2 * s) {  // (the other 16 rows lie above the diagonal)
+                  const uint2 half = from[part * kWave + ln];
+                  w = __builtin_bit_cast(bf16x8, make_uint4(half.x, half.y, 0, 0));
+                } else {
+                  w = __builtin_bit_cast(bf16x8, reinterpret_cast<const uint4*>(from)[part * kWave + ln]);
+                }
+                o = mfma(zf, w, o);
+              }
+            };
+            add(O[t], 0);
+            if constexpr (RATE) add(OD[t], PAIRS);
           }
         }
       } else {
         f32x4 P[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-          P[i] = pairs[i * kWave + ln];
+          const f32x4* parts = reinterpret_cast<const f32x4*>(pairs) + i * kWave + ln;
+          P[i] = parts[0];
 #pragma unroll
-          for (int k = 1; k < WK; ++k) P[i] += pairs[(k * 3 + i) * kWave + ln];
+          for (int k = 1; k < WK; ++k) P[i] += parts[k * 3 * kWave];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float w = wt[C + (i == 1 ? 16 : 0) + lc - 4 * g - r];
+            const float w = pair_weight((i == 1 ? 16 : 0) + lc - 4 * g - r);
             P[i][r] = w != 0.f ? P[i][r] * w : 0.f;  // a masked pair is 0 whatever its product
           }
         }
@@ -831,7 +823,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
       }
       if (bad) {
         LAPLEX_EACH(t, IT, r) {
-          const bool hit = 16 * t + lc >= bad_row[now][wave * 16 + 4 * g + r];
+          const bool hit = 16 * t + lc >= row_byte(bad_row[now], wave * 16 + 4 * g + r);
           O[t][r] = hit ? __builtin_nanf("") : O[t][r];
           if constexpr (RATE) OD[t][r] = hit ? __builtin_nanf("") : OD[t][r];
         }
@@ -890,15 +882,12 @@ template <typename T, int KP, int NW, bool VEC>
 void attn_chunk_launch_at(const AttnChunkArgs& a, bool full, bool rate, hipStream_t s) {
   const uint64_t units = a.slots * (a.p.heads / a.group);
   const dim3 grid((unsigned)(xcd_blocks(units) * a.group * a.slices)), block(NW * kWave);
-  constexpr bool BF = sizeof(T) == 2;  // (float keeps its bits either way)
   if (full) {
-    if (rate) k_attn_chunk<T, KP, NW, true, true, false, VEC><<<grid, block, 0, s>>>(a);
-    else if (a.fine && BF) k_attn_chunk<T, KP, NW, true, false, BF, VEC><<<grid, block, 0, s>>>(a);
-    else k_attn_chunk<T, KP, NW, true, false, false, VEC><<<grid, block, 0, s>>>(a);
+    if (rate) k_attn_chunk<T, KP, NW, true, true, VEC><<<grid, block, 0, s>>>(a);
+    else k_attn_chunk<T, KP, NW, true, false, VEC><<<grid, block, 0, s>>>(a);
   } else {
-    if (rate) k_attn_chunk<T, KP, NW, false, true, false, VEC><<<grid, block, 0, s>>>(a);
-    else if (a.fine && BF) k_attn_chunk<T, KP, NW, false, false, BF, VEC><<<grid, block, 0, s>>>(a);
-    else k_attn_chunk<T, KP, NW, false, false, false, VEC><<<grid, block, 0, s>>>(a);
+    if (rate) k_attn_chunk<T, KP, NW, false, true, VEC><<<grid, block, 0, s>>>(a);
+    else k_attn_chunk<T, KP, NW, false, false, VEC><<<grid, block, 0, s>>>(a);
   }
 }
 template <typename T, bool VEC>
