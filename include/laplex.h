@@ -101,8 +101,8 @@ laplex_status laplex_sort_anchors(const float* a, uint64_t n, float* a_sorted, u
  * A look-back wait that reaches its spin limit gives up: the watchdog flag is
  * raised, the remaining passes stop at once, every kernel exits, and the
  * sort's outputs are undefined.  For failure-path tests,
- * LAPLEX_DEBUG_STALL=<k> in the environment makes laplex_sort_anchors (only
- * this entry point) run its look-back passes without publishing and with a
+ * LAPLEX_DEBUG_STALL=<k> in the environment makes laplex_sort_anchors (this
+ * entry point, and laplex_embedding_backward where it sorts) run its look-back passes without publishing and with a
  * spin limit of k, which forces that path. */
 laplex_status laplex_status_poll(const void* ws, hipStream_t stream);
 
@@ -414,8 +414,10 @@ size_t laplex_embedding_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_
  * of type dtype):  dtable_v = scale sum_{t: id_t = v} dy_t, zero where v does
  * not occur.  The tokens are sorted by id (the library's stable sort), each
  * row's terms are added in float32 in an order that the ids alone fix, and the
- * sum is rounded once to table_dtype (dtype or LAPLEX_F32).  tokens <= 2^28,
- * vocab <= 2^26. */
+ * sum is rounded once to table_dtype (dtype or LAPLEX_F32).  Should that sort
+ * stall (more than 131072 tokens, or more than 16384 and a vocabulary past
+ * 2^18; see laplex_status_poll), every row is NaN.  tokens <= 2^28, vocab <=
+ * 2^26. */
 laplex_status laplex_embedding_backward(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                                         uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, void* ws,
                                         size_t ws_bytes, hipStream_t stream);

@@ -9,7 +9,8 @@
 // one chunk is written at once; one over several chunks leaves a float32
 // partial row per chunk, and a second launch adds those in order.  Rows
 // without a token are zeroed by the same launch that adds the chunks, so every
-// element of the gradient is written once and nothing is cleared first (the
+// element of the gradient is written once and nothing is cleared first; where the general sort gave up, that launch
+// writes NaN to every row and nothing reads the undefined order (the
 // same size: 67 us for 66 MB read and 272 MB written, 5.0 TB/s; the sort
 // 16 us, the partials 12 us).
 #include "laplex_layers.hpp"
@@ -310,6 +311,8 @@ struct EmbedGrad {
   uint64_t chunk_blocks;  // blocks of the chunks; the rest zero rows
   float scale;
   float* part;  // [chunk][0: the stretch begun earlier, 1: the one that goes on][width]
+  const uint32_t* stop;  // set where the general sort gave up (its keys and places are then undefined), or null
+  __device__ __forceinline__ bool stalled() const { return stop && *stop != 0; }
 };
 
 template <typename T, typename O, int E, bool WHOLE>
@@ -318,17 +321,19 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGrad g, const T
   const uint32_t c0 = (blockIdx.y * g.lanes + threadIdx.x % g.lanes) * E;
   if (c0 >= g.width) return;
   const uint32_t c = piece_at<E, WHOLE>(c0, g.width), left = g.width - c;
+  const bool stalled = g.stalled();
   if (blockIdx.x >= g.chunk_blocks) {
     const uint64_t v0 = ((blockIdx.x - g.chunk_blocks) * groups + group) * kEmbedZeroRows;
-    float zero[E];
+    float none[E];
 #pragma unroll
-    for (int j = 0; j < E; ++j) zero[j] = 0.f;
+    for (int j = 0; j < E; ++j) none[j] = stalled ? __builtin_nanf("") : 0.f;
     for (uint64_t v = v0; v < v0 + kEmbedZeroRows && v < g.vocab; ++v) {
       const uint32_t u = key_of((int64_t)v, g.vocab, g.bits);
-      if (g.starts[u] == g.starts[u + 1]) store_row<O, E, WHOLE>(dtable + v * g.width + c, zero, 0.f, left);
+      if (stalled || g.starts[u] == g.starts[u + 1]) store_row<O, E, WHOLE>(dtable + v * g.width + c, none, 1.f, left);
     }
     return;
   }
+  if (stalled) return;
   const uint64_t ch = (uint64_t)blockIdx.x * groups + group, p0 = ch * g.chunk;
   if (p0 >= g.tokens) return;
   const uint64_t p1 = min(p0 + g.chunk, g.tokens);
@@ -374,7 +379,7 @@ template <typename O>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_join(EmbedGrad g, O* __restrict__ dtable) {
   __shared__ float sh[4][64];
   const uint64_t ch = blockIdx.x, p0 = ch * g.chunk, p1 = p0 + g.chunk;
-  if (p1 >= g.tokens) return;
+  if (p1 >= g.tokens || g.stalled()) return;
   const uint32_t u = g.keys[p1 - 1];
   if (u >> g.bits || g.keys[p1] != u || g.starts[u] < p0) return;
   const uint64_t last = ((uint64_t)g.starts[u + 1] - 1) / g.chunk, v = row_of(u, g.bits);
@@ -462,6 +467,7 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
   hipError_t e;
   const int bits = key_bits(vocab);
   const uint32_t tiles = embed_tiles(tokens, vocab);
+  const uint32_t* stop = nullptr;
   uint32_t* starts = tiles || (tokens && tokens <= (uint64_t)kEmbedSmall && bits <= kFindBits) ? w.starts : nullptr;  // found by the sort
   if (tiles) {
     const uint32_t n = (uint32_t)tokens;
@@ -484,6 +490,7 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
                   k_embed_keys<<<(unsigned)((tokens + 255) / 256), 256, 0, s>>>(ids, id_bytes, tokens, vocab, bits, w.keys));
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = sort_indices(w.sort, w.keys, tokens, 1u << bits, w.keys_s, w.perm, s)) != hipSuccess) return e;
+    stop = w.sort.header + kHdrStop;
   }
   if (!starts)
     LAPLEX_LAUNCH("k_embed_starts", vocab, s, k_embed_starts<<<(1u << bits) / 256 + 1, 256, 0, s>>>(w.keys_s, tokens, bits, w.starts));
@@ -491,7 +498,7 @@ hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* id
   const size_t te = table_dtype == LAPLEX_BF16 ? 2 : 4;
   const size_t de = dtype == LAPLEX_BF16 ? 2 : 4;
   const bool vec = embed_vec(width, de, te, {dy, dtable}), wide = width * de >= kEmbedLong;
-  const EmbedGrad g{w.keys_s, w.perm, w.starts, tokens, vocab, width, embed_chunk(tokens), 0, bits, 0, scale, w.part};
+  const EmbedGrad g{w.keys_s, w.perm, w.starts, tokens, vocab, width, embed_chunk(tokens), 0, bits, 0, scale, w.part, stop};
   auto run = [&](auto f) { f(g, dy, dtable, s); };
   LAPLEX_LAUNCH("k_embed_grad", tokens, s, {
     if (dtype != LAPLEX_BF16)

@@ -88,11 +88,12 @@ size_t route_bytes(uint64_t n);
 SortRoute carve_route(const void* base, uint64_t n);
 
 size_t sort_status_bytes(uint64_t n);
-// debug_stall: honour LAPLEX_DEBUG_STALL (only the standalone sort entry
+// debug_stall: honour LAPLEX_DEBUG_STALL (of the sorts of anchors only the standalone entry
 // point does, so that no apply ever runs on a stalled sort's outputs).
 hipError_t sort_anchors(const SortWorkspace& w, const float* a, uint64_t n, float* a_sorted, uint32_t* perm,
                         const SortRoute* route, hipStream_t s, bool debug_stall = false);
-// The same stable sort of integers up to max_key (< 2^30), with the passes their digits need.
+// The same stable sort of integers up to max_key (< 2^30), with the passes their digits need.  Honours LAPLEX_DEBUG_STALL:
+// its callers check header[kHdrStop] before they use what it wrote.
 hipError_t sort_indices(const SortWorkspace& w, const uint32_t* keys, uint64_t n, uint32_t max_key, uint32_t* keys_sorted, uint32_t* perm,
                         hipStream_t s);
 // The same sort with x (n floats, original order) carried along as the

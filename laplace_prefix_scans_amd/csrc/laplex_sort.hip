@@ -632,7 +632,7 @@ hipError_t sort_indices(const SortWorkspace& w, const uint32_t* keys, uint64_t n
                         hipStream_t s) {
   // the bits of a nonnegative int, read as a float, sort in the same order; passes over digits that are all zero are left out
   const int passes = max_key < (1u << 16) ? 2 : max_key < (1u << 24) ? 3 : 4;
-  return sort_impl(w, reinterpret_cast<const float*>(keys), n, reinterpret_cast<float*>(keys_sorted), perm, nullptr, nullptr, s, false,
+  return sort_impl(w, reinterpret_cast<const float*>(keys), n, reinterpret_cast<float*>(keys_sorted), perm, nullptr, nullptr, s, true,
                    passes);
 }
 
