@@ -111,7 +111,8 @@ def _strides(t: torch.Tensor, shape, name: str, batched: bool) -> Tuple[int, int
         raise ValueError("%s must have contiguous channels" % name)
     if not batched:
         return st[0], st[1]
-    if shape[0] > 1 and shape[1] > 0 and st[0] != shape[1] * st[1]:
+    # (an axis of one token has no stride of its own: the batch's is the token's)
+    if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
         raise ValueError("%s: the tokens of a batch must lie one sequence after the other" % name)
     return (st[0] if shape[1] == 1 else st[1]), st[2]
 
