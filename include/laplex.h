@@ -377,7 +377,10 @@ laplex_status laplex_decay_attn_backward(const laplex_attn_shape* shape, const v
  * heads x dk x dv floats; slots: NULL (row r has state r; seqs <= pool) or a
  * DEVICE array of seqs int32, row r's state.  A slot outside [0, pool) marks a
  * place without a sequence: its o row is zero and no state changes.  Two rows
- * of one call must not name the same slot. */
+ * of one call must not name the same slot.  The decay is applied with more bits
+ * than a float has and the state rounded once a step, so that thousands of
+ * steps stay with one pass over the same tokens (a rate below 2^-25 or so is
+ * less than that rounding, and leaves a state as it is). */
 laplex_status laplex_decay_attn_step(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
                                      const int32_t* slots, uint32_t pool, float* state, void* o, hipStream_t stream);
 

@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kStepBlock) void k_attn_step(AttnStep p, uint32_t l
   const T *q = static_cast<const T*>(p.q.p) + row * p.q.token + (int64_t)(h / p.q.div) * p.q.head,
           *k = static_cast<const T*>(p.k.p) + row * p.k.token + (int64_t)(h / p.k.div) * p.k.head,
           *v = static_cast<const T*>(p.v.p) + row * p.v.token + (int64_t)(h / p.v.div) * p.v.head;
-  const float w = decay(-attn_rate(p.rate[h]));
+  const AttnDecay w = attn_decay(attn_rate(p.rate[h]), 1);
   for (uint32_t i = threadIdx.x; i < p.K; i += kStepBlock) {
     qs[i] = to_f32(q[i]);
     ks[i] = to_f32(k[i]);
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(kStepBlock) void k_attn_step(AttnStep p, uint32_t l
         const float kk = ks[i], qq = qs[i];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          s[j][e] = fmaf(w, s[j][e], kk * vv[e]);
+          s[j][e] = fmaf(w.hi, s[j][e], fmaf(w.lo, s[j][e], kk * vv[e]));
           acc[e] = fmaf(qq, s[j][e], acc[e]);
         }
         vec* at = reinterpret_cast<vec*>(st + (uint64_t)i * p.V);

@@ -26,8 +26,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ float attn_rate(float r) { return r > 3.402823466e38f ? 3.402823466e38f : r; }
 
 // exp(-rate n) as the sum of two floats.  A carry is multiplied by it once per
-// chunk: with one float, the rounding of a weight near 1 would add up, the
-// same way each time, over the thousands of chunks that a slow decay reaches.
+// segment, or per single token: with one float, the rounding of a weight near 1
+// would add up, the same way each time, over the thousands of them that a slow
+// decay reaches (rate 1e-4, 6000 single tokens: 8e-5 of the state).
 struct AttnDecay {
   float hi, lo;
   __device__ __forceinline__ float of(float s) const { return fmaf(s, hi, s * lo); }
