@@ -327,8 +327,9 @@ typedef struct {
 enum { LAPLEX_ATTN_FORWARD = 0, LAPLEX_ATTN_BACKWARD = 1 };
 
 /* Bytes of workspace a decayed-attention call needs (pass: LAPLEX_ATTN_FORWARD
- * or LAPLEX_ATTN_BACKWARD; offsets, rate and strides are not looked at).
- * Returns 0 when the shape is out of range. */
+ * or LAPLEX_ATTN_BACKWARD; offsets, rate and strides are not looked at).  They
+ * serve any call with fewer tokens or sequences too.  Returns 0 when the shape
+ * is out of range, and where no workspace is needed. */
 size_t laplex_decay_attn_workspace_bytes(int pass, const laplex_attn_shape* shape);
 
 /* Decayed linear attention: the lower half of the Laplace kernel (section 2.2,
@@ -410,7 +411,8 @@ laplex_status laplex_layer_norm_backward(int dtype, uint64_t rows, uint32_t widt
 laplex_status laplex_embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* table, uint32_t vocab,
                                uint32_t width, float scale, void* y, hipStream_t stream);
 
-/* Bytes of workspace of laplex_embedding_backward; 0 when out of range. */
+/* Bytes of workspace of laplex_embedding_backward, which serve any call with
+ * fewer tokens too; 0 when out of range. */
 size_t laplex_embedding_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t width);
 
 /* Gradient of the whole table for the upstream gradient dy (tokens x width,

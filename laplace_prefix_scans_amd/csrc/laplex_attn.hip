@@ -62,17 +62,33 @@ struct AttnPlan {
   bool split;
 };
 // The split depends on K and V alike, so that a pass and the one with K and V exchanged share their segments.
-static int64_t attn_seg_len(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+struct AttnSplit {
+  uint64_t least;   // tokens of a segment, at least
+  uint64_t across;  // blocks across heads and columns
+  uint64_t blocks;  // that run at once
+};
+static AttnSplit attn_split(int dtype, uint32_t heads, uint32_t K, uint32_t V, bool rate) {
   const uint32_t wide = std::max(K, V), slices = wide > 128 ? 2 : 1;
   // Blocks that run at once: 256 CUs with two of eight waves or four of four; half with the lag-weighted carry.
   // (65536 tokens x 8 heads, 128 x 128: 234 us; with half as many blocks 274, with twice as many 263.  16384 tokens
   // x 16 heads forward and backward: 609, 680, 729.)  At least two chunks each (1000 tokens x 8 heads of
   // floats forward and backward: 173 us, with four chunks 216; 128 tokens x 64 heads in bfloat16: 16, with one chunk 36).
-  const uint64_t blocks = (wide <= 64 ? 1024 : 512) / (rate ? 2 : 1);
-  uint64_t len = std::max<uint64_t>(dtype == LAPLEX_BF16 ? 128 : 64, tokens * heads * slices / blocks);
+  return {dtype == LAPLEX_BF16 ? 128u : 64u, (uint64_t)heads * slices, (wide <= 64 ? 1024u : 512u) / (rate ? 2 : 1)};
+}
+static int64_t attn_seg_len(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+  const AttnSplit f = attn_split(dtype, heads, K, V, rate);
+  uint64_t len = std::max<uint64_t>(f.least, tokens * f.across / f.blocks);
   len = (len + 63) / 64 * 64;
   // Two segments cost more than one of twice the length (2048 tokens x 256 heads: 247 us, 208; 256 x 8: 24, 19).
   return (int64_t)(2 * len < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
+}
+// Boundaries between segments (tokens / seg_len + 1, none without a split), the most over all smaller numbers of tokens,
+// so that a workspace for many tokens serves fewer.  seg_len is at least `least`, and at least 64 / 65 of tokens *
+// across / blocks (that quotient is rounded down, then up to a multiple of 64).
+static uint64_t attn_bounds_most(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
+  const AttnSplit f = attn_split(dtype, heads, K, V, rate);
+  if (tokens <= 2 * f.least || 128 * f.across >= 65 * f.blocks) return 0;  // two segments are not less than the tokens
+  return std::min(tokens / f.least, f.blocks * 65 / (f.across * 64)) + 1;
 }
 static AttnPlan attn_plan(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   AttnPlan q;
@@ -91,8 +107,11 @@ static AttnPlan attn_plan(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, 
 }
 
 size_t attn_pass_bytes(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
-  const AttnPlan q = attn_plan(dtype, 1, heads, K, V, tokens, rate);
-  return (size_t)q.bounds * heads * K * V * 4 * (rate ? 2 : 1);
+  return (size_t)attn_bounds_most(dtype, heads, K, V, tokens, rate) * heads * K * V * 4 * (rate ? 2 : 1);
+}
+uint64_t attn_drate_parts_most(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens) {
+  // attn_slots with or without offsets, by the slices of the narrowest blocks
+  return (std::max<uint64_t>(attn_bounds_most(dtype, heads, K, V, tokens, true), 1) + seqs + 3) * ((V + 63) / 64);
 }
 uint64_t attn_drate_parts(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets) {
   const AttnPlan q = attn_plan(dtype, seqs, heads, K, V, tokens, true);
@@ -108,6 +127,10 @@ hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s) {
   const bool rate = p.drate_part != nullptr, bf = p.dtype == LAPLEX_BF16;
   const size_t e = bf ? 2 : 4;
   const AttnPlan q = attn_plan(p.dtype, p.seqs, p.heads, p.K, p.V, p.tokens, rate);
+  if (q.bounds > attn_bounds_most(p.dtype, p.heads, p.K, p.V, p.tokens, rate) ||
+      (rate && attn_drate_parts(p.dtype, p.seqs, p.heads, p.K, p.V, p.tokens, p.offsets) >
+                   attn_drate_parts_most(p.dtype, p.seqs, p.heads, p.K, p.V, p.tokens)))
+    return hipErrorInvalidValue;  // (more than the workspace was laid out for)
   AttnChunkArgs a{};
   a.p = p;
   a.g = {p.offsets, p.tokens, p.seqs, q.seg_len};

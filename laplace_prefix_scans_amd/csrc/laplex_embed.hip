@@ -433,17 +433,22 @@ hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, 
   return hipGetLastError();
 }
 
-uint32_t embed_chunk(uint64_t tokens) { return tokens <= 32768 ? 32 : 64; }
+constexpr uint64_t kEmbedShort = 32768;
+uint32_t embed_chunk(uint64_t tokens) { return tokens <= kEmbedShort ? 32 : 64; }
 uint64_t embed_starts(uint32_t vocab) { return (1ull << key_bits(vocab)) + 1; }
 // The general sort takes seven to nine launches whatever the size; tiles take two, and reads of every tile's starts
 // by every token (lookup and gradient, 49625 tokens, 58298 x 136: 82 -> 53 us; 131072 tokens, 65536 x 64: 88 -> 74).
+constexpr uint64_t kEmbedTiled = kEmbedTiles * (uint64_t)kEmbedSmall;
+uint64_t embed_tiled_most(uint64_t tokens, uint32_t vocab) {
+  return tokens > (uint64_t)kEmbedSmall && key_bits(vocab) <= kFindBits ? std::min(tokens, kEmbedTiled) : 0;
+}
+uint32_t embed_tiles_of(uint64_t tiled) { return (uint32_t)((tiled + kEmbedSmall - 1) / kEmbedSmall); }
 uint32_t embed_tiles(uint64_t tokens, uint32_t vocab) {
-  return tokens > (uint64_t)kEmbedSmall && tokens <= kEmbedTiles * (uint64_t)kEmbedSmall && key_bits(vocab) <= kFindBits
-             ? (uint32_t)((tokens + kEmbedSmall - 1) / kEmbedSmall) : 0;
+  return tokens <= kEmbedTiled ? embed_tiles_of(embed_tiled_most(tokens, vocab)) : 0;
 }
 uint64_t embed_part_floats(uint64_t tokens, uint32_t width) {
-  const uint32_t c = embed_chunk(tokens);
-  return (tokens + c - 1) / c * 2 * width;
+  auto chunks = [](uint64_t n) { return (n + embed_chunk(n) - 1) / embed_chunk(n); };
+  return std::max(chunks(tokens), chunks(std::min(tokens, kEmbedShort))) * 2 * width;
 }
 
 template <typename T, typename O, int E, bool WHOLE>

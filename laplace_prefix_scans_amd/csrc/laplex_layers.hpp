@@ -46,9 +46,10 @@ struct AttnPass {
   double* drate_part;  // partials of the rate gradient ([attn_drate_parts][head])
 };
 hipError_t attn_pass(const AttnPass& p, void* ws, hipStream_t s);
+// bytes of workspace of a pass, and partials of the rate's gradient, that serve this many tokens and any fewer
 size_t attn_pass_bytes(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate);
+uint64_t attn_drate_parts_most(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens);
 // number of partials per head an attn_pass with drate_part writes ([partial][head])
-// (largest with offsets, whatever they hold)
 uint64_t attn_drate_parts(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, const int32_t* offsets);
 hipError_t attn_drate_reduce(const double* part, uint64_t parts, uint32_t heads, float* drate, hipStream_t s);
 // dst[t][g][c] = sum of src[t][g * group + i][c] over i < group (src in float)
@@ -88,8 +89,11 @@ struct EmbedWorkspace {
   uint32_t *tile_perm, *tile_starts;
 };
 uint64_t embed_starts(uint32_t vocab);
-uint32_t embed_tiles(uint64_t tokens, uint32_t vocab);
+// sizes that serve this many tokens and any fewer: tokens that are sorted in tiles, floats of partial rows
+uint64_t embed_tiled_most(uint64_t tokens, uint32_t vocab);
 uint64_t embed_part_floats(uint64_t tokens, uint32_t width);
+uint32_t embed_tiles(uint64_t tokens, uint32_t vocab);
+uint32_t embed_tiles_of(uint64_t tiled);
 hipError_t embedding_backward(const EmbedWorkspace& w, int dtype, const void* ids, int id_bytes, uint64_t tokens, const void* dy,
                               uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, hipStream_t s);
 

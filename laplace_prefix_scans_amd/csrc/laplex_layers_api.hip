@@ -64,13 +64,6 @@ bool any_misaligned(const Extent (&v)[N], size_t a) {
   return false;
 }
 
-// partials of the rate gradient with or without offsets
-uint64_t drate_parts_most(const laplex_attn_shape& a) {
-  static const int32_t some = 0;
-  return std::max(attn_drate_parts(a.dtype, a.seqs, a.heads, a.dv, a.dk, a.tokens, &some),
-                  attn_drate_parts(a.dtype, a.seqs, a.heads, a.dv, a.dk, a.tokens, nullptr));
-}
-
 struct AttnWorkspace {
   void* pass;    // of one recurrence pass at a time
   float* sum;    // per query head gradients before they are added over a shared head
@@ -84,7 +77,7 @@ AttnWorkspace carve_attn(void* ws, int pass, const laplex_attn_shape& a, size_t*
   w.pass = c.take<void>(b);
   if (pass == LAPLEX_ATTN_BACKWARD) {
     if (a.heads != a.kv_heads) w.sum = c.take<float>(a.tokens * a.heads * std::max(a.dk, a.dv) * 4);
-    w.drate = c.take<double>(a.seqs ? drate_parts_most(a) * a.heads * 8 : 0);
+    w.drate = c.take<double>(a.seqs ? attn_drate_parts_most(a.dtype, a.seqs, a.heads, a.dv, a.dk, a.tokens) * a.heads * 8 : 0);
   }
   *total = (c.off + 255) & ~size_t(255);
   return w;
@@ -311,9 +304,9 @@ EmbedWorkspace carve_embed(void* ws, uint64_t tokens, uint32_t vocab, uint32_t w
   w.perm = c.take<uint32_t>(tokens * 4);
   w.starts = c.take<uint32_t>(embed_starts(vocab) * 4);
   w.part = c.take<float>(embed_part_floats(tokens, width) * 4);
-  const uint32_t tiles = embed_tiles(tokens, vocab);
-  w.tile_perm = c.take<uint32_t>(tiles ? tokens * 4 : 0);
-  w.tile_starts = c.take<uint32_t>(tiles * embed_starts(vocab) * 4);
+  const uint64_t tiled = embed_tiled_most(tokens, vocab);
+  w.tile_perm = c.take<uint32_t>(tiled * 4);
+  w.tile_starts = c.take<uint32_t>(embed_tiles_of(tiled) * embed_starts(vocab) * 4);
   *total = (c.off + 255) & ~size_t(255);
   return w;
 }
