@@ -7,7 +7,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._binding import _check, _ptr, _stream, lib
+from ._binding import LaplexError, _check, _ptr, _stream, lib
 
 LAPLEX_F32, LAPLEX_BF16 = 0, 1
 LAPLEX_ATTN_FORWARD, LAPLEX_ATTN_BACKWARD = 0, 1
@@ -61,6 +61,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream_of(dev: torch.device) -> int:
     return _raw_stream(dev.index) if _raw_stream is not None else _stream(dev)
+
+
+def _u32(where: str, sizes: int) -> None:
+    """Sizes (or-ed together) go to the library in 32 bits: ctypes would wrap larger ones before its checks see them."""
+    if sizes >> 32:
+        raise LaplexError(2, where)  # LAPLEX_ERR_SIZE
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -137,6 +143,7 @@ def _shape(q, k, v, rate, offsets, scale) -> _Shape:
     heads, kv_heads = qs[-2], ks[-2]
     if kv_heads == 0 or heads % kv_heads:
         raise ValueError("the %d heads of k and v must divide the %d of q" % (kv_heads, heads))
+    _u32("decayed attention", qs[0] | heads | qs[-1] | vs[-1])
     if rate is None:
         raise TypeError("rate must be a torch tensor")
     _like(rate, "rate", (heads,), torch.float32, dev)
@@ -148,6 +155,7 @@ def _shape(q, k, v, rate, offsets, scale) -> _Shape:
             raise ValueError("offsets must be a 1-D tensor of sequence starts and the end of the last")
         _like(offsets, "offsets", offsets.shape, torch.int32, dev)
         seqs = offsets.numel() - 1
+        _u32("decayed attention", seqs)
     tokens = qs[0] * qs[1] if batched else qs[0]
     (qt, qh), (kt, kh), (vt, vh) = (_strides(q, qs, "q", batched), _strides(k, ks, "k", batched),
                                     _strides(v, vs, "v", batched))
@@ -231,6 +239,7 @@ def laplex_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ra
         raise ValueError("state must be (pool, heads, dk, dv)")
     _like(state, "state", (state.shape[0], s.heads, s.dk, s.dv), torch.float32, dev)
     _like(slots, "slots", (s.seqs,), torch.int32, dev)
+    _u32("laplex_decay_attn_step", state.shape[0])
     if slots is None and s.seqs > state.shape[0]:
         raise ValueError("state must have a row for each of the %d tokens" % s.seqs)
     o = _out(o, "o", (s.seqs, s.heads, s.dv), q.dtype, dev)
@@ -247,6 +256,7 @@ def _rows(x: torch.Tensor, name: str) -> Tuple[int, int, int]:
     if not x.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     width = x.shape[-1]
+    _u32("layer norm", width)
     return code, x.numel() // width, width
 
 
@@ -304,6 +314,7 @@ def laplex_embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
     nb = _ids(ids, dev)
     if table.dim() != 2 or table.shape[1] == 0 or not table.is_contiguous():
         raise ValueError("table must be a contiguous (vocab, width) tensor")
+    _u32("laplex_embedding", table.shape[0] | table.shape[1])
     y = _out(y, "y", (*ids.shape, table.shape[1]), table.dtype, dev)
     _check(_lib().laplex_embedding(code, _ptr(ids), nb, ids.numel(), _ptr(table), table.shape[0], table.shape[1], scale, _ptr(y),
                                    _stream_of(dev)), "laplex_embedding")
@@ -323,6 +334,7 @@ def laplex_embedding_backward(ids: torch.Tensor, dy: torch.Tensor, vocab: int, s
     if vocab < 0:
         raise ValueError("vocab must not be negative")
     width = dy.shape[-1]
+    _u32("laplex_embedding_backward", vocab | width)
     dtype = (dy.dtype if dtable is None else dtable.dtype) if dtype is None else dtype
     if dtype not in (torch.float32, dy.dtype):
         raise TypeError("the table's gradient is float32 or of the type of dy")

@@ -1,4 +1,4 @@
-"""Batches of one token a sequence as slices of longer ones, workspaces larger than a call needs, and sizes past 32 bits."""
+"""Batches of one token a sequence that are slices of longer ones."""
 import pytest
 
 from gpu_util import have_gpu

@@ -53,3 +53,13 @@ def test_an_embedding_workspace_serves_fewer_tokens(L, shape):
         need = L.laplex_embedding_workspace_bytes(tokens, vocab, width)
         assert need >= last, tokens
         last = need
+
+
+def test_sizes_past_32_bits_are_refused():
+    import laplace_prefix_scans_amd as lp
+    from laplace_prefix_scans_amd._layers import _u32
+    _u32("x", 0 | 1 | (1 << 32) - 1)
+    for n in (1 << 32, (1 << 32) + 8, -1):
+        with pytest.raises(lp.LaplexError) as e:
+            _u32("x", 4 | n)
+        assert e.value.code == 2
