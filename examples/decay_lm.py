@@ -20,6 +20,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import laplace_prefix_scans_amd as lp  # noqa: E402
@@ -33,6 +34,7 @@ class Embedding(torch.autograd.Function):
         return lp.laplex_embedding(ids, table, scale=scale)
 
     @staticmethod
+    @once_differentiable  # the library has first derivatives
     def backward(ctx, g):
         (ids,) = ctx.saved_tensors
         return None, lp.laplex_embedding_backward(ids, g.contiguous(), ctx.vocab, scale=ctx.scale), None
@@ -47,8 +49,11 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable  # the library has first derivatives
     def backward(ctx, g):
         x, mean, rstd, weight = ctx.saved_tensors
+        if not any(ctx.needs_input_grad[1:]):
+            return lp.laplex_layer_norm_backward(x, g.contiguous(), mean, rstd, weight, param_grads=False)
         dx, dw, db = lp.laplex_layer_norm_backward(x, g.contiguous(), mean, rstd, weight)
         return dx, dw.to(weight.dtype), db.to(weight.dtype)
 
@@ -61,9 +66,11 @@ class DecayAttention(torch.autograd.Function):
         return lp.laplex_decay_attn(q, k, v, rate, offsets=offsets, scale=scale)
 
     @staticmethod
+    @once_differentiable  # the library has first derivatives
     def backward(ctx, g):
         q, k, v, rate, offsets = ctx.saved_tensors
-        dq, dk, dv, drate, _ = lp.laplex_decay_attn_backward(q, k, v, rate, g.contiguous(), offsets=offsets, scale=ctx.scale)
+        dq, dk, dv, drate, _ = lp.laplex_decay_attn_backward(q, k, v, rate, g.contiguous(), offsets=offsets, scale=ctx.scale,
+                                                             rate_grad=ctx.needs_input_grad[3])
         return dq, dk, dv, drate, None, None
 
 
