@@ -38,8 +38,7 @@ inline uint64_t attn_slots(const AttnSegs& g) {
   return g.tokens / g.seg_len + g.seqs + 3;
 }
 // Boundaries between two segments of one sequence lie at least seg_len tokens
-// apart over all sequences, so position / seg_len numbers them uniquely.
-inline uint64_t attn_bounds(uint64_t tokens, int64_t seg_len) { return tokens / seg_len + 1; }
+// apart over all sequences, so position / seg_len numbers them uniquely (AttnPlan::bounds).
 
 // a value that every lane holds, in scalar registers
 template <typename V>
