@@ -70,16 +70,17 @@ struct AttnSplit {
 static AttnSplit attn_split(int dtype, uint32_t heads, uint32_t K, uint32_t V, bool rate) {
   const uint32_t wide = std::max(K, V), slices = wide > 128 ? 2 : 1;
   // Blocks that run at once: 256 CUs with two of eight waves or four of four; half with the lag-weighted carry.
-  // (65536 tokens x 8 heads, 128 x 128: 234 us; with half as many blocks 274, with twice as many 263.  16384 tokens
-  // x 16 heads forward and backward: 609, 680, 729.)  At least two chunks each (1000 tokens x 8 heads of
-  // floats forward and backward: 173 us, with four chunks 216; 128 tokens x 64 heads in bfloat16: 16, with one chunk 36).
+  // (65536 tokens x 8 heads, 128 x 128: 252 us; with half as many blocks 275, with twice as many 274.  8 x 2048 tokens
+  // x 16 heads forward and backward: 600, 719, 685.)  At least two chunks each (1000 tokens x 8 heads of
+  // floats, 128 x 128, forward and backward: 139 us, with one chunk 138, with four 185; 4000 x 8 heads in bfloat16: 174, 191, 189).
   return {dtype == LAPLEX_BF16 ? 128u : 64u, (uint64_t)heads * slices, (wide <= 64 ? 1024u : 512u) / (rate ? 2 : 1)};
 }
 static int64_t attn_seg_len(int dtype, uint32_t heads, uint32_t K, uint32_t V, uint64_t tokens, bool rate) {
   const AttnSplit f = attn_split(dtype, heads, K, V, rate);
   uint64_t len = std::max<uint64_t>(f.least, tokens * f.across / f.blocks);
   len = (len + 63) / 64 * 64;
-  // Two segments cost more than one of twice the length (2048 tokens x 256 heads: 247 us, 208; 256 x 8: 24, 19).
+  // Two segments cost more than one of twice the length (2048 tokens x 256 heads: 222 us, 197; 256 x 8: 23.9, 21.9),
+  // three do not (300 x 4 heads, 64 x 64, forward and backward: 89 us, unsplit 102; 2048 x 200 heads: 198, 197).
   return (int64_t)(2 * len < tokens ? len : std::max<uint64_t>(64, (tokens + 63) / 64 * 64));
 }
 // Boundaries between segments (tokens / seg_len + 1, none without a split), the most over all smaller numbers of tokens,
@@ -94,10 +95,12 @@ static AttnPlan attn_plan(int dtype, uint32_t seqs, uint32_t heads, uint32_t K, 
   AttnPlan q;
   q.kp = K <= 64 ? 64 : K <= 128 ? 128 : 256;
   q.seg_len = attn_seg_len(dtype, heads, K, V, tokens, rate);
-  // V of at most 64 needs four waves (16384 tokens x 16 heads, 128 x 64, forward and backward: 498 us with eight, 469).
-  // Where blocks of 128 columns would leave a good part of the 256 CUs idle, blocks of 64 share a chunk's work out
-  // among twice as many (131 tokens x 4 heads, 80 x 96, float: 34 -> 25 us; 2048 x 8 heads, 128 x 128, bfloat16, 136
-  // blocks, forward and backward: 182 -> 161; at 264 blocks 209 -> 223, at 250 without backward 23 -> 26.5).
+  // V of at most 64 needs four waves (16384 tokens x 16 heads, 64 x 64, forward and backward: 333 us with eight, 300;
+  // in float 624, 533; 128 x 64: 427 either way).  Where blocks of 128 columns would leave a good part of the 256 CUs
+  // idle, blocks of 64 share a chunk's work out among twice as many (131 tokens x 4 heads, 80 x 96, float: 34 -> 25 us;
+  // 2048 x 8 heads, 128 x 128, bfloat16, 136 blocks, forward and backward: 157 -> 138; at 264 blocks 175 -> 197).  In
+  // between it depends: at 152 blocks 2304 tokens in bfloat16 take 155 -> 176, for the rate's gradient has one block a CU
+  // and then two rounds of them, but without backward 36.0 -> 36.1, and 1200 tokens in float 190 -> 175.
   const uint64_t blocks = (tokens / q.seg_len + seqs) * heads * ((V + 127) / 128);
   q.nw = q.kp <= 128 && (V <= 64 || blocks <= 160) ? 4 : 8;
   q.slices = (V + 16 * q.nw - 1) / (16 * q.nw);

@@ -433,6 +433,9 @@ hipError_t embedding(int dtype, const void* ids, int id_bytes, uint64_t tokens, 
   return hipGetLastError();
 }
 
+// Tokens of a chunk.  Gradient with chunks of 32 and of 64: 4096 tokens, 257 x 513 float, 16.5 us and 18.7; 16384,
+// 65536 x 128 bfloat16, 30 and 35, but 65536 x 2048 93 and 87; 32768, 65536 x 512, 44.7 and 45.1; 65536, the same,
+// 64 and 57; 131072, 5000 x 1024, 144 and 114 (with 128: 99).
 constexpr uint64_t kEmbedShort = 32768;
 uint32_t embed_chunk(uint64_t tokens) { return tokens <= kEmbedShort ? 32 : 64; }
 uint64_t embed_starts(uint32_t vocab) { return (1ull << key_bits(vocab)) + 1; }

@@ -12,6 +12,10 @@
 // partials.  16384 rows of 4096 bfloat16: forward 49 us, 5.4 TB/s; backward 84 us,
 // 4.8 TB/s, and 5 us for the partials.  Rows longer than 32768 bfloat16 (16384 float) elements are
 // read again instead of held.
+// The backward holds less than it should of long rows: a thread of 1024 has 128 registers, and above 8192 bfloat16 or
+// float elements 76 to 325 of its values spill to scratch.  TB/s, forward and backward, of tensors of 67 to 268 MB: bfloat16
+// 1024 columns 5.3, 5.4; 2048 4.6, 4.8; 8192 5.1, 4.1; 12288 3.8, 1.4; 32768 3.2, 0.7 (read again: 1.3, 1.0); float 1024 to
+// 8192 5.6 to 5.8, 4.8 to 5.3; 12288 and 16384 5.8, 2.2 and 2.4 (read again: 2.0, 2.0).
 #include "laplex_layers.hpp"
 #include "laplex_layers_device.hpp"
 
@@ -19,7 +23,8 @@ namespace laplex {
 
 constexpr int kNormBlock = 256;
 constexpr uint32_t kNormBlocks = 2048;  // 256-thread blocks of a forward pass (eight a CU), each taking rows in turn
-constexpr uint32_t kNormParts = 512;  // at most so many partials of the weight gradient (two 256-thread blocks a CU)
+constexpr uint32_t kNormParts = 512;  // at most so many partials of the weight gradient (two 256-thread blocks a CU; the
+                                      // shapes of 1025 to 2048 and 4097 to 8192 bfloat16 elements have registers for one or two)
 
 // ------------------------------------------------------------------ rows in registers
 // VEC: every row begins at a multiple of 16 bytes and has whole 16-byte pieces.  Without, the pieces are the same
