@@ -314,10 +314,11 @@ def laplex_embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
     nb = _ids(ids, dev)
     if table.dim() != 2 or table.shape[1] == 0 or not table.is_contiguous():
         raise ValueError("table must be a contiguous (vocab, width) tensor")
-    _u32("laplex_embedding", table.shape[0] | table.shape[1])
-    y = _out(y, "y", (*ids.shape, table.shape[1]), table.dtype, dev)
-    _check(_lib().laplex_embedding(code, _ptr(ids), nb, ids.numel(), _ptr(table), table.shape[0], table.shape[1], scale, _ptr(y),
-                                   _stream_of(dev)), "laplex_embedding")
+    vocab, width = table.shape
+    _u32("laplex_embedding", vocab | width)
+    y = _out(y, "y", (*ids.shape, width), table.dtype, dev)
+    _check(_lib().laplex_embedding(code, _ptr(ids), nb, ids.numel(), _ptr(table), vocab, width, scale, _ptr(y), _stream_of(dev)),
+           "laplex_embedding")
     return y
 
 
