@@ -383,7 +383,9 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
   __shared__ __attribute__((aligned(16))) T zs[ZB][C * BV];
   __shared__ __attribute__((aligned(16))) T dots[2][DOT ? C * BV : 8];
   __shared__ __attribute__((aligned(16))) float down[C], downlag[RATE ? C : 4];
-  __shared__ float dec[FULL ? C + 1 : 1];  // exp(-rate n)
+  // Weights of pairs by their lag and of the carry.  bf16: exp(-rate n) alone, for its LDS is full; float: the products,
+  // 0 for lags below 0, for its registers are (formed anew, 32 of the eight-wave pass spill).
+  __shared__ float dec[FULL && BF ? C + 1 : 1], wt[FULL && !BF ? 2 * C : 1], up[FULL && !BF ? C : 1];
   // bf16: operands of the weighted pairs (pair_at; the lag-weighted ones behind them); float: [wave][tile]
   constexpr int PAIRS = 10 * 3 * kWave;  // 8-byte words
   __shared__ __attribute__((aligned(16))) uint2 pairs[FULL ? (BF ? (RATE ? 2 : 1) * PAIRS : WK * 3 * kWave * 2) : 2];
@@ -476,9 +478,17 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
   }
 
   if constexpr (FULL) {
-    if (threadIdx.x <= C) dec[threadIdx.x] = decay(-rate * (float)threadIdx.x);
+    if constexpr (BF) {
+      if (threadIdx.x <= C) dec[threadIdx.x] = decay(-rate * (float)threadIdx.x);
+    } else {
+      for (int i = threadIdx.x; i < 2 * C; i += THREADS) wt[i] = i >= C ? p.c_pair * decay(-rate * (float)(i - C)) : 0.f;
+      if (threadIdx.x < C) up[threadIdx.x] = p.c_in * decay(-rate * (float)((int)threadIdx.x + lead));
+    }
   }
-  auto pair_weight = [&](int lag) { return lag >= 0 ? p.c_pair * dec[lag] : 0.f; };
+  auto pair_weight = [&](int lag) {
+    if constexpr (BF) return lag >= 0 ? p.c_pair * dec[lag] : 0.f;
+    else return wt[C + lag];
+  };
   // The carry's decay over a chunk.  As one float its rounding would add up, the same way each time, over the
   // thousands of chunks that a slow decay reaches: each chunk takes the float nearest to what brings the product
   // so far back to the exact one.
@@ -681,7 +691,7 @@ __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW =
         }
 #pragma unroll
         for (int t = 0; t < IT; ++t) {
-          const float f = p.c_in * dec[16 * t + lc + lead];
+          const float f = BF ? p.c_in * dec[16 * t + lc + lead] : up[16 * t + lc];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if constexpr (RATE) OD[t][r] = f * fmaf((float)(16 * t + lc + lead), O[t][r], OD[t][r]);
