@@ -300,7 +300,8 @@ laplex_status laplex_gram_weighted(const float* a_sorted, const uint32_t* perm_a
  * attention, layer norm, and embedding.  Their tensors are float32 or
  * bfloat16 (one type per call), states, statistics and parameter sums are
  * float32.  The conventions at the top of this header hold, with these
- * sizes: up to 2^31 - 1 tokens, up to 256 channels per head.
+ * sizes: up to 2^31 - 1 tokens, up to 256 channels per head.  A tensor is
+ * aligned to its element (bfloat16: 2 bytes; ids: 4 or 8).
  * --------------------------------------------------------------------- */
 enum { LAPLEX_F32 = 0, LAPLEX_BF16 = 1 };
 
@@ -365,7 +366,8 @@ laplex_status laplex_decay_attn(const laplex_attn_shape* shape, const void* q, c
  * states are formed again.  dq (tokens x heads x dk), dk (tokens x kv_heads x
  * dk), dv (tokens x kv_heads x dv): contiguous; drate: heads floats, or NULL;
  * dstate_in: NULL or seqs x heads x dk x dv floats.  Sums are taken in a fixed
- * order: a call repeated gives the same bits.
+ * order: a call repeated gives the same bits.  With drate, dq's sums may be cut
+ * into other segments than without.
  * ws: laplex_decay_attn_workspace_bytes(LAPLEX_ATTN_BACKWARD, shape) bytes. */
 laplex_status laplex_decay_attn_backward(const laplex_attn_shape* shape, const void* q, const void* k, const void* v,
                                          const void* go, const float* state_in, const float* dstate_out, void* dq, void* dk,
