@@ -366,10 +366,10 @@ __device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) { return __buil
 // waves share a SIMD and one's conversions run beside another's products;
 // 32 columns in half as many waves took as long without the rate's gradient, and a quarter longer with it.
 // Measured (bfloat16, 128 x 128; averages).  States alone, 65536 tokens x 8 heads: 73 us for 302 MB, 4.1 TB/s.  The whole
-// pass there: 193 us for 570 MB, 3.0 TB/s.  Reads and writes alone take 110 us; the rest is what the four waves of a SIMD do
+// pass there: 187 us for 570 MB, 3.0 TB/s.  Reads and writes alone take 110 us; the rest is what the four waves of a SIMD do
 // not hide of 119 products and about 650 vector instructions a chunk and wave.  Products that do not follow one they add to, and
 // fewer instructions to split a float (by two-element dot products), changed nothing.  With the rate's
-// gradient, 16384 tokens x 16 heads: 206 us, against 101 without; it has a second carry in three parts and registers for two
+// gradient, 16384 tokens x 16 heads: 207 us, against 103 without; it has a second carry in three parts and registers for two
 // waves a SIMD.
 template <typename T, int KP, int NW, bool FULL, bool RATE, bool VEC>
 __global__ __launch_bounds__(NW * kWave, KP == 256 || RATE || (KP == 128 && NW == 4) ? 2 : 4) void k_attn_chunk(AttnChunkArgs a) {
