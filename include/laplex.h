@@ -429,6 +429,135 @@ laplex_status laplex_embedding_backward(int dtype, const void* ids, int id_bytes
                                         uint32_t vocab, uint32_t width, float scale, int table_dtype, void* dtable, void* ws,
                                         size_t ws_bytes, hipStream_t stream);
 
+/* --------------------------------------------------------------------------
+ * A training step around those layers: the gated linear recurrence (a mixer
+ * whose decays the data give), the softmax cross entropy of a linear output
+ * table, and the AdamW update.  Conventions as for the layers above.
+ * --------------------------------------------------------------------- */
+enum { LAPLEX_GATE_RATE = 0, LAPLEX_GATE_SIGMOID = 1 };
+
+/* Tokens between two carries that laplex_gated_scan keeps for its backward. */
+#define LAPLEX_SCAN_CHUNK 16
+
+/* Shape of a gated-recurrence call.  gate and x: tokens x channels of the type
+ * dtype, channels contiguous, token t at t * gate_token (x_token) elements;
+ * strides are >= 0.  Sequences as in laplex_attn_shape: [offsets[s],
+ * offsets[s + 1]), or seqs of equal length with offsets NULL; the output and
+ * gradient rows of tokens of no sequence are zero. */
+typedef struct {
+  int32_t dtype;                  /* LAPLEX_F32 or LAPLEX_BF16: gate, x, h and their gradients */
+  int32_t gate;                   /* LAPLEX_GATE_RATE or LAPLEX_GATE_SIGMOID */
+  uint32_t seqs, channels;
+  uint64_t tokens;                /* tokens of all sequences */
+  const int32_t* offsets;         /* DEVICE, or NULL: equal lengths */
+  int64_t gate_token, x_token;    /* strides in elements */
+} laplex_scan_shape;
+
+/* Bytes of workspace of laplex_gated_scan and of its backward, which serve any
+ * call with fewer tokens or sequences too; 0 when out of range, and where none
+ * is needed. */
+size_t laplex_gated_scan_workspace_bytes(const laplex_scan_shape* shape);
+
+/* Gated linear recurrence: the affine scan of section 2.2 with decays that
+ * every token and channel brings along,
+ *     h_t = a_t h_{t-1} + w_t x_t,
+ *     LAPLEX_GATE_RATE:     a = exp(-gate), w = 1   (gate >= 0, +Inf: a = 0),
+ *     LAPLEX_GATE_SIGMOID:  a = sigmoid(gate), w = 1 - a.
+ * The state is float32 whatever the type, and decays near 1 are applied by
+ * their distance from 1.  state_in: NULL (zero) or the state before each
+ * sequence's first token (seqs x channels floats); state_out: NULL or the
+ * state after its last one (an empty sequence's is its state_in).  h: tokens x
+ * channels, contiguous.  carries: NULL, or the states that the backward reads:
+ * ceil(tokens / LAPLEX_SCAN_CHUNK) x channels floats.  A non-finite value
+ * stays in its channel and sequence, and after it in time.  A call repeated
+ * gives the same bits; another number of tokens or channels may cut a sequence
+ * into other segments, whose float32 results differ in their last bits. */
+laplex_status laplex_gated_scan(const laplex_scan_shape* shape, const void* gate, const void* x, const float* state_in,
+                                float* state_out, void* h, float* carries, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Backward of laplex_gated_scan for dh = dL/dh (tokens x channels, contiguous)
+ * and dstate_out = dL/dstate_out (NULL: zero), from the carries that the
+ * forward call with the same gate, x, offsets and state_in left.  With
+ *     l_t = dh_t + a_{t+1} l_{t+1}   (after a sequence's last token: dstate_out),
+ *     dx = w l,   rate: dgate = -a h_{t-1} l,   sigmoid: dgate = a w (h_{t-1} - x) l,
+ * and dstate_in = a_1 l_1 (NULL, or seqs x channels floats).  dgate, dx: tokens
+ * x channels, contiguous. */
+laplex_status laplex_gated_scan_backward(const laplex_scan_shape* shape, const void* gate, const void* x, const float* carries,
+                                         const void* dh, const float* state_in, const float* dstate_out, void* dgate, void* dx,
+                                         float* dstate_in, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* One token for each of `seqs` rows (shape->tokens == seqs, offsets not looked
+ * at): the state of row r moves on in place and is its output.  state: pool x
+ * channels floats; slots: as in laplex_decay_attn_step. */
+laplex_status laplex_gated_scan_step(const laplex_scan_shape* shape, const void* gate, const void* x, const int32_t* slots,
+                                     uint32_t pool, float* state, void* h, hipStream_t stream);
+
+/* Bytes of workspace of laplex_linear_cross_entropy (pass 0) and of its backward
+ * (pass 1), which serve any call with fewer tokens too; 0 when out of range. */
+size_t laplex_linear_cross_entropy_workspace_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width);
+
+/* Softmax cross entropy of rows against a linear output table, without the
+ * logits in memory:
+ *     l_tv = scale x_t . table_v,   lse_t = log sum_v exp(l_tv),   loss_t = lse_t - l_{t, target_t}.
+ * x: tokens x width and table: vocab x width, contiguous, of type dtype;
+ * targets: `tokens` integers of id_bytes (4 or 8) bytes.  A target outside [0,
+ * vocab) marks a token that is left out: its loss and lse are zero, whatever
+ * its row holds.  loss, lse: `tokens` floats.  Products are added in float32. */
+laplex_status laplex_linear_cross_entropy(int dtype, const void* targets, int id_bytes, uint64_t tokens, const void* x,
+                                          const void* table, uint32_t vocab, uint32_t width, float scale, float* loss,
+                                          float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Backward of laplex_linear_cross_entropy for dloss = dL/dloss and dlse =
+ * dL/dlse (`tokens` floats each; dlse NULL: zero), with the lse that the
+ * forward call gave:
+ *     G_tv = scale [(dloss_t + dlse_t) exp(l_tv - lse_t) - dloss_t [v = target_t]],   dx = G table,   dtable = G^T x.
+ * G is formed in pieces of the vocabulary and rounded once to dtype, as a factor
+ * of the two products.  Tokens that are left out have zero rows in dx and take
+ * no part in dtable.  dx: tokens x width of type dtype; dtable: vocab x width of
+ * type table_dtype (dtype or LAPLEX_F32); either may be NULL. */
+laplex_status laplex_linear_cross_entropy_backward(int dtype, const void* targets, int id_bytes, uint64_t tokens, const void* x,
+                                                   const void* table, uint32_t vocab, uint32_t width, float scale,
+                                                   const float* lse, const float* dloss, const float* dlse, void* dx,
+                                                   int table_dtype, void* dtable, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* One parameter of an AdamW step: n contiguous elements each.  The struct is
+ * read on the host, before the call returns; its pointers are DEVICE. */
+typedef struct {
+  void* p;                     /* of type dtype, updated */
+  const void* g;               /* of type grad_dtype */
+  void *m, *v;                 /* moments: floats, or (8 bits) e4m3 codes, of m and of sqrt(v) */
+  float *m_scale, *v_scale;    /* 8 bits: ceil(n / 256) floats each, what a code of 1 stands for; else NULL */
+  float* master;               /* NULL, or a float32 copy of p, which is then what is updated (p: its rounding) */
+  uint64_t n;
+  float weight_decay;
+} laplex_adamw_tensor;
+
+typedef struct {
+  int32_t dtype, grad_dtype;   /* LAPLEX_F32 or LAPLEX_BF16: of p, of g */
+  int32_t state_bits;          /* 32 or 8 */
+  int32_t stochastic;          /* 8 bits: round with random bits (else to nearest) */
+  uint32_t seed;               /* of those bits, which also depend on the step, the tensor's place in the list and the element */
+  uint64_t step;               /* 1 for the first step */
+  double lr, beta1, beta2, eps;
+  const int32_t* step_dev;     /* DEVICE, or NULL: read in the place of `step` (for captured graphs; below 1: 1) */
+  const float* lr_dev;         /* DEVICE, or NULL: read in the place of lr */
+  const float* grad_scale;     /* DEVICE, or NULL: factor of every gradient; where it is not finite, nothing is changed */
+} laplex_adamw_args;
+
+/* AdamW step over `count` tensors (host array):
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *     p = (1 - lr weight_decay) p - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps),
+ * in float32 without contractions.  8-bit moments are e4m3 codes in blocks of
+ * 256 elements, scaled by the block's largest finite magnitude / 448; sqrt(v) >
+ * 0 is never rounded to zero; a moment that is not finite becomes NaN (its
+ * block's others keep their values).  No two of the call's outputs may overlap,
+ * nor an output and a gradient. */
+laplex_status laplex_adamw(const laplex_adamw_args* args, const laplex_adamw_tensor* tensors, uint32_t count, hipStream_t stream);
+
+/* The values that 8-bit moments stand for: of each tensor, m's to the floats at
+ * p and v's to the floats at master (either may be NULL; g is not looked at). */
+laplex_status laplex_adamw_moments(const laplex_adamw_tensor* tensors, uint32_t count, hipStream_t stream);
+
 /* Short English description of a status code (static storage). */
 const char* laplex_status_string(laplex_status s);
 

@@ -26,6 +26,15 @@ Layers of sequence models around the same recurrence (float32 or bfloat16):
     dx, dw, db = laplex_layer_norm_backward(x, dy, mean, rstd, weight)
     y = laplex_embedding(ids, table, scale)
     dtable = laplex_embedding_backward(ids, dy, vocab, scale)
+
+and a training step around them:
+
+    h, carries = laplex_gated_scan(gate, x, "sigmoid", keep=True)  # h_t = a_t h_{t-1} + (1 - a_t) x_t, a = sigmoid(gate)
+    dgate, dx, _ = laplex_gated_scan_backward(gate, x, carries, dh, "sigmoid")
+    h = laplex_gated_scan_step(gate, x, state, "sigmoid")  # one token, the state updated in place
+    loss, lse = laplex_linear_cross_entropy(x, table, targets)  # of the logits x table^T, which are not kept
+    dx, dtable = laplex_linear_cross_entropy_backward(x, table, targets, lse, dloss)
+    laplex_adamw(params, grads, m, v, lr=3e-4, step=1)  # every tensor in place; moments of 32 or 8 bits
 """
 from ._binding import (  # noqa: F401
     LAPLEX_OP_GENERAL,
@@ -73,4 +82,16 @@ from ._layers import (  # noqa: F401
     laplex_embedding_backward,
     laplex_layer_norm,
     laplex_layer_norm_backward,
+)
+from ._training import (  # noqa: F401
+    LAPLEX_SCAN_CHUNK,
+    laplex_adamw,
+    laplex_adamw_moments,
+    laplex_gated_scan,
+    laplex_gated_scan_backward,
+    laplex_gated_scan_step,
+    laplex_gated_scan_workspace_bytes,
+    laplex_linear_cross_entropy,
+    laplex_linear_cross_entropy_backward,
+    laplex_linear_cross_entropy_workspace_bytes,
 )

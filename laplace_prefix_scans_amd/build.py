@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblaplex.so")
 SOURCES = ["laplex_sort.hip", "laplex_route.hip", "laplex_apply.hip", "laplex_api.hip", "laplex_attn.hip", "laplex_attn_bf16_vec.hip",
-           "laplex_attn_bf16_any.hip", "laplex_attn_f32_vec.hip", "laplex_attn_f32_any.hip", "laplex_norm.hip", "laplex_embed.hip", "laplex_layers_api.hip"]
+           "laplex_attn_bf16_any.hip", "laplex_attn_f32_vec.hip", "laplex_attn_f32_any.hip", "laplex_norm.hip", "laplex_embed.hip", "laplex_layers_api.hip",
+           "laplex_gated.hip", "laplex_xent.hip", "laplex_adamw.hip", "laplex_train_api.hip"]
 PROBE_LIB = os.path.join(HERE, "liblaplex_probe.so")
 PROBE_SOURCES = ["laplex_probe.hip"]
 ARCH = "gfx950"

@@ -1,0 +1,309 @@
+// AdamW over many tensors in one launch, with states in float32 or in 8 bits.
+//
+//   g' = s g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2,
+//   p = (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+//
+// A block takes 2048 elements of a tensor at a time, eight consecutive ones a
+// thread, and reads and writes everything once: bound by HBM.
+//
+// 8-bit states: a block of 256 values (32 threads) shares a float scale, its
+// largest magnitude / 448; m and sqrt(v) are e4m3 codes of the values over it.
+// Rounding is stochastic: 16 random bits below the kept mantissa are added and
+// the rest cut off, so that a state's expectation is the value itself -- rounded
+// to nearest, a second moment that changes by a thousandth a step would never
+// leave its code.  sqrt(v) > 0 never becomes 0, or a step would be divided by eps.
+// The new parameters are made from the moments before they are rounded.
+#include <cmath>
+
+#include "laplex_layers_device.hpp"
+#include "laplex_train.hpp"
+
+namespace laplex {
+
+constexpr int kAdamBlock = 256, kAdamPer = 8, kAdamChunk = kAdamBlock * kAdamPer;
+constexpr int kAdamGroup = 40;  // tensors of a launch: its arguments stay below 4 KB
+
+struct AdamTensor {
+  void* p;
+  const void* g;
+  void *m, *v;
+  float *m_scale, *v_scale, *master;
+  uint64_t n;
+  float keep;        // 1 - lr wd
+  float wd;          // (with lr from the device)
+  uint32_t chunk0;   // chunks of the launch's tensors before this one
+  uint32_t number;   // in the caller's list
+};
+struct AdamArgs {
+  AdamTensor t[kAdamGroup];
+  uint32_t count, chunks;
+  float b1, one_b1, b2, one_b2, eps, rate, root_c2;
+  uint32_t seed;
+  int32_t stochastic;
+  uint64_t step;
+  double lr, beta1, beta2;
+  const int32_t* step_dev;
+  const float *lr_dev, *grad_scale;
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
+
+// MurmurHash3's 32-bit finalizer (public domain)
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
+  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, uint64_t left, float (&v)[kAdamPer]) {
+  T e[kAdamPer];
+  if (left >= kAdamPer) {
+    __builtin_memcpy(e, p, sizeof e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kAdamPer; ++i) e[i] = i < (int)left ? p[i] : T(0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < kAdamPer; ++i) v[i] = to_f32(e[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, uint64_t left, const float (&v)[kAdamPer]) {
+  T e[kAdamPer];
+#pragma unroll
+  for (int i = 0; i < kAdamPer; ++i) e[i] = from_f32<T>(v[i]);
+  if (left >= kAdamPer) {
+    __builtin_memcpy(p, e, sizeof e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kAdamPer; ++i)
+      if (i < (int)left) p[i] = e[i];
+  }
+}
+
+// ------------------------------------------------------------------ e4m3 codes
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint64_t left, float scale, float (&v)[kAdamPer]) {
+  uint32_t w[2] = {0, 0};
+  if (left >= kAdamPer) {
+    __builtin_memcpy(w, p, 8);
+  } else {
+    for (int i = 0; i < (int)left; ++i) w[i / 4] |= (uint32_t)p[i] << i % 4 * 8;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], true);
+    v[4 * i] = a[0] * scale;
+    v[4 * i + 1] = a[1] * scale;
+    v[4 * i + 2] = b[0] * scale;
+    v[4 * i + 3] = b[1] * scale;
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, uint64_t left, const uint32_t (&c)[kAdamPer]) {
+  if (left >= kAdamPer) {
+    const uint32_t w[2] = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
+    __builtin_memcpy(p, w, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kAdamPer; ++i)
+      if (i < (int)left) p[i] = (uint8_t)c[i];
+  }
+}
+// the largest finite magnitude of the 32 threads' values
+__device__ __forceinline__ float block_most(const float (&v)[kAdamPer]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < kAdamPer; ++i) {
+    const float a = fabsf(v[i]);
+    m = fmaxf(m, a <= 3.402823466e38f ? a : 0.f);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  return m;
+}
+// Magnitudes below 2^-100 of a block's largest are kept as zeros of that scale (its reciprocal would be infinite).
+__device__ __forceinline__ float inverse_scale(float most) { return most >= 0x1p-100f ? 448.f / most : 0.f; }
+// e4m3 magnitude of |x| / scale; r: 16 random bits (0x8000: to nearest).  Subnormals, multiples of 2^-9, are those
+// of the binade from 2^-6 on, moved there by an addition.
+__device__ __forceinline__ uint32_t code_of(float x, float inverse, uint32_t r) {
+  const float y = fminf(fabsf(x) * inverse, 448.f);
+  const bool small = y < 0x1p-6f;
+  const float t = small ? y + 0x1p-6f : y;
+  const uint32_t c = ((__float_as_uint(t) + (r << 4)) >> 20) - 960u - (small ? 8u : 0u);
+  return fabsf(x) <= 3.402823466e38f ? c : 0x7Fu;  // NaN
+}
+
+// ------------------------------------------------------------------ the step
+template <typename P, typename G, int BITS>
+__global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
+  __shared__ float sh[3];
+  const float scale = a.grad_scale ? *a.grad_scale : 1.f;
+  if (!(fabsf(scale) <= 3.402823466e38f)) return;  // the step is skipped
+  float rate = a.rate, root_c2 = a.root_c2;
+  uint64_t step = a.step;
+  double lr = a.lr;
+  if (a.step_dev || a.lr_dev) {
+    if (a.step_dev) step = (uint64_t)max(*a.step_dev, 1);
+    if (a.lr_dev) lr = (double)*a.lr_dev;
+    if (threadIdx.x == 0) {
+      sh[0] = (float)(lr / (1.0 - pow(a.beta1, (double)step)));
+      sh[1] = (float)sqrt(1.0 - pow(a.beta2, (double)step));
+    }
+    __syncthreads();
+    rate = sh[0];
+    root_c2 = sh[1];
+  }
+  uint32_t k = 0;  // the tensor of the chunk before
+  for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    while (k + 1 < a.count && a.t[k + 1].chunk0 <= chunk) ++k;
+    const AdamTensor& t = a.t[k];
+    const uint64_t at = (uint64_t)(chunk - t.chunk0) * kAdamChunk + threadIdx.x * kAdamPer;
+    const uint64_t left = at < t.n ? t.n - at : 0;
+    const float keep = a.lr_dev ? (float)(1.0 - lr * (double)t.wd) : t.keep;
+    const uint64_t block = at / 256;
+    float p[kAdamPer] = {}, g[kAdamPer] = {}, m[kAdamPer] = {}, v[kAdamPer] = {};
+    if (left) {
+      if (t.master) load8(t.master + at, left, p);
+      else load8(static_cast<const P*>(t.p) + at, left, p);
+      load8(static_cast<const G*>(t.g) + at, left, g);
+      if constexpr (BITS == 32) {
+        load8(static_cast<const float*>(t.m) + at, left, m);
+        load8(static_cast<const float*>(t.v) + at, left, v);
+      } else {
+        load_codes(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[block], m);
+        load_codes(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[block], v);
+#pragma unroll
+        for (int i = 0; i < kAdamPer; ++i) v[i] *= v[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAdamPer; ++i) {
+      const float gi = a.grad_scale ? g[i] * scale : g[i];
+      m[i] = a.b1 * m[i] + a.one_b1 * gi;
+      v[i] = a.b2 * v[i] + a.one_b2 * (gi * gi);
+      const float root = sqrtf(v[i]);
+      p[i] = p[i] * keep - rate * m[i] / (root / root_c2 + a.eps);
+      if constexpr (BITS == 8) v[i] = root;
+    }
+    if (left) {
+      store8(static_cast<P*>(t.p) + at, left, p);
+      if (t.master) store8(t.master + at, left, p);
+      if constexpr (BITS == 32) {
+        store8(static_cast<float*>(t.m) + at, left, m);
+        store8(static_cast<float*>(t.v) + at, left, v);
+      }
+    }
+    if constexpr (BITS == 8) {
+      if (left < kAdamPer) {
+#pragma unroll
+        for (int i = 0; i < kAdamPer; ++i)
+          if (i >= (int)left) m[i] = v[i] = 0.f;
+      }
+      const float mm = block_most(m), vm = block_most(v);
+      const float mi = inverse_scale(mm), vi = inverse_scale(vm);
+      const uint32_t key = mix32(mix32(t.number * 0x9E3779B9u + (uint32_t)step) ^ a.seed) ^ (uint32_t)(at >> 32) * 0x85EBCA6Bu;
+      uint32_t cm[kAdamPer], cv[kAdamPer];
+#pragma unroll
+      for (int i = 0; i < kAdamPer; ++i) {
+        const uint32_t r = a.stochastic ? mix32((uint32_t)(at + i) ^ key) : 0x80008000u;
+        cm[i] = code_of(m[i], mi, r & 0xFFFFu) | (m[i] < 0.f ? 128u : 0u);
+        cv[i] = code_of(v[i], vi, r >> 16);
+        if (v[i] > 0.f && cv[i] == 0) cv[i] = 1;
+      }
+      if (left) {
+        store_codes(static_cast<uint8_t*>(t.m) + at, left, cm);
+        store_codes(static_cast<uint8_t*>(t.v) + at, left, cv);
+        if (threadIdx.x % 32 == 0) {
+          t.m_scale[block] = mm / 448.f;
+          t.v_scale[block] = vm / 448.f;
+        }
+      }
+    }
+  }
+}
+
+// Launches `run` for groups of tensors; each holds chunks of its own.
+template <typename F>
+static hipError_t by_groups(AdamArgs& a, const laplex_adamw_tensor* t, uint32_t count, double lr, F run) {
+  for (uint32_t i = 0; i < count;) {
+    a.count = 0;
+    uint64_t chunks = 0;
+    for (; i < count && a.count < kAdamGroup; ++i) {
+      if (t[i].n == 0) continue;
+      const uint64_t more = (t[i].n + kAdamChunk - 1) / kAdamChunk;
+      if (a.count && chunks + more > 0x7FFFFFFFu) break;
+      a.t[a.count++] = {t[i].p, t[i].g, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].master, t[i].n,
+                        (float)(1.0 - lr * (double)t[i].weight_decay), t[i].weight_decay, (uint32_t)chunks, i};
+      chunks += more;
+    }
+    if (a.count == 0) continue;
+    a.chunks = (uint32_t)chunks;
+    run((unsigned)std::min<uint64_t>(chunks, 4096));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+hipError_t adamw(const laplex_adamw_args& o, const laplex_adamw_tensor* t, uint32_t count, hipStream_t s) {
+  AdamArgs a{};
+  a.b1 = (float)o.beta1;
+  a.one_b1 = (float)(1.0 - o.beta1);
+  a.b2 = (float)o.beta2;
+  a.one_b2 = (float)(1.0 - o.beta2);
+  a.eps = (float)o.eps;
+  a.rate = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
+  a.root_c2 = (float)std::sqrt(1.0 - std::pow(o.beta2, (double)o.step));
+  a.seed = o.seed;
+  a.stochastic = o.stochastic;
+  a.step = o.step;
+  a.lr = o.lr;
+  a.beta1 = o.beta1;
+  a.beta2 = o.beta2;
+  a.step_dev = o.step_dev;
+  a.lr_dev = o.lr_dev;
+  a.grad_scale = o.grad_scale;
+  const bool pb = o.dtype == LAPLEX_BF16, gb = o.grad_dtype == LAPLEX_BF16;
+  return by_groups(a, t, count, o.lr, [&](unsigned blocks) {
+    LAPLEX_LAUNCH("k_adamw", a.chunks, s, {
+      if (o.state_bits == 32) {
+        if (pb) gb ? k_adamw<bf16, bf16, 32><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<bf16, float, 32><<<blocks, kAdamBlock, 0, s>>>(a);
+        else gb ? k_adamw<float, bf16, 32><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<float, float, 32><<<blocks, kAdamBlock, 0, s>>>(a);
+      } else {
+        if (pb) gb ? k_adamw<bf16, bf16, 8><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<bf16, float, 8><<<blocks, kAdamBlock, 0, s>>>(a);
+        else gb ? k_adamw<float, bf16, 8><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<float, float, 8><<<blocks, kAdamBlock, 0, s>>>(a);
+      }
+    });
+  });
+}
+
+// ------------------------------------------------------------------ 8-bit moments as floats
+// (p and master hold the outputs)
+__global__ __launch_bounds__(kAdamBlock) void k_adamw_moments(AdamArgs a) {
+  uint32_t k = 0;
+  for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    while (k + 1 < a.count && a.t[k + 1].chunk0 <= chunk) ++k;
+    const AdamTensor& t = a.t[k];
+    const uint64_t at = (uint64_t)(chunk - t.chunk0) * kAdamChunk + threadIdx.x * kAdamPer;
+    if (at >= t.n) continue;
+    const uint64_t left = t.n - at;
+    float v[kAdamPer];
+    if (t.p) {
+      load_codes(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[at / 256], v);
+      store8(static_cast<float*>(t.p) + at, left, v);
+    }
+    if (t.master) {
+      load_codes(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[at / 256], v);
+#pragma unroll
+      for (int i = 0; i < kAdamPer; ++i) v[i] *= v[i];
+      store8(t.master + at, left, v);
+    }
+  }
+}
+
+hipError_t adamw_moments(const laplex_adamw_tensor* t, uint32_t count, hipStream_t s) {
+  AdamArgs a{};
+  return by_groups(a, t, count, 0.0, [&](unsigned blocks) {
+    LAPLEX_LAUNCH("k_adamw_moments", a.chunks, s, k_adamw_moments<<<blocks, kAdamBlock, 0, s>>>(a));
+  });
+}
+
+}  // namespace laplex
