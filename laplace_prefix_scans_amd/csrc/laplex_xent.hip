@@ -77,59 +77,123 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // exp(l - m) with 1 where both are the same infinity
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.f : exp_of(l - m); }
 
+// Tile and split of this block.  Blocks are dispatched to the 8 XCDs in turn; each XCD takes a stretch of the tiles, in
+// groups of 8 tiles of M by all of N, of which the ones that run at once share rows of both factors in its L2.
+__device__ __forceinline__ void tile_of_block(const ProductArgs& a, uint32_t& tm, uint32_t& tn, uint32_t& split) {
+  constexpr uint32_t GROUP = 8;
+  const uint32_t total = a.tiles_m * a.tiles_n, all = total * a.splits;
+  const uint32_t per = all / kXcds, rest = all % kXcds, x = blockIdx.x % kXcds, y = blockIdx.x / kXcds;
+  uint32_t id = x * per + min(x, rest) + y;  // (XCD x has per blocks, and one more where x < rest)
+  split = id / total;
+  id %= total;
+  const uint32_t group = id / (GROUP * a.tiles_n), first = group * GROUP, rows = min(GROUP, a.tiles_m - first);
+  const uint32_t in = id - first * a.tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
 // ------------------------------------------------------------------ the product
-// Waves of 64 x 64, tiles of 128 x 128 and 128 bytes of k.  A row's eight 16-byte pieces lie in LDS at piece ^ (row & 7),
-// so that the reads of 16 rows' pieces spread over the banks.
+// A block of WM x WN waves makes BM x BN of C.  128 bytes of k of its rows are on their way from memory straight to LDS
+// while those before are multiplied; a row's eight 16-byte pieces lie at piece ^ (row & 7), so that the reads of 16
+// rows' pieces spread over the banks.  A step's 128 bytes are two halves, and a half's operands are read one half ahead of
+// their products, across the step's one barrier: it stands in the middle of a step, where both halves of it have been read
+// and the next one's bytes have arrived.
+template <int M, int N, int WAVES_M, int WAVES_N>
+struct Tile {
+  static constexpr int BM = M, BN = N, WM = WAVES_M, WN = WAVES_N, THREADS = WM * WN * kWave;
+  static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
+  static constexpr int LOADS = (BM + BN) / 8 / (WM * WN);  // of a wave and step: 8 rows each
+  static constexpr int STEP_BYTES = (BM + BN) * 128;
+  static_assert((BM + BN) % (8 * WM * WN) == 0 && BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "whole operands");
+};
+using TileL = Tile<256, 256, 2, 4>;
+using TileM = Tile<128, 128, 2, 2>;
+using TileS = Tile<64, 64, 2, 2>;
+using TileT = Tile<128, 32, 4, 1>;
+
+// 16 bytes of each lane from memory to lds + 16 lane
+__device__ __forceinline__ void to_lds(const char* from, char* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+// Every wave's reads of LDS are done, and its bytes on their way to LDS are there.
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 constexpr int kPieceK = 128;
-template <typename T, int EPI>
-__global__ __launch_bounds__(256) void k_product(ProductArgs a) {
-  constexpr int BM = 128, BN = 128, E = 16 / sizeof(T), BK = kPieceK / sizeof(T);
-  __shared__ __attribute__((aligned(16))) char lds[(BM + BN) * kPieceK];
+template <typename T, int EPI, typename C>
+__global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
+  constexpr int BM = C::BM, BN = C::BN, MI = C::MI, NI = C::NI, W = C::WM * C::WN;
+  __shared__ __attribute__((aligned(16))) char lds[2 * C::STEP_BYTES];
   using V = typename Frag<T>::V;
-  const uint32_t split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
-  const uint32_t tm = tile % a.tiles_m, tn = tile / a.tiles_m;
-  const int lane = lane_id(), wave = threadIdx.x / kWave, wm = wave % 2 * 64, wn = wave / 2 * 64;
-  f32x4 acc[4][4] = {};
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  uint32_t tm, tn, split;
+  tile_of_block(a, tm, tn, split);
   const uint64_t k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
-  for (uint64_t k = k0; k < k1; k += BK) {
-    __syncthreads();
+  const int steps = (int)((k1 - k0) * sizeof(T) / kPieceK);
+  // this lane's 16 bytes of each of the wave's groups of 8 rows
+  const char* from[C::LOADS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int piece = threadIdx.x + i * 256, row = piece / 8, c = piece % 8;
-      const T* p = row < BM ? static_cast<const T*>(a.A) + (int64_t)min(tm * BM + row, a.M - 1) * a.lda
-                            : static_cast<const T*>(a.B) + (int64_t)min(tn * BN + row - BM, a.N - 1) * a.ldb;
-      const uint4 v = *reinterpret_cast<const uint4*>(p + k + c * E);
-      *reinterpret_cast<uint4*>(lds + row * kPieceK + (c ^ row % 8) * 16) = v;
-    }
-    __syncthreads();
+  for (int i = 0; i < C::LOADS; ++i) {
+    const int row = (i * W + wave) * 8 + lane / 8;
+    const T* p = row < BM ? static_cast<const T*>(a.A) + (int64_t)min(tm * BM + row, a.M - 1) * a.lda
+                          : static_cast<const T*>(a.B) + (int64_t)min(tn * BN + row - BM, a.N - 1) * a.ldb;
+    from[i] = reinterpret_cast<const char*>(p + k0) + ((lane % 8) ^ (lane / 8)) * 16;
+  }
+  auto load = [&](int step) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      V fa[4], fb[4];
-      const int c = h * 4 + lane / 16;
+    for (int i = 0; i < C::LOADS; ++i) to_lds(from[i] + (int64_t)step * kPieceK, lds + (step & 1) * C::STEP_BYTES + (i * W + wave) * 8 * kPieceK);
+  };
+  f32x4 acc[MI][NI] = {};
+  const int wm = wave % C::WM * (BM / C::WM), wn = wave / C::WM * (BN / C::WN);
+  if (steps > 0) {
+    V fa[2][MI], fb[2][NI];
+    // (a row's number & 7 is the lane's)
+    const uint32_t at_a = (wm + lane % 16) * kPieceK, at_b = (BM + wn + lane % 16) * kPieceK;
+    const uint32_t piece[2] = {(uint32_t)((lane / 16) ^ (lane % 8)) * 16, (uint32_t)((4 + lane / 16) ^ (lane % 8)) * 16};
+    auto read = [&](int step, int half) {
+      const char* base = lds + (step & 1) * C::STEP_BYTES;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ra = wm + i * 16 + lane % 16, rb = BM + wn + i * 16 + lane % 16;
-        fa[i] = *reinterpret_cast<const V*>(lds + ra * kPieceK + (c ^ ra % 8) * 16);
-        fb[i] = *reinterpret_cast<const V*>(lds + rb * kPieceK + (c ^ rb % 8) * 16);
+      for (int j = 0; j < NI; ++j) fb[half][j] = *reinterpret_cast<const V*>(base + at_b + piece[half] + j * 16 * kPieceK);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[half][i] = *reinterpret_cast<const V*>(base + at_a + piece[half] + i * 16 * kPieceK);
+    };
+    auto multiply = [&](int half) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mul(fa[half][i], fb[half][j], acc[i][j]);
+      // a read after every few products
+#pragma unroll
+      for (int r = 0; r < MI + NI; ++r) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x8, MI * NI * (sizeof(T) == 4 ? 4 : 1) / (MI + NI), 0);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = Frag<T>::mul(fa[i], fb[j], acc[i][j]);
+    };
+    load(0);
+    arrived();
+    if (steps > 1) load(1);
+    read(0, 0);
+    for (int k = 0; k < steps; ++k) {
+      read(k, 1);
+      multiply(0);
+      arrived();
+      if (k + 2 < steps) load(k + 2);
+      read(k + 1, 0);  // (after the last step: bytes that nothing uses)
+      multiply(1);
     }
+    __syncthreads();
   }
   // a lane holds column n = lane % 16 and rows m = lane / 16 * 4 .. + 3 of each 16 x 16 tile
   const uint32_t m0 = tm * BM + wm + lane / 16 * 4, n0 = tn * BN + wn + lane % 16;
   if constexpr (EPI == XENT_STATS) {
     float2* sh = reinterpret_cast<float2*>(lds);  // [wave of M][BN]
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NI; ++j) {
       const uint32_t t = n0 + j * 16;
       const int64_t y = t < a.N ? target_of(a.targets, a.id_bytes, t) : -1;
       float most = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint32_t v = m0 + i * 16 + r;
@@ -141,28 +205,31 @@ __global__ __launch_bounds__(256) void k_product(ProductArgs a) {
       most = fmaxf(most, __shfl_xor(most, 16));
       most = fmaxf(most, __shfl_xor(most, 32));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum += exp_below(acc[i][j][r], most);
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (lane < 16) sh[(wave % 2) * BN + wn + j * 16 + lane] = make_float2(most, sum);
+      if (lane < 16) sh[(wave % C::WM) * BN + wn + j * 16 + lane] = make_float2(most, sum);
     }
     __syncthreads();
     if (threadIdx.x < BN && tn * BN + threadIdx.x < a.N) {
-      const float2 p = sh[threadIdx.x], q = sh[BN + threadIdx.x];
-      const float m = fmaxf(p.x, q.x);
-      a.stats[(uint64_t)tm * a.N + tn * BN + threadIdx.x] = make_float2(m, p.y * exp_below(p.x, m) + q.y * exp_below(q.x, m));
+      float m = sh[threadIdx.x].x, sum = 0.f;
+#pragma unroll
+      for (int w = 1; w < C::WM; ++w) m = fmaxf(m, sh[w * BN + threadIdx.x].x);
+#pragma unroll
+      for (int w = 0; w < C::WM; ++w) sum += sh[w * BN + threadIdx.x].y * exp_below(sh[w * BN + threadIdx.x].x, m);
+      a.stats[(uint64_t)tm * a.N + tn * BN + threadIdx.x] = make_float2(m, sum);
     }
   } else if constexpr (EPI == XENT_GRAD) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NI; ++j) {
       const uint32_t t = n0 + j * 16;
       const int64_t y = t < a.N ? target_of(a.targets, a.id_bytes, t) : -1;
       const bool in = y >= 0 && y < (int64_t)a.vocab;
       const float lse = in ? a.lse[t] : 0.f, d = in ? a.scale * a.dloss[t] : 0.f, f = in ? d + (a.dlse ? a.scale * a.dlse[t] : 0.f) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < MI; ++i) {
         T g[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -182,12 +249,12 @@ __global__ __launch_bounds__(256) void k_product(ProductArgs a) {
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NI; ++j) {
       const uint32_t n = n0 + j * 16;
       if (n >= a.N) continue;
       const bool zero = a.live_rows && !live(a, n);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint32_t m = m0 + i * 16 + r;
@@ -286,7 +353,7 @@ __global__ __launch_bounds__(256) void k_xent_sum(const float* __restrict__ part
 constexpr uint32_t kTile = 128;
 constexpr uint64_t kPiece = 1ull << 30;  // bytes of G and its transpose
 static uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
-static uint32_t tiles(uint64_t n) { return (uint32_t)((n + kTile - 1) / kTile); }
+static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + of - 1) / of); }
 
 // Sizes that a call with this many tokens keeps in its workspace; each grows with the tokens.
 struct XentPlan {
@@ -323,7 +390,7 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
   w.x_rows = c.take<void>(tokens * p.k_width * e);
   w.table_rows = c.take<void>(vocab * p.k_width * e);
   if (pass == 0) {
-    w.stats = c.take<float2>((uint64_t)tiles(vocab) * tokens * 8);
+    w.stats = c.take<float2>((uint64_t)tiles(vocab, TileS::BM) * tokens * 8);
     w.hit = c.take<float>(tokens * 4);
   } else {
     // (a piece has at most kPiece bytes, or one tile of the vocabulary, or all of it)
@@ -343,20 +410,28 @@ size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t
   return total;
 }
 
+template <typename T, typename C>
+static hipError_t product_of(const char* name, int epi, ProductArgs& a, hipStream_t s) {
+  a.tiles_m = tiles(a.M, C::BM);
+  a.tiles_n = tiles(epi == XENT_GRAD ? std::max(a.N, a.n_fill) : a.N, C::BN);
+  const uint64_t blocks = (uint64_t)a.tiles_m * a.tiles_n * a.splits;
+  LAPLEX_LAUNCH(name, blocks, s, {
+    if (epi == XENT_STATS) k_product<T, XENT_STATS, C><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    else if (epi == XENT_GRAD) k_product<T, XENT_GRAD, C><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    else k_product<T, XENT_OUT, C><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+  });
+  return hipGetLastError();
+}
 template <typename T>
 static hipError_t product(const char* name, int epi, ProductArgs& a, uint32_t splits, hipStream_t s) {
   constexpr uint64_t bk = kPieceK / sizeof(T);
-  a.tiles_m = tiles(a.M);
-  a.tiles_n = tiles(epi == XENT_GRAD ? std::max(a.N, a.n_fill) : a.N);
   a.k_split = std::max(bk, up((a.K + splits - 1) / splits, bk));
   a.splits = (uint32_t)std::max<uint64_t>(1, (a.K + a.k_split - 1) / a.k_split);
-  const uint64_t blocks = (uint64_t)a.tiles_m * a.tiles_n * a.splits;
-  LAPLEX_LAUNCH(name, blocks, s, {
-    if (epi == XENT_STATS) k_product<T, XENT_STATS><<<(unsigned)blocks, 256, 0, s>>>(a);
-    else if (epi == XENT_GRAD) k_product<T, XENT_GRAD><<<(unsigned)blocks, 256, 0, s>>>(a);
-    else k_product<T, XENT_OUT><<<(unsigned)blocks, 256, 0, s>>>(a);
-  });
-  return hipGetLastError();
+  const uint64_t l = (uint64_t)tiles(a.M, 256) * tiles(a.N, 256) * a.splits, m = (uint64_t)tiles(a.M, 128) * tiles(a.N, 128) * a.splits;
+  if (a.N <= 32) return product_of<T, TileT>(name, epi, a, s);
+  if (l >= 200) return product_of<T, TileL>(name, epi, a, s);
+  if (m >= 200) return product_of<T, TileM>(name, epi, a, s);
+  return product_of<T, TileS>(name, epi, a, s);
 }
 static unsigned some_blocks(uint64_t n) { return (unsigned)std::min<uint64_t>((n + 255) / 256, 16384); }
 
