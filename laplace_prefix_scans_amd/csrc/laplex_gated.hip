@@ -114,8 +114,9 @@ __device__ __forceinline__ uint32_t wave_or(uint32_t v) {
   return __builtin_amdgcn_readfirstlane(v);
 }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
-  return (int64_t)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32)) << 32 |
-                   __builtin_amdgcn_readfirstlane((uint32_t)v));
+  // (the builtin returns a signed word)
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32)), lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 // Which of a tile's tokens begin and end sequences, and which lie in none; tiles are taken in turn, so most need only `clear`.

@@ -15,7 +15,7 @@ namespace {
 using namespace laplex;
 
 constexpr uint64_t kMaxTokens = 0x7FFFFFFFull;  // int32 offsets
-constexpr uint32_t kMaxSeqs = 1u << 20, kMaxWidth = 1u << 24, kMaxVocab = 1u << 26;
+constexpr uint32_t kMaxSeqs = 1u << 20, kMaxWidth = 1u << 24, kMaxVocab = 1u << 26, kMaxXentWidth = 1u << 20;
 constexpr uint64_t kMaxXentTokens = 1ull << 28, kMaxBlocks = (1ull << 24) - 1;  // a launch has fewer than 2^32 threads
 
 inline size_t elem(int dtype) { return dtype == LAPLEX_BF16 ? 2 : 4; }
@@ -140,7 +140,7 @@ extern "C" laplex_status laplex_gated_scan_step(const laplex_scan_shape* shape, 
 namespace {
 laplex_status check_xent(int dtype, int id_bytes, uint64_t tokens, uint32_t vocab, uint32_t width) {
   if (!is_dtype(dtype) || (id_bytes != 4 && id_bytes != 8) || vocab == 0 || width == 0) return LAPLEX_ERR_ARG;
-  if (tokens > kMaxXentTokens || vocab > kMaxVocab || width > kMaxWidth) return LAPLEX_ERR_SIZE;
+  if (tokens > kMaxXentTokens || vocab > kMaxVocab || width > kMaxXentWidth) return LAPLEX_ERR_SIZE;
   // blocks of the products (tiles of at least 128 x 128 where there are many) and of the copies along the other axis
   const uint64_t t = tokens / 64 + 1, v = vocab / 64 + 1, d = width / 64 + 1;
   if ((t / 2 + 1) * (v / 2 + 1) > kMaxBlocks || t * d > kMaxBlocks || v * d > kMaxBlocks) return LAPLEX_ERR_SIZE;

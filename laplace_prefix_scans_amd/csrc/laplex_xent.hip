@@ -3,11 +3,11 @@
 //   l_tv = c x_t . W_v,  lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l_{t y_t},
 //   G_tv = c [(dloss_t + dlse_t) exp(l_tv - lse_t) - dloss_t [v = y_t]],  dx = G W,  dW = G^T x.
 //
-// Four matrix products (the logits twice), all of one kernel: C[n][m] = sum_k A[m][k] B[n][k] on the matrix cores, rows
-// of A and B contiguous in k.  What follows the product is fused: the forward keeps a maximum and a sum of exponentials
-// per token and tile of the vocabulary, the backward writes a tile of G and its transpose.  For the products with G the
-// other factor is laid out along k first (W and x transposed, one pass over each), which also leaves out the tokens that
-// take no part and fills odd sizes up with zeros.
+// Four matrix products (the logits twice), all of one kernel: C[n][m] = sum_k A[m][k] B[n][k] on the matrix cores, A and B
+// each contiguous along k or along their rows.  What follows the product is fused: the forward keeps a maximum and a sum
+// of exponentials per token and tile of the vocabulary, the backward writes a tile of G.  Tensors are read as they lie; rows
+// that are not whole 128-byte pieces are filled up with zeros first, and the backward takes a copy of x in which the
+// tokens that take no part are zeros.
 #include <algorithm>
 
 #include "laplex_host.hpp"
@@ -18,7 +18,8 @@ namespace laplex {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 template <typename T>
 struct Frag;
@@ -42,9 +43,10 @@ enum { XENT_STATS, XENT_GRAD, XENT_OUT };
 
 struct ProductArgs {
   const void *A, *B;
-  int64_t lda, ldb;  // elements; rows are whole 128-byte pieces (or zeros beyond their end)
-  uint32_t M, N;     // rows of A, of B
-  uint64_t K;        // a multiple of a 128-byte piece
+  int64_t lda, ldb;  // elements; rows are whole 128-byte pieces (zeros beyond their end)
+  uint32_t M, N;     // C's
+  uint64_t K;        // a multiple of a step's
+  uint64_t k_rows;   // rows that A has where it lies along M; those up to K count as its last one (B's are zeros there)
   uint32_t tiles_m, tiles_n, splits;
   uint64_t k_split;  // k of a split, the same multiple
   // XENT_STATS, XENT_GRAD: rows of A are vocabulary entries from v0 on, rows of B tokens
@@ -55,8 +57,8 @@ struct ProductArgs {
   float2* stats;     // [tile of M][token]: maximum, sum of exp(l - maximum)
   float* hit;        // [token]: the target's logit
   const float *lse, *dloss, *dlse;
-  void *G, *Gt;      // [token][ldg], [vocabulary entry][ldgt]
-  int64_t ldg, ldgt;
+  void* G;           // [token][ldg]
+  int64_t ldg;
   uint32_t n_fill, m_fill;  // rows and columns that are written, zeros from N and M on
   // XENT_OUT
   void* out;         // [N][ldo], of type out_f32 ? float : T; splits of out_f32 follow each other
@@ -111,51 +113,158 @@ using TileM = Tile<128, 128, 2, 2>;
 using TileS = Tile<64, 64, 2, 2>;
 using TileT = Tile<128, 32, 4, 1>;
 
-// 16 bytes of each lane from memory to lds + 16 lane
-__device__ __forceinline__ void to_lds(const char* from, char* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// 16 bytes of each lane, from `off` bytes past a base that the wave shares, to 16 lane past an LDS address that it shares.
+// (Written out, for with the builtin the compiler waits for these loads before every transposing read of LDS.  They give
+// no register a value; what they bring is waited for by arrived().  Nothing else here uses m0.)
+__device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory");
+}
+// Two addresses that the wave shares, in scalar registers; the wait states that a load has to keep from the vector
+// instructions that write them are here, once for all the loads that follow.
+__device__ __forceinline__ void share(const char* p, const char* q, uint64_t& a, uint64_t& b) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+  // (the builtin returns a signed word)
+  const auto word = [](uint64_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v); };
+  a = (uint64_t)word(x >> 32) << 32 | word(x);
+  b = (uint64_t)word(y >> 32) << 32 | word(y);
+  asm volatile("s_nop 4" : "+s"(a), "+s"(b));
+}
+// (the address of LDS leaves the compiler's sight here, so that it takes to_lds to write there)
+__device__ __forceinline__ uint32_t lds_address(char* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)p));
 }
 
+// The thread's number, as something the compiler takes to change with every call: what is made from it is
+// then formed where it is used instead of holding a register over the loop.
+__device__ __forceinline__ int thread_now() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
 // Every wave's reads of LDS are done, and its bytes on their way to LDS are there.
 __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 constexpr int kPieceK = 128;
-template <typename T, int EPI, typename C>
+
+// One factor's rows of a step in LDS, R0 of them (of M or N).
+// Along k: row r is 128 bytes, its eight 16-byte pieces at piece ^ (r & 7), so that reads of 16 rows' pieces spread over
+// the banks.  Along its rows (ALONG): row k of the step is R0 elements, in blocks of 16 at block ^ mix(k), so that the
+// operand reads, which go across the rows, do.  A lane's operand of a half is the same elements either way: row lane % 16 and
+// k = 8 (lane / 16) .. + 7 of 32 (bfloat16; across rows by the transposing read, which gives each of 16 lanes one of
+// 16 columns of four rows) or 4 (lane / 16) .. + 3 of 16 (float).
+template <typename T, int R0, bool ALONG>
+struct Factor {
+  static constexpr int ROW = R0 * (int)sizeof(T), BLOCK = 16 * (int)sizeof(T), BLOCKS = R0 / 16;
+  static constexpr int READS = !ALONG ? 1 : sizeof(T) == 2 ? 2 : 4;  // of an operand
+  static __device__ __forceinline__ int mix(int k) {
+    const int m = sizeof(T) == 2 ? (k & 3) | (k >> 3 & 1) << 2 : k >> 2 & 3;
+    return m & (BLOCKS - 1);
+  }
+  // where the 16 bytes at `at` of a step (a multiple of 16) come from: offset of row and column, in elements
+  static __device__ __forceinline__ void source(int at, int& row, int& col) {
+    constexpr int E = 16 / sizeof(T);
+    if constexpr (ALONG) {
+      row = at / ROW;
+      const int block = at % ROW / BLOCK ^ mix(row);
+      col = block * 16 + at % BLOCK / 16 * E;
+    } else {
+      row = at / kPieceK;
+      col = (at % kPieceK / 16 ^ (row & 7)) * E;
+    }
+  }
+  // the lane's first byte of operand 0 (rows r0 .. r0 + 15) of half 0
+  static __device__ __forceinline__ uint32_t first(int r0, int lane) {
+    if constexpr (!ALONG) return (r0 + lane % 16) * kPieceK + ((lane / 16) ^ (lane & 7)) * 16;
+    const int k = sizeof(T) == 2 ? 8 * (lane / 16) + (lane >> 2 & 3) : 4 * (lane / 16);
+    return k * ROW + ((r0 / 16) ^ mix(k)) * BLOCK + (sizeof(T) == 2 ? (lane & 3) * 8 : lane % 16 * 4);
+  }
+  // operand i of a half (r0 a multiple of the operands' rows, so that i only flips bits of the block)
+  static __device__ __forceinline__ typename Frag<T>::V read(const char* step, uint32_t first, int half, int i) {
+    using V = typename Frag<T>::V;
+    if constexpr (!ALONG) {
+      return *reinterpret_cast<const V*>(step + (first ^ half * 64) + i * 16 * kPieceK);
+    } else if constexpr (sizeof(T) == 2) {
+      const char* p = step + (first ^ i * BLOCK) + half * 32 * ROW;
+      struct { s16x4 a, b; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p), __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * ROW))};
+      return __builtin_bit_cast(V, v);
+    } else {
+      const char* p = step + (first ^ i * BLOCK) + half * 16 * ROW;
+      V v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(p + j * ROW);
+      return v;
+    }
+  }
+};
+
+// A_ALONG: A is [k][M]; B_ALONG: B is [k][N]
+template <typename T, int EPI, typename C, bool A_ALONG, bool B_ALONG>
 __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
-  constexpr int BM = C::BM, BN = C::BN, MI = C::MI, NI = C::NI, W = C::WM * C::WN;
+  constexpr int BM = C::BM, BN = C::BN, MI = C::MI, NI = C::NI, W = C::WM * C::WN, BK = kPieceK / sizeof(T), E = 16 / sizeof(T);
+  using FA = Factor<T, BM, A_ALONG>;
+  using FB = Factor<T, BN, B_ALONG>;
   __shared__ __attribute__((aligned(16))) char lds[2 * C::STEP_BYTES];
   using V = typename Frag<T>::V;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   uint32_t tm, tn, split;
   tile_of_block(a, tm, tn, split);
   const uint64_t k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
-  const int steps = (int)((k1 - k0) * sizeof(T) / kPieceK);
-  // this lane's 16 bytes of each of the wave's groups of 8 rows
-  const char* from[C::LOADS];
+  const int steps = (int)((k1 - k0) / BK);
+  // this lane's 16 bytes of each of the wave's stretches of 1024, from the tile's first element on; LOADS_A of them are A's
+  constexpr int LOADS_A = BM / 8 / W;
+  static_assert(BM % (8 * W) == 0, "a wave's stretches are A's and then B's");
+  const int64_t row_a = a.lda * (int64_t)sizeof(T), row_b = a.ldb * (int64_t)sizeof(T);
+  const char* base_a = static_cast<const char*>(a.A) + (A_ALONG ? (int64_t)k0 * row_a + (int64_t)tm * BM * sizeof(T) : (int64_t)tm * BM * row_a + (int64_t)k0 * sizeof(T));
+  const char* base_b = static_cast<const char*>(a.B) + (B_ALONG ? (int64_t)k0 * row_b + (int64_t)tn * BN * sizeof(T) : (int64_t)tn * BN * row_b + (int64_t)k0 * sizeof(T));
+  uint32_t off[C::LOADS];
 #pragma unroll
   for (int i = 0; i < C::LOADS; ++i) {
-    const int row = (i * W + wave) * 8 + lane / 8;
-    const T* p = row < BM ? static_cast<const T*>(a.A) + (int64_t)min(tm * BM + row, a.M - 1) * a.lda
-                          : static_cast<const T*>(a.B) + (int64_t)min(tn * BN + row - BM, a.N - 1) * a.ldb;
-    from[i] = reinterpret_cast<const char*>(p + k0) + ((lane % 8) ^ (lane / 8)) * 16;
+    const int at = (i * W + wave) * 1024 + lane * 16;
+    int row, col;
+    if (i < LOADS_A) {
+      FA::source(at, row, col);
+      if (A_ALONG) col = min((int64_t)col, a.lda - E - (int64_t)tm * BM);
+      else row = min((uint32_t)row, a.M - 1 - tm * BM);
+      off[i] = (uint32_t)row * (uint32_t)row_a + (uint32_t)col * (uint32_t)sizeof(T);
+    } else {
+      FB::source(at - BM * kPieceK, row, col);
+      if (B_ALONG) col = min((int64_t)col, a.ldb - E - (int64_t)tn * BN);
+      else row = min((uint32_t)row, max(a.N, tn * BN + 1) - 1 - tn * BN);
+      off[i] = (uint32_t)row * (uint32_t)row_b + (uint32_t)col * (uint32_t)sizeof(T);
+    }
   }
+  const int64_t next_a = A_ALONG ? row_a * BK : kPieceK, next_b = B_ALONG ? row_b * BK : kPieceK;
+  const uint32_t to0 = lds_address(lds) + wave * 1024;
   auto load = [&](int step) {
+    const uint32_t to = to0 + (step & 1) * C::STEP_BYTES;
+    uint64_t p, q;
+    share(base_a + step * next_a, base_b + step * next_b, p, q);
+    if (A_ALONG && k0 + (uint64_t)(step + 1) * BK > a.k_rows) {  // the last step has rows beyond the last: that one again
+      const int rows = (int)((int64_t)a.k_rows - (int64_t)(k0 + (uint64_t)step * BK));
 #pragma unroll
-    for (int i = 0; i < C::LOADS; ++i) to_lds(from[i] + (int64_t)step * kPieceK, lds + (step & 1) * C::STEP_BYTES + (i * W + wave) * 8 * kPieceK);
+      for (int i = 0; i < LOADS_A; ++i) {
+        int row, col;
+        FA::source((i * W + wave) * 1024 + thread_now() % kWave * 16, row, col);
+        to_lds(p, off[i] - (uint32_t)max(row - (rows - 1), 0) * (uint32_t)row_a, to + i * W * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS_A; ++i) to_lds(p, off[i], to + i * W * 1024);
+    }
+#pragma unroll
+    for (int i = LOADS_A; i < C::LOADS; ++i) to_lds(q, off[i], to + i * W * 1024);
   };
   f32x4 acc[MI][NI] = {};
   const int wm = wave % C::WM * (BM / C::WM), wn = wave / C::WM * (BN / C::WN);
   if (steps > 0) {
     V fa[2][MI], fb[2][NI];
-    // (a row's number & 7 is the lane's)
-    const uint32_t at_a = (wm + lane % 16) * kPieceK, at_b = (BM + wn + lane % 16) * kPieceK;
-    const uint32_t piece[2] = {(uint32_t)((lane / 16) ^ (lane % 8)) * 16, (uint32_t)((4 + lane / 16) ^ (lane % 8)) * 16};
+    const uint32_t at_a = FA::first(wm, lane), at_b = FB::first(wn, lane);
     auto read = [&](int step, int half) {
       const char* base = lds + (step & 1) * C::STEP_BYTES;
 #pragma unroll
-      for (int j = 0; j < NI; ++j) fb[half][j] = *reinterpret_cast<const V*>(base + at_b + piece[half] + j * 16 * kPieceK);
+      for (int j = 0; j < NI; ++j) fb[half][j] = FB::read(base + BM * kPieceK, at_b, half, j);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[half][i] = *reinterpret_cast<const V*>(base + at_a + piece[half] + i * 16 * kPieceK);
+      for (int i = 0; i < MI; ++i) fa[half][i] = FA::read(base, at_a, half, i);
     };
     auto multiply = [&](int half) {
 #pragma unroll
@@ -163,10 +272,11 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mul(fa[half][i], fb[half][j], acc[i][j]);
       // a read after every few products
+      constexpr int READS = MI * FA::READS + NI * FB::READS, PRODUCTS = MI * NI * (sizeof(T) == 4 ? 4 : 1);
 #pragma unroll
-      for (int r = 0; r < MI + NI; ++r) {
+      for (int r = 0; r < READS; ++r) {
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x8, MI * NI * (sizeof(T) == 4 ? 4 : 1) / (MI + NI), 0);
+        __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS / READS ? PRODUCTS / READS : 1, 0);
       }
     };
     load(0);
@@ -239,12 +349,7 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
           g[r] = from_f32<T>(in && v < a.M ? x : 0.f);
         }
         const uint32_t v = m0 + i * 16;
-        if (t < a.N && v < a.m_fill) __builtin_memcpy(static_cast<T*>(a.G) + (int64_t)t * a.ldg + v, g, sizeof g);
-        if (t < a.n_fill) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (v + r < a.M) static_cast<T*>(a.Gt)[(int64_t)(v + r) * a.ldgt + t] = g[r];
-        }
+        if (t < a.n_fill && v < a.m_fill) __builtin_memcpy(static_cast<T*>(a.G) + (int64_t)t * a.ldg + v, g, sizeof g);
       }
     }
   } else {
@@ -273,39 +378,30 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
 }
 
 // ------------------------------------------------------------------ layouts
-// dst[r][c] = src[r][c], zeros for columns from `cols` to `fill`
+// dst[r][c] = src[r][c], zeros for columns from `cols` to `fill`; targets: zeros also for rows of tokens that are left
+// out and from `rows` on
 template <typename T>
-__global__ __launch_bounds__(256) void k_xent_rows(const T* __restrict__ src, uint64_t rows, uint32_t cols, uint32_t fill, T* __restrict__ dst) {
-  const uint64_t n = rows * fill, stride = (uint64_t)gridDim.x * 256;
+__global__ __launch_bounds__(256) void k_xent_rows(const T* __restrict__ src, uint64_t rows, uint32_t cols, uint64_t rows_fill, uint32_t fill,
+                                                   T* __restrict__ dst, const void* targets, int id_bytes, uint32_t vocab) {
+  constexpr int E = 16 / sizeof(T);
+  const uint64_t n = rows_fill * (fill / E), stride = (uint64_t)gridDim.x * 256;
   for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
-    const uint64_t r = i / fill;
-    const uint32_t c = (uint32_t)(i % fill);
-    dst[i] = c < cols ? src[r * cols + c] : T(0.f);
-  }
-}
-// dst[c][r] = src[r][c] for r < rows, zeros from `rows` to `fill`; targets: rows of tokens that are left out are zeros
-template <typename T>
-__global__ __launch_bounds__(256) void k_xent_transposed(const T* __restrict__ src, uint32_t rows, uint32_t cols, uint32_t fill, T* __restrict__ dst,
-                                                         const void* targets, int id_bytes, uint32_t vocab) {
-  __shared__ T sh[64][65];
-  const uint32_t tiles_c = (cols + 63) / 64, r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
-  for (uint32_t i = threadIdx.x; i < 64 * 64; i += 256) {
-    const uint32_t r = r0 + i / 64, c = c0 + i % 64;
-    T v = T(0.f);
-    if (r < rows && c < cols) {
-      bool in = true;
-      if (targets) {
-        const int64_t y = target_of(targets, id_bytes, r);
-        in = y >= 0 && y < (int64_t)vocab;
-      }
-      if (in) v = src[(uint64_t)r * cols + c];
+    const uint64_t r = i / (fill / E);
+    const uint32_t c = (uint32_t)(i % (fill / E)) * E;
+    bool in = r < rows;
+    if (in && targets) {
+      const int64_t y = target_of(targets, id_bytes, (uint32_t)r);
+      in = y >= 0 && y < (int64_t)vocab;
     }
-    sh[i / 64][i % 64] = v;
-  }
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < 64 * 64; i += 256) {
-    const uint32_t c = c0 + i / 64, r = r0 + i % 64;
-    if (c < cols && r < fill) dst[(uint64_t)c * fill + r] = sh[i % 64][i / 64];
+    T v[E];
+    const T* p = src + r * cols + c;
+    if (in && c + E <= cols) {
+      __builtin_memcpy(v, p, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = in && c + e < cols ? p[e] : T(0.f);
+    }
+    __builtin_memcpy(dst + r * fill + c, v, 16);
   }
 }
 
@@ -351,7 +447,7 @@ __global__ __launch_bounds__(256) void k_xent_sum(const float* __restrict__ part
 
 // ------------------------------------------------------------------ plan
 constexpr uint32_t kTile = 128;
-constexpr uint64_t kPiece = 1ull << 30;  // bytes of G and its transpose
+constexpr uint64_t kPiece = 1ull << 30;  // bytes of G
 static uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + of - 1) / of); }
 
@@ -366,7 +462,7 @@ static XentPlan xent_plan(int dtype, uint64_t tokens, uint32_t vocab, uint32_t w
   XentPlan p;
   p.k_width = up(width, bk);
   p.k_tokens = up(tokens, bk);
-  const uint64_t fit = kPiece / (2 * e * std::max<uint64_t>(p.k_tokens, 1)) / kTile * kTile;
+  const uint64_t fit = kPiece / (e * std::max<uint64_t>(p.k_tokens, 1)) / kTile * kTile;
   p.piece = (uint32_t)std::min<uint64_t>(up(vocab, bk), std::max<uint64_t>(kTile, fit));
   p.k_piece = up(p.piece, bk);
   // Where dx has fewer tiles than the chip has CUs, its sums over the vocabulary are split.
@@ -378,7 +474,7 @@ struct XentWorkspace {
   void *x_rows, *table_rows;  // filled up copies, where rows are not whole pieces
   float2* stats;
   float* hit;
-  void *G, *Gt, *x_t, *table_t;
+  void* G;
   float* dx;
 };
 static bool whole_rows(const void* p, uint64_t width, uint64_t e) { return width * e % kPieceK == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -387,18 +483,15 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
   const XentPlan p = xent_plan(dtype, tokens, vocab, width);
   Carver c(ws);
   XentWorkspace w{};
-  w.x_rows = c.take<void>(tokens * p.k_width * e);
+  w.x_rows = c.take<void>(p.k_tokens * p.k_width * e);
   w.table_rows = c.take<void>(vocab * p.k_width * e);
   if (pass == 0) {
     w.stats = c.take<float2>((uint64_t)tiles(vocab, TileS::BM) * tokens * 8);
     w.hit = c.take<float>(tokens * 4);
   } else {
     // (a piece has at most kPiece bytes, or one tile of the vocabulary, or all of it)
-    const uint64_t bk = kPieceK / e, g = std::max<uint64_t>(std::min<uint64_t>(kPiece / 2, up(vocab, bk) * p.k_tokens * e), kTile * p.k_tokens * e);
+    const uint64_t bk = kPieceK / e, g = std::max<uint64_t>(std::min<uint64_t>(kPiece, up(vocab, bk) * p.k_tokens * e), kTile * p.k_tokens * e);
     w.G = c.take<void>(g);
-    w.Gt = c.take<void>(g);
-    w.x_t = c.take<void>(width * p.k_tokens * e);
-    w.table_t = c.take<void>((uint64_t)width * up(vocab, bk) * e);
     w.dx = c.take<float>((std::min<uint64_t>(tokens * 513, tokens + 512 * kTile)) * width * 4);
   }
   *total = (c.off + 255) & ~size_t(255);
@@ -410,20 +503,22 @@ size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t
   return total;
 }
 
+enum Product { LOGITS_STATS, LOGITS_GRAD, DX, DTABLE };
 template <typename T, typename C>
-static hipError_t product_of(const char* name, int epi, ProductArgs& a, hipStream_t s) {
+static hipError_t product_of(const char* name, Product epi, ProductArgs& a, hipStream_t s) {
   a.tiles_m = tiles(a.M, C::BM);
-  a.tiles_n = tiles(epi == XENT_GRAD ? std::max(a.N, a.n_fill) : a.N, C::BN);
+  a.tiles_n = tiles(epi == LOGITS_GRAD ? std::max(a.N, a.n_fill) : a.N, C::BN);
   const uint64_t blocks = (uint64_t)a.tiles_m * a.tiles_n * a.splits;
   LAPLEX_LAUNCH(name, blocks, s, {
-    if (epi == XENT_STATS) k_product<T, XENT_STATS, C><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
-    else if (epi == XENT_GRAD) k_product<T, XENT_GRAD, C><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
-    else k_product<T, XENT_OUT, C><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    if (epi == LOGITS_STATS) k_product<T, XENT_STATS, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    else if (epi == LOGITS_GRAD) k_product<T, XENT_GRAD, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    else if (epi == DX) k_product<T, XENT_OUT, C, true, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    else k_product<T, XENT_OUT, C, true, true><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
   });
   return hipGetLastError();
 }
 template <typename T>
-static hipError_t product(const char* name, int epi, ProductArgs& a, uint32_t splits, hipStream_t s) {
+static hipError_t product(const char* name, Product epi, ProductArgs& a, uint32_t splits, hipStream_t s) {
   constexpr uint64_t bk = kPieceK / sizeof(T);
   a.k_split = std::max(bk, up((a.K + splits - 1) / splits, bk));
   a.splits = (uint32_t)std::max<uint64_t>(1, (a.K + a.k_split - 1) / a.k_split);
@@ -435,14 +530,18 @@ static hipError_t product(const char* name, int epi, ProductArgs& a, uint32_t sp
 }
 static unsigned some_blocks(uint64_t n) { return (unsigned)std::min<uint64_t>((n + 255) / 256, 16384); }
 
-// x and the table with rows of whole pieces
+// rows of whole pieces (x in the backward: without the tokens that are left out)
 template <typename T>
-static hipError_t whole(const void** p, uint64_t rows, uint32_t width, uint64_t k, void* copy, hipStream_t s) {
-  if (whole_rows(*p, width, sizeof(T))) return hipSuccess;
+static hipError_t copy_rows(const void** p, uint64_t rows, uint32_t width, uint64_t rows_fill, uint64_t k, void* copy, const XentShape* tokens, hipStream_t s) {
   LAPLEX_LAUNCH("k_xent_rows", rows, s,
-                k_xent_rows<T><<<some_blocks(rows * k), 256, 0, s>>>(static_cast<const T*>(*p), rows, width, (uint32_t)k, static_cast<T*>(copy)));
+                k_xent_rows<T><<<some_blocks(rows_fill * k * sizeof(T) / 16), 256, 0, s>>>(static_cast<const T*>(*p), rows, width, rows_fill, (uint32_t)k, static_cast<T*>(copy),
+                                                                       tokens ? tokens->targets : nullptr, tokens ? tokens->id_bytes : 0, tokens ? tokens->vocab : 0));
   *p = copy;
   return hipGetLastError();
+}
+template <typename T>
+static hipError_t whole(const void** p, uint64_t rows, uint32_t width, uint64_t k, void* copy, hipStream_t s) {
+  return whole_rows(*p, width, sizeof(T)) ? hipSuccess : copy_rows<T>(p, rows, width, rows, k, copy, nullptr, s);
 }
 template <typename T>
 static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws, hipStream_t s) {
@@ -465,17 +564,9 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   a.scale = x.scale;
   a.stats = w.stats;
   a.hit = w.hit;
-  if ((err = product<T>("k_product_stats", XENT_STATS, a, 1, s)) != hipSuccess) return err;
+  if ((err = product<T>("k_product_stats", LOGITS_STATS, a, 1, s)) != hipSuccess) return err;
   LAPLEX_LAUNCH("k_xent_join", x.tokens, s,
                 k_xent_join<<<(unsigned)((x.tokens + 15) / 16), 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse));
-  return hipGetLastError();
-}
-template <typename T>
-static hipError_t transposed(const void* src, uint64_t rows, uint32_t cols, uint64_t fill, void* dst, const XentShape* tokens, hipStream_t s) {
-  const uint64_t blocks = (fill + 63) / 64 * ((cols + 63) / 64);
-  LAPLEX_LAUNCH("k_xent_transposed", rows, s,
-                k_xent_transposed<T><<<(unsigned)blocks, 256, 0, s>>>(static_cast<const T*>(src), (uint32_t)rows, cols, (uint32_t)fill, static_cast<T*>(dst),
-                                                                      tokens ? tokens->targets : nullptr, tokens ? tokens->id_bytes : 0, tokens ? tokens->vocab : 0));
   return hipGetLastError();
 }
 template <typename T>
@@ -485,17 +576,16 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   const XentPlan p = xent_plan(x.dtype, x.tokens, x.vocab, x.width);
   const XentWorkspace w = xent_carve(ws, 1, x.dtype, x.tokens, x.vocab, x.width, &total);
   const uint32_t tokens = (uint32_t)x.tokens;
-  ProductArgs l{};
-  l.A = x.table;
-  l.B = x.x;
+  const void *table = x.table, *rows = x.x;
   hipError_t err;
   if (tokens) {  // (without, dtable is a sum of nothing)
-    if ((err = whole<T>(&l.A, x.vocab, x.width, p.k_width, w.table_rows, s)) != hipSuccess) return err;
-    if ((err = whole<T>(&l.B, x.tokens, x.width, p.k_width, w.x_rows, s)) != hipSuccess) return err;
-    if (dtable && (err = transposed<T>(x.x, x.tokens, x.width, p.k_tokens, w.x_t, &x, s)) != hipSuccess) return err;
+    if ((err = whole<T>(&table, x.vocab, x.width, p.k_width, w.table_rows, s)) != hipSuccess) return err;
+    if ((err = copy_rows<T>(&rows, x.tokens, x.width, p.k_tokens, p.k_width, w.x_rows, &x, s)) != hipSuccess) return err;
   } else {
     dx = nullptr;
   }
+  ProductArgs l{};
+  l.B = rows;
   l.lda = l.ldb = (int64_t)p.k_width;
   l.K = p.k_width;
   l.N = tokens;
@@ -507,28 +597,26 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   l.dloss = dloss;
   l.dlse = dlse;
   l.G = w.G;
-  l.Gt = w.Gt;
-  l.ldgt = (int64_t)p.k_tokens;
   l.n_fill = (uint32_t)p.k_tokens;
-  const char* table = static_cast<const char*>(l.A);
   const bool once = p.splits == 1 && p.piece >= x.vocab;  // dx is one product
   uint32_t used = 1;
   for (uint32_t v0 = 0; v0 < x.vocab; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, x.vocab - v0);
     const uint64_t fill = up(n, kPieceK / sizeof(T));
-    l.A = table + (uint64_t)v0 * p.k_width * sizeof(T);
+    l.A = static_cast<const T*>(table) + v0 * p.k_width;
     l.M = n;
     l.v0 = v0;
     l.ldg = (int64_t)fill;
     l.m_fill = (uint32_t)fill;
-    if (tokens && (err = product<T>("k_product_grad", XENT_GRAD, l, 1, s)) != hipSuccess) return err;
+    if (tokens && (err = product<T>("k_product_grad", LOGITS_GRAD, l, 1, s)) != hipSuccess) return err;
     if (dx) {
-      if ((err = transposed<T>(static_cast<const T*>(x.table) + (uint64_t)v0 * x.width, n, x.width, fill, w.table_t, nullptr, s)) != hipSuccess) return err;
       ProductArgs a{};
-      a.A = w.table_t;
+      a.A = l.A;
+      a.lda = l.lda;
       a.B = w.G;
-      a.lda = a.ldb = (int64_t)fill;
+      a.ldb = (int64_t)fill;
       a.K = fill;
+      a.k_rows = n;
       a.M = x.width;
       a.N = tokens;
       a.targets = x.targets;
@@ -540,21 +628,22 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
       a.out_f32 = !once || sizeof(T) == 4;
       a.out_split = (int64_t)x.tokens * x.width;
       a.add = v0 > 0;
-      if ((err = product<T>("k_product_dx", XENT_OUT, a, p.splits, s)) != hipSuccess) return err;
+      if ((err = product<T>("k_product_dx", DX, a, p.splits, s)) != hipSuccess) return err;
       used = std::max(used, a.splits);
     }
     if (dtable) {
       ProductArgs a{};
-      a.A = w.x_t;
-      a.B = w.Gt;
-      a.lda = a.ldb = (int64_t)p.k_tokens;
-      a.K = p.k_tokens;
+      a.A = rows;
+      a.lda = (int64_t)p.k_width;
+      a.B = w.G;
+      a.ldb = (int64_t)fill;
+      a.K = a.k_rows = p.k_tokens;
       a.M = x.width;
       a.N = n;
       a.ldo = x.width;
       a.out_f32 = table_dtype == LAPLEX_F32;
       a.out = static_cast<char*>(dtable) + (uint64_t)v0 * x.width * (a.out_f32 ? 4 : 2);
-      if ((err = product<T>("k_product_dtable", XENT_OUT, a, 1, s)) != hipSuccess) return err;
+      if ((err = product<T>("k_product_dtable", DTABLE, a, 1, s)) != hipSuccess) return err;
     }
   }
   if (dx && !once) {
