@@ -3,14 +3,17 @@
 //   h_t = a_t h_{t-1} + w_t x_t,   rate: a = exp(-r), w = 1;   sigmoid: a = s(z), w = 1 - a.
 //   l_t = dh_t + a_{t+1} l_{t+1},  dx = w l,  dr = -a h_{t-1} l,  dz = a w (h_{t-1} - x) l.
 //
-// A wave takes 64 lanes' channels of one segment of the packed tokens, 16 tokens
-// at a time, so that 16 rows of each tensor are on their way at once; nothing is
+// A wave takes 64 channels of one segment of the packed tokens, 16 tokens at a
+// time, so that 16 rows of each tensor are on their way at once; nothing is
 // exchanged between lanes.  Where sequences and channels alone do not fill the
 // chip, the tokens are cut into segments: a pass over their aggregates (the
-// decay over a segment and its state from zero), then the whole pass, each
-// wave of which first joins the aggregates before its own.  Segments are cut
+// decay over a segment and its state from zero), their join, then the whole
+// pass.  Segments are cut
 // without regard to sequences: a token that begins a sequence replaces the
 // state before it, whatever that is.
+#include <algorithm>
+#include <type_traits>
+
 #include "laplex_layers_device.hpp"
 #include "laplex_train.hpp"
 
@@ -27,18 +30,10 @@ __device__ __forceinline__ bool near_one(float c) { return __float_as_int(c) < 0
 // a s
 __device__ __forceinline__ float decayed(float c, float s) { return fmaf(c, s, near_one(c) ? s : 0.f); }
 __device__ __forceinline__ float decay_value(float c) { return near_one(c) ? 1.f + c : c; }
-// the product of two decays
-__device__ __forceinline__ float decay_join(float c, float d) {
-  if (near_one(c) && near_one(d)) {
-    const float q = fmaf(c, d, c + d);  // -(1 - a b)
-    return q >= -0.5f ? (q == 0.f ? -0.f : q) : 1.f + q;
-  }
-  return near_one(c) ? fmaf(c, d, d) : near_one(d) ? fmaf(c, d, c) : c * d;
-}
 
 template <int KIND>
 struct Gate {
-  float c, a, w;  // the decay as above, itself, and the input's weight
+  float c, w;  // the decay as above, the input's weight
 };
 template <int KIND>
 __device__ __forceinline__ Gate<KIND> gate_of(float g) {
@@ -55,32 +50,17 @@ __device__ __forceinline__ Gate<KIND> gate_of(float g) {
     p = fmaf(g * p, -1.f / 3, 1.f);
     p = fmaf(g * p, -1.f / 2, 1.f);
     const float q = g < 0.3f ? g * p : 1.f - e;
-    r.a = e;
     r.w = 1.f;
     r.c = g >= 0.f && q <= 0.5f ? -q : e;
   } else {
-    const float e = __builtin_amdgcn_exp2f(-fabsf(g) * kLog2e), d = 1.f + e;
-    float big = __builtin_amdgcn_rcpf(d);
-    big = fmaf(fmaf(-d, big, 1.f), big, big);
-    const float small = e * big;
+    const float e = __builtin_amdgcn_exp2f(-fabsf(g) * kLog2e);
+    const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
     const bool up = g >= 0.f;
-    r.a = up ? big : small;
     r.w = up ? small : big;
     r.c = up ? -small : small;
   }
   return r;
 }
-
-// The decay over the tokens of a tile.
-struct TileDecay {
-  float p = 1.f, q = 0.f, most = -1.f;  // their product, one minus it, and the largest that is not near 1
-  __device__ __forceinline__ void add(float c, float a) {
-    p *= a;
-    q = fmaf(-c, 1.f - q, q);
-    most = fmaxf(most, c);
-  }
-  __device__ __forceinline__ float coded() const { return p < 0.5f || most > 0.f ? p : -q; }
-};
 
 // ------------------------------------------------------------------ sequences
 struct GateSeqs {
@@ -170,53 +150,50 @@ struct GateMarks {
 static_assert(kGateU == 16, "marks of a tile are 16 bits");
 
 // ------------------------------------------------------------------ rows
-// CV channels a lane, the row's last ones one by one.
-template <typename T>
-constexpr int kGateCV = 4 / sizeof(T);
-template <typename T>
-struct Piece {
-  T e[kGateCV<T>];
-};
-template <typename T>
-__device__ __forceinline__ Piece<T> load_piece(const T* p, int left) {
-  Piece<T> r;
-  if (left >= kGateCV<T>) {
-    __builtin_memcpy(r.e, p, sizeof r.e);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kGateCV<T>; ++i) r.e[i] = i < left ? p[i] : T(0.f);
-  }
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void store_piece(T* p, int left, const float (&v)[kGateCV<T>]) {
-  Piece<T> r;
-#pragma unroll
-  for (int i = 0; i < kGateCV<T>; ++i) r.e[i] = from_f32<T>(v[i]);
-  if (left >= kGateCV<T>) {
-    __builtin_memcpy(p, r.e, sizeof r.e);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kGateCV<T>; ++i)
-      if (i < left) p[i] = r.e[i];
-  }
-}
-template <typename T>
+// A lane has one channel; lanes past the last one have that one too, and write what it writes.  Rows are taken one after
+// the other (STEP 1 or -1): their address is the wave's, and moves on by scalar additions, to which the lane adds 32 bits.
+// Rows past the last token are read as it.
+template <typename T, int STEP>
 struct Rows {
-  const T* p;  // of the lane's first channel
-  int64_t token;
-  int left;
-  __device__ __forceinline__ void load(Piece<T> (&v)[kGateU], int64_t t0, int64_t tokens) const {
+  typedef __attribute__((address_space(1))) char* Global;
+  Global at;      // the first channel of the row that is next
+  int64_t token;  // bytes
+  uint32_t off;   // bytes to the lane's channel
+  int32_t t, last;
+  __device__ __forceinline__ Rows(const void* p, int64_t stride, int64_t channel, int64_t t0, int64_t tokens)
+      : token(STEP * stride * (int64_t)sizeof(T)), off((uint32_t)channel * (uint32_t)sizeof(T)), t((int32_t)t0), last((int32_t)tokens - 1) {
+    at = (Global)(uintptr_t)uniform64(reinterpret_cast<int64_t>(p) + min(t0, tokens - 1) * stride * (int64_t)sizeof(T));
+  }
+  __device__ __forceinline__ void move() {
+    at += (STEP > 0 ? t < last : t <= last) ? token : 0;
+    t += STEP;
+  }
+  __device__ __forceinline__ T get() {
+    const T v = *(const __attribute__((address_space(1))) T*)(at + off);
+    move();
+    return v;
+  }
+  __device__ __forceinline__ void put(bool real, float v) {
+    if (real) *(__attribute__((address_space(1))) T*)(at + off) = from_f32<T>(v);
+    move();
+  }
+  // the next tile, its tokens in order
+  __device__ __forceinline__ void load(T (&v)[kGateU]) {
 #pragma unroll
-    for (int i = 0; i < kGateU; ++i) v[i] = load_piece(p + min(t0 + i, tokens - 1) * token, left);
+    for (int j = 0; j < kGateU; ++j) v[STEP > 0 ? j : kGateU - 1 - j] = get();
   }
 };
+
+// Keeps loads from being moved ahead over more than a few tokens, where they would need registers of their own.
+__device__ __forceinline__ void every_fourth(int i) {
+  if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+}
 
 struct GateArgs {
   GateShape g;
   int64_t seg_len;  // a multiple of the tile
   uint32_t segs, ctiles;
-  float *agg_c, *agg_b;  // segs x channels: decay over a segment (coded), its state from zero
+  float *agg_c, *agg_b;  // segs x channels: decay over a segment, its state from zero and then what comes into it
   uint32_t* reset;       // segs: whether a segment holds a boundary, so that nothing passes through it
   const float* state_in;
   float* state_out;
@@ -230,326 +207,340 @@ struct GateArgs {
   float* dstate_in;
 };
 
-template <typename T>
 struct Lane {
   uint32_t seg, ctile;
-  int64_t c0, t_lo, t_hi;  // first channel, the segment's tokens
-  int left;                // channels from c0 on
+  int64_t c0, t_lo, t_hi;  // the channel, the segment's tokens
   bool valid;
   __device__ __forceinline__ Lane(const GateArgs& a) {
-    const uint64_t unit = (uint64_t)blockIdx.x * kGateWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint64_t unit = (uint64_t)blockIdx.x * kGateWaves + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     seg = (uint32_t)(unit / a.ctiles);
     ctile = (uint32_t)(unit % a.ctiles);
     valid = seg < a.segs;
-    c0 = ((int64_t)ctile * kWave + lane_id()) * kGateCV<T>;
-    left = (int)max((int64_t)0, min((int64_t)a.g.channels - c0, (int64_t)kGateCV<T>));
-    if (left == 0) c0 = 0;
+    c0 = min((int64_t)ctile * kWave + lane_id(), (int64_t)a.g.channels - 1);
     t_lo = (int64_t)seg * a.seg_len;
     t_hi = min((int64_t)a.g.tokens, t_lo + a.seg_len);
   }
+  // the channel of row j of a tensor of floats (null: 0)
+  __device__ __forceinline__ float load(const GateArgs& a, const float* p, int64_t j) const { return p ? p[j * a.g.channels + c0] : 0.f; }
+  __device__ __forceinline__ void store(const GateArgs& a, float* p, int64_t j, float v) const { p[j * a.g.channels + c0] = v; }
 };
-
-// What comes into segment `seg` from those before it (BACK: after it): aggregates joined in turn, 8 on their way.
-template <typename T, bool BACK>
-__device__ __forceinline__ void joined(const GateArgs& a, const Lane<T>& l, float (&s)[kGateCV<T>]) {
-  constexpr int CV = kGateCV<T>, N = 8;
-#pragma unroll
-  for (int e = 0; e < CV; ++e) s[e] = 0.f;
-  const int32_t n = BACK ? (int32_t)(a.segs - 1 - l.seg) : (int32_t)l.seg;
-  for (int32_t k = 0; k < n; k += N) {
-    float c[N][CV], b[N][CV];
-    uint32_t r[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t at = min(k + i, n - 1), seg = BACK ? a.segs - 1 - at : at;
-      r[i] = a.reset[seg];
-#pragma unroll
-      for (int e = 0; e < CV; ++e) {
-        const uint64_t p = (uint64_t)seg * a.g.channels + l.c0 + (e < l.left ? e : 0);
-        c[i][e] = a.agg_c[p];
-        b[i][e] = a.agg_b[p];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (k + i < n) {
-#pragma unroll
-        for (int e = 0; e < CV; ++e) s[e] = r[i] ? b[i][e] : decayed(c[i][e], s[e]) + b[i][e];
-      }
+__device__ __forceinline__ GateSeqs gate_seqs(const GateArgs& a) {
+  return {a.g.offsets, a.g.offsets ? 0 : (int64_t)(a.g.tokens / a.g.seqs), (int32_t)a.g.seqs};
+}
+// Values by a bit that all lanes share, without branches: v where the bit is set, else `other` (or 0).
+__device__ __forceinline__ float where_bit(uint32_t bits, int i, float v, float other) {
+  const uint32_t m = (uint32_t)((int32_t)(bits << (31 - i)) >> 31);
+  return __uint_as_float((__float_as_uint(v) & m) | (__float_as_uint(other) & ~m));
+}
+__device__ __forceinline__ float unless_bit(uint32_t bits, int i, float v) {
+  return __uint_as_float(__float_as_uint(v) & ~(uint32_t)((int32_t)(bits << (31 - i)) >> 31));
+}
+// For each set bit of a mask, in turn, a token of a tile: f(its sequence, the bit)
+template <typename F>
+__device__ __forceinline__ void each_marked(uint32_t mask, const GateSeqs& seqs, int64_t t0, F f) {
+  while (mask) {
+    f(seqs.of(t0 + __builtin_ctz(mask)), mask & -mask);
+    mask &= mask - 1;
   }
+}
+// Empty sequences: what comes in goes out.  A unit's share of them.
+__device__ __forceinline__ void pass_empty(const GateArgs& a, const Lane& l, const GateSeqs& seqs, const float* in, float* out) {
+  if (!a.g.offsets || !out) return;
+  for (int32_t j = l.seg; j < seqs.seqs; j += a.segs)
+    if (seqs.at(j + 1) <= seqs.at(j)) l.store(a, out, j, l.load(a, in, j));
+}
+
+// ------------------------------------------------------------------ aggregates
+// A segment's decay and its state from zero, b_n + a_n b_{n-1} + a_n a_{n-1} b_{n-2} + ..., from its last token to its first
+// (BACK: mu from zero, a_1 dh_1 + a_1 a_2 dh_2 + ..., from the first to the last): one product and one sum a token, it ends where
+// a sequence begins (BACK: ends), and it leaves in the caches what the whole pass, which goes the other way, reads first.
+template <typename T, int KIND, bool BACK>
+__global__ __launch_bounds__(kWave* kGateWaves) void k_gated_aggregate(GateArgs a) {
+  constexpr int U = kGateU;
+  const Lane l(a);
+  if (!l.valid || l.seg == (BACK ? 0 : a.segs - 1)) return;  // (nothing comes after it)
+  const GateSeqs seqs = gate_seqs(a);
+  const int64_t T_ = (int64_t)a.g.tokens;
+  float p = 1.f, s = 0.f;
+  T g[U], v[U];
+  const int64_t tiles = (l.t_hi - l.t_lo + U - 1) / U, step = BACK ? U : -U;
+  int64_t t0 = BACK ? l.t_lo : l.t_lo + (tiles - 1) * U;
+  Rows<T, BACK ? 1 : -1> rg(a.g.gate, a.g.gate_token, l.c0, BACK ? t0 : t0 + U - 1, T_),
+      rv(BACK ? a.dh : a.g.x, BACK ? (int64_t)a.g.channels : a.g.x_token, l.c0, BACK ? t0 : t0 + U - 1, T_);
+  rg.load(g);
+  rv.load(v);
+  GateMarks m;
+  m.init(seqs);
+  uint32_t none, stop;
+  const auto marks = [&] {
+    m.tile(seqs, t0);
+    const int n = (int)min((int64_t)U, l.t_hi - t0);
+    none = m.outside | (n < U ? ~0u << n & (1u << U) - 1 : 0u);
+    stop = (BACK ? m.ends : m.starts) | none;
+  };
+  const auto token = [&](float c, float b) {
+    if (BACK) p = decayed(c, p);
+    s = fmaf(p, b, s);
+    if (!BACK) p = decayed(c, p);
+  };
+  const auto input = [&](const Gate<KIND>& q, int i) { return BACK || KIND == LAPLEX_GATE_RATE ? to_f32(v[i]) : q.w * to_f32(v[i]); };
+  marks();
+  for (int64_t k = 0; k + 1 < tiles && !stop; ++k) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = BACK ? j : U - 1 - j;
+      const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
+      token(q.c, input(q, i));
+      g[i] = rg.get();  // a row of the next tile takes the place of each as it is used
+      v[i] = rv.get();
+      every_fourth(j);
+    }
+    t0 += step;
+    marks();
+  }
+  // The last tile, or the one where a sequence ends it.  The first to be met of what does: that token counts if it is one, with
+  // what comes into its sequence, those beyond do not.
+  const bool cut = stop != 0;
+  const int h = BACK ? __builtin_ctz(stop | 1u << U) : 31 - __builtin_clz(stop | 1u);
+  const uint32_t bit = cut ? 1u << h : 0u, gone = cut ? (BACK ? ~0u << h : (bit << 1) - 1) & ~(bit & ~none) : 0u;
+  const float w = bit & ~none ? l.load(a, BACK ? a.dstate_out : a.state_in, seqs.of(t0 + h)) : 0.f;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int i = BACK ? j : U - 1 - j;
+    const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
+    const float b = input(q, i);
+    token(unless_bit(gone, i, q.c), unless_bit(gone, i, where_bit(bit, i, BACK ? b + w : decayed(q.c, w) + b, b)));
+  }
+  l.store(a, a.agg_c, l.seg, p);
+  l.store(a, a.agg_b, l.seg, s);
+  if (l.ctile == 0 && lane_id() == 0) a.reset[l.seg] = cut;
 }
 
 // ------------------------------------------------------------------ forward
-// WHOLE: outputs; without, the segment's aggregate alone.
-template <typename T, int KIND, bool WHOLE>
+template <typename T, int KIND>
 __global__ __launch_bounds__(kWave* kGateWaves) void k_gated(GateArgs a) {
-  constexpr int CV = kGateCV<T>, U = kGateU;
-  const Lane<T> l(a);
+  constexpr int U = kGateU;
+  const Lane l(a);
   if (!l.valid) return;
-  const GateSeqs seqs{a.g.offsets, a.g.offsets ? 0 : (int64_t)(a.g.tokens / a.g.seqs), (int32_t)a.g.seqs};
+  const GateSeqs seqs = gate_seqs(a);
   const int64_t T_ = (int64_t)a.g.tokens;
-  const Rows<T> rg{static_cast<const T*>(a.g.gate) + l.c0, a.g.gate_token, l.left}, rx{static_cast<const T*>(a.g.x) + l.c0, a.g.x_token, l.left};
-  float s[CV] = {}, total[CV];
-#pragma unroll
-  for (int e = 0; e < CV; ++e) total[e] = -0.f;  // a decay of 1
-  uint32_t cut = 0;
-  Piece<T> g[U], x[U];
-  rg.load(g, l.t_lo, T_);
-  rx.load(x, l.t_lo, T_);
-  if (WHOLE && l.seg) joined<T, false>(a, l, s);
+  Rows<T, 1> rg(a.g.gate, a.g.gate_token, l.c0, l.t_lo, T_), rx(a.g.x, a.g.x_token, l.c0, l.t_lo, T_), rh(a.h, a.g.channels, l.c0, l.t_lo, T_);
+  float s = 0.f;
+  T g[U], x[U];
+  rg.load(g);
+  rx.load(x);
+  if (l.seg) s = l.load(a, a.agg_b, l.seg);
+  pass_empty(a, l, seqs, a.state_in, a.state_out);
   GateMarks m;
   m.init(seqs);
-  for (int64_t t0 = l.t_lo; t0 < l.t_hi; t0 += U) {
-    float c[U][CV], b[U][CV];
-    TileDecay d[CV];
+  const auto input = [&](const Gate<KIND>& q, int i) { return KIND == LAPLEX_GATE_RATE ? to_f32(x[i]) : q.w * to_f32(x[i]); };
+  for (int64_t t0 = l.t_lo;; t0 += U) {
+    // tiles without a mark but the last
+    for (;; t0 += U) {
+      m.tile(seqs, t0);
+      if (a.carries) l.store(a, a.carries, t0 / U, s);
+      if (m.starts | m.ends | m.outside || t0 + U >= l.t_hi) break;
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int e = 0; e < CV; ++e) {
-        const Gate<KIND> q = gate_of<KIND>(to_f32(g[i].e[e]));
-        c[i][e] = q.c;
-        b[i][e] = KIND == LAPLEX_GATE_RATE ? to_f32(x[i].e[e]) : q.w * to_f32(x[i].e[e]);
-        if (!WHOLE) d[e].add(q.c, q.a);
+      for (int i = 0; i < U; ++i) {
+        const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
+        s = decayed(q.c, s) + input(q, i);
+        g[i] = rg.get();  // a row of the next tile takes the place of each as it is used
+        x[i] = rx.get();
+        rh.put(true, s);
+        every_fourth(i);
       }
-    if (t0 + U < l.t_hi) {
-      rg.load(g, t0 + U, T_);
-      rx.load(x, t0 + U, T_);
     }
-    m.tile(seqs, t0);
-    if (WHOLE && a.carries && l.left) {
-      float* q = a.carries + (uint64_t)(t0 / U) * a.g.channels + l.c0;
-#pragma unroll
-      for (int e = 0; e < CV; ++e)
-        if (e < l.left) q[e] = s[e];
-    }
-    const uint32_t special = m.starts | m.ends | m.outside;
     const int n = (int)min((int64_t)U, l.t_hi - t0);
+    float c[U], b[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (i < n) {
-        if (__builtin_expect(special >> i & 1, 0)) {
-          if (m.starts >> i & 1) {
-            const int32_t q = seqs.of(t0 + i);
-#pragma unroll
-            for (int e = 0; e < CV; ++e) s[e] = a.state_in && e < l.left ? a.state_in[(uint64_t)q * a.g.channels + l.c0 + e] : 0.f;
-            cut = 1;
-          }
-          if (m.outside >> i & 1) {
-            cut = 1;
-#pragma unroll
-            for (int e = 0; e < CV; ++e) s[e] = c[i][e] = b[i][e] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < CV; ++e) s[e] = decayed(c[i][e], s[e]) + b[i][e];
-        if constexpr (WHOLE) {
-          if (l.left) store_piece(static_cast<T*>(a.h) + (uint64_t)(t0 + i) * a.g.channels + l.c0, l.left, s);
-          if (__builtin_expect(a.state_out && (m.ends >> i & 1), 0)) {
-            const int32_t q = seqs.of(t0 + i);
-#pragma unroll
-            for (int e = 0; e < CV; ++e)
-              if (e < l.left) a.state_out[(uint64_t)q * a.g.channels + l.c0 + e] = s[e];
-          }
-        }
-      }
+      const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
+      c[i] = q.c;
+      b[i] = input(q, i);
     }
-    if (!WHOLE) {
+    // a token that begins a sequence is its own state: the initial one goes into its input
+    each_marked(m.starts, seqs, t0, [&](int32_t j, uint32_t bit) {
+      const float v = l.load(a, a.state_in, j);
 #pragma unroll
-      for (int e = 0; e < CV; ++e) total[e] = decay_join(total[e], d[e].coded());
+      for (int i = 0; i < U; ++i) b[i] = where_bit(bit, i, decayed(c[i], v) + b[i], b[i]);
+    });
+    const uint32_t fresh = m.starts | m.outside;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      s = unless_bit(m.outside, i, decayed(c[i], unless_bit(fresh, i, s)) + b[i]);
+      b[i] = s;
+      rh.put(i < n, s);
     }
-  }
-  if constexpr (!WHOLE) {
+    if (a.state_out)
+      each_marked(m.ends, seqs, t0, [&](int32_t j, uint32_t bit) {
+        float v = 0.f;
 #pragma unroll
-    for (int e = 0; e < CV; ++e)
-      if (e < l.left) {
-        const uint64_t p = (uint64_t)l.seg * a.g.channels + l.c0 + e;
-        a.agg_c[p] = total[e];
-        a.agg_b[p] = s[e];
-      }
-    if (l.ctile == 0 && lane_id() == 0) a.reset[l.seg] = cut;
+        for (int i = 0; i < U; ++i) v = where_bit(bit, i, b[i], v);
+        l.store(a, a.state_out, j, v);
+      });
+    if (t0 + U >= l.t_hi) return;
+    rg.load(g);
+    rx.load(x);
   }
 }
 
 // ------------------------------------------------------------------ backward
-// The carry is mu_t = a_t l_t, which token t - 1 receives: mu_t = a_t mu_{t+1} + a_t dh_t.
-template <typename T, int KIND>
-__global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back_aggregate(GateArgs a) {
-  constexpr int CV = kGateCV<T>, U = kGateU;
-  const Lane<T> l(a);
-  if (!l.valid) return;
-  const GateSeqs seqs{a.g.offsets, a.g.offsets ? 0 : (int64_t)(a.g.tokens / a.g.seqs), (int32_t)a.g.seqs};
-  const int64_t T_ = (int64_t)a.g.tokens;
-  const Rows<T> rg{static_cast<const T*>(a.g.gate) + l.c0, a.g.gate_token, l.left},
-      rd{static_cast<const T*>(a.dh) + l.c0, (int64_t)a.g.channels, l.left};
-  float mu[CV] = {}, total[CV];
-#pragma unroll
-  for (int e = 0; e < CV; ++e) total[e] = -0.f;
-  uint32_t cut = 0;
-  Piece<T> g[U], y[U];
-  int64_t t0 = l.t_lo + (l.t_hi - l.t_lo - 1) / U * U;
-  rg.load(g, t0, T_);
-  rd.load(y, t0, T_);
-  GateMarks m;
-  m.init(seqs);
-  for (; t0 >= l.t_lo; t0 -= U) {
-    float c[U][CV], dh[U][CV];
-    TileDecay d[CV];
-    const int n = (int)min((int64_t)U, l.t_hi - t0);
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int e = 0; e < CV; ++e) {
-        const Gate<KIND> q = gate_of<KIND>(to_f32(g[i].e[e]));
-        c[i][e] = q.c;
-        dh[i][e] = to_f32(y[i].e[e]);
-        if (i < n) d[e].add(q.c, q.a);
-      }
-    if (t0 > l.t_lo) {
-      rg.load(g, t0 - U, T_);
-      rd.load(y, t0 - U, T_);
-    }
-    m.tile(seqs, t0);
-    const uint32_t special = m.ends | m.outside;
-#pragma unroll
-    for (int i = U - 1; i >= 0; --i) {
-      if (i < n) {
-        if (__builtin_expect(special >> i & 1, 0)) {
-          cut = 1;
-          const int32_t q = m.ends >> i & 1 ? seqs.of(t0 + i) : 0;
-#pragma unroll
-          for (int e = 0; e < CV; ++e) {
-            mu[e] = m.ends >> i & 1 && a.dstate_out && e < l.left ? a.dstate_out[(uint64_t)q * a.g.channels + l.c0 + e] : 0.f;
-            if (m.outside >> i & 1) c[i][e] = dh[i][e] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < CV; ++e) mu[e] = decayed(c[i][e], mu[e] + dh[i][e]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < CV; ++e) total[e] = decay_join(total[e], d[e].coded());
-  }
-#pragma unroll
-  for (int e = 0; e < CV; ++e)
-    if (e < l.left) {
-      const uint64_t p = (uint64_t)l.seg * a.g.channels + l.c0 + e;
-      a.agg_c[p] = total[e];
-      a.agg_b[p] = mu[e];
-    }
-  if (l.ctile == 0 && lane_id() == 0) a.reset[l.seg] = cut;
-}
-
+// The carry is mu_t = a_t l_t, which token t - 1 receives: mu_t = a_t (mu_{t+1} + dh_t).
 template <typename T, int KIND>
 __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back(GateArgs a) {
-  constexpr int CV = kGateCV<T>, U = kGateU;
-  const Lane<T> l(a);
+  constexpr int U = kGateU;
+  const Lane l(a);
   if (!l.valid) return;
-  const GateSeqs seqs{a.g.offsets, a.g.offsets ? 0 : (int64_t)(a.g.tokens / a.g.seqs), (int32_t)a.g.seqs};
+  const GateSeqs seqs = gate_seqs(a);
   const int64_t T_ = (int64_t)a.g.tokens;
-  const Rows<T> rg{static_cast<const T*>(a.g.gate) + l.c0, a.g.gate_token, l.left}, rx{static_cast<const T*>(a.g.x) + l.c0, a.g.x_token, l.left},
-      rd{static_cast<const T*>(a.dh) + l.c0, (int64_t)a.g.channels, l.left};
-  float mu[CV];
-  Piece<T> g[U], x[U], y[U];
-  float before[CV];
-  auto load_carry = [&](int64_t t0) {
-    const float* q = a.carries_in + (uint64_t)(t0 / U) * a.g.channels + l.c0;
-#pragma unroll
-    for (int e = 0; e < CV; ++e) before[e] = q[e < l.left ? e : 0];
-  };
+  float mu = 0.f;
+  T g[U], x[U], y[U];
   int64_t t0 = l.t_lo + (l.t_hi - l.t_lo - 1) / U * U;
-  rg.load(g, t0, T_);
-  rx.load(x, t0, T_);
-  rd.load(y, t0, T_);
-  load_carry(t0);
-  joined<T, true>(a, l, mu);
+  const int64_t from = t0 + U - 1;
+  Rows<T, -1> rg(a.g.gate, a.g.gate_token, l.c0, from, T_), rx(a.g.x, a.g.x_token, l.c0, from, T_), rd(a.dh, a.g.channels, l.c0, from, T_),
+      out_g(a.dgate, a.g.channels, l.c0, from, T_), out_x(a.dx, a.g.channels, l.c0, from, T_);
+  rg.load(g);
+  rx.load(x);
+  rd.load(y);
+  float before = l.load(a, a.carries_in, t0 / U);
+  if (l.seg + 1 < a.segs) mu = l.load(a, a.agg_b, l.seg);
+  pass_empty(a, l, seqs, a.dstate_out, a.dstate_in);
   GateMarks m;
   m.init(seqs);
   for (; t0 >= l.t_lo; t0 -= U) {
     const int n = (int)min((int64_t)U, l.t_hi - t0);
     m.tile(seqs, t0);
-    Gate<KIND> q[U][CV];
-    float hb[U][CV], s[CV], xs[U][CV], dh[U][CV];
-#pragma unroll
-    for (int e = 0; e < CV; ++e) s[e] = before[e];
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int e = 0; e < CV; ++e) {
-        q[i][e] = gate_of<KIND>(to_f32(g[i].e[e]));
-        xs[i][e] = to_f32(x[i].e[e]);
-        dh[i][e] = to_f32(y[i].e[e]);
-      }
-    if (t0 > l.t_lo) {
-      rg.load(g, t0 - U, T_);
-      rx.load(x, t0 - U, T_);
-      rd.load(y, t0 - U, T_);
-      load_carry(t0 - U);
-    }
-    // the states before each token, from the one that the forward pass kept
+    // each token's decay, the state before it, its input and gradient (and, with marks, what it hands on)
+    float c[U], hb[U] = {}, xs[U], dh[U], s = before;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (__builtin_expect(m.starts >> i & 1, 0)) {
-        const int32_t j = seqs.of(t0 + i);
-#pragma unroll
-        for (int e = 0; e < CV; ++e) s[e] = a.state_in && e < l.left ? a.state_in[(uint64_t)j * a.g.channels + l.c0 + e] : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < CV; ++e) {
-        hb[i][e] = s[e];
-        s[e] = decayed(q[i][e].c, s[e]) + (KIND == LAPLEX_GATE_RATE ? xs[i][e] : q[i][e].w * xs[i][e]);
-      }
+      c[i] = to_f32(g[i]);
+      xs[i] = to_f32(x[i]);
+      dh[i] = to_f32(y[i]);
     }
+    if (t0 > l.t_lo) {
+      rg.load(g);
+      rx.load(x);
+      rd.load(y);
+      before = l.load(a, a.carries_in, t0 / U - 1);
+    }
+    const uint32_t none = m.outside | (n < U ? ~0u << n : 0u);
+    const auto tile = [&](auto all) {
+      constexpr bool ALL = decltype(all)::value;  // no marks
+      // the states before each token, from the one that the forward pass kept
 #pragma unroll
-    for (int i = U - 1; i >= 0; --i) {
-      if (i < n) {
-        if (__builtin_expect((m.ends | m.outside) >> i & 1, 0)) {
-          const int32_t j = m.ends >> i & 1 ? seqs.of(t0 + i) : 0;
-#pragma unroll
-          for (int e = 0; e < CV; ++e)
-            mu[e] = m.ends >> i & 1 && a.dstate_out && e < l.left ? a.dstate_out[(uint64_t)j * a.g.channels + l.c0 + e] : 0.f;
-        }
-        float dg[CV], dx[CV];
-#pragma unroll
-        for (int e = 0; e < CV; ++e) {
-          const float lam = dh[i][e] + mu[e];
-          if (KIND == LAPLEX_GATE_RATE) {
-            dg[e] = -q[i][e].a * (hb[i][e] * lam);
-            dx[e] = lam;
-          } else {
-            dx[e] = q[i][e].w * lam;
-            dg[e] = q[i][e].a * ((hb[i][e] - xs[i][e]) * dx[e]);
-          }
-          mu[e] = decayed(q[i][e].c, lam);
-        }
-        if (__builtin_expect(m.outside >> i & 1, 0)) {
-#pragma unroll
-          for (int e = 0; e < CV; ++e) dg[e] = dx[e] = mu[e] = 0.f;
-        }
-        if (l.left) {
-          const uint64_t at = (uint64_t)(t0 + i) * a.g.channels + l.c0;
-          store_piece(static_cast<T*>(a.dgate) + at, l.left, dg);
-          store_piece(static_cast<T*>(a.dx) + at, l.left, dx);
-        }
-        if (__builtin_expect(a.dstate_in && (m.starts >> i & 1), 0)) {
-          const int32_t j = seqs.of(t0 + i);
-#pragma unroll
-          for (int e = 0; e < CV; ++e)
-            if (e < l.left) a.dstate_in[(uint64_t)j * a.g.channels + l.c0 + e] = mu[e];
-        }
+      for (int i = 0; i < U; ++i) {
+        const Gate<KIND> q = gate_of<KIND>(c[i]);
+        c[i] = q.c;
+        if (!ALL) s = where_bit(m.starts, i, hb[i], s);
+        hb[i] = s;
+        s = decayed(q.c, s) + (KIND == LAPLEX_GATE_RATE ? xs[i] : q.w * xs[i]);
       }
+#pragma unroll
+      for (int i = U - 1; i >= 0; --i) {
+        const float lam = dh[i] + (ALL ? mu : unless_bit(m.ends, i, mu)), av = decay_value(c[i]);
+        float dg, dx;
+        if (KIND == LAPLEX_GATE_RATE) {
+          dx = lam;
+          dg = -av * (hb[i] * lam);
+        } else {
+          dx = (near_one(c[i]) ? -c[i] : 1.f - c[i]) * lam;  // (a decay near 1 is kept as a - 1)
+          dg = av * ((hb[i] - xs[i]) * dx);
+        }
+        mu = decayed(c[i], lam);
+        if (!ALL) {
+          dg = unless_bit(none, i, dg);
+          dx = unless_bit(none, i, dx);
+          dh[i] = mu = unless_bit(none, i, mu);
+        }
+        out_g.put(ALL || i < n, dg);
+        out_x.put(ALL || i < n, dx);
+      }
+    };
+    if (__builtin_expect(!(m.starts | m.ends | m.outside) && n == U, 1)) {
+      tile(std::true_type{});
+    } else {
+      // initial states in the places of those before; what comes into a sequence's last token goes into its gradient
+      each_marked(m.starts, seqs, t0, [&](int32_t j, uint32_t bit) {
+        const float v = l.load(a, a.state_in, j);
+#pragma unroll
+        for (int i = 0; i < U; ++i) hb[i] = where_bit(bit, i, v, hb[i]);
+      });
+      each_marked(m.ends, seqs, t0, [&](int32_t j, uint32_t bit) {
+        const float v = l.load(a, a.dstate_out, j);
+#pragma unroll
+        for (int i = 0; i < U; ++i) dh[i] = where_bit(bit, i, dh[i] + v, dh[i]);
+      });
+      tile(std::false_type{});
+      if (a.dstate_in)
+        each_marked(m.starts, seqs, t0, [&](int32_t j, uint32_t bit) {
+          float v = 0.f;
+#pragma unroll
+          for (int i = 0; i < U; ++i) v = where_bit(bit, i, dh[i], v);
+          l.store(a, a.dstate_in, j, v);
+        });
     }
   }
 }
 
-// Empty sequences: what comes in goes out.
-__global__ __launch_bounds__(256) void k_gated_empty(GateSeqs s, uint32_t channels, const float* __restrict__ in, float* __restrict__ out) {
-  for (int32_t j = blockIdx.x; j < s.seqs; j += gridDim.x) {
-    if (s.at(j + 1) > s.at(j)) continue;
-    for (uint32_t c = threadIdx.x; c < channels; c += 256) {
-      const uint64_t at = (uint64_t)j * channels + c;
-      out[at] = in ? in[at] : 0.f;
+// ------------------------------------------------------------------ join
+// The segments' aggregates joined in turn: agg_b becomes what comes into each segment from those before it (BACK: after
+// it).  A block takes 16 channels, each of them in 64 stretches at once: a stretch's own aggregate, those of the stretches
+// before it, and then its segments.
+constexpr int kJoinChannels = 16, kJoinParts = 64;
+template <bool BACK>
+__global__ __launch_bounds__(kJoinChannels* kJoinParts) void k_gated_join(GateArgs a) {
+  __shared__ float sc[kJoinParts][kJoinChannels], sb[kJoinParts][kJoinChannels];
+  __shared__ uint32_t sr[kJoinParts];
+  const uint32_t lane = threadIdx.x % kJoinChannels, part = threadIdx.x / kJoinChannels;
+  const uint64_t at = (uint64_t)blockIdx.x * kJoinChannels + lane, ch = min(at, (uint64_t)a.g.channels - 1);
+  // (nothing comes after the last segment)
+  const int32_t n = a.segs - 1, per = (n + kJoinParts - 1) / kJoinParts, lo = min(n, (int32_t)part * per), hi = min(n, lo + per);
+  const auto seg = [&](int32_t k) { return (uint32_t)(BACK ? n - k : k); };
+  constexpr int N = 8;  // on their way
+  float c = 1.f, b = 0.f, vc[N], vb[N];
+  uint32_t r = 0, vr[N];
+  const auto load = [&](int32_t k) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t q = seg(min(k + i, hi - 1));
+      vr[i] = a.reset[q];
+      vc[i] = a.agg_c[(uint64_t)q * a.g.channels + ch];
+      vb[i] = a.agg_b[(uint64_t)q * a.g.channels + ch];
     }
+  };
+  for (int32_t k = lo; k < hi; k += N) {
+    load(k);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (k + i < hi) {
+        b = vr[i] ? vb[i] : fmaf(vc[i], b, vb[i]);
+        c *= vc[i];
+        r |= vr[i];
+      }
   }
+  sc[part][lane] = c;
+  sb[part][lane] = b;
+  if (lane == 0) sr[part] = r;
+  __syncthreads();
+  float s = 0.f;
+  for (uint32_t q = 0; q < part; ++q) s = sr[q] ? sb[q][lane] : fmaf(sc[q][lane], s, sb[q][lane]);
+  for (int32_t k = lo; k < hi; k += N) {
+    if (hi - lo > N) load(k);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (k + i < hi) {
+        if (at < a.g.channels) a.agg_b[(uint64_t)seg(k + i) * a.g.channels + ch] = s;
+        s = vr[i] ? vb[i] : fmaf(vc[i], s, vb[i]);
+      }
+  }
+  if (hi == n && lo < hi && at < a.g.channels) a.agg_b[(uint64_t)seg(n) * a.g.channels + ch] = s;
+}
+
+// Sequences that are all empty (there are no tokens): what comes in goes out.
+__global__ __launch_bounds__(256) void k_gated_empty(uint64_t count, const float* __restrict__ in, float* __restrict__ out) {
+  const uint64_t stride = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += stride) out[i] = in ? in[i] : 0.f;
 }
 
 // ------------------------------------------------------------------ launches
@@ -557,11 +548,12 @@ struct GatePlan {
   uint32_t segs, ctiles;
   int64_t seg_len;
 };
-// About as many waves as the chip holds at once (256 CUs x 8), segments of at least four tiles.
-constexpr uint64_t kGateUnits = 2048, kGateLeast = 64;
-static GatePlan gate_plan(uint32_t channels, uint64_t tokens, int cv) {
+// As many waves as the chip holds at once of the passes with 88 registers (five a SIMD), segments of at least four tiles
+// (16384 tokens x 4096 channels in bfloat16, forward and backward: 351 us; 4096 waves 379, 6144 363, 8192 397).
+constexpr uint64_t kGateUnits = 5120, kGateLeast = 64;
+static GatePlan gate_plan(uint32_t channels, uint64_t tokens) {
   GatePlan p;
-  p.ctiles = (channels + kWave * cv - 1) / (kWave * cv);
+  p.ctiles = (channels + kWave - 1) / kWave;
   const uint64_t want = std::max<uint64_t>(1, kGateUnits / p.ctiles);
   uint64_t len = std::max<uint64_t>(kGateLeast, (tokens + want - 1) / want);
   len = (len + kGateChunk - 1) / kGateChunk * kGateChunk;
@@ -571,14 +563,14 @@ static GatePlan gate_plan(uint32_t channels, uint64_t tokens, int cv) {
 }
 // (a segment is at least tokens / want long, so there are at most `want`, and at most tokens / least rounded up)
 size_t gated_scan_bytes(uint32_t channels, uint64_t tokens) {
-  const uint64_t ctiles = (channels + kWave * 2 - 1) / (kWave * 2);  // the fewest, with two channels a lane
+  const uint64_t ctiles = (channels + kWave - 1) / kWave;
   const uint64_t segs = std::min<uint64_t>(std::max<uint64_t>(1, kGateUnits / ctiles), (tokens + kGateLeast - 1) / kGateLeast);
   if (segs <= 1) return 0;
   return ((size_t)segs * channels * 8 + segs * 4 + 255) & ~size_t(255);
 }
 
 static hipError_t gate_ready(GateArgs& a, const GateShape& g, void* ws) {
-  const GatePlan p = gate_plan(g.channels, g.tokens, g.dtype == LAPLEX_BF16 ? 2 : 1);
+  const GatePlan p = gate_plan(g.channels, g.tokens);
   a.g = g;
   a.seg_len = p.seg_len;
   a.segs = p.segs;
@@ -598,17 +590,16 @@ static void by_type(const GateShape& g, F f) {
   else rate ? f(float{}, std::integral_constant<int, LAPLEX_GATE_RATE>{}) : f(float{}, std::integral_constant<int, LAPLEX_GATE_SIGMOID>{});
 }
 static hipError_t gate_empty(const GateShape& g, const float* in, float* out, hipStream_t s) {
-  if (!out || (!g.offsets && g.tokens)) return hipSuccess;  // (equal lengths of at least one token: no empty sequence)
-  const GateSeqs q{g.offsets, g.offsets ? 0 : (int64_t)(g.tokens / g.seqs), (int32_t)g.seqs};
-  LAPLEX_LAUNCH("k_gated_empty", g.seqs, s, k_gated_empty<<<std::min(g.seqs, 2048u), 256, 0, s>>>(q, g.channels, in, out));
+  const uint64_t n = (uint64_t)g.seqs * g.channels;
+  if (out) LAPLEX_LAUNCH("k_gated_empty", g.seqs, s, k_gated_empty<<<(unsigned)std::min<uint64_t>((n + 255) / 256, 4096), 256, 0, s>>>(n, in, out));
   return hipGetLastError();
 }
 
 hipError_t gated_scan(const GateShape& g, const float* state_in, float* state_out, void* h, float* carries, void* ws, hipStream_t s) {
-  hipError_t err = gate_empty(g, state_in, state_out, s);
-  if (err != hipSuccess || g.tokens == 0) return err;
+  if (g.tokens == 0) return gate_empty(g, state_in, state_out, s);
   GateArgs a{};
-  if ((err = gate_ready(a, g, ws)) != hipSuccess) return err;
+  const hipError_t err = gate_ready(a, g, ws);
+  if (err != hipSuccess) return err;
   a.state_in = state_in;
   a.state_out = state_out;
   a.h = h;
@@ -616,18 +607,21 @@ hipError_t gated_scan(const GateShape& g, const float* state_in, float* state_ou
   const unsigned blocks = (unsigned)(((uint64_t)a.segs * a.ctiles + kGateWaves - 1) / kGateWaves);
   by_type(g, [&](auto t, auto kind) {
     using T = decltype(t);
-    if (a.segs > 1) LAPLEX_LAUNCH("k_gated_aggregate", g.tokens, s, k_gated<T, kind(), false><<<blocks, kWave * kGateWaves, 0, s>>>(a));
-    LAPLEX_LAUNCH("k_gated", g.tokens, s, k_gated<T, kind(), true><<<blocks, kWave * kGateWaves, 0, s>>>(a));
+    if (a.segs > 1) {
+      LAPLEX_LAUNCH("k_gated_aggregate", g.tokens, s, k_gated_aggregate<T, kind(), false><<<blocks, kWave * kGateWaves, 0, s>>>(a));
+      LAPLEX_LAUNCH("k_gated_join", a.segs, s, k_gated_join<false><<<(g.channels + kJoinChannels - 1) / kJoinChannels, kJoinChannels * kJoinParts, 0, s>>>(a));
+    }
+    LAPLEX_LAUNCH("k_gated", g.tokens, s, k_gated<T, kind()><<<blocks, kWave * kGateWaves, 0, s>>>(a));
   });
   return hipGetLastError();
 }
 
 hipError_t gated_scan_backward(const GateShape& g, const float* carries, const void* dh, const float* state_in,
                                const float* dstate_out, void* dgate, void* dx, float* dstate_in, void* ws, hipStream_t s) {
-  hipError_t err = gate_empty(g, dstate_out, dstate_in, s);
-  if (err != hipSuccess || g.tokens == 0) return err;
+  if (g.tokens == 0) return gate_empty(g, dstate_out, dstate_in, s);
   GateArgs a{};
-  if ((err = gate_ready(a, g, ws)) != hipSuccess) return err;
+  const hipError_t err = gate_ready(a, g, ws);
+  if (err != hipSuccess) return err;
   a.state_in = state_in;
   a.carries_in = carries;
   a.dh = dh;
@@ -638,8 +632,10 @@ hipError_t gated_scan_backward(const GateShape& g, const float* carries, const v
   const unsigned blocks = (unsigned)(((uint64_t)a.segs * a.ctiles + kGateWaves - 1) / kGateWaves);
   by_type(g, [&](auto t, auto kind) {
     using T = decltype(t);
-    if (a.segs > 1)
-      LAPLEX_LAUNCH("k_gated_back_aggregate", g.tokens, s, k_gated_back_aggregate<T, kind()><<<blocks, kWave * kGateWaves, 0, s>>>(a));
+    if (a.segs > 1) {
+      LAPLEX_LAUNCH("k_gated_aggregate", g.tokens, s, k_gated_aggregate<T, kind(), true><<<blocks, kWave * kGateWaves, 0, s>>>(a));
+      LAPLEX_LAUNCH("k_gated_join", a.segs, s, k_gated_join<true><<<(g.channels + kJoinChannels - 1) / kJoinChannels, kJoinChannels * kJoinParts, 0, s>>>(a));
+    }
     LAPLEX_LAUNCH("k_gated_back", g.tokens, s, k_gated_back<T, kind()><<<blocks, kWave * kGateWaves, 0, s>>>(a));
   });
   return hipGetLastError();
