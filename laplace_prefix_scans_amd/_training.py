@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import array
 import ctypes
-import struct
+from itertools import chain
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
@@ -253,19 +253,20 @@ def laplex_linear_cross_entropy_backward(x: torch.Tensor, table: torch.Tensor, t
 
 
 # ------------------------------------------------------------------ AdamW
-def _list(name: str, ts, count: int, dtype, dev, sizes, blocks: bool = False):
-    """The pointers of `count` contiguous tensors of a type and of these numbers of elements (blocks: of 256 of them)."""
+def _list(name: str, ts, count: int, dtype, dev, sizes):
+    """The pointers of `count` contiguous tensors of a type and of these numbers of elements."""
     if len(ts) != count:
         raise ValueError("%s must have a tensor for each of the %d parameters, got %d" % (name, count, len(ts)))
-    got = []
-    for t, n in zip(ts, sizes):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must hold torch tensors" % name)
-        if t.dtype is not dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if t.device != dev or not t.is_contiguous() or t.numel() != (-(-n // 256) if blocks else n):
-            raise ValueError("%s must be contiguous, on %s and of its parameter's size" % (name, dev))
-        got.append(t.data_ptr())
+    at, got = dev.index, []
+    try:
+        for t, n in zip(ts, sizes):
+            if t.dtype is not dtype:
+                raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+            if t.numel() != n or t.get_device() != at or not t.is_contiguous():
+                raise ValueError("%s must be contiguous, on %s and of its parameter's size" % (name, dev))
+            got.append(t.data_ptr())
+    except AttributeError:
+        raise TypeError("%s must hold torch tensors" % name) from None
     return got
 
 
@@ -303,20 +304,21 @@ def laplex_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], 
     if (m_scale is not None and v_scale is not None) != (bits == 8) or (m_scale is None) != (v_scale is None):
         raise ValueError("m_scale and v_scale go with 8-bit moments")
     sizes = [p.numel() for p in params]
+    blocks = [-(-n // 256) for n in sizes] if bits == 8 else sizes
     code = _dtype(params[0], "params")
     zero = [0] * count
     decay = [float(weight_decay)] * count if isinstance(weight_decay, (int, float)) else [float(w) for w in weight_decay]
     if len(decay) != count:
         raise ValueError("weight_decay must be a number, or one for each parameter")
-    if isinstance(grads[0], torch.Tensor) is False or grads[0].dtype not in _DTYPES:
+    if not isinstance(grads[0], torch.Tensor) or grads[0].dtype not in _DTYPES:
         raise TypeError("grads must be float32 or bfloat16 tensors")
     columns = (_list("params", params, count, params[0].dtype, dev, sizes), _list("grads", grads, count, grads[0].dtype, dev, sizes),
                _list("m", m, count, m[0].dtype, dev, sizes), _list("v", v, count, m[0].dtype, dev, sizes),
-               _list("m_scale", m_scale, count, torch.float32, dev, sizes, True) if bits == 8 else zero,
-               _list("v_scale", v_scale, count, torch.float32, dev, sizes, True) if bits == 8 else zero,
+               _list("m_scale", m_scale, count, torch.float32, dev, blocks) if bits == 8 else zero,
+               _list("v_scale", v_scale, count, torch.float32, dev, blocks) if bits == 8 else zero,
                _list("master", master, count, torch.float32, dev, sizes) if master is not None else zero,
-               sizes, [struct.unpack("I", struct.pack("f", w))[0] for w in decay])
-    table = array.array("Q", [x for row in zip(*columns) for x in row])  # laplex_adamw_tensor, field by field
+               sizes, array.array("I", array.array("f", decay).tobytes()))
+    table = array.array("Q", chain.from_iterable(zip(*columns)))  # laplex_adamw_tensor, field by field
     step_dev, lr_dev = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
     if step_dev:
         _scalar(step, "step", torch.int32, dev)
@@ -351,13 +353,14 @@ def laplex_adamw_moments(m: Sequence[torch.Tensor], v: Sequence[torch.Tensor], m
     if not m[0].is_cuda:
         raise ValueError("moments must be on a GPU device")
     dev, sizes = m[0].device, [t.numel() for t in m]
+    blocks = [-(-n // 256) for n in sizes]
     m_out = [torch.empty(t.shape, dtype=torch.float32, device=dev) for t in m] if m_out is None else m_out
     v_out = [torch.empty(t.shape, dtype=torch.float32, device=dev) for t in v] if v_out is None else v_out
     zero = [0] * count
     columns = (_list("m_out", m_out, count, torch.float32, dev, sizes), zero, _list("m", m, count, m[0].dtype, dev, sizes),
-               _list("v", v, count, m[0].dtype, dev, sizes), _list("m_scale", m_scale, count, torch.float32, dev, sizes, True),
-               _list("v_scale", v_scale, count, torch.float32, dev, sizes, True),
+               _list("v", v, count, m[0].dtype, dev, sizes), _list("m_scale", m_scale, count, torch.float32, dev, blocks),
+               _list("v_scale", v_scale, count, torch.float32, dev, blocks),
                _list("v_out", v_out, count, torch.float32, dev, sizes), sizes, zero)
-    table = array.array("Q", [x for row in zip(*columns) for x in row])
+    table = array.array("Q", chain.from_iterable(zip(*columns)))
     _run("laplex_adamw_moments", dev, _lib().laplex_adamw_moments, table.buffer_info()[0], count)
     return m_out, v_out

@@ -3,8 +3,10 @@
 //   g' = s g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2,
 //   p = (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
 //
-// A block takes 2048 elements of a tensor at a time, eight consecutive ones a
-// thread, and reads and writes everything once: bound by HBM.
+// A block takes 2048 elements of a tensor at a time and reads and writes
+// everything once.  With float moments a thread has two pieces of four
+// consecutive elements, so that a wave's floats are whole 1024-byte stretches;
+// with 8-bit ones eight consecutive elements.
 //
 // 8-bit states: a block of 256 values (32 threads) shares a float scale, its
 // largest magnitude / 448; m and sqrt(v) are e4m3 codes of the values over it.
@@ -20,7 +22,7 @@
 
 namespace laplex {
 
-constexpr int kAdamBlock = 256, kAdamPer = 8, kAdamChunk = kAdamBlock * kAdamPer;
+constexpr int kAdamBlock = 256, kAdamChunk = 2048;
 constexpr int kAdamGroup = 40;  // tensors of a launch: its arguments stay below 4 KB
 
 struct AdamTensor {
@@ -37,7 +39,8 @@ struct AdamTensor {
 struct AdamArgs {
   AdamTensor t[kAdamGroup];
   uint32_t count, chunks;
-  float b1, one_b1, b2, one_b2, eps, rate, root_c2;
+  float b1, one_b1, b2, one_b2, eps, rate, inv_c2;  // (inv_c2: of the square root of 1 - beta2^step)
+  bool divide;  // eps is so small that its reciprocal may be infinite
   uint32_t seed;
   int32_t stochastic;
   uint64_t step;
@@ -54,42 +57,44 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, uint64_t left, float (&v)[kAdamPer]) {
-  T e[kAdamPer];
-  if (left >= kAdamPer) {
+// N consecutive elements, of which `left` are the tensor's
+template <int N, typename T>
+__device__ __forceinline__ void load_some(const T* p, int64_t left, float (&v)[N]) {
+  T e[N];
+  if (left >= N) {
     __builtin_memcpy(e, p, sizeof e);
   } else {
 #pragma unroll
-    for (int i = 0; i < kAdamPer; ++i) e[i] = i < (int)left ? p[i] : T(0.f);
+    for (int i = 0; i < N; ++i) e[i] = i < left ? p[i] : T(0.f);
   }
 #pragma unroll
-  for (int i = 0; i < kAdamPer; ++i) v[i] = to_f32(e[i]);
+  for (int i = 0; i < N; ++i) v[i] = to_f32(e[i]);
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, uint64_t left, const float (&v)[kAdamPer]) {
-  T e[kAdamPer];
+template <int N, typename T>
+__device__ __forceinline__ void store_some(T* p, int64_t left, const float (&v)[N]) {
+  T e[N];
 #pragma unroll
-  for (int i = 0; i < kAdamPer; ++i) e[i] = from_f32<T>(v[i]);
-  if (left >= kAdamPer) {
+  for (int i = 0; i < N; ++i) e[i] = from_f32<T>(v[i]);
+  if (left >= N) {
     __builtin_memcpy(p, e, sizeof e);
   } else {
 #pragma unroll
-    for (int i = 0; i < kAdamPer; ++i)
-      if (i < (int)left) p[i] = e[i];
+    for (int i = 0; i < N; ++i)
+      if (i < left) p[i] = e[i];
   }
 }
 
 // ------------------------------------------------------------------ e4m3 codes
-__device__ __forceinline__ void load_codes(const uint8_t* p, uint64_t left, float scale, float (&v)[kAdamPer]) {
-  uint32_t w[2] = {0, 0};
-  if (left >= kAdamPer) {
-    __builtin_memcpy(w, p, 8);
+template <int N>
+__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t left, float scale, float (&v)[N]) {
+  uint32_t w[N / 4] = {};
+  if (left >= N) {
+    __builtin_memcpy(w, p, N);
   } else {
     for (int i = 0; i < (int)left; ++i) w[i / 4] |= (uint32_t)p[i] << i % 4 * 8;
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < N / 4; ++i) {
     const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], true);
     v[4 * i] = a[0] * scale;
     v[4 * i + 1] = a[1] * scale;
@@ -97,47 +102,44 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint64_t left, floa
     v[4 * i + 3] = b[1] * scale;
   }
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, uint64_t left, const uint32_t (&c)[kAdamPer]) {
-  if (left >= kAdamPer) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t left, const uint32_t (&c)[8]) {
+  if (left >= 8) {
     const uint32_t w[2] = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
     __builtin_memcpy(p, w, 8);
   } else {
 #pragma unroll
-    for (int i = 0; i < kAdamPer; ++i)
-      if (i < (int)left) p[i] = (uint8_t)c[i];
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = (uint8_t)c[i];
   }
 }
-// the largest finite magnitude of the 32 threads' values
-__device__ __forceinline__ float block_most(const float (&v)[kAdamPer]) {
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+// the largest of the 32 threads' magnitudes (NaN is passed over); finite_only: of those that are finite
+__device__ __forceinline__ float block_most(const float (&v)[8], bool finite_only) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < kAdamPer; ++i) {
-    const float a = fabsf(v[i]);
-    m = fmaxf(m, a <= 3.402823466e38f ? a : 0.f);
-  }
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_only && !finite(v[i]) ? 0.f : fabsf(v[i]));
 #pragma unroll
   for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
   return m;
 }
-// Magnitudes below 2^-100 of a block's largest are kept as zeros of that scale (its reciprocal would be infinite).
+// Magnitudes below 2^-100 are kept as zeros (the reciprocal of their scale would be infinite).
 __device__ __forceinline__ float inverse_scale(float most) { return most >= 0x1p-100f ? 448.f / most : 0.f; }
 // e4m3 magnitude of |x| / scale; r: 16 random bits (0x8000: to nearest).  Subnormals, multiples of 2^-9, are those
 // of the binade from 2^-6 on, moved there by an addition.
 __device__ __forceinline__ uint32_t code_of(float x, float inverse, uint32_t r) {
   const float y = fminf(fabsf(x) * inverse, 448.f);
   const bool small = y < 0x1p-6f;
-  const float t = small ? y + 0x1p-6f : y;
-  const uint32_t c = ((__float_as_uint(t) + (r << 4)) >> 20) - 960u - (small ? 8u : 0u);
-  return fabsf(x) <= 3.402823466e38f ? c : 0x7Fu;  // NaN
+  return ((__float_as_uint(small ? y + 0x1p-6f : y) + (r << 4)) >> 20) - (small ? 968u : 960u);
 }
 
 // ------------------------------------------------------------------ the step
 template <typename P, typename G, int BITS>
 __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
-  __shared__ float sh[3];
+  __shared__ float sh[2];
+  constexpr int N = BITS == 8 ? 8 : 4, PIECES = 8 / N;
   const float scale = a.grad_scale ? *a.grad_scale : 1.f;
-  if (!(fabsf(scale) <= 3.402823466e38f)) return;  // the step is skipped
-  float rate = a.rate, root_c2 = a.root_c2;
+  if (!finite(scale)) return;  // the step is skipped
+  float rate = a.rate, inv_c2 = a.inv_c2;
   uint64_t step = a.step;
   double lr = a.lr;
   if (a.step_dev || a.lr_dev) {
@@ -145,75 +147,98 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
     if (a.lr_dev) lr = (double)*a.lr_dev;
     if (threadIdx.x == 0) {
       sh[0] = (float)(lr / (1.0 - pow(a.beta1, (double)step)));
-      sh[1] = (float)sqrt(1.0 - pow(a.beta2, (double)step));
+      sh[1] = (float)(1.0 / sqrt(1.0 - pow(a.beta2, (double)step)));
     }
     __syncthreads();
     rate = sh[0];
-    root_c2 = sh[1];
+    inv_c2 = sh[1];
   }
   uint32_t k = 0;  // the tensor of the chunk before
   for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     while (k + 1 < a.count && a.t[k + 1].chunk0 <= chunk) ++k;
     const AdamTensor& t = a.t[k];
-    const uint64_t at = (uint64_t)(chunk - t.chunk0) * kAdamChunk + threadIdx.x * kAdamPer;
-    const uint64_t left = at < t.n ? t.n - at : 0;
     const float keep = a.lr_dev ? (float)(1.0 - lr * (double)t.wd) : t.keep;
-    const uint64_t block = at / 256;
-    float p[kAdamPer] = {}, g[kAdamPer] = {}, m[kAdamPer] = {}, v[kAdamPer] = {};
-    if (left) {
-      if (t.master) load8(t.master + at, left, p);
-      else load8(static_cast<const P*>(t.p) + at, left, p);
-      load8(static_cast<const G*>(t.g) + at, left, g);
-      if constexpr (BITS == 32) {
-        load8(static_cast<const float*>(t.m) + at, left, m);
-        load8(static_cast<const float*>(t.v) + at, left, v);
-      } else {
-        load_codes(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[block], m);
-        load_codes(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[block], v);
+    float p[PIECES][N] = {}, g[PIECES][N] = {}, m[PIECES][N] = {}, v[PIECES][N] = {};
+    const uint64_t at0 = (uint64_t)(chunk - t.chunk0) * kAdamChunk + threadIdx.x * N;
 #pragma unroll
-        for (int i = 0; i < kAdamPer; ++i) v[i] *= v[i];
+    for (int q = 0; q < PIECES; ++q) {
+      const uint64_t at = at0 + q * (kAdamBlock * N);
+      const int64_t left = (int64_t)t.n - (int64_t)at;
+      if (left <= 0) continue;
+      if (t.master) load_some(t.master + at, left, p[q]);
+      else load_some(static_cast<const P*>(t.p) + at, left, p[q]);
+      load_some(static_cast<const G*>(t.g) + at, left, g[q]);
+      if constexpr (BITS == 32) {
+        load_some(static_cast<const float*>(t.m) + at, left, m[q]);
+        load_some(static_cast<const float*>(t.v) + at, left, v[q]);
+      } else {
+        load_codes(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[at / 256], m[q]);
+        load_codes(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[at / 256], v[q]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[q][i] *= v[q][i];
       }
     }
 #pragma unroll
-    for (int i = 0; i < kAdamPer; ++i) {
-      const float gi = a.grad_scale ? g[i] * scale : g[i];
-      m[i] = a.b1 * m[i] + a.one_b1 * gi;
-      v[i] = a.b2 * v[i] + a.one_b2 * (gi * gi);
-      const float root = sqrtf(v[i]);
-      p[i] = p[i] * keep - rate * m[i] / (root / root_c2 + a.eps);
-      if constexpr (BITS == 8) v[i] = root;
-    }
-    if (left) {
-      store8(static_cast<P*>(t.p) + at, left, p);
-      if (t.master) store8(t.master + at, left, p);
-      if constexpr (BITS == 32) {
-        store8(static_cast<float*>(t.m) + at, left, m);
-        store8(static_cast<float*>(t.v) + at, left, v);
+    for (int q = 0; q < PIECES; ++q) {
+      const uint64_t at = at0 + q * (kAdamBlock * N);
+      const int64_t left = (int64_t)t.n - (int64_t)at;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float gi = a.grad_scale ? g[q][i] * scale : g[q][i];
+        m[q][i] = a.b1 * m[q][i] + a.one_b1 * gi;
+        v[q][i] = a.b2 * v[q][i] + a.one_b2 * (gi * gi);
+        const float root = sqrtf(v[q][i]), d = fmaf(root, inv_c2, a.eps), up = rate * m[q][i];
+        // (a reciprocal's last bit is nothing beside lr)
+        p[q][i] = p[q][i] * keep - (a.divide ? up / d : up * __builtin_amdgcn_rcpf(d));
+        if constexpr (BITS == 8) v[q][i] = root;
+      }
+      if (left > 0) {
+        store_some(static_cast<P*>(t.p) + at, left, p[q]);
+        if (t.master) store_some(t.master + at, left, p[q]);
+        if constexpr (BITS == 32) {
+          store_some(static_cast<float*>(t.m) + at, left, m[q]);
+          store_some(static_cast<float*>(t.v) + at, left, v[q]);
+        }
       }
     }
     if constexpr (BITS == 8) {
-      if (left < kAdamPer) {
+      const uint64_t at = at0;
+      const int64_t left = (int64_t)t.n - (int64_t)at;
+      if (left < N) {
 #pragma unroll
-        for (int i = 0; i < kAdamPer; ++i)
-          if (i >= (int)left) m[i] = v[i] = 0.f;
+        for (int i = 0; i < N; ++i)
+          if (i >= left) m[0][i] = v[0][i] = 0.f;
       }
-      const float mm = block_most(m), vm = block_most(v);
+      float mm = block_most(m[0], false), vm = block_most(v[0], false);
+      // (a NaN, which has no part in a maximum, shows in the sum of squares)
+      float all = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) all += v[0][i];
+      const bool bad = __any(!finite(all) || !finite(mm));
+      if (bad) {
+        mm = block_most(m[0], true);
+        vm = block_most(v[0], true);
+      }
       const float mi = inverse_scale(mm), vi = inverse_scale(vm);
       const uint32_t key = mix32(mix32(t.number * 0x9E3779B9u + (uint32_t)step) ^ a.seed) ^ (uint32_t)(at >> 32) * 0x85EBCA6Bu;
-      uint32_t cm[kAdamPer], cv[kAdamPer];
+      uint32_t cm[N], cv[N];
 #pragma unroll
-      for (int i = 0; i < kAdamPer; ++i) {
+      for (int i = 0; i < N; ++i) {
         const uint32_t r = a.stochastic ? mix32((uint32_t)(at + i) ^ key) : 0x80008000u;
-        cm[i] = code_of(m[i], mi, r & 0xFFFFu) | (m[i] < 0.f ? 128u : 0u);
-        cv[i] = code_of(v[i], vi, r >> 16);
-        if (v[i] > 0.f && cv[i] == 0) cv[i] = 1;
+        cm[i] = code_of(m[0][i], mi, r & 0xFFFFu) | (m[0][i] < 0.f ? 128u : 0u);
+        cv[i] = code_of(v[0][i], vi, r >> 16);
+        if (v[0][i] > 0.f && cv[i] == 0) cv[i] = 1;
+        if (bad) {
+          if (!finite(m[0][i])) cm[i] = 0x7F;  // NaN
+          if (!finite(v[0][i])) cv[i] = 0x7F;
+        }
       }
-      if (left) {
+      if (left > 0) {
         store_codes(static_cast<uint8_t*>(t.m) + at, left, cm);
         store_codes(static_cast<uint8_t*>(t.v) + at, left, cv);
         if (threadIdx.x % 32 == 0) {
-          t.m_scale[block] = mm / 448.f;
-          t.v_scale[block] = vm / 448.f;
+          t.m_scale[at / 256] = mm / 448.f;
+          t.v_scale[at / 256] = vm / 448.f;
         }
       }
     }
@@ -251,7 +276,8 @@ hipError_t adamw(const laplex_adamw_args& o, const laplex_adamw_tensor* t, uint3
   a.one_b2 = (float)(1.0 - o.beta2);
   a.eps = (float)o.eps;
   a.rate = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
-  a.root_c2 = (float)std::sqrt(1.0 - std::pow(o.beta2, (double)o.step));
+  a.inv_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
+  a.divide = o.eps < 1e-30;
   a.seed = o.seed;
   a.stochastic = o.stochastic;
   a.step = o.step;
@@ -278,24 +304,30 @@ hipError_t adamw(const laplex_adamw_args& o, const laplex_adamw_tensor* t, uint3
 // ------------------------------------------------------------------ 8-bit moments as floats
 // (p and master hold the outputs)
 __global__ __launch_bounds__(kAdamBlock) void k_adamw_moments(AdamArgs a) {
+  constexpr int N = 4;
   uint32_t k = 0;
   for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     while (k + 1 < a.count && a.t[k + 1].chunk0 <= chunk) ++k;
     const AdamTensor& t = a.t[k];
-    const uint64_t at = (uint64_t)(chunk - t.chunk0) * kAdamChunk + threadIdx.x * kAdamPer;
-    if (at >= t.n) continue;
-    const uint64_t left = t.n - at;
-    float v[kAdamPer];
-    if (t.p) {
-      load_codes(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[at / 256], v);
-      store8(static_cast<float*>(t.p) + at, left, v);
-    }
-    if (t.master) {
-      load_codes(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[at / 256], v);
+    const uint64_t at0 = (uint64_t)(chunk - t.chunk0) * kAdamChunk + threadIdx.x * N;
+    const auto move = [&](const void* codes, const float* scales, float* out, bool square) {
+      float v[2][N];
 #pragma unroll
-      for (int i = 0; i < kAdamPer; ++i) v[i] *= v[i];
-      store8(t.master + at, left, v);
-    }
+      for (int q = 0; q < 2; ++q) {
+        const uint64_t at = at0 + q * kAdamBlock * N;
+        if (at < t.n) load_codes(static_cast<const uint8_t*>(codes) + at, (int64_t)(t.n - at), scales[at / 256], v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint64_t at = at0 + q * kAdamBlock * N;
+        if (square)
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[q][i] *= v[q][i];
+        if (at < t.n) store_some(out + at, (int64_t)(t.n - at), v[q]);
+      }
+    };
+    if (t.p) move(t.m, t.m_scale, static_cast<float*>(t.p), false);
+    if (t.master) move(t.v, t.v_scale, t.master, true);
   }
 }
 
