@@ -15,7 +15,9 @@
 // to nearest, a second moment that changes by a thousandth a step would never
 // leave its code.  sqrt(v) > 0 never becomes 0, or a step would be divided by eps.
 // The new parameters are made from the moments before they are rounded.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "laplex_layers_device.hpp"
 #include "laplex_train.hpp"
@@ -24,6 +26,10 @@ namespace laplex {
 
 constexpr int kAdamBlock = 256, kAdamChunk = 2048;
 constexpr int kAdamGroup = 40;  // tensors of a launch: its arguments stay below 4 KB
+// Tensors of more bytes than the Infinity Cache keeps from one step to the next are moved past the caches (float moments
+// and parameters, 268 MB: 81 us, through them 73; 335 MB: 101, 128; 4.3 GB: 1307, 1605).
+constexpr uint64_t kAdamCached = 288ull << 20;
+constexpr uint64_t kAdamBlocks = (1u << 24) - 1;  // (a launch has fewer than 2^32 threads)
 
 struct AdamTensor {
   void* p;
@@ -57,12 +63,38 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// 4, 8 or 16 bytes at the alignment of T; NT: past the caches
+template <typename T, int BYTES>
+using Words = uint32_t __attribute__((ext_vector_type(BYTES / 4), aligned(sizeof(T))));
+template <bool NT, int BYTES, typename T>
+__device__ __forceinline__ void load_bytes(const T* p, void* to) {
+  constexpr int W = BYTES < 16 ? BYTES : 16;
+  using V = Words<T, W>;
+#pragma unroll
+  for (int i = 0; i < BYTES / W; ++i) {
+    const V* q = reinterpret_cast<const V*>(reinterpret_cast<const char*>(p) + i * W);
+    const V v = NT ? __builtin_nontemporal_load(q) : *q;
+    __builtin_memcpy(static_cast<char*>(to) + i * W, &v, W);
+  }
+}
+template <bool NT, int BYTES, typename T>
+__device__ __forceinline__ void store_bytes(T* p, const void* from) {
+  constexpr int W = BYTES < 16 ? BYTES : 16;
+  using V = Words<T, W>;
+#pragma unroll
+  for (int i = 0; i < BYTES / W; ++i) {
+    V v, *q = reinterpret_cast<V*>(reinterpret_cast<char*>(p) + i * W);
+    __builtin_memcpy(&v, static_cast<const char*>(from) + i * W, W);
+    if (NT) __builtin_nontemporal_store(v, q);
+    else *q = v;
+  }
+}
 // N consecutive elements, of which `left` are the tensor's
-template <int N, typename T>
+template <bool NT, int N, typename T>
 __device__ __forceinline__ void load_some(const T* p, int64_t left, float (&v)[N]) {
   T e[N];
   if (left >= N) {
-    __builtin_memcpy(e, p, sizeof e);
+    load_bytes<NT, sizeof e>(p, e);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) e[i] = i < left ? p[i] : T(0.f);
@@ -70,13 +102,13 @@ __device__ __forceinline__ void load_some(const T* p, int64_t left, float (&v)[N
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = to_f32(e[i]);
 }
-template <int N, typename T>
+template <bool NT, int N, typename T>
 __device__ __forceinline__ void store_some(T* p, int64_t left, const float (&v)[N]) {
   T e[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) e[i] = from_f32<T>(v[i]);
   if (left >= N) {
-    __builtin_memcpy(p, e, sizeof e);
+    store_bytes<NT, sizeof e>(p, e);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -85,11 +117,11 @@ __device__ __forceinline__ void store_some(T* p, int64_t left, const float (&v)[
 }
 
 // ------------------------------------------------------------------ e4m3 codes
-template <int N>
+template <bool NT, int N>
 __device__ __forceinline__ void load_codes(const uint8_t* p, int64_t left, float scale, float (&v)[N]) {
   uint32_t w[N / 4] = {};
   if (left >= N) {
-    __builtin_memcpy(w, p, N);
+    load_bytes<NT, N>(p, w);
   } else {
     for (int i = 0; i < (int)left; ++i) w[i / 4] |= (uint32_t)p[i] << i % 4 * 8;
   }
@@ -102,10 +134,11 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int64_t left, float
     v[4 * i + 3] = b[1] * scale;
   }
 }
+template <bool NT>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t left, const uint32_t (&c)[8]) {
   if (left >= 8) {
     const uint32_t w[2] = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
-    __builtin_memcpy(p, w, 8);
+    store_bytes<NT, 8>(p, w);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -133,7 +166,7 @@ __device__ __forceinline__ uint32_t code_of(float x, float inverse, uint32_t r) 
 }
 
 // ------------------------------------------------------------------ the step
-template <typename P, typename G, int BITS>
+template <typename P, typename G, int BITS, bool NT>
 __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
   __shared__ float sh[2];
   constexpr int N = BITS == 8 ? 8 : 4, PIECES = 8 / N;
@@ -165,15 +198,15 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
       const uint64_t at = at0 + q * (kAdamBlock * N);
       const int64_t left = (int64_t)t.n - (int64_t)at;
       if (left <= 0) continue;
-      if (t.master) load_some(t.master + at, left, p[q]);
-      else load_some(static_cast<const P*>(t.p) + at, left, p[q]);
-      load_some(static_cast<const G*>(t.g) + at, left, g[q]);
+      if (t.master) load_some<NT>(t.master + at, left, p[q]);
+      else load_some<NT>(static_cast<const P*>(t.p) + at, left, p[q]);
+      load_some<NT>(static_cast<const G*>(t.g) + at, left, g[q]);
       if constexpr (BITS == 32) {
-        load_some(static_cast<const float*>(t.m) + at, left, m[q]);
-        load_some(static_cast<const float*>(t.v) + at, left, v[q]);
+        load_some<NT>(static_cast<const float*>(t.m) + at, left, m[q]);
+        load_some<NT>(static_cast<const float*>(t.v) + at, left, v[q]);
       } else {
-        load_codes(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[at / 256], m[q]);
-        load_codes(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[at / 256], v[q]);
+        load_codes<NT>(static_cast<const uint8_t*>(t.m) + at, left, t.m_scale[at / 256], m[q]);
+        load_codes<NT>(static_cast<const uint8_t*>(t.v) + at, left, t.v_scale[at / 256], v[q]);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[q][i] *= v[q][i];
       }
@@ -193,11 +226,11 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
         if constexpr (BITS == 8) v[q][i] = root;
       }
       if (left > 0) {
-        store_some(static_cast<P*>(t.p) + at, left, p[q]);
-        if (t.master) store_some(t.master + at, left, p[q]);
+        store_some<NT>(static_cast<P*>(t.p) + at, left, p[q]);
+        if (t.master) store_some<NT>(t.master + at, left, p[q]);
         if constexpr (BITS == 32) {
-          store_some(static_cast<float*>(t.m) + at, left, m[q]);
-          store_some(static_cast<float*>(t.v) + at, left, v[q]);
+          store_some<NT>(static_cast<float*>(t.m) + at, left, m[q]);
+          store_some<NT>(static_cast<float*>(t.v) + at, left, v[q]);
         }
       }
     }
@@ -234,8 +267,8 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
         }
       }
       if (left > 0) {
-        store_codes(static_cast<uint8_t*>(t.m) + at, left, cm);
-        store_codes(static_cast<uint8_t*>(t.v) + at, left, cv);
+        store_codes<NT>(static_cast<uint8_t*>(t.m) + at, left, cm);
+        store_codes<NT>(static_cast<uint8_t*>(t.v) + at, left, cv);
         if (threadIdx.x % 32 == 0) {
           t.m_scale[at / 256] = mm / 448.f;
           t.v_scale[at / 256] = vm / 448.f;
@@ -245,9 +278,9 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
   }
 }
 
-// Launches `run` for groups of tensors; each holds chunks of its own.
+// Launches `run` for groups of tensors, in at most so many blocks; each holds chunks of its own.
 template <typename F>
-static hipError_t by_groups(AdamArgs& a, const laplex_adamw_tensor* t, uint32_t count, double lr, F run) {
+static hipError_t by_groups(AdamArgs& a, const laplex_adamw_tensor* t, uint32_t count, double lr, uint64_t most, F run) {
   for (uint32_t i = 0; i < count;) {
     a.count = 0;
     uint64_t chunks = 0;
@@ -261,7 +294,7 @@ static hipError_t by_groups(AdamArgs& a, const laplex_adamw_tensor* t, uint32_t 
     }
     if (a.count == 0) continue;
     a.chunks = (uint32_t)chunks;
-    run((unsigned)std::min<uint64_t>(chunks, 4096));
+    run((unsigned)std::min<uint64_t>(chunks, most));
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -288,21 +321,27 @@ hipError_t adamw(const laplex_adamw_args& o, const laplex_adamw_tensor* t, uint3
   a.lr_dev = o.lr_dev;
   a.grad_scale = o.grad_scale;
   const bool pb = o.dtype == LAPLEX_BF16, gb = o.grad_dtype == LAPLEX_BF16;
-  return by_groups(a, t, count, o.lr, [&](unsigned blocks) {
-    LAPLEX_LAUNCH("k_adamw", a.chunks, s, {
-      if (o.state_bits == 32) {
-        if (pb) gb ? k_adamw<bf16, bf16, 32><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<bf16, float, 32><<<blocks, kAdamBlock, 0, s>>>(a);
-        else gb ? k_adamw<float, bf16, 32><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<float, float, 32><<<blocks, kAdamBlock, 0, s>>>(a);
-      } else {
-        if (pb) gb ? k_adamw<bf16, bf16, 8><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<bf16, float, 8><<<blocks, kAdamBlock, 0, s>>>(a);
-        else gb ? k_adamw<float, bf16, 8><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw<float, float, 8><<<blocks, kAdamBlock, 0, s>>>(a);
-      }
-    });
+  uint64_t bytes = 0;
+  for (uint32_t i = 0; i < count; ++i) bytes += t[i].n * ((pb ? 2 : 4) + (gb ? 2 : 4) + o.state_bits / 4 + (t[i].master ? 4 : 0));
+  // (a block takes one chunk; with the step or rate on the device, several, for each block forms the powers of beta)
+  return by_groups(a, t, count, o.lr, o.step_dev || o.lr_dev ? 8192 : kAdamBlocks, [&](unsigned blocks) {
+    const auto bits = [&](auto p, auto g, auto nt) {
+      using P = decltype(p);
+      using G = decltype(g);
+      if (o.state_bits == 32) k_adamw<P, G, 32, decltype(nt)::value><<<blocks, kAdamBlock, 0, s>>>(a);
+      else k_adamw<P, G, 8, decltype(nt)::value><<<blocks, kAdamBlock, 0, s>>>(a);
+    };
+    const auto types = [&](auto nt) {
+      if (pb) gb ? bits(bf16{}, bf16{}, nt) : bits(bf16{}, float{}, nt);
+      else gb ? bits(float{}, bf16{}, nt) : bits(float{}, float{}, nt);
+    };
+    LAPLEX_LAUNCH("k_adamw", a.chunks, s, bytes > kAdamCached ? types(std::true_type{}) : types(std::false_type{}));
   });
 }
 
 // ------------------------------------------------------------------ 8-bit moments as floats
 // (p and master hold the outputs)
+template <bool NT>
 __global__ __launch_bounds__(kAdamBlock) void k_adamw_moments(AdamArgs a) {
   constexpr int N = 4;
   uint32_t k = 0;
@@ -315,7 +354,7 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw_moments(AdamArgs a) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const uint64_t at = at0 + q * kAdamBlock * N;
-        if (at < t.n) load_codes(static_cast<const uint8_t*>(codes) + at, (int64_t)(t.n - at), scales[at / 256], v[q]);
+        if (at < t.n) load_codes<NT>(static_cast<const uint8_t*>(codes) + at, (int64_t)(t.n - at), scales[at / 256], v[q]);
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -323,7 +362,7 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw_moments(AdamArgs a) {
         if (square)
 #pragma unroll
           for (int i = 0; i < N; ++i) v[q][i] *= v[q][i];
-        if (at < t.n) store_some(out + at, (int64_t)(t.n - at), v[q]);
+        if (at < t.n) store_some<NT>(out + at, (int64_t)(t.n - at), v[q]);
       }
     };
     if (t.p) move(t.m, t.m_scale, static_cast<float*>(t.p), false);
@@ -333,8 +372,11 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw_moments(AdamArgs a) {
 
 hipError_t adamw_moments(const laplex_adamw_tensor* t, uint32_t count, hipStream_t s) {
   AdamArgs a{};
-  return by_groups(a, t, count, 0.0, [&](unsigned blocks) {
-    LAPLEX_LAUNCH("k_adamw_moments", a.chunks, s, k_adamw_moments<<<blocks, kAdamBlock, 0, s>>>(a));
+  uint64_t bytes = 0;
+  for (uint32_t i = 0; i < count; ++i) bytes += t[i].n * 10;
+  return by_groups(a, t, count, 0.0, kAdamBlocks, [&](unsigned blocks) {
+    LAPLEX_LAUNCH("k_adamw_moments", a.chunks, s,
+                  bytes > kAdamCached ? k_adamw_moments<true><<<blocks, kAdamBlock, 0, s>>>(a) : k_adamw_moments<false><<<blocks, kAdamBlock, 0, s>>>(a));
   });
 }
 
