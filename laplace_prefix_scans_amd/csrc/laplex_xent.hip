@@ -453,9 +453,8 @@ static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + 
 
 // Sizes that a call with this many tokens keeps in its workspace; each grows with the tokens.
 struct XentPlan {
-  uint64_t k_width, k_tokens, k_piece;  // extents of k, whole pieces
-  uint32_t piece;                       // vocabulary entries at a time
-  uint32_t splits;                      // of dx's product over them
+  uint64_t k_width, k_tokens;  // extents of k, whole pieces
+  uint32_t piece;              // vocabulary entries at a time
 };
 static XentPlan xent_plan(int dtype, uint64_t tokens, uint32_t vocab, uint32_t width) {
   const uint64_t e = dtype == LAPLEX_BF16 ? 2 : 4, bk = kPieceK / e;
@@ -464,18 +463,51 @@ static XentPlan xent_plan(int dtype, uint64_t tokens, uint32_t vocab, uint32_t w
   p.k_tokens = up(tokens, bk);
   const uint64_t fit = kPiece / (e * std::max<uint64_t>(p.k_tokens, 1)) / kTile * kTile;
   p.piece = (uint32_t)std::min<uint64_t>(up(vocab, bk), std::max<uint64_t>(kTile, fit));
-  p.k_piece = up(p.piece, bk);
-  // Where dx has fewer tiles than the chip has CUs, its sums over the vocabulary are split.
-  const uint64_t t = (uint64_t)tiles(std::max<uint64_t>(tokens, 1)) * tiles(width);
-  p.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(512 / t, p.k_piece / bk));
   return p;
 }
+
+// ------------------------------------------------------------------ tiles and splits of a product
+// By a model of its time: rounds of blocks over the CUs, each at the rate that its tile reaches, and for a split product the
+// pass that adds the parts.  Rates, in 10^6 operations a us and CU, are those of large products (bfloat16 16384 x 65536 x 2048:
+// 1330, 780 and 400 TFLOP/s by 256, 128 and 64 wide tiles; float 145, 140, 120).
+struct Tiling {
+  int tile;         // TILE_L .. TILE_T
+  uint32_t splits;  // of k
+};
+enum { TILE_L, TILE_M, TILE_S, TILE_T };
+constexpr uint32_t kTileM[] = {TileL::BM, TileM::BM, TileS::BM, TileT::BM}, kTileN[] = {TileL::BN, TileM::BN, TileS::BN, TileT::BN};
+static double rate_of(bool bf, int tile) {
+  const double b[] = {5.2, 3.0, 1.6, 1.2}, f[] = {.57, .55, .47, .40};
+  return bf ? b[tile] : f[tile];
+}
+// partial sums of a split product, in floats
+constexpr uint64_t kPartFloats = 8ull << 20;
+static Tiling tiling(bool bf, uint64_t M, uint64_t N, uint64_t K, bool may_split) {
+  const uint64_t bk = kPieceK / (bf ? 2 : 4), steps = std::max<uint64_t>(1, K / bk);
+  Tiling best{TILE_S, 1};
+  double least = 1e300;
+  for (int t = TILE_L; t <= TILE_T; ++t) {
+    const uint64_t blocks = tiles(M, kTileM[t]) * (uint64_t)tiles(N, kTileN[t]);
+    for (uint64_t s = 1; s <= 64; s *= 2) {
+      if (s > 1 && (!may_split || s * 4 > steps || s * M * N > kPartFloats)) break;
+      const double work = 2e-6 * kTileM[t] * kTileN[t] * (double)((steps + s - 1) / s * bk);
+      const double us = (double)((blocks * s + 255) / 256) * work / rate_of(bf, t) + (s > 1 ? 4.0 + s * M * N * 8e-6 / 4.0 : 0.0) + 2.0;
+      if (us < least) {
+        least = us;
+        best = {t, (uint32_t)s};
+      }
+    }
+  }
+  return best;
+}
+
 struct XentWorkspace {
   void *x_rows, *table_rows;  // filled up copies, where rows are not whole pieces
   float2* stats;
   float* hit;
   void* G;
-  float* dx;
+  float* dx;    // dx while pieces of the vocabulary are added to it
+  float* part;  // parts of a split product
 };
 static bool whole_rows(const void* p, uint64_t width, uint64_t e) { return width * e % kPieceK == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width, size_t* total) {
@@ -486,13 +518,14 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
   w.x_rows = c.take<void>(p.k_tokens * p.k_width * e);
   w.table_rows = c.take<void>(vocab * p.k_width * e);
   if (pass == 0) {
-    w.stats = c.take<float2>((uint64_t)tiles(vocab, TileS::BM) * tokens * 8);
+    w.stats = c.take<float2>((uint64_t)tiles(vocab, TileS::BM) * tokens * 8);  // (of the smallest tiles)
     w.hit = c.take<float>(tokens * 4);
   } else {
     // (a piece has at most kPiece bytes, or one tile of the vocabulary, or all of it)
     const uint64_t bk = kPieceK / e, g = std::max<uint64_t>(std::min<uint64_t>(kPiece, up(vocab, bk) * p.k_tokens * e), kTile * p.k_tokens * e);
     w.G = c.take<void>(g);
-    w.dx = c.take<float>((std::min<uint64_t>(tokens * 513, tokens + 512 * kTile)) * width * 4);
+    w.dx = c.take<float>(tokens * width * 4);
+    w.part = c.take<float>(kPartFloats * 4);
   }
   *total = (c.off + 255) & ~size_t(255);
   return w;
@@ -518,15 +551,16 @@ static hipError_t product_of(const char* name, Product epi, ProductArgs& a, hipS
   return hipGetLastError();
 }
 template <typename T>
-static hipError_t product(const char* name, Product epi, ProductArgs& a, uint32_t splits, hipStream_t s) {
+static hipError_t product(const char* name, Product epi, ProductArgs& a, const Tiling& t, hipStream_t s) {
   constexpr uint64_t bk = kPieceK / sizeof(T);
-  a.k_split = std::max(bk, up((a.K + splits - 1) / splits, bk));
+  a.k_split = std::max(bk, up((a.K + t.splits - 1) / t.splits, bk));
   a.splits = (uint32_t)std::max<uint64_t>(1, (a.K + a.k_split - 1) / a.k_split);
-  const uint64_t l = (uint64_t)tiles(a.M, 256) * tiles(a.N, 256) * a.splits, m = (uint64_t)tiles(a.M, 128) * tiles(a.N, 128) * a.splits;
-  if (a.N <= 32) return product_of<T, TileT>(name, epi, a, s);
-  if (l >= 200) return product_of<T, TileL>(name, epi, a, s);
-  if (m >= 200) return product_of<T, TileM>(name, epi, a, s);
-  return product_of<T, TileS>(name, epi, a, s);
+  switch (t.tile) {
+    case TILE_L: return product_of<T, TileL>(name, epi, a, s);
+    case TILE_M: return product_of<T, TileM>(name, epi, a, s);
+    case TILE_S: return product_of<T, TileS>(name, epi, a, s);
+    default: return product_of<T, TileT>(name, epi, a, s);
+  }
 }
 static unsigned some_blocks(uint64_t n) { return (unsigned)std::min<uint64_t>((n + 255) / 256, 16384); }
 
@@ -564,7 +598,7 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   a.scale = x.scale;
   a.stats = w.stats;
   a.hit = w.hit;
-  if ((err = product<T>("k_product_stats", LOGITS_STATS, a, 1, s)) != hipSuccess) return err;
+  if ((err = product<T>("k_product_stats", LOGITS_STATS, a, tiling(sizeof(T) == 2, a.M, a.N, a.K, false), s)) != hipSuccess) return err;
   LAPLEX_LAUNCH("k_xent_join", x.tokens, s,
                 k_xent_join<<<(unsigned)((x.tokens + 15) / 16), 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse));
   return hipGetLastError();
@@ -598,8 +632,25 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   l.dlse = dlse;
   l.G = w.G;
   l.n_fill = (uint32_t)p.k_tokens;
-  const bool once = p.splits == 1 && p.piece >= x.vocab;  // dx is one product
-  uint32_t used = 1;
+  // A product that may be split: to its place, or its parts and then their sum
+  const auto output = [&](const char* name, Product epi, ProductArgs& a) {
+    const Tiling t = tiling(sizeof(T) == 2, a.M, a.N, a.K, !a.add);
+    if (t.splits == 1) return product<T>(name, epi, a, t, s);
+    void* const out = a.out;
+    const bool f32 = a.out_f32;
+    a.out = w.part;
+    a.out_f32 = true;
+    a.out_split = (int64_t)a.N * a.ldo;
+    const hipError_t e = product<T>(name, epi, a, t, s);
+    if (e != hipSuccess) return e;
+    const uint64_t n = (uint64_t)a.out_split;
+    LAPLEX_LAUNCH("k_xent_sum", n, s, {
+      if (f32) k_xent_sum<float><<<some_blocks(n), 256, 0, s>>>(w.part, a.splits, n, static_cast<float*>(out));
+      else k_xent_sum<T><<<some_blocks(n), 256, 0, s>>>(w.part, a.splits, n, static_cast<T*>(out));
+    });
+    return hipGetLastError();
+  };
+  const bool once = p.piece >= x.vocab;  // dx is one product
   for (uint32_t v0 = 0; v0 < x.vocab; v0 += p.piece) {
     const uint32_t n = std::min(p.piece, x.vocab - v0);
     const uint64_t fill = up(n, kPieceK / sizeof(T));
@@ -608,7 +659,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
     l.v0 = v0;
     l.ldg = (int64_t)fill;
     l.m_fill = (uint32_t)fill;
-    if (tokens && (err = product<T>("k_product_grad", LOGITS_GRAD, l, 1, s)) != hipSuccess) return err;
+    if (tokens && (err = product<T>("k_product_grad", LOGITS_GRAD, l, tiling(sizeof(T) == 2, l.M, l.n_fill, l.K, false), s)) != hipSuccess) return err;
     if (dx) {
       ProductArgs a{};
       a.A = l.A;
@@ -626,10 +677,8 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
       a.ldo = x.width;
       a.out = once ? dx : w.dx;
       a.out_f32 = !once || sizeof(T) == 4;
-      a.out_split = (int64_t)x.tokens * x.width;
       a.add = v0 > 0;
-      if ((err = product<T>("k_product_dx", DX, a, p.splits, s)) != hipSuccess) return err;
-      used = std::max(used, a.splits);
+      if ((err = output("k_product_dx", DX, a)) != hipSuccess) return err;
     }
     if (dtable) {
       ProductArgs a{};
@@ -643,12 +692,12 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
       a.ldo = x.width;
       a.out_f32 = table_dtype == LAPLEX_F32;
       a.out = static_cast<char*>(dtable) + (uint64_t)v0 * x.width * (a.out_f32 ? 4 : 2);
-      if ((err = product<T>("k_product_dtable", DTABLE, a, 1, s)) != hipSuccess) return err;
+      if ((err = output("k_product_dtable", DTABLE, a)) != hipSuccess) return err;
     }
   }
   if (dx && !once) {
     const uint64_t n = x.tokens * x.width;
-    LAPLEX_LAUNCH("k_xent_sum", n, s, k_xent_sum<T><<<some_blocks(n), 256, 0, s>>>(w.dx, used, n, static_cast<T*>(dx)));
+    LAPLEX_LAUNCH("k_xent_sum", n, s, k_xent_sum<T><<<some_blocks(n), 256, 0, s>>>(w.dx, 1, n, static_cast<T*>(dx)));
   }
   return hipGetLastError();
 }
