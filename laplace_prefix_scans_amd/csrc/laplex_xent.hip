@@ -9,6 +9,7 @@
 // that are not whole 128-byte pieces are filled up with zeros first, and the backward takes a copy of x in which the
 // tokens that take no part are zeros.
 #include <algorithm>
+#include <type_traits>
 
 #include "laplex_host.hpp"
 #include "laplex_layers_device.hpp"
@@ -79,13 +80,11 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // exp(l - m) with 1 where both are the same infinity
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.f : exp_of(l - m); }
 
-// Tile and split of this block.  Blocks are dispatched to the 8 XCDs in turn; each XCD takes a stretch of the tiles, in
-// groups of 8 tiles of M by all of N, of which the ones that run at once share rows of both factors in its L2.
-__device__ __forceinline__ void tile_of_block(const ProductArgs& a, uint32_t& tm, uint32_t& tn, uint32_t& split) {
+// Tile and split number `id`: groups of 8 tiles of M by all of N, of which the ones that run at once share rows of both
+// factors in an XCD's L2.
+__device__ __forceinline__ void tile_of(const ProductArgs& a, uint32_t id, uint32_t& tm, uint32_t& tn, uint32_t& split) {
   constexpr uint32_t GROUP = 8;
-  const uint32_t total = a.tiles_m * a.tiles_n, all = total * a.splits;
-  const uint32_t per = all / kXcds, rest = all % kXcds, x = blockIdx.x % kXcds, y = blockIdx.x / kXcds;
-  uint32_t id = x * per + min(x, rest) + y;  // (XCD x has per blocks, and one more where x < rest)
+  const uint32_t total = a.tiles_m * a.tiles_n;
   split = id / total;
   id %= total;
   const uint32_t group = id / (GROUP * a.tiles_n), first = group * GROUP, rows = min(GROUP, a.tiles_m - first);
@@ -95,29 +94,35 @@ __device__ __forceinline__ void tile_of_block(const ProductArgs& a, uint32_t& tm
 }
 
 // ------------------------------------------------------------------ the product
-// A block of WM x WN waves makes BM x BN of C.  128 bytes of k of its rows are on their way from memory straight to LDS
+// A block of WM x WN waves makes BM x BN of C, and then of other tiles, whose first bytes are on their way while it finishes
+// one.  128 bytes of k of its rows are on their way from memory straight to LDS
 // while those before are multiplied; a row's eight 16-byte pieces lie at piece ^ (row & 7), so that the reads of 16
 // rows' pieces spread over the banks.  A step's 128 bytes are two halves, and a half's operands are read one half ahead of
 // their products, across the step's one barrier: it stands in the middle of a step, where both halves of it have been read
 // and the next one's bytes have arrived.
-template <int M, int N, int WAVES_M, int WAVES_N>
+template <int M, int N, int WAVES_M, int WAVES_N, int BLOCKS>
 struct Tile {
+  static constexpr int PER_CU = BLOCKS;  // that fit a CU at once
   static constexpr int BM = M, BN = N, WM = WAVES_M, WN = WAVES_N, THREADS = WM * WN * kWave;
   static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   static constexpr int LOADS = (BM + BN) / 8 / (WM * WN);  // of a wave and step: 8 rows each
   static constexpr int STEP_BYTES = (BM + BN) * 128;
   static_assert((BM + BN) % (8 * WM * WN) == 0 && BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "whole operands");
 };
-using TileL = Tile<256, 256, 2, 4>;
-using TileM = Tile<128, 128, 2, 2>;
-using TileS = Tile<64, 64, 2, 2>;
-using TileT = Tile<128, 32, 4, 1>;
+using TileL = Tile<256, 256, 2, 4, 1>;
+using TileM = Tile<128, 128, 2, 2, 2>;
+using TileS = Tile<64, 64, 2, 2, 4>;
+using TileT = Tile<128, 32, 4, 1, 3>;
 
 // 16 bytes of each lane, from `off` bytes past a base that the wave shares, to 16 lane past an LDS address that it shares.
 // (Written out, for with the builtin the compiler waits for these loads before every transposing read of LDS.  They give
 // no register a value; what they bring is waited for by arrived().  Nothing else here uses m0.)
 __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory");
+}
+// 4 bytes of each lane, to 4 lane past the LDS address
+__device__ __forceinline__ void word_to_lds(uint64_t base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory");
 }
 // Two addresses that the wave shares, in scalar registers; the wait states that a load has to keep from the vector
 // instructions that write them are here, once for all the loads that follow.
@@ -143,6 +148,9 @@ __device__ __forceinline__ int thread_now() {
 }
 // Every wave's reads of LDS are done, and its bytes on their way to LDS are there.
 __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The same for LDS alone.
+__device__ __forceinline__ void written() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 constexpr int kPieceK = 128;
 
@@ -197,46 +205,61 @@ struct Factor {
   }
 };
 
+// What the logits' products need of each token of a tile, in LDS: words of the target, lse, dloss, dlse.
+enum { INFO_LOW, INFO_HIGH, INFO_LSE, INFO_DLOSS, INFO_DLSE, INFO_WORDS };
+
 // A_ALONG: A is [k][M]; B_ALONG: B is [k][N]
 template <typename T, int EPI, typename C, bool A_ALONG, bool B_ALONG>
 __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
   constexpr int BM = C::BM, BN = C::BN, MI = C::MI, NI = C::NI, W = C::WM * C::WN, BK = kPieceK / sizeof(T), E = 16 / sizeof(T);
+  constexpr int INFO = EPI == XENT_OUT ? 0 : EPI == XENT_STATS ? INFO_LSE : INFO_WORDS;
   using FA = Factor<T, BM, A_ALONG>;
   using FB = Factor<T, BN, B_ALONG>;
   __shared__ __attribute__((aligned(16))) char lds[2 * C::STEP_BYTES];
+  __shared__ uint32_t info[INFO ? INFO : 1][INFO ? (BN + 63) / 64 * 64 : 1];
+  __shared__ float2 part[EPI == XENT_STATS ? C::WM : 1][EPI == XENT_STATS ? BN : 1];
   using V = typename Frag<T>::V;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  uint32_t tm, tn, split;
-  tile_of_block(a, tm, tn, split);
-  const uint64_t k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
-  const int steps = (int)((k1 - k0) / BK);
+  // Blocks are dispatched to the 8 XCDs in turn; each XCD's blocks take a stretch of the tiles, one after the other.
+  const uint32_t all = a.tiles_m * a.tiles_n * a.splits, xcd = blockIdx.x % kXcds, rest = all % kXcds;
+  const uint32_t next_id = gridDim.x / kXcds + (xcd < gridDim.x % kXcds), end = (xcd + 1) * (all / kXcds) + min(xcd + 1, rest);
+  uint32_t id = xcd * (all / kXcds) + min(xcd, rest) + blockIdx.x / kXcds;
+
   // this lane's 16 bytes of each of the wave's stretches of 1024, from the tile's first element on; LOADS_A of them are A's
   constexpr int LOADS_A = BM / 8 / W;
   static_assert(BM % (8 * W) == 0, "a wave's stretches are A's and then B's");
   const int64_t row_a = a.lda * (int64_t)sizeof(T), row_b = a.ldb * (int64_t)sizeof(T);
-  const char* base_a = static_cast<const char*>(a.A) + (A_ALONG ? (int64_t)k0 * row_a + (int64_t)tm * BM * sizeof(T) : (int64_t)tm * BM * row_a + (int64_t)k0 * sizeof(T));
-  const char* base_b = static_cast<const char*>(a.B) + (B_ALONG ? (int64_t)k0 * row_b + (int64_t)tn * BN * sizeof(T) : (int64_t)tn * BN * row_b + (int64_t)k0 * sizeof(T));
-  uint32_t off[C::LOADS];
-#pragma unroll
-  for (int i = 0; i < C::LOADS; ++i) {
-    const int at = (i * W + wave) * 1024 + lane * 16;
-    int row, col;
-    if (i < LOADS_A) {
-      FA::source(at, row, col);
-      if (A_ALONG) col = min((int64_t)col, a.lda - E - (int64_t)tm * BM);
-      else row = min((uint32_t)row, a.M - 1 - tm * BM);
-      off[i] = (uint32_t)row * (uint32_t)row_a + (uint32_t)col * (uint32_t)sizeof(T);
-    } else {
-      FB::source(at - BM * kPieceK, row, col);
-      if (B_ALONG) col = min((int64_t)col, a.ldb - E - (int64_t)tn * BN);
-      else row = min((uint32_t)row, max(a.N, tn * BN + 1) - 1 - tn * BN);
-      off[i] = (uint32_t)row * (uint32_t)row_b + (uint32_t)col * (uint32_t)sizeof(T);
-    }
-  }
   const int64_t next_a = A_ALONG ? row_a * BK : kPieceK, next_b = B_ALONG ? row_b * BK : kPieceK;
   const uint32_t to0 = lds_address(lds) + wave * 1024;
+  uint32_t off[C::LOADS], tm, tn, split;
+  const char *base_a, *base_b;
+  uint64_t k0;
+  int steps, first = 0;  // `first`: the buffer of step 0
+  const auto choose = [&] {
+    tile_of(a, id, tm, tn, split);
+    k0 = split * a.k_split;
+    steps = (int)((min(a.K, k0 + a.k_split) - k0) / BK);
+    base_a = static_cast<const char*>(a.A) + (A_ALONG ? (int64_t)k0 * row_a + (int64_t)tm * BM * sizeof(T) : (int64_t)tm * BM * row_a + (int64_t)k0 * sizeof(T));
+    base_b = static_cast<const char*>(a.B) + (B_ALONG ? (int64_t)k0 * row_b + (int64_t)tn * BN * sizeof(T) : (int64_t)tn * BN * row_b + (int64_t)k0 * sizeof(T));
+#pragma unroll
+    for (int i = 0; i < C::LOADS; ++i) {
+      const int at = (i * W + wave) * 1024 + thread_now() % kWave * 16;
+      int row, col;
+      if (i < LOADS_A) {
+        FA::source(at, row, col);
+        if (A_ALONG) col = min((int64_t)col, a.lda - E - (int64_t)tm * BM);
+        else row = min((uint32_t)row, a.M - 1 - tm * BM);
+        off[i] = (uint32_t)row * (uint32_t)row_a + (uint32_t)col * (uint32_t)sizeof(T);
+      } else {
+        FB::source(at - BM * kPieceK, row, col);
+        if (B_ALONG) col = min((int64_t)col, a.ldb - E - (int64_t)tn * BN);
+        else row = min((uint32_t)row, max(a.N, tn * BN + 1) - 1 - tn * BN);
+        off[i] = (uint32_t)row * (uint32_t)row_b + (uint32_t)col * (uint32_t)sizeof(T);
+      }
+    }
+  };
   auto load = [&](int step) {
-    const uint32_t to = to0 + (step & 1) * C::STEP_BYTES;
+    const uint32_t to = to0 + ((first + step) & 1) * C::STEP_BYTES;
     uint64_t p, q;
     share(base_a + step * next_a, base_b + step * next_b, p, q);
     if (A_ALONG && k0 + (uint64_t)(step + 1) * BK > a.k_rows) {  // the last step has rows beyond the last: that one again
@@ -254,126 +277,218 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
 #pragma unroll
     for (int i = LOADS_A; i < C::LOADS; ++i) to_lds(q, off[i], to + i * W * 1024);
   };
-  f32x4 acc[MI][NI] = {};
+  // the tile's tokens' words, an array a wave
+  const auto load_info = [&] {
+#pragma unroll
+    for (int w = 0; w < INFO; ++w) {
+      if (wave != w % W || (w == INFO_HIGH && a.id_bytes == 4) || (w == INFO_DLSE && !a.dlse)) continue;
+      const char* p = w <= INFO_HIGH ? static_cast<const char*>(a.targets) + w * 4 : reinterpret_cast<const char*>(w == INFO_LSE ? a.lse : w == INFO_DLOSS ? a.dloss : a.dlse);
+      const uint32_t pitch = w <= INFO_HIGH ? a.id_bytes : 4, to = lds_address(reinterpret_cast<char*>(info[w]));
+      uint64_t base, none;
+      share(p, p, base, none);
+#pragma unroll
+      for (int i = 0; i < (BN + 63) / 64; ++i) word_to_lds(base, min(tn * BN + i * kWave + lane, a.N - 1) * pitch, to + i * 256);
+    }
+  };
   const int wm = wave % C::WM * (BM / C::WM), wn = wave / C::WM * (BN / C::WN);
-  if (steps > 0) {
-    V fa[2][MI], fb[2][NI];
-    const uint32_t at_a = FA::first(wm, lane), at_b = FB::first(wn, lane);
-    auto read = [&](int step, int half) {
-      const char* base = lds + (step & 1) * C::STEP_BYTES;
+  const uint32_t at_a = FA::first(wm, lane), at_b = FB::first(wn, lane);
+  if (id >= end) return;
+  choose();
+  if (steps > 0) load(0);
+  if (steps > 1) load(1);
+  for (;;) {
+    f32x4 acc[MI][NI] = {};
+    if (steps > 0) {
+      V fa[2][MI], fb[2][NI];
+      auto read = [&](int step, int half) {
+        const char* base = lds + ((first + step) & 1) * C::STEP_BYTES;
 #pragma unroll
-      for (int j = 0; j < NI; ++j) fb[half][j] = FB::read(base + BM * kPieceK, at_b, half, j);
+        for (int j = 0; j < NI; ++j) fb[half][j] = FB::read(base + BM * kPieceK, at_b, half, j);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[half][i] = FA::read(base, at_a, half, i);
-    };
-    auto multiply = [&](int half) {
+        for (int i = 0; i < MI; ++i) fa[half][i] = FA::read(base, at_a, half, i);
+      };
+      auto multiply = [&](int half) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mul(fa[half][i], fb[half][j], acc[i][j]);
-      // a read after every few products
-      constexpr int READS = MI * FA::READS + NI * FB::READS, PRODUCTS = MI * NI * (sizeof(T) == 4 ? 4 : 1);
+          for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mul(fa[half][i], fb[half][j], acc[i][j]);
+        // a read after every few products
+        constexpr int READS = MI * FA::READS + NI * FB::READS, PRODUCTS = MI * NI * (sizeof(T) == 4 ? 4 : 1);
 #pragma unroll
-      for (int r = 0; r < READS; ++r) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS / READS ? PRODUCTS / READS : 1, 0);
-      }
-    };
-    load(0);
-    arrived();
-    if (steps > 1) load(1);
-    read(0, 0);
-    for (int k = 0; k < steps; ++k) {
-      read(k, 1);
-      multiply(0);
+        for (int r = 0; r < READS; ++r) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS / READS ? PRODUCTS / READS : 1, 0);
+        }
+      };
       arrived();
-      if (k + 2 < steps) load(k + 2);
-      read(k + 1, 0);  // (after the last step: bytes that nothing uses)
-      multiply(1);
-    }
-    __syncthreads();
-  }
-  // a lane holds column n = lane % 16 and rows m = lane / 16 * 4 .. + 3 of each 16 x 16 tile
-  const uint32_t m0 = tm * BM + wm + lane / 16 * 4, n0 = tn * BN + wn + lane % 16;
-  if constexpr (EPI == XENT_STATS) {
-    float2* sh = reinterpret_cast<float2*>(lds);  // [wave of M][BN]
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const uint32_t t = n0 + j * 16;
-      const int64_t y = t < a.N ? target_of(a.targets, a.id_bytes, t) : -1;
-      float most = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t v = m0 + i * 16 + r;
-          const float l = a.scale * acc[i][j][r];
-          acc[i][j][r] = v < a.M ? l : -INFINITY;
-          if ((int64_t)v + a.v0 == y && v < a.M) a.hit[t] = l;
-          most = fmaxf(most, acc[i][j][r]);
-        }
-      most = fmaxf(most, __shfl_xor(most, 16));
-      most = fmaxf(most, __shfl_xor(most, 32));
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum += exp_below(acc[i][j][r], most);
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (lane < 16) sh[(wave % C::WM) * BN + wn + j * 16 + lane] = make_float2(most, sum);
-    }
-    __syncthreads();
-    if (threadIdx.x < BN && tn * BN + threadIdx.x < a.N) {
-      float m = sh[threadIdx.x].x, sum = 0.f;
-#pragma unroll
-      for (int w = 1; w < C::WM; ++w) m = fmaxf(m, sh[w * BN + threadIdx.x].x);
-#pragma unroll
-      for (int w = 0; w < C::WM; ++w) sum += sh[w * BN + threadIdx.x].y * exp_below(sh[w * BN + threadIdx.x].x, m);
-      a.stats[(uint64_t)tm * a.N + tn * BN + threadIdx.x] = make_float2(m, sum);
-    }
-  } else if constexpr (EPI == XENT_GRAD) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const uint32_t t = n0 + j * 16;
-      const int64_t y = t < a.N ? target_of(a.targets, a.id_bytes, t) : -1;
-      const bool in = y >= 0 && y < (int64_t)a.vocab;
-      const float lse = in ? a.lse[t] : 0.f, d = in ? a.scale * a.dloss[t] : 0.f, f = in ? d + (a.dlse ? a.scale * a.dlse[t] : 0.f) : 0.f;
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        T g[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t v = m0 + i * 16 + r;
-          float x = f * exp_of(a.scale * acc[i][j][r] - lse);
-          if ((int64_t)v + a.v0 == y) x -= d;
-          g[r] = from_f32<T>(in && v < a.M ? x : 0.f);
-        }
-        const uint32_t v = m0 + i * 16;
-        if (t < a.n_fill && v < a.m_fill) __builtin_memcpy(static_cast<T*>(a.G) + (int64_t)t * a.ldg + v, g, sizeof g);
+      if (INFO) load_info();  // (every wave is past the tile before; it is there after the next arrived())
+      read(0, 0);
+      for (int k = 0; k < steps; ++k) {
+        read(k, 1);
+        multiply(0);
+        arrived();
+        if (k + 2 < steps) load(k + 2);
+        read(k + 1, 0);  // (after the last step: bytes that nothing uses)
+        multiply(1);
       }
     }
-  } else {
+    // the next tile's first bytes: every wave has read all it will of this one's
+    const uint32_t m_tile = tm * BM, n_tile = tn * BN, this_split = split;
+    id += next_id;
+    const bool more = id < end;
+    if (more) {
+      first = (first + steps) & 1;
+      choose();
+      if (steps > 0) load(0);
+      if (steps > 1) load(1);
+    }
+    // a lane holds column n = lane % 16 and rows m = lane / 16 * 4 .. + 3 of each 16 x 16 tile
+    const uint32_t m0 = m_tile + wm + lane / 16 * 4, n0 = n_tile + wn + lane % 16;
+    const bool whole = m_tile + BM <= a.M;
+    if constexpr (EPI != XENT_OUT) {
+      // which of the wave's rows is the token's target, in this lane: the element's number, or -1
+      const auto target = [&](int j, bool& in) {
+        const int c = wn + j * 16 + lane % 16;
+        const int64_t y = a.id_bytes == 4 ? (int64_t)(int32_t)info[INFO_LOW][c] : (int64_t)((uint64_t)info[INFO_HIGH][c] << 32 | info[INFO_LOW][c]);
+        in = n_tile + c < a.N && y >= 0 && y < (int64_t)a.vocab;
+        const int64_t at = y - a.v0 - (m_tile + wm);
+        return in && at >= 0 && at < BM / C::WM && (at >> 2 & 3) == lane / 16 ? (int)((at >> 4) * 4 + (at & 3)) : -1;
+      };
+      if constexpr (EPI == XENT_STATS) {
+        // Maxima and sums of exp(l - max), l = scale acc: an element takes a maximum, a product and sum, an exponential of
+        // base 2 and a sum.
+        float scale = a.scale;
+        const auto all_of = [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const uint32_t n = n0 + j * 16;
-      if (n >= a.N) continue;
-      const bool zero = a.live_rows && !live(a, n);
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+            for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t m = m0 + i * 16 + r;
-          if (m >= a.M) continue;
-          float x = zero ? 0.f : acc[i][j][r];
+              for (int r = 0; r < 4; ++r) acc[i][j][r] = f(acc[i][j][r], m0 + i * 16 + r);
+        };
+        if (scale < 0.f) {
+          scale = -scale;
+          all_of([](float x, uint32_t) { return -x; });
+        }
+        if (scale == 0.f) {
+          scale = 1.f;
+          all_of([](float x, uint32_t) { return 0.f * x; });
+        }
+        if (!whole) all_of([&](float x, uint32_t v) { return v < a.M ? x : -INFINITY; });
+        const float s2 = scale * kLog2e;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          bool in;
+          const int hit = target(j, in);
+          if (__any(hit >= 0)) {
+            float l = 0.f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) l = hit == i * 4 + r ? acc[i][j][r] : l;
+            if (hit >= 0) a.hit[n0 + j * 16] = scale * l;
+          }
+          float most = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) most = fmaxf(most, acc[i][j][r]);
+          most = fmaxf(most, __shfl_xor(most, 16));
+          most = fmaxf(most, __shfl_xor(most, 32));
+          const float m2 = most * s2;
+          const bool odd = !(fabsf(m2) < 0x1p18f);  // (m2's rounding is that of the maximum in the result, but for this in the exponents)
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], s2, -m2));
+          if (__any(odd)) {
+            float again = 0.f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) again += exp_below(acc[i][j][r] * scale, most * scale);
+            sum = odd ? again : sum;
+          }
+          sum += __shfl_xor(sum, 16);
+          sum += __shfl_xor(sum, 32);
+          if (lane < 16) part[wave % C::WM][wn + j * 16 + lane] = make_float2(most * scale, sum);
+        }
+        written();
+        if (threadIdx.x < BN && n_tile + threadIdx.x < a.N) {
+          float m = part[0][threadIdx.x].x, sum = 0.f;
+#pragma unroll
+          for (int w = 1; w < C::WM; ++w) m = fmaxf(m, part[w][threadIdx.x].x);
+#pragma unroll
+          for (int w = 0; w < C::WM; ++w) sum += part[w][threadIdx.x].y * exp_below(part[w][threadIdx.x].x, m);
+          a.stats[(uint64_t)(m_tile / BM) * a.N + n_tile + threadIdx.x] = make_float2(m, sum);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          const int c = wn + j * 16 + lane % 16;
+          const uint32_t t = n0 + j * 16;
+          bool in;
+          const int hit = target(j, in);
+          const float lse = __uint_as_float(info[INFO_LSE][c]), d = a.scale * __uint_as_float(info[INFO_DLOSS][c]);
+          const float f = a.dlse ? d + a.scale * __uint_as_float(info[INFO_DLSE][c]) : d;
+          T* row = static_cast<T*>(a.G) + (int64_t)t * a.ldg;
+          const auto column = [&](auto plain) {  // without a target, inside the vocabulary
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              T g[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                float x = f * exp_of(fmaf(acc[i][j][r], a.scale, -lse));
+                if (!decltype(plain)::value) {
+                  if (hit == i * 4 + r) x -= d;
+                  if (m0 + i * 16 + r >= a.M) x = 0.f;
+                }
+                g[r] = from_f32<T>(in ? x : 0.f);
+              }
+              const uint32_t v = m0 + i * 16;
+              if (t < a.n_fill && (decltype(plain)::value || v < a.m_fill)) __builtin_memcpy(row + v, g, sizeof g);
+            }
+          };
+          if (whole && !__any(hit >= 0)) column(std::true_type{});
+          else column(std::false_type{});
+        }
+      }
+    } else {
+      typedef T Four __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+      typedef float Four32 __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const uint32_t n = n0 + j * 16;
+        if (n >= a.N) continue;
+        const bool zero = a.live_rows && !live(a, n);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const uint32_t m = m0 + i * 16;
           const uint64_t at = (uint64_t)n * a.ldo + m;
-          if (a.out_f32) {
-            float* o = static_cast<float*>(a.out) + split * a.out_split + at;
-            *o = a.add ? *o + x : x;
+          f32x4 x = zero ? f32x4{} : acc[i][j];
+          float* o = static_cast<float*>(a.out) + this_split * a.out_split + at;
+          if (m + 4 <= a.M) {
+            if (a.out_f32) {
+              if (a.add) x += *reinterpret_cast<const Four32*>(o);
+              *reinterpret_cast<Four32*>(o) = x;
+            } else {
+              Four y;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) y[r] = from_f32<T>(x[r]);
+              *reinterpret_cast<Four*>(static_cast<T*>(a.out) + at) = y;
+            }
           } else {
-            static_cast<T*>(a.out)[at] = from_f32<T>(x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (m + r < a.M) {
+                if (a.out_f32) o[r] = a.add ? o[r] + x[r] : x[r];
+                else static_cast<T*>(a.out)[at + r] = from_f32<T>(x[r]);
+              }
           }
         }
+      }
     }
+    if (!more) return;
   }
 }
 
@@ -541,8 +656,8 @@ template <typename T, typename C>
 static hipError_t product_of(const char* name, Product epi, ProductArgs& a, hipStream_t s) {
   a.tiles_m = tiles(a.M, C::BM);
   a.tiles_n = tiles(epi == LOGITS_GRAD ? std::max(a.N, a.n_fill) : a.N, C::BN);
-  const uint64_t blocks = (uint64_t)a.tiles_m * a.tiles_n * a.splits;
-  LAPLEX_LAUNCH(name, blocks, s, {
+  const uint64_t all = (uint64_t)a.tiles_m * a.tiles_n * a.splits, blocks = std::min<uint64_t>(all, 256 * C::PER_CU);
+  LAPLEX_LAUNCH(name, all, s, {
     if (epi == LOGITS_STATS) k_product<T, XENT_STATS, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
     else if (epi == LOGITS_GRAD) k_product<T, XENT_GRAD, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
     else if (epi == DX) k_product<T, XENT_OUT, C, true, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
