@@ -112,7 +112,7 @@ struct Tile {
 using TileL = Tile<256, 256, 2, 4, 1>;
 using TileM = Tile<128, 128, 2, 2, 2>;
 using TileS = Tile<64, 64, 2, 2, 4>;
-using TileT = Tile<128, 32, 4, 1, 3>;
+using TileT = Tile<64, 32, 2, 2, 6>;
 
 // 16 bytes of each lane, from `off` bytes past a base that the wave shares, to 16 lane past an LDS address that it shares.
 // (Written out, for with the builtin the compiler waits for these loads before every transposing read of LDS.  They give
@@ -492,6 +492,95 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ few tokens
+// The statistics where the table's bytes are all that counts: at most 8 tokens, whose rows lie in LDS.  A wave takes four
+// rows of the table at a time as they lie, 1024 bytes a load, and a block joins its waves' maxima and sums.  (1 token, 65536 x
+// 2048 in bfloat16: by the tiles of a product 76 us.)
+constexpr int kFewTokens = 8, kFewRows = 4;
+constexpr uint32_t kFewBytes = 128 << 10;  // of tokens in LDS
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_xent_few(ProductArgs a, uint32_t width, uint32_t fill) {
+  constexpr int E = 16 / sizeof(T);
+  extern __shared__ __attribute__((aligned(16))) char shared[];
+  T* const x = reinterpret_cast<T*>(shared);  // [N][fill], zeros from `width` on
+  __shared__ float2 part[4][N];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  for (uint32_t i = threadIdx.x; i < N * fill; i += 256) {
+    const uint32_t n = i / fill, c = i % fill;
+    x[i] = c < width && n < a.N ? static_cast<const T*>(a.B)[(uint64_t)n * width + c] : T(0.f);
+  }
+  __syncthreads();
+  int64_t y[N];
+  float most[N], sum[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    y[n] = (uint32_t)n < a.N ? target_of(a.targets, a.id_bytes, n) : -1;
+    most[n] = -INFINITY;
+    sum[n] = 0.f;
+  }
+  const uint32_t stride = gridDim.x * 4 * kFewRows;
+  for (uint64_t v0 = (blockIdx.x * 4 + wave) * kFewRows; v0 < a.M; v0 += stride) {
+    float acc[kFewRows][N] = {};
+    const T* row[kFewRows];
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r) row[r] = static_cast<const T*>(a.A) + min(v0 + r, (uint64_t)a.M - 1) * width;
+    // (the last stretch, which a row need not fill, on its own)
+    const auto stretch = [&](uint32_t c, auto full) {
+      float w[kFewRows][E];
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r) {
+        T e[E];
+        if (decltype(full)::value || c + E <= width) {
+          __builtin_memcpy(e, row[r] + c, 16);
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; ++k) e[k] = c + k < width ? row[r][c + k] : T(0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[r][k] = to_f32(e[k]);
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        T e[E];
+        __builtin_memcpy(e, __builtin_assume_aligned(x + n * fill + c, 16), 16);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+#pragma unroll
+          for (int r = 0; r < kFewRows; ++r) acc[r][n] = fmaf(w[r][k], to_f32(e[k]), acc[r][n]);
+      }
+    };
+    uint32_t c = lane * E;
+#pragma unroll 4
+    for (; c - lane * E + kWave * E <= width; c += kWave * E) stretch(c, std::true_type{});
+    if (c - lane * E < width) stretch(c, std::false_type{});
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float l = a.scale * wave_sum(acc[r][n]);
+        if (v0 + r < a.M) {
+          const float m = fmaxf(most[n], l);
+          sum[n] = sum[n] * exp_below(most[n], m) + exp_below(l, m);
+          most[n] = m;
+          if ((int64_t)(v0 + r) == y[n] && lane == 0) a.hit[n] = l;
+        }
+      }
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) part[wave][n] = make_float2(most[n], sum[n]);
+  }
+  __syncthreads();
+  if (threadIdx.x < a.N) {
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, part[w][threadIdx.x].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s += part[w][threadIdx.x].y * exp_below(part[w][threadIdx.x].x, m);
+    a.stats[(uint64_t)blockIdx.x * a.N + threadIdx.x] = make_float2(m, s);
+  }
+}
+
 // ------------------------------------------------------------------ layouts
 // dst[r][c] = src[r][c], zeros for columns from `cols` to `fill`; targets: zeros also for rows of tokens that are left
 // out and from `rows` on
@@ -521,28 +610,38 @@ __global__ __launch_bounds__(256) void k_xent_rows(const T* __restrict__ src, ui
 }
 
 // ------------------------------------------------------------------ joins
-// lse and loss of each token from its tiles' maxima and sums: 16 threads a token, 16 tokens a block
+// lse and loss of each token from its tiles' maxima and sums: TOKENS of them a block, 256 / TOKENS threads each
+template <int TOKENS>
 __global__ __launch_bounds__(256) void k_xent_join(const float2* __restrict__ stats, uint32_t tiles, uint32_t tokens, const float* __restrict__ hit,
                                                    const void* targets, int id_bytes, uint32_t vocab, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 sh[16][17];
-  const uint32_t i = threadIdx.x % 16, k = threadIdx.x / 16, t = blockIdx.x * 16 + i;
+  constexpr int PARTS = 256 / TOKENS, N = 4;  // (loads on their way)
+  __shared__ float2 sh[PARTS][TOKENS + 1];
+  const uint32_t i = threadIdx.x % TOKENS, k = threadIdx.x / TOKENS, t = blockIdx.x * TOKENS + i;
   float m = -INFINITY, s = 0.f;
-  if (t < tokens)
-    for (uint32_t j = k; j < tiles; j += 16) {
-      const float2 p = stats[(uint64_t)j * tokens + t];
-      const float n = fmaxf(m, p.x);
-      s = s * exp_below(m, n) + p.y * exp_below(p.x, n);
-      m = n;
-    }
-  sh[k][i] = make_float2(m, s);
-  __syncthreads();
-  if (k || t >= tokens) return;
-  for (int j = 1; j < 16; ++j) {
-    const float2 p = sh[j][i];
+  const auto add = [&](float2 p) {
     const float n = fmaxf(m, p.x);
     s = s * exp_below(m, n) + p.y * exp_below(p.x, n);
     m = n;
+  };
+  if (t < tokens)
+    for (uint32_t j = k; j < tiles; j += PARTS * N) {
+      float2 p[N];
+#pragma unroll
+      for (int q = 0; q < N; ++q) p[q] = stats[(uint64_t)min(j + q * PARTS, tiles - 1) * tokens + t];
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (j + q * PARTS < tiles) add(p[q]);
+    }
+  sh[k][i] = make_float2(m, s);
+#pragma unroll
+  for (int half = PARTS / 2; half; half /= 2) {
+    __syncthreads();
+    if (k < (uint32_t)half) {
+      add(sh[k + half][i]);
+      sh[k][i] = make_float2(m, s);
+    }
   }
+  if (k || t >= tokens) return;
   const int64_t y = target_of(targets, id_bytes, t);
   const bool in = y >= 0 && y < (int64_t)vocab;
   const float e = in ? m + logf(s) : 0.f;
@@ -592,7 +691,7 @@ struct Tiling {
 enum { TILE_L, TILE_M, TILE_S, TILE_T };
 constexpr uint32_t kTileM[] = {TileL::BM, TileM::BM, TileS::BM, TileT::BM}, kTileN[] = {TileL::BN, TileM::BN, TileS::BN, TileT::BN};
 static double rate_of(bool bf, int tile) {
-  const double b[] = {5.2, 3.0, 1.6, 1.2}, f[] = {.57, .55, .47, .40};
+  const double b[] = {5.2, 3.0, 1.6, 1.0}, f[] = {.57, .55, .47, .47};
   return bf ? b[tile] : f[tile];
 }
 // partial sums of a split product, in floats
@@ -692,6 +791,20 @@ template <typename T>
 static hipError_t whole(const void** p, uint64_t rows, uint32_t width, uint64_t k, void* copy, hipStream_t s) {
   return whole_rows(*p, width, sizeof(T)) ? hipSuccess : copy_rows<T>(p, rows, width, rows, k, copy, nullptr, s);
 }
+template <typename T, int N = kFewTokens>
+static hipError_t few(ProductArgs& a, uint32_t width, hipStream_t s) {
+  if constexpr (N > 1)
+    if (a.N <= N / 2) return few<T, N / 2>(a, width, s);
+  const uint32_t fill = (uint32_t)up(width, kWave * 16 / sizeof(T)), bytes = N * fill * (uint32_t)sizeof(T);
+  const uint32_t blocks = std::min(tiles(a.M, TileS::BM), (a.M + 4 * kFewRows - 1) / (4 * kFewRows));
+  if (bytes > (48u << 10)) {
+    const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(k_xent_few<T, N>), hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewBytes);
+    if (err != hipSuccess) return err;
+  }
+  LAPLEX_LAUNCH("k_xent_few", a.M, s, k_xent_few<T, N><<<blocks, 256, bytes, s>>>(a, width, fill));
+  a.tiles_m = blocks;
+  return hipGetLastError();
+}
 template <typename T>
 static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws, hipStream_t s) {
   size_t total;
@@ -700,11 +813,6 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   ProductArgs a{};
   a.A = x.table;
   a.B = x.x;
-  hipError_t err;
-  if ((err = whole<T>(&a.A, x.vocab, x.width, p.k_width, w.table_rows, s)) != hipSuccess) return err;
-  if ((err = whole<T>(&a.B, x.tokens, x.width, p.k_width, w.x_rows, s)) != hipSuccess) return err;
-  a.lda = a.ldb = (int64_t)p.k_width;
-  a.K = p.k_width;
   a.M = x.vocab;
   a.N = (uint32_t)x.tokens;
   a.targets = x.targets;
@@ -713,9 +821,20 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   a.scale = x.scale;
   a.stats = w.stats;
   a.hit = w.hit;
-  if ((err = product<T>("k_product_stats", LOGITS_STATS, a, tiling(sizeof(T) == 2, a.M, a.N, a.K, false), s)) != hipSuccess) return err;
-  LAPLEX_LAUNCH("k_xent_join", x.tokens, s,
-                k_xent_join<<<(unsigned)((x.tokens + 15) / 16), 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse));
+  hipError_t err;
+  if (x.tokens <= kFewTokens && kFewTokens * up(x.width, kWave * 16 / sizeof(T)) * sizeof(T) <= kFewBytes) {
+    if ((err = few<T>(a, x.width, s)) != hipSuccess) return err;
+  } else {
+    if ((err = whole<T>(&a.A, x.vocab, x.width, p.k_width, w.table_rows, s)) != hipSuccess) return err;
+    if ((err = whole<T>(&a.B, x.tokens, x.width, p.k_width, w.x_rows, s)) != hipSuccess) return err;
+    a.lda = a.ldb = (int64_t)p.k_width;
+    a.K = p.k_width;
+    if ((err = product<T>("k_product_stats", LOGITS_STATS, a, tiling(sizeof(T) == 2, a.M, a.N, a.K, false), s)) != hipSuccess) return err;
+  }
+  LAPLEX_LAUNCH("k_xent_join", x.tokens, s, {
+    if (x.tokens <= 64) k_xent_join<1><<<(unsigned)x.tokens, 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse);
+    else k_xent_join<16><<<(unsigned)((x.tokens + 15) / 16), 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse);
+  });
   return hipGetLastError();
 }
 template <typename T>
