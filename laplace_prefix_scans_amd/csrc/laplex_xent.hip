@@ -583,29 +583,41 @@ __global__ __launch_bounds__(256) void k_xent_few(ProductArgs a, uint32_t width,
 
 // ------------------------------------------------------------------ layouts
 // dst[r][c] = src[r][c], zeros for columns from `cols` to `fill`; targets: zeros also for rows of tokens that are left
-// out and from `rows` on
+// out and from `rows` on.  Two tensors a launch, of which either may have no rows.
+struct RowsCopy {
+  const void* src;
+  void* dst;
+  uint64_t rows, rows_fill;
+  uint32_t cols, fill;
+  const void* targets;
+  int id_bytes;
+  uint32_t vocab;
+};
+struct RowsCopies {
+  RowsCopy c[2];
+};
 template <typename T>
-__global__ __launch_bounds__(256) void k_xent_rows(const T* __restrict__ src, uint64_t rows, uint32_t cols, uint64_t rows_fill, uint32_t fill,
-                                                   T* __restrict__ dst, const void* targets, int id_bytes, uint32_t vocab) {
+__global__ __launch_bounds__(256) void k_xent_rows(RowsCopies a) {
   constexpr int E = 16 / sizeof(T);
-  const uint64_t n = rows_fill * (fill / E), stride = (uint64_t)gridDim.x * 256;
-  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
-    const uint64_t r = i / (fill / E);
-    const uint32_t c = (uint32_t)(i % (fill / E)) * E;
-    bool in = r < rows;
-    if (in && targets) {
-      const int64_t y = target_of(targets, id_bytes, (uint32_t)r);
-      in = y >= 0 && y < (int64_t)vocab;
+  const uint64_t n0 = a.c[0].rows_fill * (a.c[0].fill / E), n = n0 + a.c[1].rows_fill * (a.c[1].fill / E), stride = (uint64_t)gridDim.x * 256;
+  for (uint64_t k = (uint64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += stride) {
+    const RowsCopy& q = a.c[k >= n0];
+    const uint64_t i = k >= n0 ? k - n0 : k, r = i / (q.fill / E);
+    const uint32_t c = (uint32_t)(i % (q.fill / E)) * E;
+    bool in = r < q.rows;
+    if (in && q.targets) {
+      const int64_t y = target_of(q.targets, q.id_bytes, (uint32_t)r);
+      in = y >= 0 && y < (int64_t)q.vocab;
     }
     T v[E];
-    const T* p = src + r * cols + c;
-    if (in && c + E <= cols) {
+    const T* p = static_cast<const T*>(q.src) + r * q.cols + c;
+    if (in && c + E <= q.cols) {
       __builtin_memcpy(v, p, 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = in && c + e < cols ? p[e] : T(0.f);
+      for (int e = 0; e < E; ++e) v[e] = in && c + e < q.cols ? p[e] : T(0.f);
     }
-    __builtin_memcpy(dst + r * fill + c, v, 16);
+    __builtin_memcpy(static_cast<T*>(q.dst) + r * q.fill + c, v, 16);
   }
 }
 
@@ -778,19 +790,25 @@ static hipError_t product(const char* name, Product epi, ProductArgs& a, const T
 }
 static unsigned some_blocks(uint64_t n) { return (unsigned)std::min<uint64_t>((n + 255) / 256, 16384); }
 
-// rows of whole pieces (x in the backward: without the tokens that are left out)
+// x and the table in rows of whole pieces, as they lie or copied (x in the backward always: without the tokens that are
+// left out, and with rows of zeros up to a whole step)
 template <typename T>
-static hipError_t copy_rows(const void** p, uint64_t rows, uint32_t width, uint64_t rows_fill, uint64_t k, void* copy, const XentShape* tokens, hipStream_t s) {
-  LAPLEX_LAUNCH("k_xent_rows", rows, s,
-                k_xent_rows<T><<<some_blocks(rows_fill * k * sizeof(T) / 16), 256, 0, s>>>(static_cast<const T*>(*p), rows, width, rows_fill, (uint32_t)k, static_cast<T*>(copy),
-                                                                       tokens ? tokens->targets : nullptr, tokens ? tokens->id_bytes : 0, tokens ? tokens->vocab : 0));
-  *p = copy;
+static hipError_t whole(const XentShape& x, const XentPlan& p, const XentWorkspace& w, bool back, const void** rows, const void** table, hipStream_t s) {
+  RowsCopies c{};
+  *rows = x.x;
+  *table = x.table;
+  const auto copy = [&](int i, const void** at, void* to, uint64_t n, uint64_t fill) {
+    c.c[i] = {*at, to, n, fill, x.width, (uint32_t)p.k_width, i == 0 && back ? x.targets : nullptr, x.id_bytes, x.vocab};
+    *at = to;
+  };
+  if (back || !whole_rows(x.x, x.width, sizeof(T))) copy(0, rows, w.x_rows, x.tokens, back ? p.k_tokens : x.tokens);
+  if (!whole_rows(x.table, x.width, sizeof(T))) copy(1, table, w.table_rows, x.vocab, x.vocab);
+  const uint64_t n = (c.c[0].rows_fill + c.c[1].rows_fill) * p.k_width * sizeof(T) / 16;
+  for (RowsCopy& q : c.c) q.fill = (uint32_t)p.k_width;
+  if (n) LAPLEX_LAUNCH("k_xent_rows", n, s, k_xent_rows<T><<<some_blocks(n), 256, 0, s>>>(c));
   return hipGetLastError();
 }
-template <typename T>
-static hipError_t whole(const void** p, uint64_t rows, uint32_t width, uint64_t k, void* copy, hipStream_t s) {
-  return whole_rows(*p, width, sizeof(T)) ? hipSuccess : copy_rows<T>(p, rows, width, rows, k, copy, nullptr, s);
-}
+
 template <typename T, int N = kFewTokens>
 static hipError_t few(ProductArgs& a, uint32_t width, hipStream_t s) {
   if constexpr (N > 1)
@@ -825,8 +843,7 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   if (x.tokens <= kFewTokens && kFewTokens * up(x.width, kWave * 16 / sizeof(T)) * sizeof(T) <= kFewBytes) {
     if ((err = few<T>(a, x.width, s)) != hipSuccess) return err;
   } else {
-    if ((err = whole<T>(&a.A, x.vocab, x.width, p.k_width, w.table_rows, s)) != hipSuccess) return err;
-    if ((err = whole<T>(&a.B, x.tokens, x.width, p.k_width, w.x_rows, s)) != hipSuccess) return err;
+    if ((err = whole<T>(x, p, w, false, &a.B, &a.A, s)) != hipSuccess) return err;
     a.lda = a.ldb = (int64_t)p.k_width;
     a.K = p.k_width;
     if ((err = product<T>("k_product_stats", LOGITS_STATS, a, tiling(sizeof(T) == 2, a.M, a.N, a.K, false), s)) != hipSuccess) return err;
@@ -847,8 +864,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   const void *table = x.table, *rows = x.x;
   hipError_t err;
   if (tokens) {  // (without, dtable is a sum of nothing)
-    if ((err = whole<T>(&table, x.vocab, x.width, p.k_width, w.table_rows, s)) != hipSuccess) return err;
-    if ((err = copy_rows<T>(&rows, x.tokens, x.width, p.k_tokens, p.k_width, w.x_rows, &x, s)) != hipSuccess) return err;
+    if ((err = whole<T>(x, p, w, true, &rows, &table, s)) != hipSuccess) return err;
   } else {
     dx = nullptr;
   }
