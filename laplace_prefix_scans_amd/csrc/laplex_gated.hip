@@ -161,14 +161,14 @@ struct Rows {
   Global at;      // the first channel of the row that is next
   int64_t token;  // bytes
   uint32_t off;   // bytes to the lane's channel
-  int32_t t, last;
+  int32_t left;   // tokens behind it
   __device__ __forceinline__ Rows(const void* p, int64_t stride, int64_t channel, int64_t t0, int64_t tokens)
-      : token(STEP * stride * (int64_t)sizeof(T)), off((uint32_t)channel * (uint32_t)sizeof(T)), t((int32_t)t0), last((int32_t)tokens - 1) {
+      : token(STEP * stride * (int64_t)sizeof(T)), off((uint32_t)channel * (uint32_t)sizeof(T)), left((int32_t)(tokens - 1 - t0)) {
     at = (Global)(uintptr_t)uniform64(reinterpret_cast<int64_t>(p) + min(t0, tokens - 1) * stride * (int64_t)sizeof(T));
   }
   __device__ __forceinline__ void move() {
-    at += (STEP > 0 ? t < last : t <= last) ? token : 0;
-    t += STEP;
+    at += (STEP > 0 ? left > 0 : left >= 0) ? token : 0;
+    left -= STEP;
   }
   __device__ __forceinline__ T get() {
     const __attribute__((address_space(1))) T* p = (const __attribute__((address_space(1))) T*)(at + off);

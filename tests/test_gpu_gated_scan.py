@@ -289,3 +289,26 @@ def test_another_stream():
         got.record_stream(s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_as_many_tokens_as_offsets_can_name():
+    """2^31 - 1 tokens of one channel: constant inputs, whose states and gradients settle to those of an endless sequence."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    n = 2 ** 31 - 1
+    gate, x = torch.full((1, 1), 1.0, device="cuda").expand(n, 1), torch.ones(n, 1, device="cuda")
+    h, carries = lp.laplex_gated_scan(gate, x, keep=True)
+    a = float(np.exp(-1.0))
+    want = 1 / (1 - a)
+    # the decay is off by 14 roundings, and what it multiplies is 1 / (1 - a) times as much; each token adds two
+    tol = 16 * ref.U * want / (1 - a)
+    settled = h[40:]  # (e^-40 of the beginning is left)
+    assert abs(float(settled.max()) - want) <= tol and abs(float(settled.min()) - want) <= tol and abs(float(h[0]) - 1) <= ref.U
+    dgate, dx, _ = lp.laplex_gated_scan_backward(gate, x, carries, h.fill_(1.0))
+    del h
+    assert abs(float(dx[:-40].max()) - want) <= tol and abs(float(dx[:-40].min()) - want) <= tol and float(dx[-1]) == 1.0
+    del dx
+    settled = dgate[41:-41]
+    want = -a * want * want
+    tol = 3 * tol * abs(want)
+    assert abs(float(settled.max()) - want) <= tol and abs(float(settled.min()) - want) <= tol and float(dgate[0]) == 0.0
