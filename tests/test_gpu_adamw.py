@@ -289,3 +289,37 @@ def test_a_tensor_past_2_32_bytes():
     m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
     lp.laplex_adamw([p], [g], [m], [v], step=1, lr=0.5)
     assert bool((p == p[0]).all()) and abs(float(p[0]) + 0.5) < 1e-6 and bool((m == m[0]).all()) and bool((v == v[0]).all())
+
+
+@pytest.mark.parametrize("types", ["ff", "bb", "fb"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_parameters_larger_than_the_caches_as_in_parts(types, bits):
+    """A step's result does not depend on how many bytes it moves: one call for all, and one for each part."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    part, count = 5_000_192, 16 if types == "ff" else 24  # more than 288 MiB together, each part less
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = part * count - 100
+    p = torch.randn(n, generator=g, device="cuda").to(dtypes(types[0]))
+    grad = (1e-2 * torch.randn(n, generator=g, device="cuda")).to(dtypes(types[1]))
+    kind = torch.float32 if bits == 32 else torch.uint8
+    state = {k: torch.zeros(n, dtype=kind, device="cuda") for k in ("m", "v")}
+    if bits == 8:
+        state.update({k: torch.zeros(-(-n // 256), device="cuda") for k in ("m_scale", "v_scale")})
+    else:
+        state["m"].copy_(1e-3 * grad.float())
+        state["v"].copy_(1e-3 * grad.float() ** 2)
+    if types == "bb":
+        state["master"] = p.float()
+    q, other = p.clone(), {k: v.clone() for k, v in state.items()}
+    for step in (1, 2):
+        lp.laplex_adamw([p], [grad], step=step, weight_decay=0.1, **{k: [v] for k, v in state.items()}, **HYPER)
+        for i in range(0, n, part):
+            cut = {k: [v[i // 256:(i + part) // 256] if k.endswith("scale") and i + part < n else v[i // 256:] if k.endswith("scale") else v[i:i + part]]
+                   for k, v in other.items()}
+            lp.laplex_adamw([q[i:i + part]], [grad[i:i + part]], step=step, weight_decay=0.1, **cut, **HYPER)
+        assert torch.equal(p, q) and all(torch.equal(v, other[k]) for k, v in state.items())
+    if bits == 8:
+        m, v = lp.laplex_adamw_moments(*[[state[k]] for k in ("m", "v", "m_scale", "v_scale")])
+        small = lp.laplex_adamw_moments(*[[state[k][:1000]] for k in ("m", "v")], *[[state[k][:4]] for k in ("m_scale", "v_scale")])
+        assert torch.equal(m[0][:1000], small[0][0]) and torch.equal(v[0][:1000], small[1][0])

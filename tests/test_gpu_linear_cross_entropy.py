@@ -278,3 +278,79 @@ def test_shapes_no_tokens_and_streams():
     assert lp.laplex_linear_cross_entropy(e, x["table"], ye)[0].shape == (0,)
     dx, dt = lp.laplex_linear_cross_entropy_backward(e, x["table"], ye, f, f)
     assert dx.shape == (0, 32) and dt.shape == (90, 32) and not dt.any()
+
+
+# ------------------------------------------------------------------ a few tokens
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4, 5, 7, 8, 9])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_few_tokens(tokens, dt):
+    run_case(tokens, 2003, 520, dt, seed=tokens)
+
+
+# rows of less than a load of a wave, of whole loads, with ends of every kind; tokens that fill 128 KB, and one element more
+@pytest.mark.parametrize("width", [1, 3, 64, 255, 256, 257, 511, 512, 513, 4096, 4097, 8192, 8193])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_few_tokens_of_any_width(width, dt):
+    run_case(6, 77, width, dt, seed=width)
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 63, 65, 33000])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_few_tokens_of_any_vocabulary(vocab, dt):
+    import torch
+    run_case(5, vocab, 40, dt, seed=vocab, ids=torch.int32, scale=-0.7, dlse=True)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_few_tokens_that_begin_anywhere(dt):
+    import torch
+    import laplace_prefix_scans_amd as lp
+    for width in (128, 1024, 1001):
+        c = {k: v.cuda() for k, v in make(4, 90, width, dtype_of(dt)).items()}
+        loss, lse = lp.laplex_linear_cross_entropy(c["x"], c["table"], c["y"])
+
+        def moved(t):
+            flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:]
+            return flat.copy_(t.reshape(-1)).view(t.shape)
+        loss2, lse2 = lp.laplex_linear_cross_entropy(moved(c["x"]), moved(c["table"]), c["y"])
+        assert torch.equal(lse, lse2) and torch.equal(loss, loss2)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [4, 20])
+def test_a_token_has_nothing_of_its_neighbours(tokens, dt):
+    """A token's loss and lse have the same bits whatever the others hold, infinities and huge logits among them."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    c = {k: v.cuda() for k, v in make(tokens, 300, 200, dtype_of(dt)).items()}
+    y = c["y"].clamp(0, 299)
+    loss, lse = lp.laplex_linear_cross_entropy(c["x"], c["table"], y)
+    for bad in (float("inf"), float("nan"), 1e30):
+        x = c["x"].clone()
+        x[1::2] = bad
+        loss2, lse2 = lp.laplex_linear_cross_entropy(x, c["table"], y)
+        assert torch.equal(loss2[::2], loss[::2]) and torch.equal(lse2[::2], lse[::2]), bad
+
+
+# ------------------------------------------------------------------ more tiles than run at once
+# Each tile shape of each product, with a second round of tiles for its blocks, and split sums among them
+@pytest.mark.parametrize("dims", [(33, 3001, 1500), (33, 9001, 640), (33, 20001, 1500), (33, 40001, 640), (100, 40001, 33), (200, 20001, 40),
+                                  (500, 40001, 72), (700, 40001, 32), (700, 3001, 1500), (3001, 100, 1500)], ids=str)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_more_tiles_than_run_at_once(dims, dt):
+    run_case(*dims, dt, seed=2)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("dims", [(3, 1000, 256), (300, 9001, 640)], ids=str)
+def test_a_repeated_call_gives_the_same_bits(dims, dt):
+    import torch
+    import laplace_prefix_scans_amd as lp
+    c = {k: v.cuda() for k, v in make(*dims, dtype_of(dt)).items()}
+
+    def both():
+        loss, lse = lp.laplex_linear_cross_entropy(c["x"], c["table"], c["y"])
+        return (loss, lse, *lp.laplex_linear_cross_entropy_backward(c["x"], c["table"], c["y"], lse, c["dloss"], c["dlse"]))
+    first = both()
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(both(), first))
