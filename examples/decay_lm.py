@@ -1,11 +1,15 @@
 """A small language model on the library's sequence layers, trained and run.
 
-    python examples/decay_lm.py [--steps 200] [--dtype bf16]
+    python examples/decay_lm.py [--steps 200] [--dtype bf16] [--mixer gated] [--fused] [--moments 8]
 
 embedding -> blocks of [layer norm, decayed linear attention, layer norm, gated
 feed-forward] -> layer norm -> tied output table.  The decay rates are learned
 with the weights (started so that the heads remember from a few tokens to
-hundreds).  Training packs documents of different lengths into one row of
+hundreds).  With --mixer gated the attention's place is taken by a gated linear
+recurrence, whose decays each token sets for itself.  With --fused the loss is
+formed from the last layer's rows and the table, without the logits in memory,
+and one launch updates all parameters (with --moments 8, moments of one byte).
+Training packs documents of different lengths into one row of
 tokens; generation reads a prompt in one pass, which leaves each layer's state,
 and continues token by token from it.  The task is synthetic: a document's first
 token names one of a few fixed permutations of the vocabulary, and each later
@@ -74,13 +78,79 @@ class DecayAttention(torch.autograd.Function):
         return dq, dk, dv, drate, None, None
 
 
+class GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, x, offsets):
+        h, carries = lp.laplex_gated_scan(gate, x, "sigmoid", offsets=offsets, keep=True)
+        ctx.save_for_backward(gate, x, offsets, carries)
+        return h
+
+    @staticmethod
+    @once_differentiable  # the library has first derivatives
+    def backward(ctx, g):
+        gate, x, offsets, carries = ctx.saved_tensors
+        dgate, dx, _ = lp.laplex_gated_scan_backward(gate, x, carries, g.contiguous(), "sigmoid", offsets=offsets)
+        return dgate, dx, None
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """The loss of each token (zero where its target is outside the vocabulary), in float32."""
+
+    @staticmethod
+    def forward(ctx, x, table, targets):
+        x = x.contiguous()
+        loss, lse = lp.laplex_linear_cross_entropy(x, table, targets)
+        ctx.save_for_backward(x, table, targets, lse)
+        return loss
+
+    @staticmethod
+    @once_differentiable  # the library has first derivatives
+    def backward(ctx, g):
+        x, table, targets, lse = ctx.saved_tensors
+        return (*lp.laplex_linear_cross_entropy_backward(x, table, targets, lse, g.contiguous(), x_grad=ctx.needs_input_grad[0],
+                                                         table_grad=ctx.needs_input_grad[1]), None)
+
+
+class AdamW:
+    """All parameters in one call for each type of theirs; bfloat16 ones have float32 copies, which are what is updated."""
+
+    def __init__(self, params, lr, weight_decay=0.01, bits=32):
+        self.lr, self.weight_decay, self.bits, self.count = lr, weight_decay, bits, 0
+        self.groups = []
+        params = list(params)
+        for dtype in (torch.float32, torch.bfloat16):
+            ps = [p for p in params if p.dtype is dtype]
+            if ps:
+                kind = torch.float32 if bits == 32 else torch.uint8
+                state = {k: [torch.zeros(p.shape, dtype=kind, device=p.device) for p in ps] for k in ("m", "v")}
+                if bits == 8:
+                    for k in ("m_scale", "v_scale"):
+                        state[k] = [torch.zeros(-(-p.numel() // 256), device=p.device) for p in ps]
+                if dtype is torch.bfloat16:
+                    state["master"] = [p.detach().float() for p in ps]
+                self.groups.append((ps, state))
+
+    @torch.no_grad()
+    def step(self):
+        self.count += 1
+        for ps, state in self.groups:
+            lp.laplex_adamw([p.detach() for p in ps], [p.grad for p in ps], lr=self.lr, step=self.count, weight_decay=self.weight_decay,
+                            seed=self.count if self.bits == 8 else None, **state)
+
+    def zero_grad(self):
+        for ps, _ in self.groups:
+            for p in ps:
+                p.grad = None
+
+
 class DecayLM:
     """Parameters in a dict; forward() for packed documents, prefill() and step() for generation."""
 
-    def __init__(self, vocab=64, width=256, heads=4, layers=2, dtype=torch.float32, device="cuda", seed=0):
+    def __init__(self, vocab=64, width=256, heads=4, layers=2, dtype=torch.float32, device="cuda", seed=0, mixer="attention"):
+        assert mixer in ("attention", "gated"), mixer
         g = torch.Generator().manual_seed(seed)
         self.vocab, self.width, self.heads, self.layers, self.dtype = vocab, width, heads, layers, dtype
-        self.head = width // heads
+        self.head, self.mixer = width // heads, mixer
         self.scale = self.head ** -0.5
 
         def normal(*shape, std):
@@ -92,13 +162,20 @@ class DecayLM:
         p = {"table": normal(vocab, width, std=width ** -0.5), "norm.w": const(width, 1.0), "norm.b": const(width, 0.0)}
         for i in range(layers):
             p.update({"%d.n1.w" % i: const(width, 1.0), "%d.n1.b" % i: const(width, 0.0), "%d.n2.w" % i: const(width, 1.0),
-                      "%d.n2.b" % i: const(width, 0.0), "%d.qkv" % i: normal(width, 3 * width, std=width ** -0.5),
+                      "%d.n2.b" % i: const(width, 0.0)})
+            if mixer == "attention":
+                p["%d.qkv" % i] = normal(width, 3 * width, std=width ** -0.5)
+            else:
+                p["%d.gx" % i] = normal(width, 2 * width, std=width ** -0.5)
+                # decays 1 - 1 / m where the projection gives 0: memories m of 4 to 400 tokens
+                p["%d.gate.b" % i] = torch.log(torch.logspace(math.log10(4), math.log10(400), width) - 1).to(device, dtype).requires_grad_()
+            p.update({
                       "%d.out" % i: normal(width, width, std=0.5 * width ** -0.5),
                       "%d.up" % i: normal(width, 4 * width, std=width ** -0.5),
-                      "%d.down" % i: normal(2 * width, width, std=0.5 * width ** -0.5),
-                      # the rates' logarithms: memories of about 4 to 400 tokens
-                      "%d.rate" % i: torch.log(torch.logspace(math.log10(0.25), math.log10(0.0025), heads)).to(device)
-                      .requires_grad_()})
+                      "%d.down" % i: normal(2 * width, width, std=0.5 * width ** -0.5)})
+            if mixer == "attention":
+                # the rates' logarithms: memories of about 4 to 400 tokens
+                p["%d.rate" % i] = torch.log(torch.logspace(math.log10(0.25), math.log10(0.0025), heads)).to(device).requires_grad_()
         self.p = p
 
     def _qkv(self, x, i):
@@ -107,23 +184,41 @@ class DecayLM:
         # slices of one projection: the attention takes them as they lie
         return y.view(t, 3, self.heads, self.head).unbind(1)
 
+    def _gate_x(self, x, i):
+        y = LayerNorm.apply(x, self.p["%d.n1.w" % i], self.p["%d.n1.b" % i]) @ self.p["%d.gx" % i]
+        gate, v = y.chunk(2, -1)  # the recurrence takes the second slice as it lies
+        return gate + self.p["%d.gate.b" % i], v
+
     def _rest(self, x, o, i):
         x = x + o.reshape(x.shape) @ self.p["%d.out" % i]
         a, b = (LayerNorm.apply(x, self.p["%d.n2.w" % i], self.p["%d.n2.b" % i]) @ self.p["%d.up" % i]).chunk(2, -1)
         return x + (torch.nn.functional.silu(a) * b) @ self.p["%d.down" % i]
 
+    def _last(self, x):
+        return LayerNorm.apply(x, self.p["norm.w"], self.p["norm.b"])
+
     def _logits(self, x):
-        return (LayerNorm.apply(x, self.p["norm.w"], self.p["norm.b"]) @ self.p["table"].t()).float()
+        return (self._last(x) @ self.p["table"].t()).float()
 
     def _rate(self, i):
         return torch.exp(self.p["%d.rate" % i])
 
-    def forward(self, ids, offsets):
+    def _blocks(self, ids, offsets):
         x = Embedding.apply(ids, self.p["table"], math.sqrt(self.width))
         for i in range(self.layers):
+            if self.mixer == "gated":
+                x = self._rest(x, GatedScan.apply(*self._gate_x(x, i), offsets), i)
+                continue
             q, k, v = self._qkv(x, i)
             x = self._rest(x, DecayAttention.apply(q, k, v, self._rate(i), offsets, self.scale), i)
-        return self._logits(x)
+        return x
+
+    def forward(self, ids, offsets):
+        return self._logits(self._blocks(ids, offsets))
+
+    def losses(self, ids, offsets, targets):
+        """The cross entropy of each token's target (a target of -1: zero), without the logits in memory."""
+        return LinearCrossEntropy.apply(self._last(self._blocks(ids, offsets)), self.p["table"], targets)
 
     @torch.no_grad()
     def prefill(self, ids, offsets):
@@ -131,6 +226,12 @@ class DecayLM:
         x = lp.laplex_embedding(ids, self.p["table"], scale=math.sqrt(self.width))
         states = []
         for i in range(self.layers):
+            if self.mixer == "gated":
+                state = torch.empty(offsets.numel() - 1, self.width, device=x.device)
+                o = lp.laplex_gated_scan(*self._gate_x(x, i), "sigmoid", offsets=offsets, state_out=state)
+                states.append(state)
+                x = self._rest(x, o, i)
+                continue
             q, k, v = self._qkv(x, i)
             state = torch.empty(offsets.numel() - 1, self.heads, self.head, self.head, device=x.device)
             o = lp.laplex_decay_attn(q, k, v, self._rate(i), offsets=offsets, scale=self.scale, state_out=state)
@@ -143,6 +244,9 @@ class DecayLM:
         """One token for each row; the states move on in place."""
         x = lp.laplex_embedding(ids, self.p["table"], scale=math.sqrt(self.width))
         for i in range(self.layers):
+            if self.mixer == "gated":
+                x = self._rest(x, lp.laplex_gated_scan_step(*self._gate_x(x, i), states[i], "sigmoid", slots=slots), i)
+                continue
             q, k, v = self._qkv(x, i)
             o = lp.laplex_decay_attn_step(q, k, v, self._rate(i), states[i], slots=slots, scale=self.scale)
             x = self._rest(x, o, i)
@@ -172,19 +276,21 @@ def documents(count, vocab, gen, device="cuda"):
     return torch.cat(parts).to(device), torch.tensor(ends, dtype=torch.int32, device=device)
 
 
-def train(model, steps, docs=32, lr=2e-3, seed=1, log=None):
+def train(model, steps, docs=32, lr=2e-3, seed=1, log=None, fused=False, moments=32):
     gen = torch.Generator().manual_seed(seed)
-    opt = torch.optim.AdamW(model.p.values(), lr=lr)
+    opt = AdamW(model.p.values(), lr, bits=moments) if fused else torch.optim.AdamW(model.p.values(), lr=lr)
     losses = []
     for s in range(steps):
         ids, offsets = documents(docs, model.vocab, gen)
-        logits = model.forward(ids, offsets)
         target = torch.roll(ids, -1)
         last = offsets[1:].long() - 1
         mask = torch.ones_like(ids, dtype=torch.bool)
         mask[last] = False  # a document's last token has nothing after it
         mask[offsets[:-1].long()] = False  # and what follows the key is free
-        loss = torch.nn.functional.cross_entropy(logits[mask], target[mask])
+        if fused:
+            loss = model.losses(ids, offsets, target.masked_fill(~mask, -1)).sum() / mask.sum()
+        else:
+            loss = torch.nn.functional.cross_entropy(model.forward(ids, offsets)[mask], target[mask])
         opt.zero_grad()
         loss.backward()
         opt.step()
@@ -209,9 +315,14 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--dtype", choices=("f32", "bf16"), default="f32")
+    ap.add_argument("--mixer", choices=("attention", "gated"), default="attention")
+    ap.add_argument("--fused", action="store_true")
+    ap.add_argument("--moments", type=int, choices=(32, 8), default=32)
     a = ap.parse_args()
-    model = DecayLM(dtype=torch.float32 if a.dtype == "f32" else torch.bfloat16)
-    train(model, a.steps, log=20)
+    if a.moments == 8 and not a.fused:
+        ap.error("--moments 8 goes with --fused")
+    model = DecayLM(dtype=torch.float32 if a.dtype == "f32" else torch.bfloat16, mixer=a.mixer)
+    train(model, a.steps, log=20, fused=a.fused, moments=a.moments)
     ids, offsets = documents(4, model.vocab, torch.Generator().manual_seed(99))
     got = generate(model, ids, offsets, 12).tolist()
     table = follower(model.vocab)
