@@ -34,7 +34,10 @@ __device__ __forceinline__ float decay_value(float c) { return near_one(c) ? 1.f
 template <int KIND>
 struct Gate {
   float c, w;  // the decay as above, the input's weight
+  bool near;   // near_one(c)
 };
+template <int KIND>
+__device__ __forceinline__ float decayed(const Gate<KIND>& q, float s) { return fmaf(q.c, s, q.near ? s : 0.f); }
 template <int KIND>
 __device__ __forceinline__ Gate<KIND> gate_of(float g) {
   Gate<KIND> r;
@@ -51,13 +54,14 @@ __device__ __forceinline__ Gate<KIND> gate_of(float g) {
     p = fmaf(g * p, -1.f / 2, 1.f);
     const float q = g < 0.3f ? g * p : 1.f - e;
     r.w = 1.f;
-    r.c = g >= 0.f && q <= 0.5f ? -q : e;
+    r.near = g >= 0.f && q <= 0.5f;
+    r.c = r.near ? -q : e;
   } else {
     const float e = __builtin_amdgcn_exp2f(-fabsf(g) * kLog2e);
     const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
-    const bool up = g >= 0.f;
-    r.w = up ? small : big;
-    r.c = up ? -small : small;
+    r.near = g >= 0.f;
+    r.w = r.near ? small : big;
+    r.c = r.near ? -small : small;
   }
   return r;
 }
@@ -151,39 +155,57 @@ static_assert(kGateU == 16, "marks of a tile are 16 bits");
 
 // ------------------------------------------------------------------ rows
 // A lane has one channel; lanes past the last one have that one too, and write what it writes.  Rows are taken one after
-// the other (STEP 1 or -1): their address is the wave's, and moves on by scalar additions, to which the lane adds 32 bits.
+// the other (STEP 1 or -1): their address is the wave's, and moves on by scalar additions, to which a load adds 32 bits.
 // Rows past the last token are read as it.  What the whole pass reads (LAST) and writes goes past the caches, which are left
 // to what the aggregates have read (16384 tokens x 4096 channels in bfloat16, forward and backward: 316 us, through the
-// caches 350; 65536 x 256 in float 74, 83).
+// caches 350; 65536 x 256 in float 74, 83; the loads alone, as all of this is now: 302 and 304, 68 and 71).
+// A bfloat16 is held as the word that its load makes, and becomes a float where it is used: held as what it is, two are packed
+// into a register, or masked, as soon as they arrive, which is waited for at the end of each tile (16384 tokens x 4096 channels,
+// aggregates of the forward and the backward: 84 and 67 us so, 52 and 46 now).  Which width avoids that differs by loop.
+template <typename T, bool LAST>
+using Raw = std::conditional_t<sizeof(T) == 2, std::conditional_t<LAST, uint32_t, uint16_t>, float>;
+__device__ __forceinline__ float value_of(float v) { return v; }
+__device__ __forceinline__ float value_of(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float value_of(uint16_t v) { return value_of((uint32_t)v); }
 template <typename T, int STEP, bool LAST>
 struct Rows {
   typedef __attribute__((address_space(1))) char* Global;
   Global at;      // the first channel of the row that is next
   int64_t token;  // bytes
-  uint32_t off;   // bytes to the lane's channel
   int32_t left;   // tokens behind it
-  __device__ __forceinline__ Rows(const void* p, int64_t stride, int64_t channel, int64_t t0, int64_t tokens)
-      : token(STEP * stride * (int64_t)sizeof(T)), off((uint32_t)channel * (uint32_t)sizeof(T)), left((int32_t)(tokens - 1 - t0)) {
+  __device__ __forceinline__ Rows(const void* p, int64_t stride, int64_t t0, int64_t tokens)
+      : token(STEP * stride * (int64_t)sizeof(T)), left((int32_t)(tokens - 1 - t0)) {
     at = (Global)(uintptr_t)uniform64(reinterpret_cast<int64_t>(p) + min(t0, tokens - 1) * stride * (int64_t)sizeof(T));
   }
+  // (INSIDE: neither this row nor the next one is past the last token)
+  template <bool INSIDE>
   __device__ __forceinline__ void move() {
-    at += (STEP > 0 ? left > 0 : left >= 0) ? token : 0;
+    at += INSIDE || (STEP > 0 ? left > 0 : left >= 0) ? token : 0;
     left -= STEP;
   }
-  __device__ __forceinline__ T get() {
-    const __attribute__((address_space(1))) T* p = (const __attribute__((address_space(1))) T*)(at + off);
-    const T v = LAST ? __builtin_nontemporal_load(p) : *p;
-    move();
+  template <bool INSIDE>
+  __device__ __forceinline__ Raw<T, LAST> get(uint32_t off) {
+    using W = std::conditional_t<sizeof(T) == 2, uint16_t, float>;
+    const __attribute__((address_space(1))) W* p = (const __attribute__((address_space(1))) W*)(at + off);
+    const Raw<T, LAST> v = LAST ? __builtin_nontemporal_load(p) : *p;
+    move<INSIDE>();
     return v;
   }
-  __device__ __forceinline__ void put(bool real, float v) {
+  template <bool INSIDE>
+  __device__ __forceinline__ void put(uint32_t off, bool real, float v) {
     if (real) __builtin_nontemporal_store(from_f32<T>(v), (__attribute__((address_space(1))) T*)(at + off));
-    move();
+    move<INSIDE>();
   }
-  // the next tile, its tokens in order
-  __device__ __forceinline__ void load(T (&v)[kGateU]) {
-#pragma unroll
-    for (int j = 0; j < kGateU; ++j) v[STEP > 0 ? j : kGateU - 1 - j] = get();
+};
+// bytes to the lane's channel, given anew for each tile: else its 64-bit form is kept, and each row's address is formed in
+// vector registers
+struct Off {
+  uint32_t bytes;
+  template <typename T>
+  __device__ __forceinline__ Off(T, int64_t channel) : bytes((uint32_t)channel * (uint32_t)sizeof(T)) {}
+  __device__ __forceinline__ uint32_t now() {
+    asm volatile("" : "+v"(bytes));
+    return bytes;
   }
 };
 
@@ -191,6 +213,21 @@ struct Rows {
 __device__ __forceinline__ void every_fourth(int i) {
   if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
 }
+
+// The rows of a tile of two tensors, token by token, as they will be used
+template <bool INSIDE, typename T, int STEP, bool LAST>
+__device__ __forceinline__ void load_tile(uint32_t off, Rows<T, STEP, LAST>& p, Raw<T, LAST> (&v)[kGateU], Rows<T, STEP, LAST>& q, Raw<T, LAST> (&w)[kGateU]) {
+#pragma unroll
+  for (int j = 0; j < kGateU; ++j) {
+    const int i = STEP > 0 ? j : kGateU - 1 - j;
+    v[i] = p.template get<INSIDE>(off);
+    w[i] = q.template get<INSIDE>(off);
+    every_fourth(j);
+  }
+}
+// A value that is there before what follows: a loop's first one that was still on its way would be waited for, with all
+// that is, in every round; and one that is needed only later would be formed later, after the loads that follow it.
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 
 struct GateArgs {
   GateShape g;
@@ -265,13 +302,13 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_aggregate(GateArgs 
   const GateSeqs seqs = gate_seqs(a);
   const int64_t T_ = (int64_t)a.g.tokens;
   float p = 1.f, s = 0.f;
-  T g[U], v[U];
+  Raw<T, false> g[U], v[U];
   const int64_t tiles = (l.t_hi - l.t_lo + U - 1) / U, step = BACK ? U : -U;
   int64_t t0 = BACK ? l.t_lo : l.t_lo + (tiles - 1) * U;
-  Rows<T, BACK ? 1 : -1, false> rg(a.g.gate, a.g.gate_token, l.c0, BACK ? t0 : t0 + U - 1, T_),
-      rv(BACK ? a.dh : a.g.x, BACK ? (int64_t)a.g.channels : a.g.x_token, l.c0, BACK ? t0 : t0 + U - 1, T_);
-  rg.load(g);
-  rv.load(v);
+  const int64_t from = BACK ? t0 : t0 + U - 1;
+  Rows<T, BACK ? 1 : -1, false> rg(a.g.gate, a.g.gate_token, from, T_), rv(BACK ? a.dh : a.g.x, BACK ? (int64_t)a.g.channels : a.g.x_token, from, T_);
+  Off off(T{}, l.c0);
+  load_tile<false>(off.now(), rg, g, rv, v);
   GateMarks m;
   m.init(seqs);
   uint32_t none, stop;
@@ -281,23 +318,36 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_aggregate(GateArgs 
     none = m.outside | (n < U ? ~0u << n & (1u << U) - 1 : 0u);
     stop = (BACK ? m.ends : m.starts) | none;
   };
-  const auto token = [&](float c, float b) {
-    if (BACK) p = decayed(c, p);
-    s = fmaf(p, b, s);
-    if (!BACK) p = decayed(c, p);
+  const auto input = [&](const Gate<KIND>& q, int i) { return BACK || KIND == LAPLEX_GATE_RATE ? value_of(v[i]) : q.w * value_of(v[i]); };
+  // a tile, four tokens at a time, whose places the next one's rows take
+  const auto tile = [&](auto inside) {
+    const uint32_t o = off.now();
+#pragma unroll
+    for (int j0 = 0; j0 < U; j0 += 4) {
+#pragma unroll
+      for (int j = j0; j < j0 + 4; ++j) {
+        const int i = BACK ? j : U - 1 - j;
+        const Gate<KIND> q = gate_of<KIND>(value_of(g[i]));
+        const float b = input(q, i);
+        if (BACK) p = decayed(q, p);
+        s = fmaf(p, b, s);
+        if (!BACK) p = decayed(q, p);
+      }
+      settle(p);
+      settle(s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = j0; j < j0 + 4; ++j) {
+        const int i = BACK ? j : U - 1 - j;
+        g[i] = rg.template get<decltype(inside)::value>(o);
+        v[i] = rv.template get<decltype(inside)::value>(o);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  const auto input = [&](const Gate<KIND>& q, int i) { return BACK || KIND == LAPLEX_GATE_RATE ? to_f32(v[i]) : q.w * to_f32(v[i]); };
   marks();
   for (int64_t k = 0; k + 1 < tiles && !stop; ++k) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int i = BACK ? j : U - 1 - j;
-      const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
-      token(q.c, input(q, i));
-      g[i] = rg.get();  // a row of the next tile takes the place of each as it is used
-      v[i] = rv.get();
-      every_fourth(j);
-    }
+    tile(std::integral_constant<bool, !BACK>{});  // (backwards, the next one may be the last)
     t0 += step;
     marks();
   }
@@ -310,9 +360,12 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_aggregate(GateArgs 
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int i = BACK ? j : U - 1 - j;
-    const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
+    const Gate<KIND> q = gate_of<KIND>(value_of(g[i]));
     const float b = input(q, i);
-    token(unless_bit(gone, i, q.c), unless_bit(gone, i, where_bit(bit, i, BACK ? b + w : decayed(q.c, w) + b, b)));
+    const float c = unless_bit(gone, i, q.c), d = unless_bit(gone, i, where_bit(bit, i, BACK ? b + w : decayed(q, w) + b, b));
+    if (BACK) p = decayed(c, p);
+    s = fmaf(p, d, s);
+    if (!BACK) p = decayed(c, p);
   }
   l.store(a, a.agg_c, l.seg, p);
   l.store(a, a.agg_b, l.seg, s);
@@ -327,29 +380,30 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated(GateArgs a) {
   if (!l.valid) return;
   const GateSeqs seqs = gate_seqs(a);
   const int64_t T_ = (int64_t)a.g.tokens;
-  Rows<T, 1, true> rg(a.g.gate, a.g.gate_token, l.c0, l.t_lo, T_), rx(a.g.x, a.g.x_token, l.c0, l.t_lo, T_), rh(a.h, a.g.channels, l.c0, l.t_lo, T_);
-  float s = 0.f;
-  T g[U], x[U];
-  rg.load(g);
-  rx.load(x);
-  if (l.seg) s = l.load(a, a.agg_b, l.seg);
+  Rows<T, 1, true> rg(a.g.gate, a.g.gate_token, l.t_lo, T_), rx(a.g.x, a.g.x_token, l.t_lo, T_), rh(a.h, a.g.channels, l.t_lo, T_);
+  Off off(T{}, l.c0);
+  float s = l.seg ? l.load(a, a.agg_b, l.seg) : 0.f;
+  Raw<T, true> g[U], x[U];
+  load_tile<false>(off.now(), rg, g, rx, x);
+  settle(s);
   pass_empty(a, l, seqs, a.state_in, a.state_out);
   GateMarks m;
   m.init(seqs);
-  const auto input = [&](const Gate<KIND>& q, int i) { return KIND == LAPLEX_GATE_RATE ? to_f32(x[i]) : q.w * to_f32(x[i]); };
+  const auto input = [&](const Gate<KIND>& q, int i) { return KIND == LAPLEX_GATE_RATE ? value_of(x[i]) : q.w * value_of(x[i]); };
   for (int64_t t0 = l.t_lo;; t0 += U) {
-    // tiles without a mark but the last
+    // tiles without a mark but the last, and but one that has the last tokens behind it
     for (;; t0 += U) {
       m.tile(seqs, t0);
       if (a.carries) l.store(a, a.carries, t0 / U, s);
-      if (m.starts | m.ends | m.outside || t0 + U >= l.t_hi) break;
+      if (m.starts | m.ends | m.outside || t0 + U >= l.t_hi || t0 + 2 * U >= T_) break;
+      const uint32_t o = off.now();
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
-        s = decayed(q.c, s) + input(q, i);
-        g[i] = rg.get();  // a row of the next tile takes the place of each as it is used
-        x[i] = rx.get();
-        rh.put(true, s);
+        const Gate<KIND> q = gate_of<KIND>(value_of(g[i]));
+        s = decayed(q, s) + input(q, i);
+        g[i] = rg.template get<true>(o);  // a row of the next tile takes the place of each as it is used
+        x[i] = rx.template get<true>(o);
+        rh.template put<true>(o, true, s);
         every_fourth(i);
       }
     }
@@ -357,7 +411,7 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated(GateArgs a) {
     float c[U], b[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const Gate<KIND> q = gate_of<KIND>(to_f32(g[i]));
+      const Gate<KIND> q = gate_of<KIND>(value_of(g[i]));
       c[i] = q.c;
       b[i] = input(q, i);
     }
@@ -372,7 +426,7 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated(GateArgs a) {
     for (int i = 0; i < U; ++i) {
       s = unless_bit(m.outside, i, decayed(c[i], unless_bit(fresh, i, s)) + b[i]);
       b[i] = s;
-      rh.put(i < n, s);
+      rh.template put<false>(off.bytes, i < n, s);
     }
     if (a.state_out)
       each_marked(m.ends, seqs, t0, [&](int32_t j, uint32_t bit) {
@@ -382,8 +436,7 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated(GateArgs a) {
         l.store(a, a.state_out, j, v);
       });
     if (t0 + U >= l.t_hi) return;
-    rg.load(g);
-    rx.load(x);
+    load_tile<false>(off.now(), rg, g, rx, x);
   }
 }
 
@@ -396,17 +449,24 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back(GateArgs a) {
   if (!l.valid) return;
   const GateSeqs seqs = gate_seqs(a);
   const int64_t T_ = (int64_t)a.g.tokens;
-  float mu = 0.f;
-  T g[U], x[U], y[U];
+  float mu = l.seg + 1 < a.segs ? l.load(a, a.agg_b, l.seg) : 0.f;
+  Raw<T, true> g[U], x[U], y[U];
   int64_t t0 = l.t_lo + (l.t_hi - l.t_lo - 1) / U * U;
   const int64_t from = t0 + U - 1;
-  Rows<T, -1, true> rg(a.g.gate, a.g.gate_token, l.c0, from, T_), rx(a.g.x, a.g.x_token, l.c0, from, T_), rd(a.dh, a.g.channels, l.c0, from, T_),
-      out_g(a.dgate, a.g.channels, l.c0, from, T_), out_x(a.dx, a.g.channels, l.c0, from, T_);
-  rg.load(g);
-  rx.load(x);
-  rd.load(y);
+  Rows<T, -1, true> rg(a.g.gate, a.g.gate_token, from, T_), rx(a.g.x, a.g.x_token, from, T_), rd(a.dh, a.g.channels, from, T_),
+      out_g(a.dgate, a.g.channels, from, T_), out_x(a.dx, a.g.channels, from, T_);
+  Off off(T{}, l.c0);
+  const auto rows = [&](auto inside, uint32_t o) {
+#pragma unroll
+    for (int i = U - 1; i >= 0; --i) {
+      g[i] = rg.template get<decltype(inside)::value>(o);
+      x[i] = rx.template get<decltype(inside)::value>(o);
+      y[i] = rd.template get<decltype(inside)::value>(o);
+    }
+  };
+  rows(std::false_type{}, off.now());
   float before = l.load(a, a.carries_in, t0 / U);
-  if (l.seg + 1 < a.segs) mu = l.load(a, a.agg_b, l.seg);
+  settle(mu);
   pass_empty(a, l, seqs, a.dstate_out, a.dstate_in);
   GateMarks m;
   m.init(seqs);
@@ -417,14 +477,13 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back(GateArgs a) {
     float c[U], hb[U] = {}, xs[U], dh[U], s = before;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      c[i] = to_f32(g[i]);
-      xs[i] = to_f32(x[i]);
-      dh[i] = to_f32(y[i]);
+      c[i] = value_of(g[i]);
+      xs[i] = value_of(x[i]);
+      dh[i] = value_of(y[i]);
     }
+    const uint32_t o = off.now();
     if (t0 > l.t_lo) {
-      rg.load(g);
-      rx.load(x);
-      rd.load(y);
+      rows(std::true_type{}, o);
       before = l.load(a, a.carries_in, t0 / U - 1);
     }
     const uint32_t none = m.outside | (n < U ? ~0u << n : 0u);
@@ -437,7 +496,7 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back(GateArgs a) {
         c[i] = q.c;
         if (!ALL) s = where_bit(m.starts, i, hb[i], s);
         hb[i] = s;
-        s = decayed(q.c, s) + (KIND == LAPLEX_GATE_RATE ? xs[i] : q.w * xs[i]);
+        s = decayed(q, s) + (KIND == LAPLEX_GATE_RATE ? xs[i] : q.w * xs[i]);
       }
 #pragma unroll
       for (int i = U - 1; i >= 0; --i) {
@@ -456,8 +515,8 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back(GateArgs a) {
           dx = unless_bit(none, i, dx);
           dh[i] = mu = unless_bit(none, i, mu);
         }
-        out_g.put(ALL || i < n, dg);
-        out_x.put(ALL || i < n, dx);
+        out_g.template put<ALL>(o, ALL || i < n, dg);
+        out_x.template put<ALL>(o, ALL || i < n, dx);
       }
     };
     if (__builtin_expect(!(m.starts | m.ends | m.outside) && n == U, 1)) {
@@ -488,19 +547,20 @@ __global__ __launch_bounds__(kWave* kGateWaves) void k_gated_back(GateArgs a) {
 
 // ------------------------------------------------------------------ join
 // The segments' aggregates joined in turn: agg_b becomes what comes into each segment from those before it (BACK: after
-// it).  A block takes 16 channels, each of them in 64 stretches at once: a stretch's own aggregate, those of the stretches
-// before it, and then its segments.
-constexpr int kJoinChannels = 16, kJoinParts = 64;
+// it).  A block takes a few channels, each of them in many stretches at once: a stretch's own aggregate, those of the
+// stretches before it joined in steps of 1, 2, 4, ..., and then its segments, which registers hold meanwhile (1024 segments of
+// 256 channels: 8.5 us of what is mostly latency; stretch after stretch, with 8 segments held, 13.3).
+constexpr int kJoinChannels = 16, kJoinParts = 64, kJoinHeld = 16;
 template <bool BACK>
 __global__ __launch_bounds__(kJoinChannels* kJoinParts) void k_gated_join(GateArgs a) {
-  __shared__ float sc[kJoinParts][kJoinChannels], sb[kJoinParts][kJoinChannels];
-  __shared__ uint32_t sr[kJoinParts];
+  __shared__ float sc[2][kJoinParts][kJoinChannels], sb[2][kJoinParts][kJoinChannels];
+  __shared__ uint32_t sr[2][kJoinParts];
   const uint32_t lane = threadIdx.x % kJoinChannels, part = threadIdx.x / kJoinChannels;
   const uint64_t at = (uint64_t)blockIdx.x * kJoinChannels + lane, ch = min(at, (uint64_t)a.g.channels - 1);
   // (nothing comes after the last segment)
   const int32_t n = a.segs - 1, per = (n + kJoinParts - 1) / kJoinParts, lo = min(n, (int32_t)part * per), hi = min(n, lo + per);
   const auto seg = [&](int32_t k) { return (uint32_t)(BACK ? n - k : k); };
-  constexpr int N = 8;  // on their way
+  constexpr int N = kJoinHeld;  // on their way
   float c = 1.f, b = 0.f, vc[N], vb[N];
   uint32_t r = 0, vr[N];
   const auto load = [&](int32_t k) {
@@ -522,12 +582,22 @@ __global__ __launch_bounds__(kJoinChannels* kJoinParts) void k_gated_join(GateAr
         r |= vr[i];
       }
   }
-  sc[part][lane] = c;
-  sb[part][lane] = b;
-  if (lane == 0) sr[part] = r;
-  __syncthreads();
-  float s = 0.f;
-  for (uint32_t q = 0; q < part; ++q) s = sr[q] ? sb[q][lane] : fmaf(sc[q][lane], s, sb[q][lane]);
+  // aggregates of all stretches up to this one
+  int buf = 0;
+#pragma unroll
+  for (int step = 1; step <= kJoinParts; step *= 2, buf ^= 1) {
+    sc[buf][part][lane] = c;
+    sb[buf][part][lane] = b;
+    if (lane == 0) sr[buf][part] = r;
+    __syncthreads();
+    if (step < kJoinParts && part >= (uint32_t)step) {
+      const uint32_t q = part - step;
+      if (!r) b = fmaf(c, sb[buf][q][lane], b);
+      c *= sc[buf][q][lane];
+      r |= sr[buf][q];
+    }
+  }
+  float s = part ? sb[buf ^ 1][part - 1][lane] : 0.f;
   for (int32_t k = lo; k < hi; k += N) {
     if (hi - lo > N) load(k);
 #pragma unroll
@@ -552,7 +622,7 @@ struct GatePlan {
   int64_t seg_len;
 };
 // As many waves as the chip holds at once of the passes with 88 registers (five a SIMD), segments of at least four tiles
-// (16384 tokens x 4096 channels in bfloat16, forward and backward: 351 us; 4096 waves 379, 6144 363, 8192 397).
+// (16384 tokens x 4096 channels in bfloat16, forward and backward: 302 us; 4096 waves 327, 6144 303, 8192 338).
 constexpr uint64_t kGateUnits = 5120, kGateLeast = 64;
 static GatePlan gate_plan(uint32_t channels, uint64_t tokens) {
   GatePlan p;
@@ -659,7 +729,7 @@ __global__ __launch_bounds__(256) void k_gated_step(GateShape g, const int32_t* 
   const Gate<KIND> q = gate_of<KIND>(to_f32(static_cast<const T*>(g.gate)[row * g.gate_token + c]));
   const float x = to_f32(static_cast<const T*>(g.x)[row * g.x_token + c]);
   float* at = state + (uint64_t)slot * g.channels + c;
-  const float s = decayed(q.c, *at) + (KIND == LAPLEX_GATE_RATE ? x : q.w * x);
+  const float s = decayed(q, *at) + (KIND == LAPLEX_GATE_RATE ? x : q.w * x);
   *at = s;
   *out = from_f32<T>(s);
 }
