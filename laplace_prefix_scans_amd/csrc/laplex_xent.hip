@@ -621,6 +621,79 @@ __global__ __launch_bounds__(256) void k_xent_rows(RowsCopies a) {
   }
 }
 
+// ------------------------------------------------------------------ logits of a split product
+// Where tokens and vocabulary are too few tiles for the chip, the logits' products are split over the width, and what follows
+// them is done here, from the parts, which are the only place where logits are in memory (kPartFloats at most).
+struct LogitParts {
+  const float* part;  // [split][N][M]
+  uint32_t splits;
+};
+constexpr int kStretch = 4 * kWave;  // vocabulary entries of a wave
+// The sums of the parts at N places, a part's loads together and four parts' on their way
+template <int N>
+__device__ __forceinline__ void sum_parts(const LogitParts& p, const ProductArgs& a, const uint64_t (&at)[N], float (&x)[N]) {
+  const uint64_t size = (uint64_t)a.N * a.M;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = p.part[at[i]];
+  uint32_t k = 1;
+  for (; k + 4 <= p.splits; k += 4) {
+    float y[4][N];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[q][i] = p.part[(k + q) * size + at[i]];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += y[q][i];
+  }
+  for (; k < p.splits; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += p.part[k * size + at[i]];
+}
+// A wave's token and stretch of the vocabulary: maximum and sum, in the place of a tile's.
+__global__ __launch_bounds__(256) void k_xent_parts_stats(ProductArgs a, LogitParts p) {
+  const uint32_t stretches = (a.M + kStretch - 1) / kStretch, unit = blockIdx.x * 4 + threadIdx.x / kWave;
+  const uint32_t t = unit / stretches, c = unit % stretches, lane = lane_id();
+  if (t >= a.N) return;
+  const int64_t y = target_of(a.targets, a.id_bytes, t);
+  float l[4], m = -INFINITY, s = 0.f;
+  uint64_t at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) at[i] = (uint64_t)t * a.M + min(c * kStretch + i * kWave + lane, a.M - 1);
+  sum_parts(p, a, at, l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = c * kStretch + i * kWave + lane;
+    l[i] = v < a.M ? a.scale * l[i] : -INFINITY;
+    if ((int64_t)v == y && v < a.M) a.hit[t] = l[i];
+    m = fmaxf(m, l[i]);
+  }
+#pragma unroll
+  for (int off = 32; off; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c * kStretch + i * kWave + lane < a.M) s += exp_below(l[i], m);
+  s = wave_sum(s);
+  if (lane == 0) a.stats[(uint64_t)c * a.N + t] = make_float2(m, s);
+}
+template <typename T>
+__global__ __launch_bounds__(256) void k_xent_parts_grad(ProductArgs a, LogitParts p) {
+  const uint64_t n = (uint64_t)a.n_fill * a.m_fill, stride = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
+    const uint32_t t = (uint32_t)(i / a.m_fill), v = (uint32_t)(i % a.m_fill);
+    float x[1] = {};
+    if (t < a.N && v < a.M && live(a, t)) {
+      const uint64_t at[1] = {(uint64_t)t * a.M + v};
+      sum_parts(p, a, at, x);
+      const float d = a.scale * a.dloss[t], f = a.dlse ? d + a.scale * a.dlse[t] : d;
+      x[0] = f * exp_of(fmaf(x[0], a.scale, -a.lse[t]));
+      if ((int64_t)a.v0 + v == target_of(a.targets, a.id_bytes, t)) x[0] -= d;
+    }
+    static_cast<T*>(a.G)[(uint64_t)t * a.ldg + v] = from_f32<T>(x[0]);
+  }
+}
+
 // ------------------------------------------------------------------ joins
 // lse and loss of each token from its tiles' maxima and sums: TOKENS of them a block, 256 / TOKENS threads each
 template <int TOKENS>
@@ -692,6 +765,10 @@ static XentPlan xent_plan(int dtype, uint64_t tokens, uint32_t vocab, uint32_t w
   return p;
 }
 
+// Blocks of k_xent_few: one turn of rows a wave at least (4 tokens, 2418 x 1770 in float: 18 us; with four turns 37), and at
+// most four a CU (1 token, 65536 x 2048 in bfloat16: 57.5 us; eight 60).
+static uint32_t few_blocks(uint32_t vocab) { return std::min(1024u, (vocab + 4 * kFewRows - 1) / (4 * kFewRows)); }
+
 // ------------------------------------------------------------------ tiles and splits of a product
 // By a model of its time: rounds of blocks over the CUs, each at the rate that its tile reaches, and for a split product the
 // pass that adds the parts.  Rates, in 10^6 operations a us and CU, are those of large products (bfloat16 16384 x 65536 x 2048:
@@ -707,14 +784,14 @@ static double rate_of(bool bf, int tile) {
   return bf ? b[tile] : f[tile];
 }
 // partial sums of a split product, in floats
-constexpr uint64_t kPartFloats = 8ull << 20;
+constexpr uint64_t kPartFloats = 8ull << 20, kMostSplits = 64;
 static Tiling tiling(bool bf, uint64_t M, uint64_t N, uint64_t K, bool may_split) {
   const uint64_t bk = kPieceK / (bf ? 2 : 4), steps = std::max<uint64_t>(1, K / bk);
   Tiling best{TILE_S, 1};
   double least = 1e300;
   for (int t = TILE_L; t <= TILE_T; ++t) {
     const uint64_t blocks = tiles(M, kTileM[t]) * (uint64_t)tiles(N, kTileN[t]);
-    for (uint64_t s = 1; s <= 64; s *= 2) {
+    for (uint64_t s = 1; s <= kMostSplits; s *= 2) {
       if (s > 1 && (!may_split || s * 4 > steps || s * M * N > kPartFloats)) break;
       const double work = 2e-6 * kTileM[t] * kTileN[t] * (double)((steps + s - 1) / s * bk);
       const double us = (double)((blocks * s + 255) / 256) * work / rate_of(bf, t) + (s > 1 ? 4.0 + s * M * N * 8e-6 / 4.0 : 0.0) + 2.0;
@@ -744,8 +821,10 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
   w.x_rows = c.take<void>(p.k_tokens * p.k_width * e);
   w.table_rows = c.take<void>(vocab * p.k_width * e);
   if (pass == 0) {
-    w.stats = c.take<float2>((uint64_t)tiles(vocab, TileS::BM) * tokens * 8);  // (of the smallest tiles)
+    // (of the smallest tiles, or of a few tokens' blocks)
+    w.stats = c.take<float2>(std::max<uint64_t>(tiles(vocab, TileS::BM) * tokens, few_blocks(vocab) * std::min<uint64_t>(tokens, kFewTokens)) * 8);
     w.hit = c.take<float>(tokens * 4);
+    w.part = c.take<float>(std::min<uint64_t>(kPartFloats, kMostSplits * tokens * vocab) * 4);
   } else {
     // (a piece has at most kPiece bytes, or one tile of the vocabulary, or all of it)
     const uint64_t bk = kPieceK / e, g = std::max<uint64_t>(std::min<uint64_t>(kPiece, up(vocab, bk) * p.k_tokens * e), kTile * p.k_tokens * e);
@@ -762,7 +841,7 @@ size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t
   return total;
 }
 
-enum Product { LOGITS_STATS, LOGITS_GRAD, DX, DTABLE };
+enum Product { LOGITS_STATS, LOGITS_GRAD, LOGITS_PARTS, DX, DTABLE };
 template <typename T, typename C>
 static hipError_t product_of(const char* name, Product epi, ProductArgs& a, hipStream_t s) {
   a.tiles_m = tiles(a.M, C::BM);
@@ -771,6 +850,7 @@ static hipError_t product_of(const char* name, Product epi, ProductArgs& a, hipS
   LAPLEX_LAUNCH(name, all, s, {
     if (epi == LOGITS_STATS) k_product<T, XENT_STATS, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
     else if (epi == LOGITS_GRAD) k_product<T, XENT_GRAD, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
+    else if (epi == LOGITS_PARTS) k_product<T, XENT_OUT, C, false, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
     else if (epi == DX) k_product<T, XENT_OUT, C, true, false><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
     else k_product<T, XENT_OUT, C, true, true><<<(unsigned)blocks, C::THREADS, 0, s>>>(a);
   });
@@ -814,7 +894,7 @@ static hipError_t few(ProductArgs& a, uint32_t width, hipStream_t s) {
   if constexpr (N > 1)
     if (a.N <= N / 2) return few<T, N / 2>(a, width, s);
   const uint32_t fill = (uint32_t)up(width, kWave * 16 / sizeof(T)), bytes = N * fill * (uint32_t)sizeof(T);
-  const uint32_t blocks = std::min(tiles(a.M, TileS::BM), (a.M + 4 * kFewRows - 1) / (4 * kFewRows));
+  const uint32_t blocks = few_blocks(a.M);
   if (bytes > (48u << 10)) {
     const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(k_xent_few<T, N>), hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewBytes);
     if (err != hipSuccess) return err;
@@ -822,6 +902,23 @@ static hipError_t few(ProductArgs& a, uint32_t width, hipStream_t s) {
   LAPLEX_LAUNCH("k_xent_few", a.M, s, k_xent_few<T, N><<<blocks, 256, bytes, s>>>(a, width, fill));
   a.tiles_m = blocks;
   return hipGetLastError();
+}
+// Whether the logits' product is better split, and how it is tiled
+template <typename T>
+static bool in_parts(const ProductArgs& l, uint64_t n_tiles, Tiling& t) {
+  t = tiling(sizeof(T) == 2, l.M, n_tiles, l.K, true);
+  return t.splits > 1;
+}
+template <typename T>
+static hipError_t logit_parts(const ProductArgs& l, const Tiling& t, float* part, LogitParts& p, hipStream_t s) {
+  ProductArgs a = l;
+  a.out = part;
+  a.out_f32 = true;
+  a.ldo = a.M;
+  a.out_split = (int64_t)a.N * a.M;
+  const hipError_t err = product<T>("k_product_logits", LOGITS_PARTS, a, t, s);
+  p = {part, a.splits};
+  return err;
 }
 template <typename T>
 static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws, hipStream_t s) {
@@ -846,7 +943,16 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
     if ((err = whole<T>(x, p, w, false, &a.B, &a.A, s)) != hipSuccess) return err;
     a.lda = a.ldb = (int64_t)p.k_width;
     a.K = p.k_width;
-    if ((err = product<T>("k_product_stats", LOGITS_STATS, a, tiling(sizeof(T) == 2, a.M, a.N, a.K, false), s)) != hipSuccess) return err;
+    Tiling t;
+    if (in_parts<T>(a, a.N, t)) {
+      LogitParts parts;
+      if ((err = logit_parts<T>(a, t, w.part, parts, s)) != hipSuccess) return err;
+      a.tiles_m = tiles(a.M, kStretch);
+      LAPLEX_LAUNCH("k_xent_parts_stats", a.N, s, k_xent_parts_stats<<<(unsigned)((x.tokens * a.tiles_m + 3) / 4), 256, 0, s>>>(a, parts));
+      if ((err = hipGetLastError()) != hipSuccess) return err;
+    } else if ((err = product<T>("k_product_stats", LOGITS_STATS, a, t, s)) != hipSuccess) {
+      return err;
+    }
   }
   LAPLEX_LAUNCH("k_xent_join", x.tokens, s, {
     if (x.tokens <= 64) k_xent_join<1><<<(unsigned)x.tokens, 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse);
@@ -909,7 +1015,16 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
     l.v0 = v0;
     l.ldg = (int64_t)fill;
     l.m_fill = (uint32_t)fill;
-    if (tokens && (err = product<T>("k_product_grad", LOGITS_GRAD, l, tiling(sizeof(T) == 2, l.M, l.n_fill, l.K, false), s)) != hipSuccess) return err;
+    Tiling t;
+    if (tokens && in_parts<T>(l, l.n_fill, t)) {
+      LogitParts parts;
+      if ((err = logit_parts<T>(l, t, w.part, parts, s)) != hipSuccess) return err;
+      const uint64_t all = (uint64_t)l.n_fill * l.m_fill;
+      LAPLEX_LAUNCH("k_xent_parts_grad", l.N, s, k_xent_parts_grad<T><<<some_blocks(all), 256, 0, s>>>(l, parts));
+      if ((err = hipGetLastError()) != hipSuccess) return err;
+    } else if (tokens && (err = product<T>("k_product_grad", LOGITS_GRAD, l, t, s)) != hipSuccess) {
+      return err;
+    }
     if (dx) {
       ProductArgs a{};
       a.A = l.A;
