@@ -771,21 +771,25 @@ static uint32_t few_blocks(uint32_t vocab) { return std::min(1024u, (vocab + 4 *
 
 // ------------------------------------------------------------------ tiles and splits of a product
 // By a model of its time: rounds of blocks over the CUs, each at the rate that its tile reaches, and for a split product the
-// pass that adds the parts.  Rates, in 10^6 operations a us and CU, are those of large products (bfloat16 16384 x 65536 x 2048:
-// 1330, 780 and 400 TFLOP/s by 256, 128 and 64 wide tiles; float 145, 140, 120).
+// pass that adds the parts.  Rates, in 10^6 operations a us and CU, are those of large products with one tile for all of them:
+// 16384 x 16384 x 2048 in bfloat16, forward (along k) 1371, 974, 716 and 443 TFLOP/s by tiles L, M, S and T, with the
+// backward (a third of it along k, the rest across) 1266, 974, 550 and 284; 4096 x 16384 x 1024 in float 147, 140, 138 and 129, and
+// 106, 136, 135 and 124.  A step takes kStepLeast us however little there is to do in it (32 tokens, 2000 x 2048 in bfloat16: the
+// forward unsplit 12.5 us, split 11.5; the backward 31.7 and 26.8).
 struct Tiling {
   int tile;         // TILE_L .. TILE_T
   uint32_t splits;  // of k
 };
 enum { TILE_L, TILE_M, TILE_S, TILE_T };
 constexpr uint32_t kTileM[] = {TileL::BM, TileM::BM, TileS::BM, TileT::BM}, kTileN[] = {TileL::BN, TileM::BN, TileS::BN, TileT::BN};
-static double rate_of(bool bf, int tile) {
-  const double b[] = {5.2, 3.0, 1.6, 1.0}, f[] = {.57, .55, .47, .47};
-  return bf ? b[tile] : f[tile];
+static double rate_of(bool bf, bool across, int tile) {
+  const double rates[2][2][4] = {{{.57, .55, .54, .50}, {.41, .53, .53, .48}}, {{5.4, 3.8, 2.8, 1.7}, {4.9, 3.8, 2.1, 1.1}}};
+  return rates[bf][across][tile];
 }
 // partial sums of a split product, in floats
 constexpr uint64_t kPartFloats = 8ull << 20, kMostSplits = 64;
-static Tiling tiling(bool bf, uint64_t M, uint64_t N, uint64_t K, bool may_split) {
+constexpr double kStepLeast = 0.25;
+static Tiling tiling(bool bf, bool across, uint64_t M, uint64_t N, uint64_t K, bool may_split) {
   const uint64_t bk = kPieceK / (bf ? 2 : 4), steps = std::max<uint64_t>(1, K / bk);
   Tiling best{TILE_S, 1};
   double least = 1e300;
@@ -793,8 +797,9 @@ static Tiling tiling(bool bf, uint64_t M, uint64_t N, uint64_t K, bool may_split
     const uint64_t blocks = tiles(M, kTileM[t]) * (uint64_t)tiles(N, kTileN[t]);
     for (uint64_t s = 1; s <= kMostSplits; s *= 2) {
       if (s > 1 && (!may_split || s * 4 > steps || s * M * N > kPartFloats)) break;
-      const double work = 2e-6 * kTileM[t] * kTileN[t] * (double)((steps + s - 1) / s * bk);
-      const double us = (double)((blocks * s + 255) / 256) * work / rate_of(bf, t) + (s > 1 ? 4.0 + s * M * N * 8e-6 / 4.0 : 0.0) + 2.0;
+      const double step = 2e-6 * kTileM[t] * kTileN[t] * bk / rate_of(bf, across, t);
+      const double us = (double)((steps + s - 1) / s) * std::max((double)((blocks * s + 255) / 256) * step, kStepLeast) +
+                        (s > 1 ? 4.0 + s * M * N * 8e-6 / 4.0 : 0.0) + 2.0;
       if (us < least) {
         least = us;
         best = {t, (uint32_t)s};
@@ -906,7 +911,7 @@ static hipError_t few(ProductArgs& a, uint32_t width, hipStream_t s) {
 // Whether the logits' product is better split, and how it is tiled
 template <typename T>
 static bool in_parts(const ProductArgs& l, uint64_t n_tiles, Tiling& t) {
-  t = tiling(sizeof(T) == 2, l.M, n_tiles, l.K, true);
+  t = tiling(sizeof(T) == 2, false, l.M, n_tiles, l.K, true);
   return t.splits > 1;
 }
 template <typename T>
@@ -990,7 +995,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   l.n_fill = (uint32_t)p.k_tokens;
   // A product that may be split: to its place, or its parts and then their sum
   const auto output = [&](const char* name, Product epi, ProductArgs& a) {
-    const Tiling t = tiling(sizeof(T) == 2, a.M, a.N, a.K, !a.add);
+    const Tiling t = tiling(sizeof(T) == 2, true, a.M, a.N, a.K, !a.add);
     if (t.splits == 1) return product<T>(name, epi, a, t, s);
     void* const out = a.out;
     const bool f32 = a.out_f32;
