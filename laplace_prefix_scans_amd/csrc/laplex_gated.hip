@@ -129,7 +129,7 @@ struct GateMarks {
       const bool real = j <= s.seqs;
       const int64_t o = real ? s.at(j) : INT64_MAX;
       if (real && o <= t0 + U) {
-        if (o < t0 + U && j < s.seqs && s.at(j + 1) > o) m |= 1u << (o - t0);
+        if (o >= t0 && o < t0 + U && j < s.seqs && s.at(j + 1) > o) m |= 1u << (o - t0);  // (offsets need not ascend)
         if (o > t0 && j > 0 && s.at(j - 1) < o) m |= 0x10000u << (o - 1 - t0);
       }
       const uint64_t beyond = __ballot(real && o > t0 + U);

@@ -493,10 +493,11 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
 }
 
 // ------------------------------------------------------------------ few tokens
-// The statistics where the table's bytes are all that counts: at most 8 tokens, whose rows lie in LDS.  A wave takes four
-// rows of the table at a time as they lie, 1024 bytes a load, and a block joins its waves' maxima and sums.  (1 token, 65536 x
-// 2048 in bfloat16: by the tiles of a product 76 us.)
-constexpr int kFewTokens = 8, kFewRows = 4;
+// The statistics where the table's bytes are all that counts: at most 4 tokens, whose rows lie in LDS.  A wave takes four
+// rows of the table at a time as they lie, 1024 bytes a load, and a block joins its waves' maxima and sums.  Up to 2 tokens
+// where a product reads rows as they lie too (65536 x 2048 in bfloat16, 1 token: 57 us, by a product's tiles 67; 2000 x 1024, 2 tokens:
+// 9.5 and 10.0, 3: 12.8 and 10.1), up to 4 where it would have to copy them (15167 x 442 in float, 4 tokens: 15 and 26 us, 8: 33 and 27).
+constexpr int kFewTokens = 4, kFewTokensWhole = 2, kFewRows = 4;
 constexpr uint32_t kFewBytes = 128 << 10;  // of tokens in LDS
 template <typename T, int N>
 __global__ __launch_bounds__(256) void k_xent_few(ProductArgs a, uint32_t width, uint32_t fill) {
@@ -746,7 +747,8 @@ __global__ __launch_bounds__(256) void k_xent_sum(const float* __restrict__ part
 
 // ------------------------------------------------------------------ plan
 constexpr uint32_t kTile = 128;
-constexpr uint64_t kPiece = 1ull << 30;  // bytes of G
+// bytes of G (16384 tokens, 65536 x 2048 in bfloat16: 13394 us; twice as many 13604, half 13826)
+constexpr uint64_t kPiece = 1ull << 29;
 static uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + of - 1) / of); }
 
@@ -942,7 +944,7 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   a.stats = w.stats;
   a.hit = w.hit;
   hipError_t err;
-  if (x.tokens <= kFewTokens && kFewTokens * up(x.width, kWave * 16 / sizeof(T)) * sizeof(T) <= kFewBytes) {
+  if (x.tokens <= (x.width * sizeof(T) % kPieceK ? kFewTokens : kFewTokensWhole) && kFewTokens * up(x.width, kWave * 16 / sizeof(T)) * sizeof(T) <= kFewBytes) {
     if ((err = few<T>(a, x.width, s)) != hipSuccess) return err;
   } else {
     if ((err = whole<T>(x, p, w, false, &a.B, &a.A, s)) != hipSuccess) return err;

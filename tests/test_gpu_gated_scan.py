@@ -312,3 +312,26 @@ def test_as_many_tokens_as_offsets_can_name():
     want = -a * want * want
     tol = 3 * tol * abs(want)
     assert abs(float(settled.max()) - want) <= tol and abs(float(settled.min()) - want) <= tol and float(dgate[0]) == 0.0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_offsets_outside_the_tokens_touch_nothing_else(dt):
+    """Offsets that are not ascending, negative or past the tokens: whatever they give, it stays inside the call's tensors."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    dtype = dtype_of(dt)
+    tokens, channels, guard = 300, 70, 1 << 16
+    g = torch.Generator().manual_seed(0)
+    gate, x, dh = (torch.randn(tokens, channels, generator=g).to(dtype).cuda() for _ in range(3))
+    for bad in ([0, 100, 50, 300], [-40, 20, 20, 290], [0, 10, 400, 70000], [2 ** 31 - 1, 0, 5, 300], [300, 200, 100, 0], [-5, -4, -3, -2]):
+        offsets = torch.tensor(bad, dtype=torch.int32).cuda()
+        whole = torch.full((guard + 3 * channels + guard,), 7.0, device="cuda")
+        state_out = whole[guard:guard + 3 * channels].view(3, channels)
+        buf = torch.full((guard + tokens * channels + guard,), 7.0, dtype=dtype, device="cuda")
+        state_in = torch.ones(3, channels, device="cuda")
+        h, carries = lp.laplex_gated_scan(gate, x, "sigmoid", offsets=offsets, state_in=state_in, state_out=state_out, keep=True,
+                                          h=buf[guard:guard + tokens * channels].view(tokens, channels))
+        lp.laplex_gated_scan_backward(gate, x, carries, dh, "sigmoid", offsets=offsets, state_in=state_in)
+        torch.cuda.synchronize()
+        for t, n in ((whole, 3 * channels), (buf, tokens * channels)):
+            assert (t[:guard] == 7).all() and (t[guard + n:] == 7).all(), bad
