@@ -60,6 +60,7 @@ struct ProductArgs {
   const float *lse, *dloss, *dlse;
   void* G;           // [token][ldg]
   int64_t ldg;
+  int64_t rest;      // bytes from G (XENT_OUT: B) to a second part of it, what its rounding left out; 0: there is none
   uint32_t n_fill, m_fill;  // rows and columns that are written, zeros from N and M on
   // XENT_OUT
   void* out;         // [N][ldo], of type out_f32 ? float : T; splits of out_f32 follow each other
@@ -236,11 +237,15 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
   uint32_t off[C::LOADS], tm, tn, split;
   const char *base_a, *base_b;
   uint64_t k0;
-  int steps, first = 0;  // `first`: the buffer of step 0
+  int steps, turn, first = 0;  // steps of one part of B; the buffer of step 0
   const auto choose = [&] {
     tile_of(a, id, tm, tn, split);
     k0 = split * a.k_split;
     steps = (int)((min(a.K, k0 + a.k_split) - k0) / BK);
+    if (EPI == XENT_OUT) {
+      turn = steps;
+      if (a.rest) steps *= 2;
+    }
     base_a = static_cast<const char*>(a.A) + (A_ALONG ? (int64_t)k0 * row_a + (int64_t)tm * BM * sizeof(T) : (int64_t)tm * BM * row_a + (int64_t)k0 * sizeof(T));
     base_b = static_cast<const char*>(a.B) + (B_ALONG ? (int64_t)k0 * row_b + (int64_t)tn * BN * sizeof(T) : (int64_t)tn * BN * row_b + (int64_t)k0 * sizeof(T));
 #pragma unroll
@@ -262,8 +267,13 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
   };
   auto load = [&](int step) {
     const uint32_t to = to0 + ((first + step) & 1) * C::STEP_BYTES;
+    const char* from_b = base_b;
+    if (EPI == XENT_OUT && step >= turn) {  // B's second part, by the same rows of A
+      step -= turn;
+      from_b += a.rest;
+    }
     uint64_t p, q;
-    share(base_a + step * next_a, base_b + step * next_b, p, q);
+    share(base_a + step * next_a, from_b + step * next_b, p, q);
     if (A_ALONG && k0 + (uint64_t)(step + 1) * BK > a.k_rows) {  // the last step has rows beyond the last: that one again
       const int rows = (int)((int64_t)a.k_rows - (int64_t)(k0 + (uint64_t)step * BK));
 #pragma unroll
@@ -437,7 +447,7 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
           const auto column = [&](auto plain) {  // without a target, inside the vocabulary
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-              T g[4];
+              T g[4], left[4];
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 float x = f * exp_of(fmaf(acc[i][j][r], a.scale, -lse));
@@ -446,9 +456,13 @@ __global__ __launch_bounds__(C::THREADS) void k_product(ProductArgs a) {
                   if (m0 + i * 16 + r >= a.M) x = 0.f;
                 }
                 g[r] = from_f32<T>(in ? x : 0.f);
+                left[r] = from_f32<T>((in ? x : 0.f) - to_f32(g[r]));
               }
               const uint32_t v = m0 + i * 16;
-              if (t < a.n_fill && (decltype(plain)::value || v < a.m_fill)) __builtin_memcpy(row + v, g, sizeof g);
+              if (t < a.n_fill && (decltype(plain)::value || v < a.m_fill)) {
+                __builtin_memcpy(row + v, g, sizeof g);
+                if (a.rest) __builtin_memcpy(reinterpret_cast<char*>(row + v) + a.rest, left, sizeof left);
+              }
             }
           };
           if (whole && !__any(hit >= 0)) column(std::true_type{});
@@ -693,7 +707,9 @@ __global__ __launch_bounds__(256) void k_xent_parts_grad(ProductArgs a, LogitPar
       x[0] = f * exp_of(fmaf(x[0], a.scale, -a.lse[t]));
       if ((int64_t)a.v0 + v == target_of(a.targets, a.id_bytes, t)) x[0] -= d;
     }
-    static_cast<T*>(a.G)[(uint64_t)t * a.ldg + v] = from_f32<T>(x[0]);
+    T* const to = static_cast<T*>(a.G) + (uint64_t)t * a.ldg + v;
+    *to = from_f32<T>(x[0]);
+    if (a.rest) *reinterpret_cast<T*>(reinterpret_cast<char*>(to) + a.rest) = from_f32<T>(x[0] - to_f32(*to));
   }
 }
 
@@ -755,8 +771,14 @@ static uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + of - 1) / of); }
 
 // Sizes that a call with this many tokens keeps in its workspace; each grows with the tokens.
+// G in two parts of bfloat16, which hold 16 of its bits, for so many tokens: half a step of the one that a token's row of dx
+// is mostly made of shows in the row, and among few tokens in the whole (11 tokens, 227 x 2696: dx off by 0.0030 of its size, with
+// two parts 0.0017, which is its own rounding; the backward of 200 tokens, 500 x 4096 takes 33 us instead of 26, of 64, 65536 x 2048 404
+// instead of 278).  Among more it is 0.0024, and the products that the matrix cores bound would be six instead of four.
+constexpr uint64_t kTwoParts = 512;
 struct XentPlan {
   uint64_t k_width, k_tokens;  // extents of k, whole pieces
+  uint32_t parts;              // of G
   uint32_t piece;              // vocabulary entries at a time
 };
 static XentPlan xent_plan(int dtype, uint64_t tokens, uint32_t vocab, uint32_t width) {
@@ -764,7 +786,8 @@ static XentPlan xent_plan(int dtype, uint64_t tokens, uint32_t vocab, uint32_t w
   XentPlan p;
   p.k_width = up(width, bk);
   p.k_tokens = up(tokens, bk);
-  const uint64_t fit = kPiece / (e * std::max<uint64_t>(p.k_tokens, 1)) / kTile * kTile;
+  p.parts = dtype == LAPLEX_BF16 && tokens <= kTwoParts ? 2 : 1;
+  const uint64_t fit = kPiece / (e * p.parts * std::max<uint64_t>(p.k_tokens, 1)) / kTile * kTile;
   p.piece = (uint32_t)std::min<uint64_t>(up(vocab, bk), std::max<uint64_t>(kTile, fit));
   return p;
 }
@@ -836,8 +859,11 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
     w.part = c.take<float>(std::min<uint64_t>(kPartFloats, kMostSplits * tokens * vocab) * 4);
   } else {
     // (a piece has at most kPiece bytes, or one tile of the vocabulary, or all of it)
-    const uint64_t bk = kPieceK / e, g = std::max<uint64_t>(std::min<uint64_t>(kPiece, up(vocab, bk) * p.k_tokens * e), kTile * p.k_tokens * e);
-    w.G = c.take<void>(g);
+    const uint64_t bk = kPieceK / e;
+    const auto g = [&](uint64_t rows) { return std::max<uint64_t>(std::min<uint64_t>(kPiece, up(vocab, bk) * rows * e), kTile * rows * e); };
+    // (of more tokens' one part, or those at the switch, of which there are two)
+    const uint64_t two = dtype == LAPLEX_BF16 ? up(std::min(tokens, kTwoParts), bk) * 2 : 0;
+    w.G = c.take<void>(std::max(g(p.k_tokens), g(two)));
     w.dx = c.take<float>(tokens * width * 4);
     w.part = c.take<float>(kPartFloats * 4);
   }
@@ -921,6 +947,7 @@ static bool in_parts(const ProductArgs& l, uint64_t n_tiles, Tiling& t) {
 template <typename T>
 static hipError_t logit_parts(const ProductArgs& l, const Tiling& t, float* part, LogitParts& p, hipStream_t s) {
   ProductArgs a = l;
+  a.rest = 0;
   a.out = part;
   a.out_f32 = true;
   a.ldo = a.M;
@@ -999,7 +1026,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   l.n_fill = (uint32_t)p.k_tokens;
   // A product that may be split: to its place, or its parts and then their sum
   const auto output = [&](const char* name, Product epi, ProductArgs& a) {
-    const Tiling t = tiling(sizeof(T) == 2, true, a.M, a.N, a.K, !a.add);
+    const Tiling t = tiling(sizeof(T) == 2, true, a.M, a.N, a.K * p.parts, !a.add);
     if (t.splits == 1) return product<T>(name, epi, a, t, s);
     void* const out = a.out;
     const bool f32 = a.out_f32;
@@ -1024,6 +1051,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
     l.v0 = v0;
     l.ldg = (int64_t)fill;
     l.m_fill = (uint32_t)fill;
+    l.rest = p.parts > 1 ? (int64_t)(p.k_tokens * fill * sizeof(T)) : 0;
     Tiling t;
     if (tokens && in_parts<T>(l, l.n_fill, t)) {
       LogitParts parts;
@@ -1040,6 +1068,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
       a.lda = l.lda;
       a.B = w.G;
       a.ldb = (int64_t)fill;
+      a.rest = l.rest;
       a.K = fill;
       a.k_rows = n;
       a.M = x.width;
@@ -1060,6 +1089,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
       a.lda = (int64_t)p.k_width;
       a.B = w.G;
       a.ldb = (int64_t)fill;
+      a.rest = l.rest;
       a.K = a.k_rows = p.k_tokens;
       a.M = x.width;
       a.N = n;

@@ -354,3 +354,45 @@ def test_a_repeated_call_gives_the_same_bits(dims, dt):
     first = both()
     for _ in range(3):
         assert all(torch.equal(p, q) for p, q in zip(both(), first))
+
+
+# ------------------------------------------------------------------ the gradient's factor in two parts
+@pytest.mark.parametrize("dims", [(1, 300, 100), (11, 227, 2696), (64, 65, 64), (100, 9001, 72), (512, 700, 130)], ids=str)
+def test_gradients_of_few_tokens_are_off_by_their_own_rounding(dims):
+    """In bfloat16: the factor G is held in two parts, whose second is off by half a step (2^-8) of what the first left
+    out (2^-8 of G at most): 2^-16 of G, 2^-8 of what train_ref.cross_entropy allows for one part."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    x = make(*dims, torch.bfloat16, seed=7)
+    c = {k: v.cuda() for k, v in x.items()}
+    _, lse = lp.laplex_linear_cross_entropy(c["x"], c["table"], c["y"])
+    dx, dtable = lp.laplex_linear_cross_entropy_backward(c["x"], c["table"], c["y"], lse, c["dloss"], c["dlse"])
+    npf = {k: v.float().numpy() if v.is_floating_point() else v.numpy() for k, v in x.items()}
+    one, none = (ref.cross_entropy(npf["x"], npf["table"], npf["y"], 1.0, npf["dloss"], npf["dlse"], b) for b in (True, False))
+    for name, got in (("dx", dx), ("dtable", dtable)):
+        exact = none["~" + name]
+        check(name, got, none[name], exact + 2.0 ** -8 * (one["~" + name] - exact), True)
+
+
+def test_two_parts_of_a_vocabulary_in_pieces():
+    """As many tokens as have two parts, and a vocabulary of two pieces: against float64 on the GPU."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    tokens, vocab, width = 512, 270001, 8
+    x = {k: v.cuda() for k, v in make(tokens, vocab, width, torch.bfloat16, seed=1).items()}
+    _, lse = lp.laplex_linear_cross_entropy(x["x"], x["table"], x["y"])
+    dx, dtable = lp.laplex_linear_cross_entropy_backward(x["x"], x["table"], x["y"], lse, x["dloss"], dtype=torch.float32)
+    inside = (x["y"] >= 0) & (x["y"] < vocab)
+    logits = x["x"].double() @ x["table"].double().t()
+    want = torch.logsumexp(logits, 1)
+    assert ((lse.double() - want)[inside].abs() < 2e-5).all()
+    d = torch.where(inside, x["dloss"], 0.0).double()[:, None]
+    p = torch.softmax(logits, 1) * d
+    # errors of a logit, of the lse (2e-5, above) and of the exponential, as in train_ref.cross_entropy
+    e = p.abs() * ((8.0 ** 0.5 * 8 + 4) * ref.U * (x["x"].double().abs() @ x["table"].double().abs().t()) + 2e-5 + 8 * ref.U
+                   + 3 * ref.U * (logits - want[:, None]).abs())
+    p[torch.arange(tokens, device="cuda"), x["y"].clamp(0, vocab - 1)] -= d[:, 0]
+    e += (2.0 ** -16 + 2 * ref.U) * p.abs()
+    for got, half, w, off, size, n in ((dx, 2.0 ** -8, p @ x["table"].double(), e @ x["table"].double().abs(), p.abs() @ x["table"].double().abs(), vocab),
+                                       (dtable, 2.0 ** -24, p.t() @ x["x"].double(), e.t() @ x["x"].double().abs(), p.abs().t() @ x["x"].double().abs(), tokens)):
+        assert ((got.double() - w).abs() <= half * w.abs() + off + 8 * n ** 0.5 * ref.U * size + 1e-30).all()
