@@ -774,8 +774,9 @@ static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + 
 // G in two parts of bfloat16, which hold 16 of its bits, for so many tokens: half a step of the one that a token's row of dx
 // is mostly made of shows in the row, and among few tokens in the whole (11 tokens, 227 x 2696: dx off by 0.0030 of its size, with
 // two parts 0.0017, which is its own rounding; the backward of 200 tokens, 500 x 4096 takes 33 us instead of 26, of 64, 65536 x 2048 404
-// instead of 278).  Among more it is 0.0024, and the products that the matrix cores bound would be six instead of four.
-constexpr uint64_t kTwoParts = 512;
+// instead of 278, of 1000, 8000 x 1024 128 instead of 90).  Among 600 it still is up to 1.5 times its own rounding, among more 0.0024 and no more than that, where the
+// products, which the matrix cores bound, would be six instead of four.
+constexpr uint64_t kTwoParts = 2048;
 struct XentPlan {
   uint64_t k_width, k_tokens;  // extents of k, whole pieces
   uint32_t parts;              // of G
