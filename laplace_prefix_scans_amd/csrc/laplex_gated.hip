@@ -59,7 +59,7 @@ __device__ __forceinline__ Gate<KIND> gate_of(float g) {
     const float q = g < 0.3f ? g * p : 1.f - e;
     r.w = 1.f;
     r.near = g >= 0.f && q <= 0.5f;
-    r.c = r.near ? -q : e;
+    r.c = r.near ? -fabsf(q) : e;  // (a rate of -0.0 has a distance of -0.0, which would lose the mark)
   } else {
     const float e = __builtin_amdgcn_exp2f(-fabsf(g) * kLog2e);
     const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
