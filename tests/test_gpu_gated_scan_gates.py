@@ -1,4 +1,5 @@
-"""The gated linear recurrence at gates that are easy to get wrong: rates of minus zero and of zero, and gates that are NaN."""
+"""The gated linear recurrence at gates that are easy to get wrong: rates of minus zero and of zero, gates that are NaN, and
+decays far from 1, whose exponentials have to keep their bits."""
 import numpy as np
 import pytest
 
@@ -101,3 +102,53 @@ def test_gates_that_are_nan_stay_in_their_sequence_and_channel(kind, dt):
                       ("dstate_in", ends)):
         assert torch.isnan(got[name][hit]).all(), name
         assert torch.isfinite(clean[name]).all() and torch.equal(got[name][~hit], clean[name][~hit]), name
+
+
+@pytest.mark.parametrize("kind", ["rate", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_decays_and_weights_keep_their_bits_however_small(dt, kind):
+    """A step from a state of 1 without an input leaves the decay as the state, one of an input of 1 from zero its weight, in
+    float32: the hardware's exponential and reciprocal are off by a step (2 U) each, the factor for what the product with
+    log2 e leaves out, the product by it, the sum 1 + e and the last product by U each, and the one sum that a decay near 1 takes
+    by U: 9 U of the value, whatever the gate.  In bfloat16 the factor is 1 - 80 ln 2 7.1e-6 at least, in which the square of what is
+    taken from 1 is left out: half of (3.9e-4)^2, less than 2 U."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    g = torch.Generator().manual_seed(5)
+    z = torch.cat([torch.linspace(-80, 80, 6401), 3 * torch.randn(4000, generator=g), 30 * torch.randn(4000, generator=g).clamp(-2.5, 2.5)])
+    if kind == "rate":
+        z = z.abs()
+    z = z.to(dtype_of(dt)).cuda()[None]
+    most = 9 if dt == "f32" else 11
+    one, none = torch.ones_like(z), torch.zeros_like(z)
+    e = z.double().cpu().numpy()
+    cases = [(none, one, np.exp(-e) if kind == "rate" else 1 / (1 + np.exp(-e)))]
+    if kind == "sigmoid":
+        cases.append((one, none, 1 / (1 + np.exp(e))))
+    for x, before, want in cases:
+        state = before.float().clone()
+        lp.laplex_gated_scan_step(z, x, state, kind)
+        off = np.abs(host(state).astype(np.float64) - want) / want / ref.U
+        print("off by %.2f U" % off.max())
+        assert off.max() <= most
+
+
+@pytest.mark.parametrize("kind", ["rate", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gates_too_large_for_an_exponential(kind, dt):
+    """Decays and weights that are too small for a float are zeros, not NaN: gates up to infinity."""
+    import torch
+    import laplace_prefix_scans_amd as lp
+    inf = float("inf")
+    z = torch.tensor([200.0, 1e4, 2.5e38, 3.3e38, inf, 104.0, 88.0], device="cuda").to(dtype_of(dt))[None]
+    assert torch.isfinite(z[0, 3])
+    x, state = torch.full_like(z, 3.0), torch.full(z.shape, 2.0, device="cuda")
+    # (e^-88 is next to the smallest normal float: lost beside 2 and 3, as all the others are)
+    if kind == "rate":
+        cases = [(z, 3.0)]  # the decay is 0
+    else:
+        cases = [(z, 2.0), (-z, 3.0)]  # the state stays, the weight is 0; the other way round
+    for gate, want in cases:
+        h = lp.laplex_gated_scan(gate, x, kind, state_in=state)
+        assert (h == want).all()
+        assert torch.equal(h, lp.laplex_gated_scan_step(gate, x, state.clone(), kind))
