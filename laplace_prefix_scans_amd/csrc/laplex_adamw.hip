@@ -243,10 +243,10 @@ __global__ __launch_bounds__(kAdamBlock) void k_adamw(AdamArgs a) {
           if (i >= left) m[0][i] = v[0][i] = 0.f;
       }
       float mm = block_most(m[0], false), vm = block_most(v[0], false);
-      // (a NaN, which has no part in a maximum, shows in the sum of squares)
+      // (a NaN, which has no part in a maximum, shows in sums; a square that is too large only costs the second look)
       float all = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) all += v[0][i];
+      for (int i = 0; i < N; ++i) all = fmaf(m[0][i], m[0][i], all + v[0][i]);
       const bool bad = __any(!finite(all) || !finite(mm));
       if (bad) {
         mm = block_most(m[0], true);
