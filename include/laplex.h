@@ -550,10 +550,14 @@ typedef struct {
 /* AdamW step over `count` tensors (host array):
  *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
  *     p = (1 - lr weight_decay) p - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps),
- * in float32 without contractions.  8-bit moments are e4m3 codes in blocks of
- * 256 elements, scaled by the block's largest finite magnitude / 448; sqrt(v) >
- * 0 is never rounded to zero; a moment that is not finite becomes NaN (its
- * block's others keep their values).  No two of the call's outputs may overlap,
+ * in float32: m and v operation by operation, the quotient's denominator by a
+ * fused product (with 1 / sqrt(1 - beta2^step), rounded) and sum, the quotient by
+ * the denominator's reciprocal to one ulp (eps < 1e-30: by a division): off by at
+ * most 8.5 x 2^-24 of itself.  8-bit moments are e4m3 codes in blocks of 256
+ * elements, scaled by the block's largest finite magnitude / 448, rounded to
+ * nearest with ties away from zero, or with 16 random bits; sqrt(v) > 0 is never
+ * rounded to zero; a moment that is not finite becomes NaN (its block's others
+ * keep their values).  No two of the call's outputs may overlap,
  * nor an output and a gradient. */
 laplex_status laplex_adamw(const laplex_adamw_args* args, const laplex_adamw_tensor* tensors, uint32_t count, hipStream_t stream);
 

@@ -10,10 +10,10 @@
 //
 // 8-bit states: a block of 256 values (32 threads) shares a float scale, its
 // largest magnitude / 448; m and sqrt(v) are e4m3 codes of the values over it.
-// Rounding is stochastic: 16 random bits below the kept mantissa are added and
-// the rest cut off, so that a state's expectation is the value itself -- rounded
-// to nearest, a second moment that changes by a thousandth a step would never
-// leave its code.  sqrt(v) > 0 never becomes 0, or a step would be divided by eps.
+// Rounding is stochastic if asked for: 16 random bits below the kept mantissa are
+// added and the rest cut off, so that a state's expectation is the value itself --
+// rounded to nearest (half a step is added, so that ties go away from zero), a
+// second moment that changes by a thousandth a step would never leave its code.  sqrt(v) > 0 never becomes 0, or a step would be divided by eps.
 // The new parameters are made from the moments before they are rounded.
 #include <algorithm>
 #include <cmath>
