@@ -504,8 +504,8 @@ size_t laplex_linear_cross_entropy_workspace_bytes(int pass, int dtype, uint64_t
  * targets: `tokens` integers of id_bytes (4 or 8) bytes.  A target outside [0,
  * vocab) marks a token that is left out: its loss and lse are zero, whatever
  * its row holds.  loss, lse: `tokens` floats; either may be NULL.  Products are
- * added in float32.  tokens <= 2^28, vocab <= 2^26, width <= 2^20, and tokens x
- * vocab below about 2^38. */
+ * added in float32.  tokens <= 2^28, vocab <= 2^26, width <= 2^20, tokens x vocab
+ * below about 2^38, and tokens x width and vocab x width below about 2^42. */
 laplex_status laplex_linear_cross_entropy(int dtype, const void* targets, int id_bytes, uint64_t tokens, const void* x,
                                           const void* table, uint32_t vocab, uint32_t width, float scale, float* loss,
                                           float* lse, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -16,7 +16,7 @@ using namespace laplex;
 
 constexpr uint64_t kMaxTokens = 0x7FFFFFFFull;  // int32 offsets
 constexpr uint32_t kMaxSeqs = 1u << 20, kMaxWidth = 1u << 24, kMaxVocab = 1u << 26, kMaxXentWidth = 1u << 20;
-constexpr uint64_t kMaxXentTokens = 1ull << 28, kMaxBlocks = (1ull << 24) - 1;  // a launch has fewer than 2^32 threads
+constexpr uint64_t kMaxXentTokens = 1ull << 28, kMaxTiles = (1ull << 24) - 1, kMaxBlocks = (1ull << 24) - 1;  // a launch has fewer than 2^32 threads
 
 inline size_t elem(int dtype) { return dtype == LAPLEX_BF16 ? 2 : 4; }
 inline bool is_dtype(int dtype) { return dtype == LAPLEX_F32 || dtype == LAPLEX_BF16; }
@@ -141,9 +141,10 @@ namespace {
 laplex_status check_xent(int dtype, int id_bytes, uint64_t tokens, uint32_t vocab, uint32_t width) {
   if (!is_dtype(dtype) || (id_bytes != 4 && id_bytes != 8) || vocab == 0 || width == 0) return LAPLEX_ERR_ARG;
   if (tokens > kMaxXentTokens || vocab > kMaxVocab || width > kMaxXentWidth) return LAPLEX_ERR_SIZE;
-  // blocks of the products (tiles of at least 128 x 128 where there are many) and of the copies along the other axis
-  const uint64_t t = tokens / 64 + 1, v = vocab / 64 + 1, d = width / 64 + 1;
-  if ((t / 2 + 1) * (v / 2 + 1) > kMaxBlocks || t * d > kMaxBlocks || v * d > kMaxBlocks) return LAPLEX_ERR_SIZE;
+  // logits: 2^38 of them, in tiles of 128 x 128
+  if ((tokens / 128 + 1) * (vocab / 128 + 1) > kMaxTiles) return LAPLEX_ERR_SIZE;
+  // tiles of the gradients' products, at the smallest 64 of the width by 32, are counted in 32 bits
+  if ((width / 64 + 1ull) * (std::max<uint64_t>(tokens, vocab) / 32 + 1) >= 1ull << 31) return LAPLEX_ERR_SIZE;
   return LAPLEX_OK;
 }
 }  // namespace
