@@ -714,13 +714,13 @@ __global__ __launch_bounds__(256) void k_xent_parts_grad(ProductArgs a, LogitPar
 }
 
 // ------------------------------------------------------------------ joins
-// lse and loss of each token from its tiles' maxima and sums: TOKENS of them a block, 256 / TOKENS threads each
+// lse and loss of each token from t0 on from its tiles' maxima and sums: TOKENS of them a block, 256 / TOKENS threads each
 template <int TOKENS>
-__global__ __launch_bounds__(256) void k_xent_join(const float2* __restrict__ stats, uint32_t tiles, uint32_t tokens, const float* __restrict__ hit,
+__global__ __launch_bounds__(256) void k_xent_join(const float2* __restrict__ stats, uint32_t tiles, uint32_t t0, uint32_t tokens, const float* __restrict__ hit,
                                                    const void* targets, int id_bytes, uint32_t vocab, float* __restrict__ loss, float* __restrict__ lse) {
   constexpr int PARTS = 256 / TOKENS, N = 4;  // (loads on their way)
   __shared__ float2 sh[PARTS][TOKENS + 1];
-  const uint32_t i = threadIdx.x % TOKENS, k = threadIdx.x / TOKENS, t = blockIdx.x * TOKENS + i;
+  const uint32_t i = threadIdx.x % TOKENS, k = threadIdx.x / TOKENS, t = t0 + blockIdx.x * TOKENS + i;
   float m = -INFINITY, s = 0.f;
   const auto add = [&](float2 p) {
     const float n = fmaxf(m, p.x);
@@ -814,6 +814,8 @@ static double rate_of(bool bf, bool across, int tile) {
   const double rates[2][2][4] = {{{.57, .55, .54, .50}, {.41, .53, .53, .48}}, {{5.4, 3.8, 2.8, 1.7}, {4.9, 3.8, 2.1, 1.1}}};
   return rates[bf][across][tile];
 }
+// tokens of a launch of the join, which has 16 threads for each (a launch has fewer than 2^32)
+constexpr uint64_t kJoinMost = 1ull << 27;
 // partial sums of a split product, in floats
 constexpr uint64_t kPartFloats = 8ull << 20, kMostSplits = 64;
 constexpr double kStepLeast = 0.25;
@@ -991,10 +993,14 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
       return err;
     }
   }
-  LAPLEX_LAUNCH("k_xent_join", x.tokens, s, {
-    if (x.tokens <= 64) k_xent_join<1><<<(unsigned)x.tokens, 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse);
-    else k_xent_join<16><<<(unsigned)((x.tokens + 15) / 16), 256, 0, s>>>(w.stats, a.tiles_m, a.N, w.hit, x.targets, x.id_bytes, x.vocab, loss, lse);
-  });
+  const auto join = [&](auto tokens, uint64_t t0, uint64_t n) {
+    constexpr int TOKENS = decltype(tokens)::value;
+    LAPLEX_LAUNCH("k_xent_join", n, s,
+                  k_xent_join<TOKENS><<<(unsigned)((n + TOKENS - 1) / TOKENS), 256, 0, s>>>(w.stats, a.tiles_m, (uint32_t)t0, a.N, w.hit, x.targets, x.id_bytes,
+                                                                                          x.vocab, loss, lse));
+  };
+  if (x.tokens <= 64) join(std::integral_constant<int, 1>{}, 0, x.tokens);
+  else for (uint64_t t0 = 0; t0 < x.tokens; t0 += kJoinMost) join(std::integral_constant<int, 16>{}, t0, std::min(kJoinMost, x.tokens - t0));
   return hipGetLastError();
 }
 template <typename T>
