@@ -47,11 +47,13 @@ def _lib():
         L.laplex_gated_scan_backward.argtypes = [scan] + [vp] * 10 + [sz, vp]
         L.laplex_gated_scan_step.argtypes = [scan, vp, vp, vp, u32, vp, vp, vp]
         L.laplex_linear_cross_entropy_workspace_bytes.argtypes = [i32, i32, u64, u32, u32]
+        L.laplex_linear_cross_entropy_workspace_bytes_aligned.argtypes = [i32, i32, u64, u32, u32]
         L.laplex_linear_cross_entropy.argtypes = [i32, vp, i32, u64, vp, vp, u32, u32, f32, vp, vp, vp, sz, vp]
         L.laplex_linear_cross_entropy_backward.argtypes = [i32, vp, i32, u64, vp, vp, u32, u32, f32, vp, vp, vp, vp, i32, vp, vp, sz, vp]
         L.laplex_adamw.argtypes = [ctypes.POINTER(_AdamArgs), vp, u32, vp]
         L.laplex_adamw_moments.argtypes = [vp, u32, vp]
-        for f in (L.laplex_gated_scan_workspace_bytes, L.laplex_linear_cross_entropy_workspace_bytes):
+        for f in (L.laplex_gated_scan_workspace_bytes, L.laplex_linear_cross_entropy_workspace_bytes,
+                  L.laplex_linear_cross_entropy_workspace_bytes_aligned):
             f.restype = sz
         for f in (L.laplex_gated_scan, L.laplex_gated_scan_backward, L.laplex_gated_scan_step, L.laplex_linear_cross_entropy,
                   L.laplex_linear_cross_entropy_backward, L.laplex_adamw, L.laplex_adamw_moments):
@@ -206,10 +208,19 @@ def _xent(x, table, targets) -> Tuple[int, int, int, int, int]:
     return code, nb, targets.numel(), vocab, width
 
 
+def _xent_bytes(backward: bool, x, table, code: int, tokens: int, vocab: int, width: int) -> int:
+    L = _lib()
+    f = L.laplex_linear_cross_entropy_workspace_bytes
+    if (x.data_ptr() | table.data_ptr()) % 16 == 0:
+        f = L.laplex_linear_cross_entropy_workspace_bytes_aligned
+    return int(f(1 if backward else 0, code, tokens, vocab, width))
+
+
 def laplex_linear_cross_entropy_workspace_bytes(backward: bool, x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor) -> int:
-    """Bytes of workspace of laplex_linear_cross_entropy (or its backward) for these tensors."""
+    """Bytes of workspace of laplex_linear_cross_entropy (or its backward) for these tensors: also for fewer tokens, and
+    for other tensors of these sizes, but that where x and table begin at multiples of 16 bytes, they have to as well."""
     code, _, tokens, vocab, width = _xent(x, table, targets)
-    return int(_lib().laplex_linear_cross_entropy_workspace_bytes(1 if backward else 0, code, tokens, vocab, width))
+    return _xent_bytes(backward, x, table, code, tokens, vocab, width)
 
 
 def laplex_linear_cross_entropy(x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, scale: float = 1.0,
@@ -221,7 +232,7 @@ def laplex_linear_cross_entropy(x: torch.Tensor, table: torch.Tensor, targets: t
     dev = x.device
     loss, lse = torch.empty((2, *targets.shape), dtype=torch.float32, device=dev).unbind(0)
     L = _lib()
-    ws, ws_bytes = _bytes(ws, L.laplex_linear_cross_entropy_workspace_bytes(0, code, tokens, vocab, width), dev)
+    ws, ws_bytes = _bytes(ws, _xent_bytes(False, x, table, code, tokens, vocab, width), dev)
     _run("laplex_linear_cross_entropy", dev, L.laplex_linear_cross_entropy, code, _ptr(targets), nb, tokens, _ptr(x), _ptr(table), vocab,
          width, scale, _ptr(loss), _ptr(lse), _ptr(ws), ws_bytes)
     return loss, lse
@@ -246,7 +257,7 @@ def laplex_linear_cross_entropy_backward(x: torch.Tensor, table: torch.Tensor, t
     dx = torch.empty_like(x) if x_grad else None
     dtable = torch.empty((vocab, width), dtype=dtype, device=dev) if table_grad else None
     L = _lib()
-    ws, ws_bytes = _bytes(ws, L.laplex_linear_cross_entropy_workspace_bytes(1, code, tokens, vocab, width), dev)
+    ws, ws_bytes = _bytes(ws, _xent_bytes(True, x, table, code, tokens, vocab, width), dev)
     _run("laplex_linear_cross_entropy_backward", dev, L.laplex_linear_cross_entropy_backward, code, _ptr(targets), nb, tokens, _ptr(x),
          _ptr(table), vocab, width, scale, _ptr(lse), _ptr(dloss), _ptr(dlse), _ptr(dx), _DTYPES[dtype], _ptr(dtable), _ptr(ws), ws_bytes)
     return dx, dtable

@@ -34,7 +34,9 @@ struct XentShape {
   const void *targets, *x, *table;
   float scale;
 };
-size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width);
+// aligned: of calls whose x and table begin at multiples of 16 bytes, as xent_aligned tells
+size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width, bool aligned);
+bool xent_aligned(const void* x, const void* table);
 hipError_t xent(const XentShape& a, float* loss, float* lse, void* ws, hipStream_t s);
 hipError_t xent_backward(const XentShape& a, const float* lse, const float* dloss, const float* dlse, void* dx, int table_dtype,
                          void* dtable, void* ws, hipStream_t s);

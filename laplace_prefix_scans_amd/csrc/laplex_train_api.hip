@@ -149,9 +149,18 @@ laplex_status check_xent(int dtype, int id_bytes, uint64_t tokens, uint32_t voca
 }
 }  // namespace
 
-extern "C" size_t laplex_linear_cross_entropy_workspace_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width) {
+namespace {
+size_t xent_workspace(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width, bool aligned) {
   if ((pass != 0 && pass != 1) || check_xent(dtype, 4, tokens, vocab, width) != LAPLEX_OK) return 0;
-  return xent_bytes(pass, dtype, tokens, vocab, width);
+  return xent_bytes(pass, dtype, tokens, vocab, width, aligned);
+}
+}  // namespace
+
+extern "C" size_t laplex_linear_cross_entropy_workspace_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width) {
+  return xent_workspace(pass, dtype, tokens, vocab, width, false);
+}
+extern "C" size_t laplex_linear_cross_entropy_workspace_bytes_aligned(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width) {
+  return xent_workspace(pass, dtype, tokens, vocab, width, true);
 }
 
 extern "C" laplex_status laplex_linear_cross_entropy(int dtype, const void* targets, int id_bytes, uint64_t tokens, const void* x,
@@ -161,7 +170,7 @@ extern "C" laplex_status laplex_linear_cross_entropy(int dtype, const void* targ
   if (st != LAPLEX_OK) return st;
   if (tokens == 0) return LAPLEX_OK;
   if (!targets || !x || !table || !ws || (!loss && !lse)) return LAPLEX_ERR_NULL;
-  const size_t e = elem(dtype), need = xent_bytes(0, dtype, tokens, vocab, width);
+  const size_t e = elem(dtype), need = xent_bytes(0, dtype, tokens, vocab, width, xent_aligned(x, table));
   if (misaligned(targets, id_bytes) || misaligned(x, e) || misaligned(table, e) || misaligned(loss, 4) || misaligned(lse, 4) || misaligned(ws, 256))
     return LAPLEX_ERR_ALIGN;
   if (ws_bytes < need) return LAPLEX_ERR_WORKSPACE;
@@ -181,7 +190,7 @@ extern "C" laplex_status laplex_linear_cross_entropy_backward(int dtype, const v
   if (table_dtype != dtype && table_dtype != LAPLEX_F32) return LAPLEX_ERR_ARG;
   if ((!dx || tokens == 0) && !dtable) return LAPLEX_OK;
   if (!ws || (tokens && (!targets || !x || !table || !lse || !dloss))) return LAPLEX_ERR_NULL;
-  const size_t e = elem(dtype), te = elem(table_dtype), need = xent_bytes(1, dtype, tokens, vocab, width);
+  const size_t e = elem(dtype), te = elem(table_dtype), need = xent_bytes(1, dtype, tokens, vocab, width, xent_aligned(x, table));
   if ((tokens && misaligned(targets, id_bytes)) || misaligned(x, e) || misaligned(table, e) || misaligned(dx, e) || misaligned(dtable, te) ||
       misaligned(lse, 4) || misaligned(dloss, 4) || misaligned(dlse, 4) || misaligned(ws, 256))
     return LAPLEX_ERR_ALIGN;

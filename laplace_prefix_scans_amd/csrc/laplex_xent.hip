@@ -839,6 +839,11 @@ static Tiling tiling(bool bf, bool across, uint64_t M, uint64_t N, uint64_t K, b
   return best;
 }
 
+// Whether the forward goes by the table row after row
+static bool few_tokens(uint64_t tokens, uint64_t width, uint64_t e) {
+  return tokens <= (uint64_t)(width * e % kPieceK ? kFewTokens : kFewTokensWhole) && kFewTokens * up(width, kWave * 16 / e) * e <= kFewBytes;
+}
+
 struct XentWorkspace {
   void *x_rows, *table_rows;  // filled up copies, where rows are not whole pieces
   float2* stats;
@@ -848,18 +853,20 @@ struct XentWorkspace {
   float* part;  // parts of a split product
 };
 static bool whole_rows(const void* p, uint64_t width, uint64_t e) { return width * e % kPieceK == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width, size_t* total) {
+// aligned: x and the table begin at multiples of 16 bytes, so that rows of whole pieces need no copies
+static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width, bool aligned, size_t* total) {
   const uint64_t e = dtype == LAPLEX_BF16 ? 2 : 4;
   const XentPlan p = xent_plan(dtype, tokens, vocab, width);
   Carver c(ws);
   XentWorkspace w{};
-  w.x_rows = c.take<void>(p.k_tokens * p.k_width * e);
-  w.table_rows = c.take<void>(vocab * p.k_width * e);
+  const bool few = pass == 0 && few_tokens(tokens, width, e), lie = few || (aligned && whole_rows(nullptr, width, e));
+  if (pass == 1 || !lie) w.x_rows = c.take<void>(p.k_tokens * p.k_width * e);
+  if (!lie) w.table_rows = c.take<void>(vocab * p.k_width * e);
   if (pass == 0) {
     // (of the smallest tiles, or of a few tokens' blocks)
     w.stats = c.take<float2>(std::max<uint64_t>(tiles(vocab, TileS::BM) * tokens, few_blocks(vocab) * std::min<uint64_t>(tokens, kFewTokens)) * 8);
     w.hit = c.take<float>(tokens * 4);
-    w.part = c.take<float>(std::min<uint64_t>(kPartFloats, kMostSplits * tokens * vocab) * 4);
+    if (!few) w.part = c.take<float>(std::min<uint64_t>(kPartFloats, kMostSplits * tokens * vocab) * 4);
   } else {
     // (a piece has at most kPiece bytes, or one tile of the vocabulary, or all of it)
     const uint64_t bk = kPieceK / e;
@@ -873,11 +880,12 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
   *total = (c.off + 255) & ~size_t(255);
   return w;
 }
-size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width) {
+size_t xent_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width, bool aligned) {
   size_t total = 0;
-  xent_carve(nullptr, pass, dtype, tokens, vocab, width, &total);
+  xent_carve(nullptr, pass, dtype, tokens, vocab, width, aligned, &total);
   return total;
 }
+bool xent_aligned(const void* x, const void* table) { return (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(table)) % 16 == 0; }
 
 enum Product { LOGITS_STATS, LOGITS_GRAD, LOGITS_PARTS, DX, DTABLE };
 template <typename T, typename C>
@@ -963,7 +971,7 @@ template <typename T>
 static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws, hipStream_t s) {
   size_t total;
   const XentPlan p = xent_plan(x.dtype, x.tokens, x.vocab, x.width);
-  const XentWorkspace w = xent_carve(ws, 0, x.dtype, x.tokens, x.vocab, x.width, &total);
+  const XentWorkspace w = xent_carve(ws, 0, x.dtype, x.tokens, x.vocab, x.width, xent_aligned(x.x, x.table), &total);
   ProductArgs a{};
   a.A = x.table;
   a.B = x.x;
@@ -976,7 +984,7 @@ static hipError_t forward(const XentShape& x, float* loss, float* lse, void* ws,
   a.stats = w.stats;
   a.hit = w.hit;
   hipError_t err;
-  if (x.tokens <= (x.width * sizeof(T) % kPieceK ? kFewTokens : kFewTokensWhole) && kFewTokens * up(x.width, kWave * 16 / sizeof(T)) * sizeof(T) <= kFewBytes) {
+  if (few_tokens(x.tokens, x.width, sizeof(T))) {
     if ((err = few<T>(a, x.width, s)) != hipSuccess) return err;
   } else {
     if ((err = whole<T>(x, p, w, false, &a.B, &a.A, s)) != hipSuccess) return err;
@@ -1008,7 +1016,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
                            void* dtable, void* ws, hipStream_t s) {
   size_t total;
   const XentPlan p = xent_plan(x.dtype, x.tokens, x.vocab, x.width);
-  const XentWorkspace w = xent_carve(ws, 1, x.dtype, x.tokens, x.vocab, x.width, &total);
+  const XentWorkspace w = xent_carve(ws, 1, x.dtype, x.tokens, x.vocab, x.width, xent_aligned(x.x, x.table), &total);
   const uint32_t tokens = (uint32_t)x.tokens;
   const void *table = x.table, *rows = x.x;
   hipError_t err;
