@@ -520,8 +520,9 @@ laplex_status laplex_linear_cross_entropy(int dtype, const void* targets, int id
  * forward call gave:
  *     G_tv = scale [(dloss_t + dlse_t) exp(l_tv - lse_t) - dloss_t [v = target_t]],   dx = G table,   dtable = G^T x.
  * G is formed in pieces of the vocabulary and rounded once to dtype, as a factor
- * of the two products (bfloat16 and at most 2048 tokens: held in two parts).  Tokens that are left out have zero rows in dx and take
- * no part in dtable.  dx: tokens x width of type dtype; dtable: vocab x width of
+ * of the two products; of bfloat16 a second part holds what the rounding left out,
+ * for at most 2048 tokens and for a dtable in float32.  Tokens that are left out
+ * have zero rows in dx and take no part in dtable.  dx: tokens x width of type dtype; dtable: vocab x width of
  * type table_dtype (dtype or LAPLEX_F32); either may be NULL. */
 laplex_status laplex_linear_cross_entropy_backward(int dtype, const void* targets, int id_bytes, uint64_t tokens, const void* x,
                                                    const void* table, uint32_t vocab, uint32_t width, float scale,

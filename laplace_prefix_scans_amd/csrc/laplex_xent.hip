@@ -774,8 +774,11 @@ static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + 
 // G in two parts of bfloat16, which hold 16 of its bits, for so many tokens: half a step of the one that a token's row of dx
 // is mostly made of shows in the row, and among few tokens in the whole (11 tokens, 227 x 2696: dx off by 0.0030 of its size, with
 // two parts 0.0017, which is its own rounding; the backward of 200 tokens, 500 x 4096 takes 33 us instead of 26, of 64, 65536 x 2048 404
-// instead of 278, of 1000, 8000 x 1024 128 instead of 90).  Among 600 it still is up to 1.5 times its own rounding, among more 0.0024 and no more than that, where the
-// products, which the matrix cores bound, would be six instead of four.
+// instead of 278, of 1000, 8000 x 1024 128 instead of 90).  Among 600 it still is up to 1.5 times its own rounding.  Among more it is
+// 1.44 times that and no more, G's half step beside its own, and the products, which the matrix cores bound, would be six
+// instead of four (16384 tokens, 65536 x 2048, forward and backward: off by 0.0024 and 0.0022 of dx and dtable, 13.65 ms; with two
+// parts 0.0017 and 0.0017, 20.85 ms; 2049, 8000 x 1024: 0.0024 and 0.0023, 256 us; 0.0017 and 0.0017, 378).  A gradient
+// of the table in float32 has no rounding beside which one part's could be lost: its product takes two always.
 constexpr uint64_t kTwoParts = 2048;
 struct XentPlan {
   uint64_t k_width, k_tokens;  // extents of k, whole pieces
@@ -849,6 +852,7 @@ struct XentWorkspace {
   float2* stats;
   float* hit;
   void* G;
+  uint64_t g_bytes;
   float* dx;    // dx while pieces of the vocabulary are added to it
   float* part;  // parts of a split product
 };
@@ -873,7 +877,8 @@ static XentWorkspace xent_carve(void* ws, int pass, int dtype, uint64_t tokens, 
     const auto g = [&](uint64_t rows) { return std::max<uint64_t>(std::min<uint64_t>(kPiece, up(vocab, bk) * rows * e), kTile * rows * e); };
     // (of more tokens' one part, or those at the switch, of which there are two)
     const uint64_t two = dtype == LAPLEX_BF16 ? up(std::min(tokens, kTwoParts), bk) * 2 : 0;
-    w.G = c.take<void>(std::max(g(p.k_tokens), g(two)));
+    w.g_bytes = std::max(g(p.k_tokens), g(two));
+    w.G = c.take<void>(w.g_bytes);
     w.dx = c.take<float>(tokens * width * 4);
     w.part = c.take<float>(kPartFloats * 4);
   }
@@ -1015,11 +1020,17 @@ template <typename T>
 static hipError_t backward(const XentShape& x, const float* lse, const float* dloss, const float* dlse, void* dx, int table_dtype,
                            void* dtable, void* ws, hipStream_t s) {
   size_t total;
-  const XentPlan p = xent_plan(x.dtype, x.tokens, x.vocab, x.width);
+  XentPlan p = xent_plan(x.dtype, x.tokens, x.vocab, x.width);
   const XentWorkspace w = xent_carve(ws, 1, x.dtype, x.tokens, x.vocab, x.width, xent_aligned(x.x, x.table), &total);
   const uint32_t tokens = (uint32_t)x.tokens;
   const void *table = x.table, *rows = x.x;
   hipError_t err;
+  const bool dx_parts = p.parts > 1;  // (the table's gradient in float32 takes two where dx has one: G's place then holds fewer entries)
+  if (sizeof(T) == 2 && tokens && dtable && table_dtype == LAPLEX_F32 && !dx_parts) {
+    p.parts = 2;
+    const uint64_t fit = w.g_bytes / (2 * sizeof(T) * p.k_tokens);  // (at least 64: there is room for 128 of one part)
+    p.piece = (uint32_t)std::min<uint64_t>(p.piece, fit >= kTile ? fit / kTile * kTile : kTile / 2);
+  }
   if (tokens) {  // (without, dtable is a sum of nothing)
     if ((err = whole<T>(x, p, w, true, &rows, &table, s)) != hipSuccess) return err;
   } else {
@@ -1041,7 +1052,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
   l.n_fill = (uint32_t)p.k_tokens;
   // A product that may be split: to its place, or its parts and then their sum
   const auto output = [&](const char* name, Product epi, ProductArgs& a) {
-    const Tiling t = tiling(sizeof(T) == 2, true, a.M, a.N, a.K * p.parts, !a.add);
+    const Tiling t = tiling(sizeof(T) == 2, true, a.M, a.N, a.rest ? 2 * a.K : a.K, !a.add);
     if (t.splits == 1) return product<T>(name, epi, a, t, s);
     void* const out = a.out;
     const bool f32 = a.out_f32;
@@ -1083,7 +1094,7 @@ static hipError_t backward(const XentShape& x, const float* lse, const float* dl
       a.lda = l.lda;
       a.B = w.G;
       a.ldb = (int64_t)fill;
-      a.rest = l.rest;
+      a.rest = dx_parts ? l.rest : 0;
       a.K = fill;
       a.k_rows = n;
       a.M = x.width;
