@@ -11,10 +11,11 @@
 // pass.  Segments are cut without regard to sequences: a token that begins a
 // sequence replaces the state before it, whatever that is.
 //
-// Memory bounds the passes: 8 x 2048 tokens x 4096 channels in bfloat16 take 53 us
-// for the forward's aggregates (5.1 TB/s), 78 for the whole pass (5.4), 45 and
-// 128 for the backward's (6.0 with what the caches hold, 5.4), 6 for each join;
-// together 302 us, where the bytes that cannot be done without take 219.
+// Memory bounds the passes: under the profiler 8 x 2048 tokens x 4096 channels in
+// bfloat16 take 52 us for the forward's aggregates (5.1 TB/s), 78 for the whole
+// pass (5.4), 46 and 128 for the backward's (5.9 with what the caches hold, 5.4),
+// 6 for each join, 316 together; without it the calls take 303, where the bytes
+// that cannot be done without take 169 at the rate of a plain copy (6.35 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -179,7 +180,8 @@ static_assert(kGateU == 16, "marks of a tile are 16 bits");
 // the other (STEP 1 or -1): their address is the wave's, and moves on by scalar additions, to which a load adds 32 bits.
 // Rows past the last token are read as it.  What the whole pass reads (LAST) and writes goes past the caches, which are left
 // to what the aggregates have read (16384 tokens x 4096 channels in bfloat16, forward and backward: 316 us, through the
-// caches 350; 65536 x 256 in float 74, 83; the loads alone, as all of this is now: 302 and 304, 68 and 71).
+// caches 350; 65536 x 256 in float 74, 83; the loads alone, as all of this is now: 303 and 306, 69 and 72 for inputs that change from
+// call to call; for the same ones again, which a part of the caches still holds, 304 and 300, 65 and 62).
 // A bfloat16 is held as the word that its load makes, and becomes a float where it is used: held as what it is, two are packed
 // into a register, or masked, as soon as they arrive, which is waited for at the end of each tile (16384 tokens x 4096 channels,
 // aggregates of the forward and the backward: 84 and 67 us so, 52 and 46 now).  Which width avoids that differs by loop.
@@ -643,7 +645,7 @@ struct GatePlan {
   int64_t seg_len;
 };
 // As many waves as the chip holds at once of the passes with 88 registers (five a SIMD), segments of at least four tiles
-// (16384 tokens x 4096 channels in bfloat16, forward and backward: 302 us; 4096 waves 327, 6144 303, 8192 338).
+// (16384 tokens x 4096 channels in bfloat16, forward and backward: 304 us; 4096 waves 331, 6144 307, 8192 342).
 constexpr uint64_t kGateUnits = 5120, kGateLeast = 64;
 static GatePlan gate_plan(uint32_t channels, uint64_t tokens) {
   GatePlan p;

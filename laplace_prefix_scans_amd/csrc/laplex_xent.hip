@@ -100,8 +100,8 @@ __device__ __forceinline__ void tile_of(const ProductArgs& a, uint32_t id, uint3
 // while those before are multiplied; a row's eight 16-byte pieces lie at piece ^ (row & 7), so that the reads of 16
 // rows' pieces spread over the banks.  A step's 128 bytes are two halves, and a half's operands are read one half ahead of
 // their products, across the step's one barrier: it stands in the middle of a step, where both halves of it have been read
-// and the next one's bytes have arrived.  (16384 tokens, 65536 x 2048 in bfloat16, forward and backward: 13.5 ms, 1301 TFLOP/s;
-// forward of 2043 tokens 420 us, of whose cycles the matrix cores are busy in two thirds.  Four steps in LDS instead of two for
+// and the next one's bytes have arrived.  (16384 tokens, 65536 x 2048 in bfloat16, forward and backward: 13.6 to 13.7 ms by card,
+// 1290 TFLOP/s; forward of 2043 tokens 383 to 425 us by card and clock, the matrix cores busy in 0.7 of the cycles.  Four steps in LDS instead of two for
 // the 64 x 32 tiles: 4096 tokens, 257 x 513 in float 91 us instead of 88.)
 template <int M, int N, int WAVES_M, int WAVES_N, int BLOCKS>
 struct Tile {
@@ -765,7 +765,7 @@ __global__ __launch_bounds__(256) void k_xent_sum(const float* __restrict__ part
 
 // ------------------------------------------------------------------ plan
 constexpr uint32_t kTile = 128;
-// bytes of G (16384 tokens, 65536 x 2048 in bfloat16: 13394 us; twice as many 13604, half 13826)
+// bytes of G (16384 tokens, 65536 x 2048 in bfloat16, forward and backward, on one card in turn: 13.60 ms; twice as many 13.77, half 13.81)
 constexpr uint64_t kPiece = 1ull << 29;
 static uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 static uint32_t tiles(uint64_t n, uint32_t of = kTile) { return (uint32_t)((n + of - 1) / of); }
