@@ -494,8 +494,8 @@ laplex_status laplex_gated_scan_step(const laplex_scan_shape* shape, const void*
                                      uint32_t pool, float* state, void* h, hipStream_t stream);
 
 /* Bytes of workspace of laplex_linear_cross_entropy (pass 0) and of its backward
- * (pass 1), which serve any call with fewer tokens too; 0 when out of range.  The
- * second one's serve calls whose x and table both begin at multiples of 16 bytes:
+ * (pass 1), which serve any call with fewer tokens too; 0 when out of range, and
+ * for a forward of no tokens.  The second one's serve calls whose x and table both begin at multiples of 16 bytes:
  * where rows are whole 128-byte pieces, such tensors are read as they lie, and
  * there is no room for copies of them (of the table: vocab x width elements).
  * A call asks for what its own pointers need. */
