@@ -495,10 +495,10 @@ laplex_status laplex_gated_scan_step(const laplex_scan_shape* shape, const void*
 
 /* Bytes of workspace of laplex_linear_cross_entropy (pass 0) and of its backward
  * (pass 1), which serve any call with fewer tokens too; 0 when out of range, and
- * for a forward of no tokens.  The second one's serve calls whose x and table both begin at multiples of 16 bytes:
- * where rows are whole 128-byte pieces, such tensors are read as they lie, and
- * there is no room for copies of them (of the table: vocab x width elements).
- * A call asks for what its own pointers need. */
+ * for a forward of no tokens.  The second one's serve calls whose x and table
+ * both begin at multiples of 16 bytes: where rows are whole 128-byte pieces, such
+ * tensors are read as they lie, and there is no room for copies of them (of the
+ * table: vocab x width elements).  A call asks for what its own pointers need. */
 size_t laplex_linear_cross_entropy_workspace_bytes(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width);
 size_t laplex_linear_cross_entropy_workspace_bytes_aligned(int pass, int dtype, uint64_t tokens, uint32_t vocab, uint32_t width);
 
